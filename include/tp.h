@@ -23,7 +23,8 @@
  *     RoPE table and a small device status word, all freed by tp_free.
  *   - Errors: argument and rule violations are returned before anything is
  *     launched.  Errors found on the device (a token id >= vocab, a pipeline
- *     wait that ran out) set the model's device status word; tp_check_device
+ *     wait that ran out, an index outside its table) set the model's device
+ *     status word; tp_check_device
  *     reads and clears it.  No call aborts the process or throws.
  *   - Workspace: calls that take (ws, ws_bytes) need at least
  *     tp_workspace_bytes(model, M) bytes, zero-filled before the first use
@@ -53,7 +54,10 @@ typedef enum {
   TP_ERR_CUDA = 6,           /* a CUDA runtime call failed */
   TP_ERR_DEVICE_TIMEOUT = 7, /* (device) a bounded pipeline wait ran out */
   TP_ERR_UNSUPPORTED = 8,    /* shape outside the kernels' envelope (see tp_config) */
-  TP_ERR_WORKSPACE = 9       /* workspace missing or smaller than tp_workspace_bytes */
+  TP_ERR_WORKSPACE = 9,      /* workspace missing or smaller than tp_workspace_bytes
+                                (tp_step_workspace_bytes for the paged calls) */
+  TP_ERR_TABLE_RANGE = 10    /* (device) a length, page, slot, position or row index of the
+                                paged calls outside its table, or no free page left */
 } tp_status;
 
 /* Model shape.  The caller fills the first block; tp_config validates it and
@@ -461,7 +465,8 @@ tp_status tp_profile_read(tp_model* m, void* stream, tp_kernel_time_t* out, int3
                           int32_t* n);
 
 /* Synchronises `stream`, returns the device status word (TP_OK,
- * TP_ERR_TOKEN_RANGE or TP_ERR_DEVICE_TIMEOUT) and clears it. */
+ * TP_ERR_TOKEN_RANGE, TP_ERR_DEVICE_TIMEOUT or TP_ERR_TABLE_RANGE: the first
+ * one found) and clears it. */
 tp_status tp_check_device(tp_model* m, void* stream);
 
 /* Failure-detection self-test (no counterpart on the pages): launches one
@@ -472,6 +477,201 @@ tp_status tp_check_device(tp_model* m, void* stream);
  * nothing faults and the context stays usable.  tp_check_device reports and
  * clears the status. */
 tp_status tp_selftest_wait_timeout(tp_model* m, int32_t milliseconds, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Paged KV cache, drafted trees and logit rules (no counterpart on the pages'
+ * forward; the calls a serving loop makes around it).  One verification step:
+ *   tp_step_tables    -> slots, positions and tree masks of the drafted tokens
+ *   per layer: tp_column_linear(TP_QKV) -> tp_cache_append -> tp_tree_attention
+ *              -> tp_row_linear_reduce(TP_O) ...
+ *   tp_lm_head_gather -> tp_process_logits, and the caller accepts a path
+ *   tp_cache_append of the kept qkv rows, the accepted path's rows at the
+ *   sequence's first slots of the step and slot -1 elsewhere; tp_step_tables
+ *   with the shorter lengths returns the pages no longer needed.
+ * A single new token is a tree of one; a prompt chunk is a chain.
+ *
+ * Cache (per layer, caller-owned, bf16): K or V of copy c, page p, KV head g
+ * (local to the copy), offset x in the page, element e lives at
+ *   base[(((c*n_pages + p)*kv_heads_per_rank + g)*page_size + x)*head_dim + e]
+ * with copies and local heads as in tp_batch_t.  Slot s is offset s % page_size
+ * of page s / page_size.  Position l of sequence b sits in page
+ * table[b*ld_table + l/page_size].  The cache needs no initialisation: slots
+ * that no token owns are never used, whatever they hold.
+ * Every call returns TP_ERR_ARG when the current device is not the one that
+ * tp_load_shards ran on. */
+
+/* The page tables.  page_size: a multiple of 8, 8..65536, and n_pages *
+ * page_size < 2^31 (TP_ERR_UNSUPPORTED otherwise). */
+typedef struct {
+  int32_t n_pages;
+  int32_t page_size;
+  int32_t ld_table;            /* pages a row of the table can hold */
+  int32_t* table;              /* [rows][ld_table], at least n_seqs rows */
+  int32_t* free_ring;          /* [n_pages]: the free pages are ring entries
+                                  first, first+1, ... first+count-1 (mod n_pages) */
+  const int32_t* free_state;   /* [2]: first, count */
+  int32_t* free_next;          /* [2]: first, count after tp_step_tables; may be
+                                  free_state itself.  With another buffer the
+                                  call proposes: repeated with the same
+                                  free_state it gives the same tables. */
+} tp_pages_t;
+
+/* One step of n_seqs sequences: sequence b goes from old_lens[b] to
+ * new_lens[b] tokens, its T_b = max(new - old, 0) new tokens are rows
+ * q_start[b] .. q_start[b] + T_b - 1 of the step's token arrays.
+ * n_tokens is the capacity of those arrays; rows behind the last sequence's
+ * are padding.  A sequence not in use has old = new = 0. */
+typedef struct {
+  int32_t n_seqs;              /* 1..8192 */
+  int32_t n_tokens;
+  int32_t max_new;             /* host: no T_b is larger */
+  int32_t max_ctx;             /* host: no length is larger */
+  int32_t tree_words;          /* 64-bit words of a tree mask row (with tree_mask) */
+  const int32_t* old_lens;     /* [n_seqs] */
+  const int32_t* new_lens;     /* [n_seqs] */
+  const int32_t* parents;      /* [n_tokens] or NULL (chains): the parent of token i of a
+                                  sequence is its token parents[q_start + i] < i, or -1
+                                  for a child of the old tokens */
+  int32_t* q_start;            /* [n_seqs + 1] */
+  int32_t* slots;              /* [n_tokens] */
+  int32_t* positions;          /* [n_tokens] */
+  int32_t* token_seq;          /* [n_tokens] */
+  uint64_t* tree_mask;         /* [n_tokens][tree_words] or NULL: bit t of row i = new
+                                  token t of the sequence is i or an ancestor of i */
+} tp_step_t;
+
+/* Workspace bytes of tp_step_tables and tp_tree_attention for steps of up to
+ * n_seqs sequences with up to max_new new tokens each (0 for sizes outside
+ * the calls' limits).  Zero-fill it once with tp_workspace_init; the kernels
+ * leave it zero where it has to be.  Calls that may overlap on the GPU (two
+ * streams, two graphs replayed at once) need a workspace each. */
+size_t tp_step_workspace_bytes(const tp_model* m, int32_t n_seqs, int32_t max_new);
+
+/* Block tables and slot map of a step from its lengths, in one launch.
+ * With pages(x) = ceil(x / page_size), a growing sequence takes
+ * pages(new) - pages(old) pages from the front of the ring, sequences in
+ * order, into its row of the table; a shrinking one returns its pages from
+ * pages(new) on to the ring's end (usable from the next call on; its row
+ * keeps their numbers).  Writes
+ *   q_start, slots (of logical position old + i), token_seq,
+ *   positions: old + i, or with parents old + the number of i's ancestors,
+ *   tree_mask, when not NULL (with parents NULL: bits 0..i),
+ *   free_next.
+ * Padding rows get slot -1, position 0, token_seq -1 and an empty mask.
+ * With tree_mask or parents, max_new <= 256; with tree_mask also
+ * max_new <= 64 * tree_words (TP_ERR_UNSUPPORTED otherwise).
+ * Errors on the device (TP_ERR_TABLE_RANGE): a length below 0, above max_ctx
+ * or above ld_table * page_size, more than max_new new tokens in a sequence
+ * or n_tokens in all, fewer free pages than needed, a ring state outside the
+ * ring.  Then no page moves (free_next = free_state), q_start is all 0 and
+ * every row is padding.  A parent not below its token counts as -1, and a
+ * page number outside [0, n_pages) gives slot -1, each with that status. */
+tp_status tp_step_tables(const tp_model* m, const tp_pages_t* pages, const tp_step_t* step,
+                         void* ws, size_t ws_bytes, void* stream);
+
+/* RoPE on q and k, and the new K and V rows into their cache slots.
+ *   qkv       : output of tp_column_linear(TP_QKV): rank r's [M, N_r] at
+ *               qkv + r*rank_stride (elements, a multiple of 8, >= M*N_r)
+ *   positions : [M], in [0, max_positions)
+ *   slots     : [M]; -1: the row is not stored
+ *   k, v      : the layer's cache (read above; pages gives n_pages and
+ *               page_size, its other fields are not used)
+ *   q         : [M, n_heads*d] with row stride ld_q (a multiple of 8), rotated
+ *               queries in global head order; NULL: not wanted
+ * Arithmetic in fp32, one rounding to bf16; V is copied.  Of replica ranks the
+ * first one's K and V are stored.  qkv, q, k and v must not overlap, and no
+ * two rows may name the same slot.  A position outside the RoPE table (its q
+ * row becomes zeros and nothing is stored) or a slot outside the cache (not
+ * stored) sets TP_ERR_TABLE_RANGE. */
+tp_status tp_cache_append(const tp_model* m, const tp_bf16* qkv, int64_t rank_stride, int32_t M,
+                          const int32_t* positions, const int32_t* slots,
+                          const tp_pages_t* pages, tp_bf16* k, tp_bf16* v, tp_bf16* q,
+                          int64_t ld_q, void* stream);
+
+/* Attention of a step's new tokens over the paged cache, per rank on its own
+ * heads as in the decoder layer.  Row i of sequence b sees the old tokens
+ * 0..old_lens[b]-1 and, of the new ones, token t (at position old_lens[b] + t
+ * of the cache) when bit t of its tree mask is set; with tree_mask NULL, when
+ * t <= i.  A row that sees nothing gets zeros.  Scores and softmax in fp32
+ * (probabilities rounded to bf16 before the product with V, as V is), scale
+ * 1/sqrt(d), one rounding of the output.  The result does not depend on what
+ * cache slots hold that the row does not see, infinities and NaN included.
+ *   q, o  : [n_tokens, n_heads*d], row strides ld_q, ld_o (multiples of 8);
+ *           they must not overlap.  Padding rows of o are not written.
+ *   pages : n_pages, page_size, ld_table and table are used
+ *   step  : n_seqs, n_tokens, max_new (<= 256), max_ctx (>= every old + T),
+ *           old_lens, q_start, tree_mask and tree_words are used; the
+ *           others may be NULL
+ *   k, v  : the layer's cache, 16-byte aligned
+ * Deterministic.  Errors on the device (TP_ERR_TABLE_RANGE): a sequence whose
+ * q_start or length leaves its bounds is skipped (its rows of o are not
+ * written); a page number outside [0, n_pages) reads as keys and values of
+ * zero. */
+tp_status tp_tree_attention(const tp_model* m, const tp_bf16* q, int64_t ld_q, tp_bf16* o,
+                            int64_t ld_o, const tp_pages_t* pages, const tp_step_t* step,
+                            const tp_bf16* k, const tp_bf16* v, void* ws, size_t ws_bytes,
+                            void* stream);
+
+/* What tp_process_logits applies.  Row s of the logits belongs to request
+ * row_req[s] (NULL: request s); a row with row_req -1 is left as it was.
+ * A pointer that is NULL leaves its rule out. */
+typedef struct {
+  int32_t n_reqs;
+  const int32_t* row_req;        /* [S] */
+  /* penalties, per request: history[r*ld_history + 0 .. history_lens[r]) is
+   * its text, the first prompt_lens[r] of it (NULL: none) the prompt.  Ids
+   * outside [0, vocab) are ignored. */
+  const int32_t* history;
+  int64_t ld_history;
+  const int32_t* history_lens;   /* [n_reqs], with history */
+  const int32_t* prompt_lens;    /* [n_reqs] */
+  const float* repetition;       /* [n_reqs], > 0 */
+  const float* frequency;        /* [n_reqs] */
+  const float* presence;         /* [n_reqs] */
+  /* drafted paths: row s is token s of a step, and the drafted tokens on its
+   * path (bit t of its mask: token draft_tokens[q_start[r] + t]) count as
+   * written by the model, itself included.  All three, or none. */
+  const int32_t* draft_tokens;   /* [S] */
+  const uint64_t* tree_mask;     /* [S][tree_words], 1 <= tree_words <= 4 */
+  const int32_t* q_start;        /* [n_reqs + 1] */
+  int32_t tree_words;
+  /* biases: request r adds bias_values[i] to token bias_ids[i] for i in
+   * [bias_start[r], bias_start[r+1]), in that order when a token is named
+   * more than once; ids outside [0, vocab) are ignored. */
+  int32_t n_biases;
+  const int32_t* bias_start;     /* [n_reqs + 1] */
+  const int32_t* bias_ids;       /* [n_biases] */
+  const float* bias_values;      /* [n_biases] */
+  /* grammar: bit v % 32 of allowed[a*ld_allowed + v/32] = token v may follow,
+   * with a = allowed_row[s] (NULL: s); -1: everything may. */
+  int32_t n_allowed;             /* rows of allowed */
+  int64_t ld_allowed;            /* words, >= ceil(vocab / 32) */
+  const uint32_t* allowed;
+  const int32_t* allowed_row;    /* [S] */
+} tp_logit_rules_t;
+
+/* Penalties, biases and grammar masks on logits, in this order and in fp32:
+ *   x = logit
+ *   x = x > 0 ? x / repetition : x * repetition   for tokens in the request's
+ *                                  prompt, output or drafted path
+ *   x = x - frequency * (times in output and path)
+ *   x = x - presence                              for tokens in output or path
+ *   x = x + bias
+ *   x = -infinity                                 for tokens not allowed,
+ *                                  whatever the logit is (NaN too)
+ * and one rounding when the output is bf16.  A row whose mask allows nothing
+ * becomes all -infinity.
+ *   logits : [S, vocab] bf16, row stride ld_logits >= vocab
+ *   out    : [S, vocab], row stride ld_out >= vocab; fp32 with out_fp32 = 1,
+ *            else bf16, and then it may be the logits buffer itself with
+ *            ld_out = ld_logits.  Otherwise they must not overlap.
+ * Deterministic.  Errors on the device (TP_ERR_TABLE_RANGE): a row_req
+ * outside [-1, n_reqs) leaves its row; lengths are cut to [0, ld_history] and the
+ * prompt to the length; a bias range outside [0, n_biases] or a path outside the
+ * rows adds nothing; an allowed_row outside [-1, n_allowed) allows nothing. */
+tp_status tp_process_logits(const tp_model* m, const tp_bf16* logits, int64_t ld_logits,
+                            int32_t S, const tp_logit_rules_t* rules, void* out, int64_t ld_out,
+                            int32_t out_fp32, void* stream);
 
 const char* tp_strerror(tp_status s);
 

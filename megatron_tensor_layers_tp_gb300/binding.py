@@ -18,7 +18,7 @@ TP_DECODE, TP_PREFILL = 0, 1
 STATUS_NAMES = {
     0: "TP_OK", 1: "TP_ERR_ARG", 2: "TP_ERR_DIVISIBILITY", 3: "TP_ERR_KV_REPLICA",
     4: "TP_ERR_TOKEN_RANGE", 5: "TP_ERR_OOM", 6: "TP_ERR_CUDA", 7: "TP_ERR_DEVICE_TIMEOUT",
-    8: "TP_ERR_UNSUPPORTED", 9: "TP_ERR_WORKSPACE",
+    8: "TP_ERR_UNSUPPORTED", 9: "TP_ERR_WORKSPACE", 10: "TP_ERR_TABLE_RANGE",
 }
 STATUS = {v: k for k, v in STATUS_NAMES.items()}
 
@@ -61,6 +61,27 @@ class tp_stats_t(Structure):
 
 class tp_kernel_time_t(Structure):
     _fields_ = [("name", ctypes.c_char * 24), ("launches", c_int64), ("total_ms", ctypes.c_double)]
+
+
+class tp_pages_t(Structure):
+    _fields_ = [("n_pages", c_int32), ("page_size", c_int32), ("ld_table", c_int32)] + \
+               [(n, c_void_p) for n in ("table", "free_ring", "free_state", "free_next")]
+
+
+class tp_step_t(Structure):
+    _fields_ = [(n, c_int32) for n in ("n_seqs", "n_tokens", "max_new", "max_ctx", "tree_words")] + \
+               [(n, c_void_p) for n in ("old_lens", "new_lens", "parents", "q_start", "slots",
+                                        "positions", "token_seq", "tree_mask")]
+
+
+class tp_logit_rules_t(Structure):
+    _fields_ = [("n_reqs", c_int32), ("row_req", c_void_p), ("history", c_void_p),
+                ("ld_history", c_int64), ("history_lens", c_void_p), ("prompt_lens", c_void_p),
+                ("repetition", c_void_p), ("frequency", c_void_p), ("presence", c_void_p),
+                ("draft_tokens", c_void_p), ("tree_mask", c_void_p), ("q_start", c_void_p),
+                ("tree_words", c_int32), ("n_biases", c_int32), ("bias_start", c_void_p),
+                ("bias_ids", c_void_p), ("bias_values", c_void_p), ("n_allowed", c_int32),
+                ("ld_allowed", c_int64), ("allowed", c_void_p), ("allowed_row", c_void_p)]
 
 
 class TPError(RuntimeError):
@@ -110,6 +131,18 @@ _SIGS = {
                                                c_int64, c_int32, c_void_p, c_void_p, c_void_p]),
     "tp_row_linear_reduce_noalloc_fits": (c_int32, [c_int32, c_int32, c_int32]),
     "tp_rmsnorm": (c_int32, [c_void_p, c_void_p, c_void_p, c_int32, c_void_p, c_void_p]),
+    "tp_step_workspace_bytes": (c_size_t, [c_void_p, c_int32, c_int32]),
+    "tp_step_tables": (c_int32, [c_void_p, POINTER(tp_pages_t), POINTER(tp_step_t), c_void_p,
+                                 c_size_t, c_void_p]),
+    "tp_cache_append": (c_int32, [c_void_p, c_void_p, c_int64, c_int32, c_void_p, c_void_p,
+                                  POINTER(tp_pages_t), c_void_p, c_void_p, c_void_p, c_int64,
+                                  c_void_p]),
+    "tp_tree_attention": (c_int32, [c_void_p, c_void_p, c_int64, c_void_p, c_int64,
+                                    POINTER(tp_pages_t), POINTER(tp_step_t), c_void_p, c_void_p,
+                                    c_void_p, c_size_t, c_void_p]),
+    "tp_process_logits": (c_int32, [c_void_p, c_void_p, c_int64, c_int32,
+                                    POINTER(tp_logit_rules_t), c_void_p, c_int64, c_int32,
+                                    c_void_p]),
     "tp_get_stats": (c_int32, [c_void_p, POINTER(tp_stats_t)]),
     "tp_reset_stats": (None, [c_void_p]),
     "tp_check_device": (c_int32, [c_void_p, c_void_p]),
@@ -273,6 +306,32 @@ def tp_graph_free(graph) -> None:
 
 def tp_rmsnorm(model, x, w, M, y, stream) -> int:
     return lib().tp_rmsnorm(model, x, w, M, y, stream)
+
+
+def tp_step_workspace_bytes(model, n_seqs: int, max_new: int) -> int:
+    return lib().tp_step_workspace_bytes(model, n_seqs, max_new)
+
+
+def tp_step_tables(model, pages: tp_pages_t, step: tp_step_t, ws, ws_bytes, stream) -> int:
+    return lib().tp_step_tables(model, ctypes.byref(pages), ctypes.byref(step), ws, ws_bytes, stream)
+
+
+def tp_cache_append(model, qkv, rank_stride, M, positions, slots, pages: tp_pages_t, k, v, q, ld_q,
+                    stream) -> int:
+    return lib().tp_cache_append(model, qkv, rank_stride, M, positions, slots, ctypes.byref(pages),
+                                 k, v, q, ld_q, stream)
+
+
+def tp_tree_attention(model, q, ld_q, o, ld_o, pages: tp_pages_t, step: tp_step_t, k, v, ws,
+                      ws_bytes, stream) -> int:
+    return lib().tp_tree_attention(model, q, ld_q, o, ld_o, ctypes.byref(pages),
+                                   ctypes.byref(step), k, v, ws, ws_bytes, stream)
+
+
+def tp_process_logits(model, logits, ld_logits, S, rules: tp_logit_rules_t, out, ld_out, out_fp32,
+                      stream) -> int:
+    return lib().tp_process_logits(model, logits, ld_logits, S, ctypes.byref(rules), out, ld_out,
+                                   out_fp32, stream)
 
 
 def tp_get_stats(model) -> tp_stats_t:

@@ -1,7 +1,7 @@
 """Builds the in-tree shared library ``_build/libtp_gb300.so`` for sm_103a.
 
 Translation units compile in parallel (one per GEMM epilogue, plus attention,
-the small kernels and the host API), then nvcc links them.  No cmake.
+the small kernels, the paged-cache kernels and the host API), then nvcc links them.  No cmake.
 """
 from __future__ import annotations
 
@@ -24,7 +24,8 @@ N_EPI = 8
 
 def _units():
     units = []
-    for name in ("small", "attention", "tp_api", "no_alloc"):
+    for name in ("small", "attention", "tp_api", "no_alloc", "step_tables", "cache_append",
+                 "tree_attn", "logits", "paged_api"):
         units.append((os.path.join(CSRC, name + ".cu"), os.path.join(BUILD, name + ".o"), []))
     for e in range(N_EPI):
         units.append((os.path.join(CSRC, "gemm_inst.cu"), os.path.join(BUILD, f"gemm_epi{e}.o"),

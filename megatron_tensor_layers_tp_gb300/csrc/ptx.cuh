@@ -10,6 +10,7 @@ namespace tpk {
 // Device status word codes (mirrors tp_status values).
 constexpr int kStatusTokenRange = 4;
 constexpr int kStatusTimeout = 7;
+constexpr int kStatusTableRange = 10;
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));

@@ -72,6 +72,185 @@ class Batch:
         return b
 
 
+def _check(t: torch.Tensor, name: str, dtype, shape, device, rows: bool = False) -> None:
+    """Raises ValueError unless t is a tensor on `device` of that dtype and shape (None: any
+    size), contiguous; with `rows`, a matrix whose rows are contiguous (any row stride)."""
+    if t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name}: {dtype} on {device} expected, got {t.dtype} on {t.device}")
+    if len(t.shape) != len(shape) or any(w is not None and g != w for g, w in zip(t.shape, shape)):
+        raise ValueError(f"{name}: shape {tuple(shape)} expected, got {tuple(t.shape)}")
+    if rows:
+        if t.shape[1] > 1 and t.stride(1) != 1 or t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+            raise ValueError(f"{name}: rows must be contiguous and not overlap")
+    elif not t.is_contiguous():
+        raise ValueError(f"{name}: contiguous tensor expected")
+
+
+def _ld(t: torch.Tensor) -> int:
+    """Row stride of a matrix (a single row may carry any)."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+class PageTable:
+    """The page tables of a paged KV cache (see tp_pages_t).
+
+    table [rows, ld] int32, free_ring [n_pages] int32 and free_state [2] int32 (first, count) as
+    the C ABI wants them; free_next (default: free_state itself) receives the ring's state after
+    step_tables.  For cache_append alone page_size and n_pages suffice, for tree_attention also
+    the table.  The tensors' addresses are kept: refresh their contents, not the objects.
+    """
+
+    def __init__(self, page_size: int, table: Optional[torch.Tensor] = None,
+                 free_ring: Optional[torch.Tensor] = None,
+                 free_state: Optional[torch.Tensor] = None,
+                 free_next: Optional[torch.Tensor] = None, n_pages: Optional[int] = None):
+        if n_pages is None:
+            if free_ring is None:
+                raise ValueError("n_pages or free_ring is needed")
+            n_pages = free_ring.numel()
+        if table is not None:
+            _check(table, "table", torch.int32, (None, None), table.device)
+        if free_ring is not None:
+            if table is None or free_state is None:
+                raise ValueError("a free_ring comes with its table and free_state")
+            if free_next is None:
+                free_next = free_state
+            _check(free_ring, "free_ring", torch.int32, (n_pages,), table.device)
+            _check(free_state, "free_state", torch.int32, (2,), table.device)
+            _check(free_next, "free_next", torch.int32, (2,), table.device)
+        self.page_size, self.n_pages = page_size, n_pages
+        self.table, self.free_ring = table, free_ring
+        self.free_state, self.free_next = free_state, free_next
+        c = self.c = B.tp_pages_t()
+        c.n_pages, c.page_size = n_pages, page_size
+        c.ld_table = 0 if table is None else table.shape[1]
+        c.table, c.free_ring = _ptr(table), _ptr(free_ring)
+        c.free_state, c.free_next = _ptr(free_state), _ptr(free_next)
+
+    @classmethod
+    def alloc(cls, n_seqs: int, n_pages: int, page_size: int, max_len: int,
+              device="cuda") -> "PageTable":
+        """An empty table for n_seqs sequences of up to max_len tokens; every page is free."""
+        ld = max(1, -(-max_len // page_size))
+        return cls(page_size, torch.zeros((n_seqs, ld), dtype=torch.int32, device=device),
+                   torch.arange(n_pages, dtype=torch.int32, device=device),
+                   torch.tensor([0, n_pages], dtype=torch.int32, device=device))
+
+
+class Step:
+    """One step's lengths and index tables (see tp_step_t).
+
+    step_tables fills q_start, slots, positions, token_seq and tree_mask; tree_attention reads
+    old_lens, q_start and tree_mask.  What a call does not use may be None.  tree_mask is
+    [n_tokens, words] int64 (the 64-bit words' patterns).
+    """
+
+    def __init__(self, n_tokens: int, max_new: int, max_ctx: int, old_lens: torch.Tensor,
+                 new_lens: Optional[torch.Tensor] = None, parents: Optional[torch.Tensor] = None,
+                 q_start: Optional[torch.Tensor] = None, slots: Optional[torch.Tensor] = None,
+                 positions: Optional[torch.Tensor] = None,
+                 token_seq: Optional[torch.Tensor] = None,
+                 tree_mask: Optional[torch.Tensor] = None):
+        n, dev = old_lens.numel(), old_lens.device
+        for name, t, shape in (("old_lens", old_lens, (n,)), ("new_lens", new_lens, (n,)),
+                               ("parents", parents, (n_tokens,)), ("q_start", q_start, (n + 1,)),
+                               ("slots", slots, (n_tokens,)), ("positions", positions, (n_tokens,)),
+                               ("token_seq", token_seq, (n_tokens,))):
+            if t is not None:
+                _check(t, name, torch.int32, shape, dev)
+        if tree_mask is not None:
+            _check(tree_mask, "tree_mask", torch.int64, (n_tokens, None), dev)
+        self.n_seqs, self.n_tokens, self.max_new, self.max_ctx = n, n_tokens, max_new, max_ctx
+        self.old_lens, self.new_lens, self.parents = old_lens, new_lens, parents
+        self.q_start, self.slots, self.positions = q_start, slots, positions
+        self.token_seq, self.tree_mask = token_seq, tree_mask
+        c = self.c = B.tp_step_t()
+        c.n_seqs, c.n_tokens, c.max_new, c.max_ctx = n, n_tokens, max_new, max_ctx
+        c.tree_words = 0 if tree_mask is None else tree_mask.shape[1]
+        for name in ("old_lens", "new_lens", "parents", "q_start", "slots", "positions",
+                     "token_seq", "tree_mask"):
+            setattr(c, name, _ptr(getattr(self, name)))
+
+    @classmethod
+    def alloc(cls, n_seqs: int, n_tokens: int, max_new: int, max_ctx: int,
+              old_lens: Optional[torch.Tensor] = None, new_lens: Optional[torch.Tensor] = None,
+              parents: Optional[torch.Tensor] = None, tree_words: int = 0,
+              device="cuda") -> "Step":
+        """A step with its output tables allocated (and lengths of 0 where none are given);
+        tree_words > 0 adds the tree masks."""
+        def ints(*shape):
+            return torch.zeros(shape, dtype=torch.int32, device=device)
+        mask = torch.zeros((n_tokens, tree_words), dtype=torch.int64, device=device) \
+            if tree_words else None
+        return cls(n_tokens, max_new, max_ctx, ints(n_seqs) if old_lens is None else old_lens,
+                   ints(n_seqs) if new_lens is None else new_lens, parents, ints(n_seqs + 1),
+                   ints(n_tokens), ints(n_tokens), ints(n_tokens), mask)
+
+
+class LogitRules:
+    """The rules process_logits applies (see tp_logit_rules_t); None leaves a rule out.
+
+    Per request: history [R, ld] int32 with history_lens and prompt_lens [R] int32, repetition,
+    frequency and presence [R] float32, biases as bias_start [R+1], bias_ids [n] int32 and
+    bias_values [n] float32.  Per row: row_req [S] int32, draft_tokens [S] int32 with tree_mask
+    [S, words] int64 and q_start [R+1] int32, allowed [rows, words] int32 (bit patterns) with
+    allowed_row [S] int32.
+    """
+
+    def __init__(self, row_req=None, history=None, history_lens=None, prompt_lens=None,
+                 repetition=None, frequency=None, presence=None, draft_tokens=None, tree_mask=None,
+                 q_start=None, bias_start=None, bias_ids=None, bias_values=None, allowed=None,
+                 allowed_row=None, n_reqs: Optional[int] = None):
+        i32, f32 = torch.int32, torch.float32
+        if (history is None) != (history_lens is None):
+            raise ValueError("history and history_lens come together")
+        if len({draft_tokens is None, tree_mask is None, q_start is None}) > 1:
+            raise ValueError("draft_tokens, tree_mask and q_start come together")
+        if len({bias_start is None, bias_ids is None, bias_values is None}) > 1:
+            raise ValueError("bias_start, bias_ids and bias_values come together")
+        per_req = [t.shape[0] for t in (history, prompt_lens, repetition, frequency, presence)
+                   if t is not None]
+        per_req += [t.numel() - 1 for t in (q_start, bias_start) if t is not None]
+        per_row = [t.shape[0] for t in (row_req, draft_tokens, allowed_row) if t is not None]
+        if allowed is not None and allowed_row is None:
+            per_row.append(allowed.shape[0])
+        self.n_rows = per_row[0] if per_row else None
+        if n_reqs is None:
+            if per_req:
+                n_reqs = per_req[0]
+            elif self.n_rows is not None and row_req is None:
+                n_reqs = self.n_rows
+            else:
+                raise ValueError("n_reqs is needed: no rule here is given per request")
+        if row_req is None and self.n_rows is not None and self.n_rows != n_reqs:
+            raise ValueError("rows and requests differ in number: row_req is needed")
+        R, S = n_reqs, self.n_rows
+        tensors = {"row_req": (row_req, i32, (S,)), "history": (history, i32, (R, None)),
+                   "history_lens": (history_lens, i32, (R,)),
+                   "prompt_lens": (prompt_lens, i32, (R,)),
+                   "repetition": (repetition, f32, (R,)), "frequency": (frequency, f32, (R,)),
+                   "presence": (presence, f32, (R,)), "draft_tokens": (draft_tokens, i32, (S,)),
+                   "tree_mask": (tree_mask, torch.int64, (S, None)),
+                   "q_start": (q_start, i32, (R + 1,)), "bias_start": (bias_start, i32, (R + 1,)),
+                   "bias_ids": (bias_ids, i32, (None,)),
+                   "bias_values": (bias_values, f32, None if bias_ids is None else bias_ids.shape),
+                   "allowed": (allowed, i32, (None, None)), "allowed_row": (allowed_row, i32, (S,))}
+        given = [t for t, _, _ in tensors.values() if t is not None]
+        self.device = given[0].device if given else None
+        self._keep = given
+        c = self.c = B.tp_logit_rules_t()
+        for name, (t, dtype, shape) in tensors.items():
+            if t is not None:
+                _check(t, name, dtype, shape, self.device, rows=name == "allowed")
+            setattr(c, name, _ptr(t))
+        c.n_reqs = R
+        c.ld_history = 0 if history is None else history.shape[1]
+        c.tree_words = 0 if tree_mask is None else tree_mask.shape[1]
+        c.n_biases = 0 if bias_ids is None else bias_ids.numel()
+        c.n_allowed = 0 if allowed is None else allowed.shape[0]
+        c.ld_allowed = 0 if allowed is None else _ld(allowed)
+
+
 class TPModel:
     """Owns one tp_model (the t ranks' shards) plus a workspace."""
 
@@ -100,6 +279,9 @@ class TPModel:
         self.handle = B.tp_load_shards(cfg, w, _stream(stream))
         self.max_tokens = 0
         self.ws = None
+        self.device = torch.device("cuda", torch.cuda.current_device())
+        self.step_ws = None
+        self._old_step_ws = []
         self.ensure_workspace(max_tokens, stream)
 
     # ------------------------------------------------------------------ utils
@@ -246,6 +428,142 @@ class TPModel:
         B.check(B.tp_stage_send(self.handle, src.data_ptr(), dst.data_ptr(), src.shape[0],
                                 _stream(stream)), "tp_stage_send")
         return dst
+
+    # ------------------------------------------------------- paged cache
+    def alloc_pages(self, n_pages: int, page_size: int) -> torch.Tensor:
+        """K or V pages of one layer (contents undefined, as alloc_kv's)."""
+        c = self.cfg
+        return torch.empty((c.kv_copies, n_pages, c.kv_heads_per_rank, page_size, c.head_dim),
+                           dtype=torch.bfloat16, device=self.device)
+
+    def step_workspace(self, n_seqs: int, max_new: int, stream=None) -> torch.Tensor:
+        """A workspace for step_tables and tree_attention on steps of up to n_seqs sequences with
+        up to max_new new tokens each.  Calls that may overlap on the GPU (two streams, two graphs
+        replayed at once) need one each; the others can share the model's own."""
+        n = B.tp_step_workspace_bytes(self.handle, n_seqs, max_new)
+        if n == 0:
+            raise ValueError(f"step of {n_seqs} sequences with {max_new} new tokens: outside limits")
+        ws = self._out((n,), torch.uint8, stream)
+        B.tp_workspace_init(ws.data_ptr(), n, _stream(stream))
+        return ws
+
+    def ensure_step_workspace(self, n_seqs: int, max_new: int, stream=None) -> torch.Tensor:
+        """The model's own step workspace, grown when too small (not inside a graph capture)."""
+        n = B.tp_step_workspace_bytes(self.handle, n_seqs, max_new)
+        if self.step_ws is None or self.step_ws.numel() < n or n == 0:
+            if torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("call ensure_step_workspace before the graph capture")
+            ws = self.step_workspace(n_seqs, max_new, stream)
+            if self.step_ws is not None:
+                self._old_step_ws.append(self.step_ws)  # captured graphs may still use it
+            self.step_ws = ws
+        return self.step_ws
+
+    def _out(self, shape, dtype, stream) -> torch.Tensor:
+        """An output buffer that belongs to the stream the call runs on."""
+        if stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(_stream(stream), device=self.device)
+        with torch.cuda.stream(stream):
+            return torch.empty(shape, dtype=dtype, device=self.device)
+
+    def step_tables(self, pages: PageTable, step: Step, ws: Optional[torch.Tensor] = None,
+                    stream=None) -> Step:
+        """Block tables, slots, positions and tree masks of the step from its lengths."""
+        t = pages.table
+        if t is None or pages.free_ring is None or step.new_lens is None or step.q_start is None:
+            raise ValueError("step_tables needs a page table with its ring, and a step with "
+                             "new_lens and its output tables")
+        if t.shape[0] < step.n_seqs or t.device != self.device or step.old_lens.device != self.device:
+            raise ValueError("the page table has too few rows, or the tables are on another device")
+        if ws is None:
+            ws = self.ensure_step_workspace(step.n_seqs, step.max_new, stream)
+        B.check(B.tp_step_tables(self.handle, pages.c, step.c, ws.data_ptr(), ws.numel(),
+                                 _stream(stream)), "tp_step_tables")
+        return step
+
+    def cache_append(self, qkv: torch.Tensor, positions: torch.Tensor, slots: torch.Tensor,
+                     pages: PageTable, k: torch.Tensor, v: torch.Tensor,
+                     q: Optional[torch.Tensor] = None, want_q: bool = True,
+                     stream=None) -> Optional[torch.Tensor]:
+        """RoPE and the new K/V rows into their slots; returns the rotated queries
+        [M, n_heads*d] (into q when given; None with want_q False).  qkv: column_linear's
+        output [ranks, M, N_r]."""
+        c = self.cfg
+        M = qkv.shape[1]
+        dev = self.device
+        _check(qkv, "qkv", torch.bfloat16, (c.attn_tp, M, self.qkv_rows()), dev)
+        _check(positions, "positions", torch.int32, (M,), dev)
+        _check(slots, "slots", torch.int32, (M,), dev)
+        self._check_pool(k, "k", pages)
+        self._check_pool(v, "v", pages)
+        if q is not None:
+            _check(q, "q", torch.bfloat16, (M, c.n_heads * c.head_dim), dev, rows=True)
+        elif want_q:
+            q = self._out((M, c.n_heads * c.head_dim), torch.bfloat16, stream)
+        B.check(B.tp_cache_append(self.handle, qkv.data_ptr(), M * qkv.shape[2], M,
+                                  positions.data_ptr(), slots.data_ptr(), pages.c, k.data_ptr(),
+                                  v.data_ptr(), _ptr(q), 0 if q is None else _ld(q),
+                                  _stream(stream)), "tp_cache_append")
+        return q
+
+    def tree_attention(self, q: torch.Tensor, step: Step, pages: PageTable, k: torch.Tensor,
+                       v: torch.Tensor, out: Optional[torch.Tensor] = None,
+                       ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """Attention of the step's tokens over the paged cache; q, out [n_tokens, n_heads*d].
+        Padding rows of out are not written (undefined in a buffer allocated here)."""
+        c = self.cfg
+        t = pages.table
+        shape = (step.n_tokens, c.n_heads * c.head_dim)
+        _check(q, "q", torch.bfloat16, shape, self.device, rows=True)
+        if step.q_start is None or t is None or t.shape[0] < step.n_seqs or \
+                t.device != self.device or step.old_lens.device != self.device:
+            raise ValueError("tree_attention needs q_start and a table row for every sequence, on "
+                             "the model's device")
+        self._check_pool(k, "k", pages)
+        self._check_pool(v, "v", pages)
+        if out is None:
+            out = self._out(shape, torch.bfloat16, stream)
+        else:
+            _check(out, "out", torch.bfloat16, shape, self.device, rows=True)
+        if ws is None:
+            ws = self.ensure_step_workspace(step.n_seqs, step.max_new, stream)
+        B.check(B.tp_tree_attention(self.handle, q.data_ptr(), _ld(q), out.data_ptr(), _ld(out),
+                                    pages.c, step.c, k.data_ptr(), v.data_ptr(), ws.data_ptr(),
+                                    ws.numel(), _stream(stream)), "tp_tree_attention")
+        return out
+
+    def _check_pool(self, t: torch.Tensor, name: str, pages: PageTable) -> None:
+        c = self.cfg
+        _check(t, name, torch.bfloat16, (c.kv_copies, pages.n_pages, c.kv_heads_per_rank,
+                                         pages.page_size, c.head_dim), self.device)
+
+    def process_logits(self, logits: torch.Tensor, rules: LogitRules,
+                       out: Optional[torch.Tensor] = None, dtype=torch.float32,
+                       stream=None) -> torch.Tensor:
+        """Penalties, biases and grammar masks on bf16 logits [S, vocab]; the result in a new
+        tensor of `dtype` (float32 or bfloat16), or in `out`, which may be `logits` itself.
+        Rows with row_req -1 are not written (undefined in a tensor allocated here)."""
+        S, V = logits.shape[0], self.cfg.vocab
+        _check(logits, "logits", torch.bfloat16, (S, V), self.device, rows=True)
+        n = rules.c.n_reqs if rules.n_rows is None else rules.n_rows
+        if n != S:
+            raise ValueError(f"the rules are for {n} rows, not {S}")
+        if rules.device is not None and rules.device != self.device:
+            raise ValueError("the rules' tensors are on another device")
+        if out is None:
+            if dtype not in (torch.float32, torch.bfloat16):
+                raise ValueError("dtype: float32 or bfloat16 expected")
+            out = self._out((S, V), dtype, stream)
+        else:
+            if out.dtype not in (torch.float32, torch.bfloat16):
+                raise ValueError("out: float32 or bfloat16 expected")
+            _check(out, "out", out.dtype, (S, V), self.device, rows=True)
+        B.check(B.tp_process_logits(self.handle, logits.data_ptr(), _ld(logits), S, rules.c,
+                                    out.data_ptr(), _ld(out), int(out.dtype == torch.float32),
+                                    _stream(stream)), "tp_process_logits")
+        return out
 
     def capture_forward(self, ids: torch.Tensor, batch: Batch, h: torch.Tensor,
                         logits: torch.Tensor, stream, fused: bool = True,
