@@ -602,7 +602,8 @@ tp_status tp_cache_append(const tp_model* m, const tp_bf16* qkv, int64_t rank_st
  *   step  : n_seqs, n_tokens, max_new (<= 256), max_ctx (>= every old + T),
  *           old_lens, q_start, tree_mask and tree_words are used; the
  *           others may be NULL
- *   k, v  : the layer's cache, 16-byte aligned
+ *   k, v  : the layer's cache, 16-byte aligned; n_kv_heads * n_pages < 2^31 - 1
+ *           (TP_ERR_UNSUPPORTED otherwise)
  * Deterministic.  Errors on the device (TP_ERR_TABLE_RANGE): a sequence whose
  * q_start or length leaves its bounds is skipped (its rows of o are not
  * written); a page number outside [0, n_pages) reads as keys and values of

@@ -53,11 +53,14 @@ struct CacheAppendArgs {
 cudaError_t launch_cache_append(const CacheAppendArgs& a, cudaStream_t st);
 
 struct TreeAttnArgs {
+  CUtensorMap tmK, tmV;       // (d, page_size, copies * n_pages * kv_r), box (64, box_rows, 1)
+  int box_rows;               // keys a box brings: a power of two that divides page_size
+  int slices;                 // the third extent: coordinates from here on read zeros
   const uint16_t* q;
   int64_t ld_q;
   uint16_t* o;
   int64_t ld_o;
-  const uint16_t *k, *v;
+  const uint16_t* v;
   int n_pages, page_size, ld_table;
   FastDiv div_page;
   const int32_t* table;
@@ -68,8 +71,16 @@ struct TreeAttnArgs {
   int n_heads, n_kv, kv_r, group, head_dim;
   FastDiv div_group;
   float scale_log2;           // log2(e) / sqrt(d)
+  int kv_once;                // 1: no sequence has more than one query tile, K and V are read once
+  int q_tiles_max;            // query tiles of max_new tokens
+  int grid;
+  float* partials;            // [grid][2][128][d]
+  float2* ml;                 // [grid][2][128]
+  int* tickets;               // [n_seqs][n_kv][q_tiles_max], zero on entry and exit
   int* status;
 };
+constexpr int kTreeRows = 128;  // query rows (tokens x Q heads of a KV head) of a tile
+constexpr int kTreeKeys = 128;  // keys of a tile
 cudaError_t launch_tree_attn(const TreeAttnArgs& a, cudaStream_t st);
 
 struct LogitsArgs {

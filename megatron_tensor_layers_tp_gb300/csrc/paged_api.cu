@@ -49,6 +49,28 @@ bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
   return x < y + (uintptr_t)b_bytes && y < x + (uintptr_t)a_bytes;
 }
 
+// Query tiles of a KV head for n tokens.
+int query_tiles(const tp_model* m, int n) {
+  return cdiv((int64_t)n * (m->cfg.n_heads / m->cfg.n_kv_heads), kTreeRows);
+}
+
+// Workspace regions: the step tables' ticket, then tree attention's tickets,
+// pieces and their (m, l).  Steps of more new tokens than tree attention takes
+// (prompts) need its smallest tables only.
+struct StepWs {
+  size_t tickets, partials, ml, total;
+};
+StepWs step_ws(const tp_model* m, int n_seqs, int max_new) {
+  StepWs w;
+  const size_t pieces = (size_t)m->num_sms * 2 * kTreeRows;
+  const int tiles = query_tiles(m, std::min(max_new, kMaxTreeTokens));
+  w.tickets = kStepTicketBytes;
+  w.ml = align_up(w.tickets + (size_t)n_seqs * m->cfg.n_kv_heads * tiles * sizeof(int), 256);
+  w.partials = align_up(w.ml + pieces * sizeof(float2), 256);
+  w.total = w.partials + pieces * m->cfg.head_dim * sizeof(float);
+  return w;
+}
+
 // Bytes from the first to past the last element of [rows, cols] at a row stride.
 int64_t span_bytes(int64_t rows, int64_t ld, int64_t cols, int elem) {
   return ((rows - 1) * ld + cols) * elem;
@@ -60,7 +82,7 @@ extern "C" {
 
 size_t tp_step_workspace_bytes(const tp_model* m, int32_t n_seqs, int32_t max_new) {
   if (!m || n_seqs < 1 || n_seqs > kMaxStepSeqs || max_new < 0) return 0;
-  return kStepTicketBytes;
+  return step_ws(m, n_seqs, max_new).total;
 }
 
 tp_status tp_step_tables(const tp_model* m, const tp_pages_t* pages, const tp_step_t* step,
@@ -199,8 +221,17 @@ tp_status tp_tree_attention(const tp_model* m, const tp_bf16* q, int64_t ld_q, t
     a.ld_q = ld_q;
     a.o = o;
     a.ld_o = ld_o;
-    a.k = k;
     a.v = v;
+    // boxes of as many keys as divide the page (and the key tile)
+    a.box_rows = 8;
+    while (a.box_rows < kTreeKeys && pages->page_size % (2 * a.box_rows) == 0) a.box_rows *= 2;
+    const uint64_t slices =
+        (uint64_t)c.kv_copies * pages->n_pages * c.kv_heads_per_rank, d = c.head_dim;
+    if (slices >= INT32_MAX) return TP_ERR_UNSUPPORTED;  // a tensor map coordinate
+    a.slices = (int)slices;
+    if (!make_tmap(&a.tmK, k, d, pages->page_size, slices, d * 2, pages->page_size * d * 2, a.box_rows) ||
+        !make_tmap(&a.tmV, v, d, pages->page_size, slices, d * 2, pages->page_size * d * 2, a.box_rows))
+      return TP_ERR_CUDA;
     a.n_pages = pages->n_pages;
     a.page_size = pages->page_size;
     a.ld_table = pages->ld_table;
@@ -221,6 +252,14 @@ tp_status tp_tree_attention(const tp_model* m, const tp_bf16* q, int64_t ld_q, t
     a.head_dim = c.head_dim;
     a.div_group = make_fastdiv((uint32_t)a.group);
     a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)c.head_dim));
+    a.q_tiles_max = query_tiles(m, step->max_new);
+    a.kv_once = a.q_tiles_max == 1;
+    a.grid = m->num_sms;
+    const StepWs w = step_ws(m, step->n_seqs, step->max_new);
+    uint8_t* base = static_cast<uint8_t*>(ws);
+    a.tickets = reinterpret_cast<int*>(base + w.tickets);
+    a.ml = reinterpret_cast<float2*>(base + w.ml);
+    a.partials = reinterpret_cast<float*>(base + w.partials);
     a.status = m->status;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     return cuda_status(launch(m, "tree_attn", st, [&] { return launch_tree_attn(a, st); }));

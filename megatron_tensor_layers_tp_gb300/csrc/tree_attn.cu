@@ -1,12 +1,45 @@
-// Attention of a step's new tokens over the paged KV cache.
+// Attention of a step's new tokens over the paged KV cache, on the tensor
+// cores (tcgen05).
 //
 // Row (token i of sequence b, Q head h) sees the old tokens 0..old-1 and the
 // new tokens t of its sequence whose bit is set in its tree mask (chains:
 // t <= i).  o = sum_j exp(s_j - m) v_j / sum_j exp(s_j - m) with s_j = q.k_j /
 // sqrt(d) and the running maximum m, in one pass over the keys.
 //
-// One warp per row: the lanes share the head's elements, a key's score is a
-// warp sum.
+// Every Q head of a KV head and every new token of a sequence share its keys:
+// they are the rows of 128-row query tiles (row = token * group + head), so K
+// and V are read once for up to 128 / group tokens.  With one tile per
+// sequence and KV head the cache's bytes bound the kernel: a 128-key tile of K
+// and V (64 KB at d = 128) takes an SM 1.5 us at its share of the memory rate,
+// its two products 0.3 us and its exponentials 0.3-0.6 us.
+//
+// Work is the flat sequence of (sequence, KV head, query tile, key tile),
+// split evenly over one CTA per SM.  A CTA finds its range from the lengths on
+// the GPU, so a captured launch follows them.  An item cut between CTAs leaves
+// unnormalised fp32 pieces; the last CTA to finish one (ticket, no waiting)
+// joins them in key order: the result is deterministic.
+//
+// Roles of the 12 warps:
+//   warp 0     : K and V tiles by TMA into a ring, one box per lane, through
+//                the page table (boxes end where pages end);
+//   warp 1     : one thread issues S = Q K^T (tensor memory) and O += P V, with
+//                P read from tensor memory and V as it lies in the page (the
+//                head's elements contiguous);
+//   warps 4-7, 8-11: two softmax groups.  They take alternate key tiles, each
+//                with its own S, running maximum, sum and O, so that one
+//                tile's exponentials overlap the other's products without
+//                exchanging maxima; the two states meet at the item's end.  A
+//                thread owns a row.
+// P overwrites S in place (bf16, half the columns).  O is rescaled only when a
+// row's maximum rose by more than 2^8 since its last rescaling: the sums are
+// relative to the older maximum until then, which is exact algebra and keeps
+// every p below 2^8.
+//
+// What rows do not see must not reach them: masked scores become -inf by a
+// select, and in tiles that hold new tokens (or the end) the softmax group
+// clears V rows behind the end, and takes infinities and NaN out of the new
+// tokens' V (0 * inf would spread them to rows that do not see the token); the
+// rows that do see such an element get it added at the end (nonfinite_v).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -17,87 +50,620 @@
 
 namespace tpk {
 
-// Sequence b's first row, new tokens and old length; an inconsistent one has
-// no tokens (and sets the status).
+constexpr int kTreeThreads = 384;
+constexpr int kTreeSoftmax = 256;        // threads of the two softmax groups
+constexpr float kRescaleLog2 = 8.f;
+
+template <int D>
+struct TreeSmem {
+  static constexpr int kTile = kTreeKeys * D * 2;   // a K or V tile; also the query tile
+  static constexpr int kStages = D == 128 ? 6 : 12;
+  static constexpr int kRing = kTile;                // byte offset of the ring (after Q)
+  static constexpr int kBars = kRing + kStages * kTile;
+  static constexpr int kTotal = kBars + 512 + 1024;  // + alignment of the base
+  static_assert(kTotal <= 227 * 1024, "shared memory of one CTA");
+};
+// after the ring
+struct TreeCtl {
+  uint64_t full[12], empty[12];
+  uint64_t s_full[2], p_ready[2], pv_done[2], q_full, drain;
+  long long warp_sum[12];
+  long long total, u0;
+  int b0;
+  int last;
+  int poison[2];
+  uint32_t tmem;
+};
+static_assert(sizeof(TreeCtl) <= 512, "control block");
+
+// Sequence b's first row, new tokens, old length and tiles; an inconsistent
+// one has no tokens (and sets the status).
 struct SeqInfo {
-  int q0, T, old;
+  int q0, T, old, qt, nt;
 };
 __device__ __forceinline__ SeqInfo seq_info(const TreeAttnArgs& a, int b) {
   SeqInfo s;
   s.q0 = a.q_start[b];
   const int q1 = a.q_start[b + 1];
   s.old = a.old_lens[b];
-  s.T = q1 - s.q0;
-  if (s.q0 < 0 || q1 < s.q0 || q1 > a.n_tokens || s.T > a.max_new || s.old < 0 ||
-      (int64_t)s.old + s.T > a.cap) {
+  const int64_t T = (int64_t)q1 - s.q0;
+  s.T = (int)T;
+  if (s.q0 < 0 || T < 0 || q1 > a.n_tokens || T > a.max_new || s.old < 0 ||
+      s.old + T > a.cap) {
     record_status(a.status, kStatusTableRange);
     s.T = 0;
   }
+  s.qt = (s.T * a.group + kTreeRows - 1) / kTreeRows;
+  s.nt = s.T ? (s.old + s.T + kTreeKeys - 1) / kTreeKeys : 0;
   return s;
 }
 
-template <int D>
-__global__ void __launch_bounds__(256) tree_attn_kernel(const TreeAttnArgs a) {
-  pdl_launch_dependents();
-  pdl_wait();
-  constexpr int E = D / 32;  // elements of a lane
-  const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  const int row = (int)(w / a.n_heads), h = (int)(w % a.n_heads);
-  if (row >= a.n_tokens) return;
-  int b = -1;
-  SeqInfo s = {0, 0, 0};
-  for (int i = 0; i < a.n_seqs && b < 0; ++i) {
-    s = seq_info(a, i);
-    if (row >= s.q0 && row < s.q0 + s.T) b = i;
+// One CTA's part of an item: key tiles [k0, k1) of (sequence b, KV head g,
+// query tile qi); x: the flat index of the item's tile 0.
+struct Seg {
+  SeqInfo s;
+  int b, g, qi, k0, k1;
+  int64_t x;
+};
+struct SegIter {
+  const TreeAttnArgs& a;
+  int64_t x, x1, u;  // flat position, its end, position inside sequence b
+  int b;
+  SeqInfo s;
+  __device__ __forceinline__ SegIter(const TreeAttnArgs& a_, int64_t x_, int64_t x1_, int64_t u_,
+                                     int b_)
+      : a(a_), x(x_), x1(x1_), u(u_), b(b_) {
+    if (x < x1) s = seq_info(a, b);
   }
-  if (b < 0) return;
-  const int i = row - s.q0, g = h / a.group, copy = g / a.kv_r, local = g % a.kv_r;
-  float q[E], o[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    q[e] = bf16_to_f(a.q[row * a.ld_q + h * D + lane * E + e]);
-    o[e] = 0.f;
-  }
-  float m = -INFINITY, l = 0.f;
-  for (int j = 0; j < s.old + s.T; ++j) {
-    const int t = j - s.old;
-    if (t >= 0) {
-      const bool sees = a.tree_mask
-                            ? (a.tree_mask[(int64_t)row * a.tree_words + (t >> 6)] >> (t & 63)) & 1
-                            : t <= i;
-      if (!sees) continue;
+  __device__ __forceinline__ bool next(Seg& sg) {
+    if (x >= x1) return false;
+    while (u >= (int64_t)a.n_kv * s.qt * s.nt) {  // at most to the last sequence: x < x1 <= total
+      u -= (int64_t)a.n_kv * s.qt * s.nt;
+      if (++b >= a.n_seqs) return false;
+      s = seq_info(a, b);
     }
-    const int pg = (int)fast_div((uint32_t)j, a.div_page);
-    const int page = a.table[(int64_t)b * a.ld_table + pg];
-    const bool ok = page >= 0 && page < a.n_pages;
-    if (!ok) record_status(a.status, kStatusTableRange);
-    const int64_t at =
-        ((((int64_t)copy * a.n_pages + (ok ? page : 0)) * a.kv_r + local) * a.page_size + j -
-         pg * a.page_size) * D + lane * E;
-    float x = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) x += ok ? q[e] * bf16_to_f(a.k[at + e]) : 0.f;
-#pragma unroll
-    for (int f = 16; f; f >>= 1) x += __shfl_xor_sync(0xffffffffu, x, f);
-    x *= a.scale_log2;
-    const float mn = fmaxf(m, x);
-    const float al = m == -INFINITY ? 0.f : exp2f(m - mn), p = exp2f(x - mn);
-    m = mn;
-    l = l * al + p;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = o[e] * al + (ok ? p * bf16_to_f(a.v[at + e]) : 0.f);
+    const int64_t item = u / s.nt;
+    sg.s = s;
+    sg.b = b;
+    sg.k0 = (int)(u - item * s.nt);
+    sg.g = (int)(item / s.qt);
+    sg.qi = (int)(item - (int64_t)sg.g * s.qt);
+    const int64_t left = x1 - x;
+    sg.k1 = (int)(left < s.nt - sg.k0 ? sg.k0 + left : s.nt);
+    sg.x = x - sg.k0;
+    x += sg.k1 - sg.k0;
+    u += sg.k1 - sg.k0;
+    return true;
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+};
+
+// 32 bits: which of the keys key0 .. key0 + 31 row `row` (token i of its
+// sequence) sees.
+__device__ __forceinline__ uint32_t sees32(const TreeAttnArgs& a, const SeqInfo& s, int i, int key0) {
+  const int base = key0 - s.old;  // drafted token of bit 0
+  if (base <= -32) return 0xFFFFFFFFu;
+  uint32_t m = 0xFFFFFFFFu;
+  int n = s.T - base;  // bits that exist
+  if (a.tree_mask) {
+    const uint32_t* w =
+        reinterpret_cast<const uint32_t*>(a.tree_mask + (int64_t)(s.q0 + i) * a.tree_words);
+    const int words = 2 * a.tree_words;
+    if (base < 0) {
+      m = (w[0] << -base) | ((1u << -base) - 1);
+    } else {
+      const int wi = base >> 5, sh = base & 31;
+      const uint32_t lo = wi < words ? w[wi] : 0, hi = wi + 1 < words ? w[wi + 1] : 0;
+      m = __funnelshift_r(lo, hi, sh);
+    }
+  } else {
+    n = min(n, i + 1 - base);
+  }
+  return n >= 32 ? m : (n <= 0 ? 0 : m & ((1u << n) - 1));
+}
+
+// The page a key lies in; outside the cache: -1 (with the status).
+__device__ __forceinline__ int page_of(const TreeAttnArgs& a, int b, int pg) {
+  const int p = a.table[(int64_t)b * a.ld_table + pg];
+  if (p >= 0 && p < a.n_pages) return p;
+  record_status(a.status, kStatusTableRange);
+  return -1;
+}
+
+// Infinities and NaN among the V elements e0 .. e0 + 15 of the new tokens that
+// row i sees in keys [key0, key1): added to the row's o.
+__device__ __noinline__ void nonfinite_v(const TreeAttnArgs& a, const SeqInfo& s, int b, int g, int i,
+                                         int key0, int key1, int e0, float (&o)[16]) {
+  for (int j = max(key0, s.old); j < min(key1, s.old + s.T); ++j) {
+    if (!(sees32(a, s, i, j) & 1)) continue;
+    const int pg = (int)fast_div((uint32_t)j, a.div_page), page = page_of(a, b, pg);
+    if (page < 0) continue;
+    const uint16_t* v =
+        a.v + ((((int64_t)(g / a.kv_r) * a.n_pages + page) * a.kv_r + g % a.kv_r) * a.page_size + j -
+               pg * a.page_size) * a.head_dim + e0;
+    for (int e = 0; e < 16; ++e)
+      if ((v[e] & 0x7F80) == 0x7F80) o[e] += bf16_to_f(v[e]);
+  }
+}
+
+__device__ __forceinline__ uint32_t pack_p(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+__device__ __forceinline__ bool has_nonfinite(uint32_t x) {
+  return (x & 0x7F80u) == 0x7F80u || (x & 0x7F800000u) == 0x7F800000u;
+}
+__device__ __forceinline__ uint32_t drop_nonfinite(uint32_t x) {
+  if ((x & 0x7F80u) == 0x7F80u) x &= 0xFFFF0000u;
+  if ((x & 0x7F800000u) == 0x7F800000u) x &= 0x0000FFFFu;
+  return x;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kTreeThreads, 1)
+tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
+  using SM = TreeSmem<D>;
+  constexpr int NST = SM::kStages, HB = kTreeKeys * 128;  // bytes of 64 elements of a tile
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  uint8_t* sQ = smem;
+  uint8_t* ring = smem + SM::kRing;
+  TreeCtl& ctl = *reinterpret_cast<TreeCtl*>(smem + SM::kBars);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  pdl_launch_dependents();
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NST; ++i) { mbar_init(&ctl.full[i], 1); mbar_init(&ctl.empty[i], 1); }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl.s_full[i], 1);
+      mbar_init(&ctl.p_ready[i], 4);
+      mbar_init(&ctl.pv_done[i], 1);
+      ctl.poison[i] = 0;
+    }
+    mbar_init(&ctl.q_full, kTreeSoftmax / 32);
+    mbar_init(&ctl.drain, 1);
+    fence_barrier_init();
+    fence_proxy_async_smem();
+    tma_prefetch_desc(&a.tmK);
+    tma_prefetch_desc(&a.tmV);
+  }
+  if (warp == 1) { tmem_alloc(&ctl.tmem, 512); tmem_relinquish(); }
+  pdl_wait();
+
+  // This CTA's range: thread t sums the tiles of a run of sequences; the
+  // thread whose run holds the range's begin looks it up.
+  // No more CTAs take part than there are tiles, so that an item's pieces lie
+  // with consecutive CTAs.
+  int G = gridDim.x;
+  const int c = blockIdx.x;
+  {
+    const int per = (a.n_seqs + kTreeThreads - 1) / kTreeThreads;
+    const int lo = min(a.n_seqs, (int)threadIdx.x * per), hi = min(a.n_seqs, lo + per);
+    long long sum = 0;
+    for (int b = lo; b < hi; ++b) {
+      const SeqInfo s = seq_info(a, b);
+      sum += (long long)a.n_kv * s.qt * s.nt;
+    }
+    long long incl = sum;
 #pragma unroll
-  for (int e = 0; e < E; ++e) a.o[row * a.ld_o + h * D + lane * E + e] = f_to_bf16(o[e] * inv);
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) ctl.warp_sum[warp] = incl;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    long long before = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < kTreeThreads / 32; ++w) {
+      const long long y = ctl.warp_sum[w];
+      if (w < warp) before += y;
+      total += y;
+    }
+    long long at = before + incl - sum;
+    if (total < G) G = (int)total;
+    const long long x0 = c < G ? range_begin(c, total, G) : total;
+    if (x0 >= at && x0 < at + sum) {
+      int b = lo;
+      while (true) {
+        const SeqInfo s = seq_info(a, b);
+        const long long n = (long long)a.n_kv * s.qt * s.nt;
+        if (x0 < at + n) break;
+        at += n;
+        ++b;
+      }
+      ctl.b0 = b;
+      ctl.u0 = x0 - at;
+    }
+    if (threadIdx.x == 0) ctl.total = total;
+    __syncthreads();
+  }
+  const uint32_t tmem = ctl.tmem;
+  const int64_t W = ctl.total;
+  const int64_t x0 = c < G ? range_begin(c, W, G) : W, x1 = c < G ? range_begin(c + 1, W, G) : W;
+
+  // A wait that runs out is remembered and nothing waits after it: every role
+  // then runs to its end without touching the copies or products.
+  bool ok = true;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (ok) ok = mbar_wait(bar, parity, a.status);
+  };
+  auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
+    wait(bar, parity);
+    __syncwarp();
+  };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ K and V
+    SegIter it(a, x0, x1, ctl.u0, ctl.b0);
+    Seg sg;
+    const uint64_t pol = policy_evict_first();
+    const int R = a.box_rows, boxes = kTreeKeys / R;
+    uint32_t n = 0;  // ring fills
+    while (ok && it.next(sg)) {
+      const int copy = sg.g / a.kv_r, local = sg.g - copy * a.kv_r;
+      const int len = sg.s.old + sg.s.T;
+      // lane -> (box, 64-element half)
+      const int box = D == 128 ? lane >> 1 : lane, half = D == 128 ? lane & 1 : 0;
+      auto look_up = [&](int kt, int& z, int& off) {
+        const int key = kt * kTreeKeys + box * R;
+        z = -1;
+        off = 0;
+        if (box < boxes && kt < sg.k1 && key < len) {
+          const int pg = (int)fast_div((uint32_t)key, a.div_page);
+          const int page = page_of(a, sg.b, pg);
+          off = key - pg * a.page_size;
+          z = page < 0 ? a.slices : (copy * a.n_pages + page) * a.kv_r + local;
+        }
+      };
+      int z, off;
+      look_up(sg.k0, z, off);
+      for (int kt = sg.k0; ok && kt < sg.k1; ++kt) {
+        int zn, offn;
+        look_up(kt + 1, zn, offn);  // in flight while this tile waits for its place
+        const int here = min(boxes, (len - kt * kTreeKeys + R - 1) / R);
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          const uint32_t st = n % NST;
+          wait(&ctl.empty[st], (n / NST & 1) ^ 1);
+          ok = __all_sync(0xffffffffu, ok);
+          if (ok) {
+            ++n;
+            if (lane == 0) mbar_arrive_expect_tx(&ctl.full[st], here * R * D * 2);
+            __syncwarp();
+            if (z >= 0) {
+              uint8_t* dst = ring + st * SM::kTile + half * HB + box * R * 128;
+              const CUtensorMap* tm = kv ? &a.tmV : &a.tmK;
+              if (a.kv_once) tma_load_3d(dst, tm, &ctl.full[st], half * 64, off, z, pol);
+              else tma_load_3d_plain(dst, tm, &ctl.full[st], half * 64, off, z);
+            }
+          }
+        }
+        z = zn;
+        off = offn;
+      }
+    }
+    // never leave with copies still landing in shared memory
+    if (lane == 0) {
+      for (uint32_t i = n > NST ? n - NST : 0; i < n; ++i)
+        if (!mbar_wait(&ctl.full[i % NST], (i / NST) & 1, a.status)) break;
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ products
+    if (lane == 0) {
+      SegIter it(a, x0, x1, ctl.u0, ctl.b0);
+      Seg sg;
+      constexpr uint32_t idS = idesc_bf16_f32(kTreeRows, kTreeKeys);
+      constexpr uint32_t idO = idesc_bf16_f32_bmn(kTreeRows, D);
+      uint32_t seg = 0, gt = 0;       // segments, key tiles so far
+      uint32_t pv[2] = {0, 0};        // P V products issued per group
+      auto issue_pv = [&](uint32_t t, int s, bool acc) {  // t: the tile's number
+        wait(&ctl.p_ready[s], pv[s] & 1);
+        const uint32_t st = (2 * t + 1) % NST;
+        wait(&ctl.full[st], ((2 * t + 1) / NST) & 1);
+        if (ok) {
+          tc_fence_after();
+          const uint64_t db = smem_desc_mn_sw128(ring + st * SM::kTile, HB);
+          const uint32_t dO = tmem + 256 + s * D, aP = tmem + s * kTreeKeys;
+#pragma unroll
+          for (int kk = 0; kk < kTreeKeys / 16; ++kk)
+            tc_mma_f16_ta(dO, aP + 8 * kk, db + 128 * kk, idO, acc || kk > 0);
+          tc_commit(&ctl.pv_done[s]);
+          tc_commit(&ctl.empty[st]);
+        }
+        ++pv[s];
+      };
+      while (it.next(sg)) {
+        wait(&ctl.q_full, seg & 1);
+        const int n = sg.k1 - sg.k0;
+        for (int i = 0; i < n; ++i, ++gt) {
+          const int s = i & 1;
+          if (i >= 2) wait(&ctl.pv_done[s], (pv[s] - 1) & 1);  // P of tile i - 2 was read
+          const uint32_t st = (2 * gt) % NST;
+          wait(&ctl.full[st], ((2 * gt) / NST) & 1);
+          if (ok) {
+            tc_fence_after();
+            const uint64_t dq = smem_desc_sw128(sQ), dk = smem_desc_sw128(ring + st * SM::kTile);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const int step = (kk >> 2) * (HB >> 4) + (kk & 3) * 2;
+              tc_mma_f16(tmem + s * kTreeKeys, dq + step, dk + step, idS, kk > 0);
+            }
+            tc_commit(&ctl.s_full[s]);
+            tc_commit(&ctl.empty[st]);
+          }
+          if (i >= 1) issue_pv(gt - 1, (i - 1) & 1, i - 1 >= 2);
+        }
+        issue_pv(gt - 1, (n - 1) & 1, n - 1 >= 2);
+        ++seg;
+      }
+      tc_commit(&ctl.drain);
+      mbar_wait(&ctl.drain, 0, a.status);
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ softmax
+    const int grp = (warp - 4) >> 2, quad = warp & 3;
+    const int tid = threadIdx.x - 128;       // 0..255 over both groups
+    const int r = quad * 32 + lane;          // the thread's row of the tile
+    const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+    const uint32_t tS = tmem + lanes + grp * kTreeKeys, tO = tmem + lanes + 256 + grp * D;
+    SegIter it(a, x0, x1, ctl.u0, ctl.b0);
+    Seg sg;
+    uint32_t seg = 0, gt0 = 0;  // segments, key tiles before this one
+    uint32_t cnt = 0;           // this group's tiles so far
+    while (it.next(sg)) {
+      const SeqInfo& s = sg.s;
+      const int row0 = sg.qi * kTreeRows, rows = min(kTreeRows, s.T * a.group - row0);
+      // the query tile: 128-byte rows of 64 elements, 16-byte chunks swizzled by row
+      for (int x = tid; x < kTreeRows * (D / 8); x += kTreeSoftmax) {
+        const int rr = x / (D / 8), ch = x % (D / 8);
+        uint4 val = make_uint4(0, 0, 0, 0);
+        if (rr < rows) {
+          const int i = (int)fast_div((uint32_t)(row0 + rr), a.div_group);
+          const int h = row0 + rr - i * a.group;
+          val = *reinterpret_cast<const uint4*>(a.q + (s.q0 + i) * a.ld_q +
+                                                (sg.g * a.group + h) * D + ch * 8);
+        }
+        *reinterpret_cast<uint4*>(sQ + (ch >> 3) * HB + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4)) = val;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl.q_full);
+
+      const bool warp_live = quad * 32 < rows;
+      const int tok = (int)fast_div((uint32_t)(row0 + min(r, rows - 1)), a.div_group);
+      const int n = sg.k1 - sg.k0, len = s.old + s.T;
+      float m = -INFINITY, l = 0.f;  // in units of log2
+      for (int i = grp; i < n; i += 2, ++cnt) {
+        const int key0 = (sg.k0 + i) * kTreeKeys;
+        const bool tail = key0 + kTreeKeys > s.old;
+        if (tail) {
+          // V of keys behind the end and non-finite V of new tokens: thread = key
+          const uint32_t f = 2 * (gt0 + i) + 1, st = f % NST;
+          warp_wait(&ctl.full[st], (f / NST) & 1);
+          const int key = key0 + r;
+          if (key >= s.old) {
+            uint8_t* v = ring + st * SM::kTile + r * 128;
+            bool found = false;
+#pragma unroll
+            for (int h = 0; h < D / 64; ++h)
+#pragma unroll
+              for (int ch = 0; ch < 8; ++ch) {
+                uint4* p = reinterpret_cast<uint4*>(v + h * HB + (((ch ^ r) & 7) << 4));
+                if (key >= len) {
+                  *p = make_uint4(0, 0, 0, 0);
+                } else {
+                  const uint4 w = *p;
+                  if (has_nonfinite(w.x) || has_nonfinite(w.y) || has_nonfinite(w.z) ||
+                      has_nonfinite(w.w)) {
+                    *p = make_uint4(drop_nonfinite(w.x), drop_nonfinite(w.y), drop_nonfinite(w.z),
+                                    drop_nonfinite(w.w));
+                    found = true;
+                  }
+                }
+              }
+            if (found) ctl.poison[seg & 1] = 1;
+          }
+          fence_proxy_async_smem();
+        }
+        warp_wait(&ctl.s_full[grp], cnt & 1);
+        tc_fence_after();
+        if (warp_live) {
+          uint32_t vis[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) vis[q] = tail ? sees32(a, s, tok, key0 + 32 * q) : 0xFFFFFFFFu;
+          float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            float x[32];
+            tmem_ld32(tS + 32 * q, x);
+            tmem_ld_wait();
+            if (tail) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                tops[e & 3] = fmaxf(tops[e & 3], (vis[q] >> e & 1) ? x[e] : -INFINITY);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) tops[e & 3] = fmaxf(tops[e & 3], x[e]);
+            }
+          }
+          const float top =
+              fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * a.scale_log2;
+          const bool rise = top > m + kRescaleLog2 || (m == -INFINITY && top > m);
+          const float mn = rise ? top : m;
+          if (i >= 2 && __any_sync(0xffffffffu, rise)) {
+            const float al = rise ? ex2_approx(m - mn) : 1.f;  // m = -inf: 0
+            warp_wait(&ctl.pv_done[grp], (cnt - 1) & 1);
+            tc_fence_after();
+#pragma unroll
+            for (int q = 0; q < D / 16; ++q) {
+              float x[16];
+              uint32_t y[16];
+              tmem_ld16(tO + 16 * q, x);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(x[e] * al);
+              tmem_st16(tO + 16 * q, y);
+            }
+            l *= al;
+          }
+          m = mn;
+          const float sub = m == -INFINITY ? 0.f : m;
+          float sums[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            float x[32];
+            uint32_t y[16];
+            tmem_ld32(tS + 32 * q, x);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              x[e] = ex2_approx(fmaf(x[e], a.scale_log2, -sub));
+              if (tail) x[e] = (vis[q] >> e & 1) ? x[e] : 0.f;
+              sums[e & 3] += x[e];
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) y[e] = pack_p(x[2 * e], x[2 * e + 1]);
+            tmem_st16(tS + 16 * q, y);  // over scores already read
+          }
+          l += (sums[0] + sums[1]) + (sums[2] + sums[3]);
+          tmem_st_wait();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl.p_ready[grp]);
+      }
+
+      // The two groups' states meet: each leaves (m, l) where its scores were,
+      // then takes one half of the head's elements of both O.
+      if (n > grp) warp_wait(&ctl.pv_done[grp], (cnt - 1) & 1);
+      tc_fence_after();
+      tmem_st2(tS, __float_as_uint(m), __float_as_uint(l));
+      tmem_st_wait();
+      tc_fence_before();
+      bar_sync(1, kTreeSoftmax);
+      tc_fence_after();
+      float mg[2], lg[2];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        uint32_t x, y;
+        tmem_ld2(tmem + lanes + q * kTreeKeys, x, y);
+        tmem_ld_wait();
+        mg[q] = __uint_as_float(x);
+        lg[q] = __uint_as_float(y);
+      }
+      const bool two = n > 1;
+      const float M = two ? fmaxf(mg[0], mg[1]) : mg[0];
+      const float w0 = mg[0] == -INFINITY ? 0.f : ex2_approx(mg[0] - M);
+      const float w1 = !two || mg[1] == -INFINITY ? 0.f : ex2_approx(mg[1] - M);
+      const float L = lg[0] * w0 + (two ? lg[1] * w1 : 0.f);
+      const bool whole = sg.k0 == 0 && sg.k1 == s.nt;
+      const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
+      const int h = row0 + min(r, rows - 1) - tok * a.group;
+      const bool poison = ctl.poison[seg & 1] != 0;
+      const bool live = r < rows;
+      const int slot = range_begin(c, W, G) >= sg.x ? 0 : 1;
+      const int64_t prow = ((int64_t)c * 2 + slot) * kTreeRows + r;
+#pragma unroll
+      for (int q = 0; q < D / 32; ++q) {  // 16 elements a turn of this group's half
+        const int e0 = grp * (D / 2) + 16 * q;
+        float o0[16], o1[16];
+        tmem_ld16(tmem + lanes + 256 + e0, o0);
+        if (two) tmem_ld16(tmem + lanes + 256 + D + e0, o1);
+        tmem_ld_wait();
+        if (live) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o0[e] = two ? o0[e] * w0 + o1[e] * w1 : o0[e] * w0;
+          if (L == 0.f) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o0[e] = 0.f;
+          }
+          if (poison) nonfinite_v(a, s, sg.b, sg.g, tok, sg.k0 * kTreeKeys, sg.k1 * kTreeKeys, e0, o0);
+          if (whole) {
+            uint32_t y[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = pack_bf16x2(o0[2 * e] * inv, o0[2 * e + 1] * inv);
+            uint4* dst = reinterpret_cast<uint4*>(a.o + (s.q0 + tok) * a.ld_o +
+                                                  (sg.g * a.group + h) * D + e0);
+            dst[0] = make_uint4(y[0], y[1], y[2], y[3]);
+            dst[1] = make_uint4(y[4], y[5], y[6], y[7]);
+          } else {
+            float4* dst = reinterpret_cast<float4*>(a.partials + prow * D + e0);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              dst[e] = make_float4(o0[4 * e], o0[4 * e + 1], o0[4 * e + 2], o0[4 * e + 3]);
+          }
+        }
+      }
+      if (!whole && live && grp == 0) a.ml[prow] = make_float2(M, L);
+      tc_fence_before();
+      if (tid == 0) ctl.poison[(seg + 1) & 1] = 0;
+      bar_sync(1, kTreeSoftmax);  // O, S, Q and the pieces: both groups are done with them
+      if (!whole) {
+        if (tid == 0) {
+          const int first = owner_of(sg.x, W, G), last = owner_of(sg.x + s.nt - 1, W, G);
+          fence_acq_rel_gpu();
+          int* ticket = a.tickets + ((int64_t)sg.b * a.n_kv + sg.g) * a.q_tiles_max + sg.qi;
+          const int got = atomicAdd(ticket, 1);
+          ctl.last = got == last - first ? 1 : 0;
+          if (ctl.last) *ticket = 0;
+          fence_acq_rel_gpu();
+        }
+        bar_sync(1, kTreeSoftmax);
+        if (ctl.last) {
+          const int first = owner_of(sg.x, W, G), last = owner_of(sg.x + s.nt - 1, W, G);
+          for (int x = tid; x < rows * (D / 4); x += kTreeSoftmax) {
+            const int rr = x / (D / 4), e = x % (D / 4) * 4;
+            float Mx = -INFINITY, Lx = 0.f;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int p = first; p <= last; ++p) {
+              const int64_t at =
+                  ((int64_t)p * 2 + (range_begin(p, W, G) >= sg.x ? 0 : 1)) * kTreeRows + rr;
+              const float2 ml = __ldcg(a.ml + at);
+              const float4 y = __ldcg(reinterpret_cast<const float4*>(a.partials + at * D + e));
+              if (ml.x == -INFINITY) continue;
+              const float Mn = fmaxf(Mx, ml.x);
+              const float u = Mx == -INFINITY ? 0.f : ex2_approx(Mx - Mn), w = ex2_approx(ml.x - Mn);
+              Mx = Mn;
+              Lx = Lx * u + ml.y * w;
+              o.x = o.x * u + y.x * w;
+              o.y = o.y * u + y.y * w;
+              o.z = o.z * u + y.z * w;
+              o.w = o.w * u + y.w * w;
+            }
+            const float iv = Lx > 0.f || Lx != Lx ? 1.f / Lx : 0.f;
+            const int i = (int)fast_div((uint32_t)(row0 + rr), a.div_group);
+            const int hh = row0 + rr - i * a.group;
+            *reinterpret_cast<uint2*>(a.o + (s.q0 + i) * a.ld_o + (sg.g * a.group + hh) * D + e) =
+                make_uint2(pack_bf16x2(o.x * iv, o.y * iv), pack_bf16x2(o.z * iv, o.w * iv));
+          }
+        }
+        bar_sync(1, kTreeSoftmax);  // ctl.last was read
+      }
+      gt0 += n;
+      ++seg;
+    }
+  }
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D>
+static cudaError_t launch_tree(const TreeAttnArgs& a, cudaStream_t st) {
+  cudaError_t e = cudaFuncSetAttribute(tree_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       TreeSmem<D>::kTotal);
+  if (e != cudaSuccess) return e;
+  return launch_k(tree_attn_kernel<D>, dim3(a.grid), dim3(kTreeThreads), TreeSmem<D>::kTotal, st, a);
 }
 
 cudaError_t launch_tree_attn(const TreeAttnArgs& a, cudaStream_t st) {
-  const int64_t warps = (int64_t)a.n_tokens * a.n_heads;
-  const dim3 grid((unsigned)((warps + 7) / 8));
-  return a.head_dim == 128 ? launch_k(tree_attn_kernel<128>, grid, dim3(256), 0, st, a)
-                           : launch_k(tree_attn_kernel<64>, grid, dim3(256), 0, st, a);
+  return a.head_dim == 128 ? launch_tree<128>(a, st) : launch_tree<64>(a, st);
 }
 
 }  // namespace tpk
