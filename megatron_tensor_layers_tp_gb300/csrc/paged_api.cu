@@ -49,23 +49,16 @@ bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
   return x < y + (uintptr_t)b_bytes && y < x + (uintptr_t)a_bytes;
 }
 
-// Query tiles of a KV head for n tokens.
-int query_tiles(const tp_model* m, int n) {
-  return cdiv((int64_t)n * (m->cfg.n_heads / m->cfg.n_kv_heads), kTreeRows);
-}
-
-// Workspace regions: the step tables' ticket, then tree attention's tickets,
-// pieces and their (m, l).  Steps of more new tokens than tree attention takes
-// (prompts) need its smallest tables only.
+// Workspace regions: the step tables' ticket, then tree attention's pieces,
+// their (m, l) and the list of cut items.
 struct StepWs {
-  size_t tickets, partials, ml, total;
+  size_t splits, ml, partials, total;
 };
-StepWs step_ws(const tp_model* m, int n_seqs, int max_new) {
+StepWs step_ws(const tp_model* m) {
   StepWs w;
   const size_t pieces = (size_t)m->num_sms * 2 * kTreeRows;
-  const int tiles = query_tiles(m, std::min(max_new, kMaxTreeTokens));
-  w.tickets = kStepTicketBytes;
-  w.ml = align_up(w.tickets + (size_t)n_seqs * m->cfg.n_kv_heads * tiles * sizeof(int), 256);
+  w.splits = kStepTicketBytes;
+  w.ml = align_up(w.splits + m->num_sms * sizeof(TreeSplit), 256);
   w.partials = align_up(w.ml + pieces * sizeof(float2), 256);
   w.total = w.partials + pieces * m->cfg.head_dim * sizeof(float);
   return w;
@@ -82,7 +75,7 @@ extern "C" {
 
 size_t tp_step_workspace_bytes(const tp_model* m, int32_t n_seqs, int32_t max_new) {
   if (!m || n_seqs < 1 || n_seqs > kMaxStepSeqs || max_new < 0) return 0;
-  return step_ws(m, n_seqs, max_new).total;
+  return step_ws(m).total;
 }
 
 tp_status tp_step_tables(const tp_model* m, const tp_pages_t* pages, const tp_step_t* step,
@@ -252,17 +245,21 @@ tp_status tp_tree_attention(const tp_model* m, const tp_bf16* q, int64_t ld_q, t
     a.head_dim = c.head_dim;
     a.div_group = make_fastdiv((uint32_t)a.group);
     a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)c.head_dim));
-    a.q_tiles_max = query_tiles(m, step->max_new);
-    a.kv_once = a.q_tiles_max == 1;
+    const int64_t rows = (int64_t)step->max_new * a.group;
+    a.kv_once = rows <= kTreeRows;
     a.grid = m->num_sms;
-    const StepWs w = step_ws(m, step->n_seqs, step->max_new);
+    const StepWs w = step_ws(m);
     uint8_t* base = static_cast<uint8_t*>(ws);
-    a.tickets = reinterpret_cast<int*>(base + w.tickets);
+    a.splits = reinterpret_cast<TreeSplit*>(base + w.splits);
     a.ml = reinterpret_cast<float2*>(base + w.ml);
     a.partials = reinterpret_cast<float*>(base + w.partials);
     a.status = m->status;
+    const TreeJoinArgs j = {a.partials, a.ml, a.splits, o, ld_o, a.group, a.div_group};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return cuda_status(launch(m, "tree_attn", st, [&] { return launch_tree_attn(a, st); }));
+    TP_CHECK_CUDA(launch(m, "tree_attn", st, [&] { return launch_tree_attn(a, st); }));
+    return cuda_status(launch(m, "tree_join", st, [&] {
+      return launch_tree_join(j, c.head_dim, a.grid, (int)std::min<int64_t>(rows, kTreeRows), st);
+    }));
   });
 }
 

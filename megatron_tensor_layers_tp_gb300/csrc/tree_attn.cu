@@ -16,8 +16,10 @@
 // Work is the flat sequence of (sequence, KV head, query tile, key tile),
 // split evenly over one CTA per SM.  A CTA finds its range from the lengths on
 // the GPU, so a captured launch follows them.  An item cut between CTAs leaves
-// unnormalised fp32 pieces; the last CTA to finish one (ticket, no waiting)
-// joins them in key order: the result is deterministic.
+// unnormalised fp32 pieces, and a second small kernel joins them in key order
+// (deterministic).  Measured against the join by the last CTA to finish a
+// piece: that CTA alone pulls every piece (64 KB each at 128 rows), 268 us
+// for prompt chunks instead of @@ us.
 //
 // Roles of the 12 warps:
 //   warp 0     : K and V tiles by TMA into a ring, one box per lane, through
@@ -45,6 +47,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "paged.h"
 #include "ptx.cuh"
 
@@ -70,7 +74,6 @@ struct TreeCtl {
   long long warp_sum[12];
   long long total, u0;
   int b0;
-  int last;
   int poison[2];
   uint32_t tmem;
 };
@@ -306,23 +309,25 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
       const int len = sg.s.old + sg.s.T;
       // lane -> (box, 64-element half)
       const int box = D == 128 ? lane >> 1 : lane, half = D == 128 ? lane & 1 : 0;
-      auto look_up = [&](int kt, int& z, int& off) {
+      // the page number, used one tile later: its load is in flight while the
+      // tile before waits for its place in the ring
+      auto look_up = [&](int kt) {
         const int key = kt * kTreeKeys + box * R;
-        z = -1;
-        off = 0;
-        if (box < boxes && kt < sg.k1 && key < len) {
-          const int pg = (int)fast_div((uint32_t)key, a.div_page);
-          const int page = page_of(a, sg.b, pg);
-          off = key - pg * a.page_size;
-          z = page < 0 ? a.slices : (copy * a.n_pages + page) * a.kv_r + local;
-        }
+        return box < boxes && kt < sg.k1 && key < len
+                   ? a.table[(int64_t)sg.b * a.ld_table + fast_div((uint32_t)key, a.div_page)]
+                   : 0;
       };
-      int z, off;
-      look_up(sg.k0, z, off);
+      int page = look_up(sg.k0);
       for (int kt = sg.k0; ok && kt < sg.k1; ++kt) {
-        int zn, offn;
-        look_up(kt + 1, zn, offn);  // in flight while this tile waits for its place
+        const int page_next = look_up(kt + 1);
         const int here = min(boxes, (len - kt * kTreeKeys + R - 1) / R);
+        const int key = kt * kTreeKeys + box * R;
+        const int off = key - (int)fast_div((uint32_t)key, a.div_page) * a.page_size;
+        int z = (copy * a.n_pages + page) * a.kv_r + local;
+        if (page < 0 || page >= a.n_pages) {
+          record_status(a.status, kStatusTableRange);
+          z = a.slices;  // outside the tensor map: zeros
+        }
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
           const uint32_t st = n % NST;
@@ -332,7 +337,7 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
             ++n;
             if (lane == 0) mbar_arrive_expect_tx(&ctl.full[st], here * R * D * 2);
             __syncwarp();
-            if (z >= 0) {
+            if (box < here) {
               uint8_t* dst = ring + st * SM::kTile + half * HB + box * R * 128;
               const CUtensorMap* tm = kv ? &a.tmV : &a.tmK;
               if (a.kv_once) tma_load_3d(dst, tm, &ctl.full[st], half * 64, off, z, pol);
@@ -340,8 +345,7 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
             }
           }
         }
-        z = zn;
-        off = offn;
+        page = page_next;
       }
     }
     // never leave with copies still landing in shared memory
@@ -414,20 +418,37 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
     Seg sg;
     uint32_t seg = 0, gt0 = 0;  // segments, key tiles before this one
     uint32_t cnt = 0;           // this group's tiles so far
+    TreeSplit split = {0, 0, 0, 0, 0, -1};
     while (it.next(sg)) {
       const SeqInfo& s = sg.s;
       const int row0 = sg.qi * kTreeRows, rows = min(kTreeRows, s.T * a.group - row0);
-      // the query tile: 128-byte rows of 64 elements, 16-byte chunks swizzled by row
-      for (int x = tid; x < kTreeRows * (D / 8); x += kTreeSoftmax) {
-        const int rr = x / (D / 8), ch = x % (D / 8);
-        uint4 val = make_uint4(0, 0, 0, 0);
-        if (rr < rows) {
-          const int i = (int)fast_div((uint32_t)(row0 + rr), a.div_group);
-          const int h = row0 + rr - i * a.group;
-          val = *reinterpret_cast<const uint4*>(a.q + (s.q0 + i) * a.ld_q +
-                                                (sg.g * a.group + h) * D + ch * 8);
+      // the query tile: 128-byte rows of 64 elements, 16-byte chunks swizzled
+      // by row; every load is in flight before the first store.  Rows past the
+      // item's are zeros up to the next 32 and undefined behind (no warp reads
+      // their scores).
+      {
+        constexpr int kPer = kTreeRows * (D / 8) / kTreeSoftmax;  // chunks of a thread
+        constexpr int kRowStep = kTreeSoftmax / (D / 8);
+        const int ch = tid % (D / 8), r0 = tid / (D / 8);
+        uint4 val[kPer];
+#pragma unroll
+        for (int y = 0; y < kPer; ++y) {
+          const int rr = r0 + y * kRowStep;
+          val[y] = make_uint4(0, 0, 0, 0);
+          if (rr < rows) {
+            const int i = (int)fast_div((uint32_t)(row0 + rr), a.div_group);
+            const int h = row0 + rr - i * a.group;
+            val[y] = *reinterpret_cast<const uint4*>(a.q + (s.q0 + i) * a.ld_q +
+                                                     (sg.g * a.group + h) * D + ch * 8);
+          }
         }
-        *reinterpret_cast<uint4*>(sQ + (ch >> 3) * HB + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4)) = val;
+#pragma unroll
+        for (int y = 0; y < kPer; ++y) {
+          const int rr = r0 + y * kRowStep;
+          if (rr < ((rows + 31) & ~31))
+            *reinterpret_cast<uint4*>(sQ + (ch >> 3) * HB + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4)) =
+                val[y];
+        }
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -437,6 +458,66 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
       const int tok = (int)fast_div((uint32_t)(row0 + min(r, rows - 1)), a.div_group);
       const int n = sg.k1 - sg.k0, len = s.old + s.T;
       float m = -INFINITY, l = 0.f;  // in units of log2
+      // one tile of the group: scores from tensor memory, P back into it
+      uint32_t vis[4];
+      auto tile = [&](auto tail_tag, int i) {
+        constexpr bool kTail = decltype(tail_tag)::value;
+        float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float x[32];
+          tmem_ld32(tS + 32 * q, x);
+          tmem_ld_wait();
+          if constexpr (kTail) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              tops[e & 3] = fmaxf(tops[e & 3], (vis[q] >> e & 1) ? x[e] : -INFINITY);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) tops[e & 3] = fmaxf(tops[e & 3], x[e]);
+          }
+        }
+        const float top =
+            fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * a.scale_log2;
+        const bool rise = top > m + kRescaleLog2 || (m == -INFINITY && top > m);
+        const float mn = rise ? top : m;
+        if (i >= 2 && __any_sync(0xffffffffu, rise)) {
+          const float al = rise ? ex2_approx(m - mn) : 1.f;  // m = -inf: 0
+          warp_wait(&ctl.pv_done[grp], (cnt - 1) & 1);
+          tc_fence_after();
+#pragma unroll
+          for (int q = 0; q < D / 16; ++q) {
+            float x[16];
+            uint32_t y[16];
+            tmem_ld16(tO + 16 * q, x);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(x[e] * al);
+            tmem_st16(tO + 16 * q, y);
+          }
+          l *= al;
+        }
+        m = mn;
+        const float sub = m == -INFINITY ? 0.f : m;
+        float sums[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float x[32];
+          uint32_t y[16];
+          tmem_ld32(tS + 32 * q, x);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            x[e] = ex2_approx(fmaf(x[e], a.scale_log2, -sub));
+            if constexpr (kTail) x[e] = (vis[q] >> e & 1) ? x[e] : 0.f;
+            sums[e & 3] += x[e];
+          }
+#pragma unroll
+          for (int e = 0; e < 16; ++e) y[e] = pack_p(x[2 * e], x[2 * e + 1]);
+          tmem_st16(tS + 16 * q, y);  // over scores already read
+        }
+        l += (sums[0] + sums[1]) + (sums[2] + sums[3]);
+      };
       for (int i = grp; i < n; i += 2, ++cnt) {
         const int key0 = (sg.k0 + i) * kTreeKeys;
         const bool tail = key0 + kTreeKeys > s.old;
@@ -445,91 +526,39 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
           const uint32_t f = 2 * (gt0 + i) + 1, st = f % NST;
           warp_wait(&ctl.full[st], (f / NST) & 1);
           const int key = key0 + r;
-          if (key >= s.old) {
-            uint8_t* v = ring + st * SM::kTile + r * 128;
+          uint8_t* v = ring + st * SM::kTile + r * 128;
+          if (key >= len) {
+#pragma unroll
+            for (int ch = 0; ch < D / 8; ++ch)
+              *reinterpret_cast<uint4*>(v + (ch >> 3) * HB + (((ch ^ r) & 7) << 4)) =
+                  make_uint4(0, 0, 0, 0);
+          } else if (key >= s.old) {
             bool found = false;
 #pragma unroll
-            for (int h = 0; h < D / 64; ++h)
-#pragma unroll
-              for (int ch = 0; ch < 8; ++ch) {
-                uint4* p = reinterpret_cast<uint4*>(v + h * HB + (((ch ^ r) & 7) << 4));
-                if (key >= len) {
-                  *p = make_uint4(0, 0, 0, 0);
-                } else {
-                  const uint4 w = *p;
-                  if (has_nonfinite(w.x) || has_nonfinite(w.y) || has_nonfinite(w.z) ||
-                      has_nonfinite(w.w)) {
-                    *p = make_uint4(drop_nonfinite(w.x), drop_nonfinite(w.y), drop_nonfinite(w.z),
-                                    drop_nonfinite(w.w));
-                    found = true;
-                  }
-                }
+            for (int ch = 0; ch < D / 8; ++ch) {
+              const uint4 w = *reinterpret_cast<const uint4*>(v + (ch >> 3) * HB + (((ch ^ r) & 7) << 4));
+              found = found || has_nonfinite(w.x) || has_nonfinite(w.y) || has_nonfinite(w.z) ||
+                      has_nonfinite(w.w);
+            }
+            if (found) {
+              ctl.poison[seg & 1] = 1;
+              for (int ch = 0; ch < D / 8; ++ch) {
+                uint4* p = reinterpret_cast<uint4*>(v + (ch >> 3) * HB + (((ch ^ r) & 7) << 4));
+                *p = make_uint4(drop_nonfinite(p->x), drop_nonfinite(p->y), drop_nonfinite(p->z),
+                                drop_nonfinite(p->w));
               }
-            if (found) ctl.poison[seg & 1] = 1;
+            }
           }
+          // what the thread's row sees, before the scores are there
+#pragma unroll
+          for (int q = 0; q < 4; ++q) vis[q] = sees32(a, s, tok, key0 + 32 * q);
           fence_proxy_async_smem();
         }
         warp_wait(&ctl.s_full[grp], cnt & 1);
         tc_fence_after();
         if (warp_live) {
-          uint32_t vis[4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) vis[q] = tail ? sees32(a, s, tok, key0 + 32 * q) : 0xFFFFFFFFu;
-          float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            float x[32];
-            tmem_ld32(tS + 32 * q, x);
-            tmem_ld_wait();
-            if (tail) {
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                tops[e & 3] = fmaxf(tops[e & 3], (vis[q] >> e & 1) ? x[e] : -INFINITY);
-            } else {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) tops[e & 3] = fmaxf(tops[e & 3], x[e]);
-            }
-          }
-          const float top =
-              fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * a.scale_log2;
-          const bool rise = top > m + kRescaleLog2 || (m == -INFINITY && top > m);
-          const float mn = rise ? top : m;
-          if (i >= 2 && __any_sync(0xffffffffu, rise)) {
-            const float al = rise ? ex2_approx(m - mn) : 1.f;  // m = -inf: 0
-            warp_wait(&ctl.pv_done[grp], (cnt - 1) & 1);
-            tc_fence_after();
-#pragma unroll
-            for (int q = 0; q < D / 16; ++q) {
-              float x[16];
-              uint32_t y[16];
-              tmem_ld16(tO + 16 * q, x);
-              tmem_ld_wait();
-#pragma unroll
-              for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(x[e] * al);
-              tmem_st16(tO + 16 * q, y);
-            }
-            l *= al;
-          }
-          m = mn;
-          const float sub = m == -INFINITY ? 0.f : m;
-          float sums[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            float x[32];
-            uint32_t y[16];
-            tmem_ld32(tS + 32 * q, x);
-            tmem_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              x[e] = ex2_approx(fmaf(x[e], a.scale_log2, -sub));
-              if (tail) x[e] = (vis[q] >> e & 1) ? x[e] : 0.f;
-              sums[e & 3] += x[e];
-            }
-#pragma unroll
-            for (int e = 0; e < 16; ++e) y[e] = pack_p(x[2 * e], x[2 * e + 1]);
-            tmem_st16(tS + 16 * q, y);  // over scores already read
-          }
-          l += (sums[0] + sums[1]) + (sums[2] + sums[3]);
+          if (tail) tile(std::true_type(), i);
+          else tile(std::false_type(), i);
           tmem_st_wait();
         }
         tc_fence_before();
@@ -599,58 +628,61 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
         }
       }
       if (!whole && live && grp == 0) a.ml[prow] = make_float2(M, L);
+      if (sg.k0 == 0 && !whole && tid == 0)  // this CTA opens a cut item
+        split = {s.q0, row0, rows, sg.g, slot, owner_of(sg.x + s.nt - 1, W, G)};
       tc_fence_before();
       if (tid == 0) ctl.poison[(seg + 1) & 1] = 0;
-      bar_sync(1, kTreeSoftmax);  // O, S, Q and the pieces: both groups are done with them
-      if (!whole) {
-        if (tid == 0) {
-          const int first = owner_of(sg.x, W, G), last = owner_of(sg.x + s.nt - 1, W, G);
-          fence_acq_rel_gpu();
-          int* ticket = a.tickets + ((int64_t)sg.b * a.n_kv + sg.g) * a.q_tiles_max + sg.qi;
-          const int got = atomicAdd(ticket, 1);
-          ctl.last = got == last - first ? 1 : 0;
-          if (ctl.last) *ticket = 0;
-          fence_acq_rel_gpu();
-        }
-        bar_sync(1, kTreeSoftmax);
-        if (ctl.last) {
-          const int first = owner_of(sg.x, W, G), last = owner_of(sg.x + s.nt - 1, W, G);
-          for (int x = tid; x < rows * (D / 4); x += kTreeSoftmax) {
-            const int rr = x / (D / 4), e = x % (D / 4) * 4;
-            float Mx = -INFINITY, Lx = 0.f;
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int p = first; p <= last; ++p) {
-              const int64_t at =
-                  ((int64_t)p * 2 + (range_begin(p, W, G) >= sg.x ? 0 : 1)) * kTreeRows + rr;
-              const float2 ml = __ldcg(a.ml + at);
-              const float4 y = __ldcg(reinterpret_cast<const float4*>(a.partials + at * D + e));
-              if (ml.x == -INFINITY) continue;
-              const float Mn = fmaxf(Mx, ml.x);
-              const float u = Mx == -INFINITY ? 0.f : ex2_approx(Mx - Mn), w = ex2_approx(ml.x - Mn);
-              Mx = Mn;
-              Lx = Lx * u + ml.y * w;
-              o.x = o.x * u + y.x * w;
-              o.y = o.y * u + y.y * w;
-              o.z = o.z * u + y.z * w;
-              o.w = o.w * u + y.w * w;
-            }
-            const float iv = Lx > 0.f || Lx != Lx ? 1.f / Lx : 0.f;
-            const int i = (int)fast_div((uint32_t)(row0 + rr), a.div_group);
-            const int hh = row0 + rr - i * a.group;
-            *reinterpret_cast<uint2*>(a.o + (s.q0 + i) * a.ld_o + (sg.g * a.group + hh) * D + e) =
-                make_uint2(pack_bf16x2(o.x * iv, o.y * iv), pack_bf16x2(o.z * iv, o.w * iv));
-          }
-        }
-        bar_sync(1, kTreeSoftmax);  // ctl.last was read
-      }
+      bar_sync(1, kTreeSoftmax);  // both groups are done with O, S and Q
       gt0 += n;
       ++seg;
     }
+    if (tid == 0) a.splits[c] = split;
   }
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the pieces of the items cut between CTAs, in key order: block (c, y)
+// takes rows [32 y, 32 y + 32) of the item that CTA c opened, a thread 4
+// elements of some rows.  The pieces come from L2: every load of a row's
+// pieces is independent of the others.
+template <int D>
+__global__ void __launch_bounds__(256) tree_join_kernel(const TreeJoinArgs a) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const TreeSplit s = a.splits[blockIdx.x];
+  if (s.last < 0) return;
+  constexpr int kCols = D / 4, kStep = 256 / kCols;
+  const int e = threadIdx.x % kCols * 4, end = min(s.rows, (int)blockIdx.y * 32 + 32);
+  for (int r = blockIdx.y * 32 + threadIdx.x / kCols; r < end; r += kStep) {
+    const int64_t opening = ((int64_t)blockIdx.x * 2 + s.slot) * kTreeRows + r;
+    auto at = [&](int p) {  // the later pieces begin their CTA's range
+      return p == (int)blockIdx.x ? opening : (int64_t)p * 2 * kTreeRows + r;
+    };
+    float M = -INFINITY;
+#pragma unroll 8
+    for (int p = blockIdx.x; p <= s.last; ++p) M = fmaxf(M, __ldcg(&a.ml[at(p)]).x);
+    float L = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int p = blockIdx.x; p <= s.last; ++p) {
+      const float2 ml = __ldcg(&a.ml[at(p)]);
+      const float4 y = __ldcg(reinterpret_cast<const float4*>(a.partials + at(p) * D + e));
+      const float w = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
+      L += ml.y * w;
+      o.x += y.x * w;
+      o.y += y.y * w;
+      o.z += y.z * w;
+      o.w += y.w * w;
+    }
+    const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
+    const int i = (int)fast_div((uint32_t)(s.row0 + r), a.div_group);
+    const int h = s.row0 + r - i * a.group;
+    *reinterpret_cast<uint2*>(a.o + (s.q0 + i) * a.ld_o + (s.g * a.group + h) * D + e) =
+        make_uint2(pack_p(o.x * inv, o.y * inv), pack_p(o.z * inv, o.w * inv));
   }
 }
 
@@ -664,6 +696,13 @@ static cudaError_t launch_tree(const TreeAttnArgs& a, cudaStream_t st) {
 
 cudaError_t launch_tree_attn(const TreeAttnArgs& a, cudaStream_t st) {
   return a.head_dim == 128 ? launch_tree<128>(a, st) : launch_tree<64>(a, st);
+}
+
+cudaError_t launch_tree_join(const TreeJoinArgs& a, int head_dim, int grid, int max_rows,
+                             cudaStream_t st) {
+  const dim3 g(grid, (max_rows + 31) / 32);
+  return head_dim == 128 ? launch_k(tree_join_kernel<128>, g, dim3(256), 0, st, a)
+                         : launch_k(tree_join_kernel<64>, g, dim3(256), 0, st, a);
 }
 
 }  // namespace tpk
