@@ -94,7 +94,7 @@ struct TreeJoinArgs {
   FastDiv div_group;
 };
 constexpr int kTreeRows = 128;  // query rows (tokens x Q heads of a KV head) of a tile
-constexpr int kTreeKeys = 128;  // keys of a tile
+constexpr int kTreeKeys = 64;   // keys of a tile
 cudaError_t launch_tree_attn(const TreeAttnArgs& a, cudaStream_t st);
 // max_rows: no query tile has more rows
 cudaError_t launch_tree_join(const TreeJoinArgs& a, int head_dim, int grid, int max_rows,

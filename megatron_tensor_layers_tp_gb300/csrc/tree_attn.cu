@@ -9,12 +9,13 @@
 // Every Q head of a KV head and every new token of a sequence share its keys:
 // they are the rows of 128-row query tiles (row = token * group + head), so K
 // and V are read once for up to 128 / group tokens.  With one tile per
-// sequence and KV head the cache's bytes bound the kernel: a 128-key tile of K
-// and V (64 KB at d = 128) takes an SM 1.5 us at its share of the memory rate,
-// its two products 0.3 us and its exponentials 0.3-0.6 us.
+// sequence and KV head the cache's bytes bound the kernel: a 64-key tile of K
+// and V (32 KB at d = 128) takes an SM 0.73 us at its share of the memory rate,
+// its two products 0.14 us and its exponentials 0.2 us.
 //
-// Work is the flat sequence of (sequence, KV head, query tile, key tile),
-// split evenly over one CTA per SM.  A CTA finds its range from the lengths on
+// Work is the flat sequence of (sequence, KV head, query tile, key tile), an
+// item's fixed work counted as kItemCost tiles more, split evenly over one CTA
+// per SM.  A CTA finds its range from the lengths on
 // the GPU, so a captured launch follows them.  An item cut between CTAs leaves
 // unnormalised fp32 pieces, and a second small kernel joins them in key order
 // (deterministic).  Measured against the join by the last CTA to finish a
@@ -24,14 +25,21 @@
 // Roles of the 12 warps:
 //   warp 0     : K and V tiles by TMA into a ring, one box per lane, through
 //                the page table (boxes end where pages end);
-//   warp 1     : one thread issues S = Q K^T (tensor memory) and O += P V, with
-//                P read from tensor memory and V as it lies in the page (the
-//                head's elements contiguous);
+//   warp 1     : one thread issues S = Q K^T into tensor memory;
+//   warps 2, 3 : one thread each issues O += P V of a softmax group, with P read
+//                from tensor memory and V as it lies in the page (the head's
+//                elements contiguous).  Issuing costs about 65 cycles a product
+//                and 80 a commit: one thread for all of them set the pace
+//                (1850-2000 cycles a tile, nothing else busy).
 //   warps 4-7, 8-11: two softmax groups.  They take alternate key tiles, each
-//                with its own S, running maximum, sum and O, so that one
-//                tile's exponentials overlap the other's products without
-//                exchanging maxima; the two states meet at the item's end.  A
-//                thread owns a row.
+//                with its own running maximum, sum and O, so that neither
+//                waits for the other's maxima; the two states meet at the
+//                item's end.  A thread owns a row and holds a tile's 64 scores
+//                in registers.
+// Each group has two S buffers: the products of its next tile run while it
+// works on this one.  Measured with 128-key tiles and one buffer a group, the
+// chain scores -> exponentials -> P V -> next scores left the SM waiting: an
+// 8000-key chunk of 64-element heads took 172 us instead of @@.
 // P overwrites S in place (bf16, half the columns).  O is rescaled only when a
 // row's maximum rose by more than 2^8 since its last rescaling: the sums are
 // relative to the older maximum until then, which is exact algebra and keeps
@@ -57,27 +65,28 @@ namespace tpk {
 constexpr int kTreeThreads = 384;
 constexpr int kTreeSoftmax = 256;        // threads of the two softmax groups
 constexpr float kRescaleLog2 = 8.f;
+constexpr int kItemCost = 8;             // an item's fixed work in key tiles
 
 template <int D>
 struct TreeSmem {
-  static constexpr int kTile = kTreeKeys * D * 2;   // a K or V tile; also the query tile
-  static constexpr int kStages = D == 128 ? 6 : 12;
-  static constexpr int kRing = kTile;                // byte offset of the ring (after Q)
+  static constexpr int kTile = kTreeKeys * D * 2;    // a K or V tile
+  static constexpr int kStages = D == 128 ? 12 : 24;
+  static constexpr int kRing = kTreeRows * D * 2;     // byte offset of the ring (after Q)
   static constexpr int kBars = kRing + kStages * kTile;
-  static constexpr int kTotal = kBars + 512 + 1024;  // + alignment of the base
+  static constexpr int kTotal = kBars + 1024 + 1024;  // + alignment of the base
   static_assert(kTotal <= 227 * 1024, "shared memory of one CTA");
 };
 // after the ring
 struct TreeCtl {
-  uint64_t full[12], empty[12];
-  uint64_t s_full[2], p_ready[2], pv_done[2], q_full, drain;
+  uint64_t full[24], empty[24];
+  uint64_t s_full[4], p_ready[4], pv_done[4], q_full, drain;
   long long warp_sum[12];
   long long total, u0;
   int b0;
   int poison[2];
   uint32_t tmem;
 };
-static_assert(sizeof(TreeCtl) <= 512, "control block");
+static_assert(sizeof(TreeCtl) <= 1024, "control block");
 
 // Sequence b's first row, new tokens, old length and tiles; an inconsistent
 // one has no tokens (and sets the status).
@@ -100,9 +109,15 @@ __device__ __forceinline__ SeqInfo seq_info(const TreeAttnArgs& a, int b) {
   s.nt = s.T ? (s.old + s.T + kTreeKeys - 1) / kTreeKeys : 0;
   return s;
 }
+// The flat positions of a sequence: every item's tiles after its fixed cost.
+__device__ __forceinline__ int64_t positions(const TreeAttnArgs& a, const SeqInfo& s) {
+  return (int64_t)a.n_kv * s.qt * (s.nt + kItemCost);
+}
 
 // One CTA's part of an item: key tiles [k0, k1) of (sequence b, KV head g,
-// query tile qi); x: the flat index of the item's tile 0.
+// query tile qi); x: the flat position of the item's begin.  A part that lies
+// within the item's fixed cost has no tiles and is passed over: the parts with
+// tiles are those of consecutive CTAs.
 struct Seg {
   SeqInfo s;
   int b, g, qi, k0, k1;
@@ -119,24 +134,29 @@ struct SegIter {
     if (x < x1) s = seq_info(a, b);
   }
   __device__ __forceinline__ bool next(Seg& sg) {
-    if (x >= x1) return false;
-    while (u >= (int64_t)a.n_kv * s.qt * s.nt) {  // at most to the last sequence: x < x1 <= total
-      u -= (int64_t)a.n_kv * s.qt * s.nt;
-      if (++b >= a.n_seqs) return false;
-      s = seq_info(a, b);
+    while (x < x1) {
+      while (u >= positions(a, s)) {  // at most to the last sequence: x < x1 <= total
+        u -= positions(a, s);
+        if (++b >= a.n_seqs) return false;
+        s = seq_info(a, b);
+      }
+      const int cost = s.nt + kItemCost;
+      const int64_t item = u / cost;
+      const int at = (int)(u - item * cost);
+      const int64_t left = x1 - x;
+      const int end = (int)(left < cost - at ? at + left : cost);
+      sg.s = s;
+      sg.b = b;
+      sg.g = (int)(item / s.qt);
+      sg.qi = (int)(item - (int64_t)sg.g * s.qt);
+      sg.k0 = max(at - kItemCost, 0);
+      sg.k1 = max(end - kItemCost, 0);
+      sg.x = x - at;
+      x += end - at;
+      u += end - at;
+      if (sg.k1 > sg.k0) return true;
     }
-    const int64_t item = u / s.nt;
-    sg.s = s;
-    sg.b = b;
-    sg.k0 = (int)(u - item * s.nt);
-    sg.g = (int)(item / s.qt);
-    sg.qi = (int)(item - (int64_t)sg.g * s.qt);
-    const int64_t left = x1 - x;
-    sg.k1 = (int)(left < s.nt - sg.k0 ? sg.k0 + left : s.nt);
-    sg.x = x - sg.k0;
-    x += sg.k1 - sg.k0;
-    u += sg.k1 - sg.k0;
-    return true;
+    return false;
   }
 };
 
@@ -206,7 +226,8 @@ template <int D>
 __global__ void __launch_bounds__(kTreeThreads, 1)
 tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
   using SM = TreeSmem<D>;
-  constexpr int NST = SM::kStages, HB = kTreeKeys * 128;  // bytes of 64 elements of a tile
+  constexpr int NST = SM::kStages;
+  constexpr int HB = kTreeKeys * 128, HQ = kTreeRows * 128;  // bytes of 64 elements of a K/V, Q tile
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   uint8_t* sQ = smem;
@@ -217,14 +238,14 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
   pdl_launch_dependents();
   if (threadIdx.x == 0) {
     for (int i = 0; i < NST; ++i) { mbar_init(&ctl.full[i], 1); mbar_init(&ctl.empty[i], 1); }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       mbar_init(&ctl.s_full[i], 1);
       mbar_init(&ctl.p_ready[i], 4);
       mbar_init(&ctl.pv_done[i], 1);
-      ctl.poison[i] = 0;
     }
+    ctl.poison[0] = ctl.poison[1] = 0;
     mbar_init(&ctl.q_full, kTreeSoftmax / 32);
-    mbar_init(&ctl.drain, 1);
+    mbar_init(&ctl.drain, 3);
     fence_barrier_init();
     fence_proxy_async_smem();
     tma_prefetch_desc(&a.tmK);
@@ -235,8 +256,8 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
 
   // This CTA's range: thread t sums the tiles of a run of sequences; the
   // thread whose run holds the range's begin looks it up.
-  // No more CTAs take part than there are tiles, so that an item's pieces lie
-  // with consecutive CTAs.
+  // No more CTAs take part than there are positions, so that an item's pieces
+  // lie with consecutive CTAs.
   int G = gridDim.x;
   const int c = blockIdx.x;
   {
@@ -245,7 +266,7 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
     long long sum = 0;
     for (int b = lo; b < hi; ++b) {
       const SeqInfo s = seq_info(a, b);
-      sum += (long long)a.n_kv * s.qt * s.nt;
+      sum += positions(a, s);
     }
     long long incl = sum;
 #pragma unroll
@@ -271,7 +292,7 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
       int b = lo;
       while (true) {
         const SeqInfo s = seq_info(a, b);
-        const long long n = (long long)a.n_kv * s.qt * s.nt;
+        const long long n = positions(a, s);
         if (x0 < at + n) break;
         at += n;
         ++b;
@@ -309,20 +330,28 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
       const int len = sg.s.old + sg.s.T;
       // lane -> (box, 64-element half)
       const int box = D == 128 ? lane >> 1 : lane, half = D == 128 ? lane & 1 : 0;
-      // the page number, used one tile later: its load is in flight while the
-      // tile before waits for its place in the ring
-      auto look_up = [&](int kt) {
-        const int key = kt * kTreeKeys + box * R;
-        return box < boxes && kt < sg.k1 && key < len
-                   ? a.table[(int64_t)sg.b * a.ld_table + fast_div((uint32_t)key, a.div_page)]
-                   : 0;
-      };
-      int page = look_up(sg.k0);
+      // The row of the page table through a window of 64 entries, two a lane:
+      // the second half is in flight while the first is used.  (One entry a
+      // box and tile, loaded a tile ahead, made the load's latency the tile
+      // rate: 1.06 us a tile of 64 keys.)
+      const int32_t* row = a.table + (int64_t)sg.b * a.ld_table;
+      const int last = (int)fast_div((uint32_t)min(len, sg.k1 * kTreeKeys) - 1, a.div_page);
+      auto load = [&](int pg) { return pg <= last ? row[pg] : 0; };
+      int w0 = (int)fast_div((uint32_t)(sg.k0 * kTreeKeys), a.div_page);
+      int win = load(w0 + lane), nxt = load(w0 + 32 + lane);
       for (int kt = sg.k0; ok && kt < sg.k1; ++kt) {
-        const int page_next = look_up(kt + 1);
         const int here = min(boxes, (len - kt * kTreeKeys + R - 1) / R);
-        const int key = kt * kTreeKeys + box * R;
-        const int off = key - (int)fast_div((uint32_t)key, a.div_page) * a.page_size;
+        const int key = kt * kTreeKeys + min(box, here - 1) * R;  // (spare lanes: the last box)
+        const int pg = (int)fast_div((uint32_t)key, a.div_page);
+        if (__shfl_sync(0xffffffffu, pg, 0) - w0 >= 32) {
+          w0 += 32;
+          win = nxt;
+          nxt = load(w0 + 32 + lane);
+        }
+        const int lo = __shfl_sync(0xffffffffu, win, (pg - w0) & 31);
+        const int hi = __shfl_sync(0xffffffffu, nxt, (pg - w0) & 31);
+        const int page = pg - w0 < 32 ? lo : hi;
+        const int off = key - pg * a.page_size;
         int z = (copy * a.n_pages + page) * a.kv_r + local;
         if (page < 0 || page >= a.n_pages) {
           record_status(a.status, kStatusTableRange);
@@ -345,7 +374,6 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
             }
           }
         }
-        page = page_next;
       }
     }
     // never leave with copies still landing in shared memory
@@ -354,54 +382,62 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
         if (!mbar_wait(&ctl.full[i % NST], (i / NST) & 1, a.status)) break;
     }
     __syncwarp();
-  } else if (warp == 1) {
+  } else if (warp < 4) {
     // ------------------------------------------------------------ products
     if (lane == 0) {
       SegIter it(a, x0, x1, ctl.u0, ctl.b0);
       Seg sg;
-      constexpr uint32_t idS = idesc_bf16_f32(kTreeRows, kTreeKeys);
-      constexpr uint32_t idO = idesc_bf16_f32_bmn(kTreeRows, D);
-      uint32_t seg = 0, gt = 0;       // segments, key tiles so far
-      uint32_t pv[2] = {0, 0};        // P V products issued per group
-      auto issue_pv = [&](uint32_t t, int s, bool acc) {  // t: the tile's number
-        wait(&ctl.p_ready[s], pv[s] & 1);
-        const uint32_t st = (2 * t + 1) % NST;
-        wait(&ctl.full[st], ((2 * t + 1) / NST) & 1);
-        if (ok) {
-          tc_fence_after();
-          const uint64_t db = smem_desc_mn_sw128(ring + st * SM::kTile, HB);
-          const uint32_t dO = tmem + 256 + s * D, aP = tmem + s * kTreeKeys;
-#pragma unroll
-          for (int kk = 0; kk < kTreeKeys / 16; ++kk)
-            tc_mma_f16_ta(dO, aP + 8 * kk, db + 128 * kk, idO, acc || kk > 0);
-          tc_commit(&ctl.pv_done[s]);
-          tc_commit(&ctl.empty[st]);
-        }
-        ++pv[s];
-      };
-      while (it.next(sg)) {
-        wait(&ctl.q_full, seg & 1);
-        const int n = sg.k1 - sg.k0;
-        for (int i = 0; i < n; ++i, ++gt) {
-          const int s = i & 1;
-          if (i >= 2) wait(&ctl.pv_done[s], (pv[s] - 1) & 1);  // P of tile i - 2 was read
-          const uint32_t st = (2 * gt) % NST;
-          wait(&ctl.full[st], ((2 * gt) / NST) & 1);
-          if (ok) {
+      uint32_t gt = 0;  // key tiles before this segment
+      if (warp == 1) {
+        constexpr uint32_t idS = idesc_bf16_f32(kTreeRows, kTreeKeys);
+        uint32_t par = 0;   // bit k: products into S buffer k, mod 2
+        const uint64_t dq = smem_desc_sw128(sQ), dk0 = smem_desc_sw128(ring);
+        for (uint32_t seg = 0; it.next(sg); ++seg) {
+          wait(&ctl.q_full, seg & 1);
+          const int n = sg.k1 - sg.k0;
+          for (int i = 0; i < n; ++i) {  // S buffer i % 4
+            const int k = i & 3;
+            if (i >= 4) wait(&ctl.pv_done[k], (par >> k & 1) ^ 1);  // P of tile i - 4 was read
+            par ^= 1u << k;
+            const uint32_t f = 2 * (gt + i), st = f % NST;
+            wait(&ctl.full[st], (f / NST) & 1);
+            if (!ok) break;
             tc_fence_after();
-            const uint64_t dq = smem_desc_sw128(sQ), dk = smem_desc_sw128(ring + st * SM::kTile);
+            const uint64_t dk = dk0 + st * (SM::kTile >> 4);
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const int step = (kk >> 2) * (HB >> 4) + (kk & 3) * 2;
-              tc_mma_f16(tmem + s * kTreeKeys, dq + step, dk + step, idS, kk > 0);
-            }
-            tc_commit(&ctl.s_full[s]);
+            for (int kk = 0; kk < D / 16; ++kk)
+              tc_mma_f16(tmem + k * kTreeKeys, dq + (kk >> 2) * (HQ >> 4) + (kk & 3) * 2,
+                         dk + (kk >> 2) * (HB >> 4) + (kk & 3) * 2, idS, kk > 0);
+            tc_commit(&ctl.s_full[k]);
             tc_commit(&ctl.empty[st]);
           }
-          if (i >= 1) issue_pv(gt - 1, (i - 1) & 1, i - 1 >= 2);
+          gt += n;
         }
-        issue_pv(gt - 1, (n - 1) & 1, n - 1 >= 2);
-        ++seg;
+      } else {
+        constexpr uint32_t idO = idesc_bf16_f32_bmn(kTreeRows, D);
+        const int grp = warp - 2;
+        const uint32_t dO = tmem + 256 + grp * D;
+        const uint64_t dv0 = smem_desc_mn_sw128(ring, HB);
+        uint32_t par = 0;  // bit k: products with P from S buffer k, mod 2
+        while (it.next(sg)) {
+          const int n = sg.k1 - sg.k0;
+          for (int i = grp; i < n; i += 2) {
+            const int k = i & 3;
+            wait(&ctl.p_ready[k], par >> k & 1);
+            par ^= 1u << k;
+            const uint32_t f = 2 * (gt + i) + 1, st = f % NST;
+            wait(&ctl.full[st], (f / NST) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t dv = dv0 + st * (SM::kTile >> 4);
+#pragma unroll
+            for (int kk = 0; kk < kTreeKeys / 16; ++kk)
+              tc_mma_f16_ta(dO, tmem + k * kTreeKeys + 8 * kk, dv + 128 * kk, idO, i >= 2 || kk > 0);
+            tc_commit(&ctl.pv_done[k]);
+            tc_commit(&ctl.empty[st]);
+          }
+          gt += n;
+        }
       }
       tc_commit(&ctl.drain);
       mbar_wait(&ctl.drain, 0, a.status);
@@ -413,11 +449,11 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
     const int tid = threadIdx.x - 128;       // 0..255 over both groups
     const int r = quad * 32 + lane;          // the thread's row of the tile
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-    const uint32_t tS = tmem + lanes + grp * kTreeKeys, tO = tmem + lanes + 256 + grp * D;
+    const uint32_t tS = tmem + lanes, tO = tmem + lanes + 256 + grp * D;
     SegIter it(a, x0, x1, ctl.u0, ctl.b0);
     Seg sg;
     uint32_t seg = 0, gt0 = 0;  // segments, key tiles before this one
-    uint32_t cnt = 0;           // this group's tiles so far
+    uint32_t par = 0;           // bit k: tiles taken from S buffer k, mod 2
     TreeSplit split = {0, 0, 0, 0, 0, -1};
     while (it.next(sg)) {
       const SeqInfo& s = sg.s;
@@ -446,7 +482,7 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
         for (int y = 0; y < kPer; ++y) {
           const int rr = r0 + y * kRowStep;
           if (rr < ((rows + 31) & ~31))
-            *reinterpret_cast<uint4*>(sQ + (ch >> 3) * HB + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4)) =
+            *reinterpret_cast<uint4*>(sQ + (ch >> 3) * HQ + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4)) =
                 val[y];
         }
       }
@@ -459,118 +495,122 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
       const int n = sg.k1 - sg.k0, len = s.old + s.T;
       float m = -INFINITY, l = 0.f;  // in units of log2
       // one tile of the group: scores from tensor memory, P back into it
-      uint32_t vis[4];
+      uint32_t vis[2];
+      // tile i: scores from tensor memory, P back into it
       auto tile = [&](auto tail_tag, int i) {
         constexpr bool kTail = decltype(tail_tag)::value;
+        const uint32_t t = tS + (i & 3) * kTreeKeys;
+        float x[2][32];
+        tmem_ld32(t, x[0]);
+        tmem_ld32(t + 32, x[1]);
+        tmem_ld_wait();
+        if constexpr (kTail) {
+#pragma unroll
+          for (int e = 0; e < 64; ++e)
+            x[e >> 5][e & 31] = (vis[e >> 5] >> (e & 31) & 1) ? x[e >> 5][e & 31] : -INFINITY;
+        }
         float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          float x[32];
-          tmem_ld32(tS + 32 * q, x);
-          tmem_ld_wait();
-          if constexpr (kTail) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              tops[e & 3] = fmaxf(tops[e & 3], (vis[q] >> e & 1) ? x[e] : -INFINITY);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) tops[e & 3] = fmaxf(tops[e & 3], x[e]);
-          }
-        }
+        for (int e = 0; e < 64; ++e) tops[e & 3] = fmaxf(tops[e & 3], x[e >> 5][e & 31]);
         const float top =
             fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * a.scale_log2;
         const bool rise = top > m + kRescaleLog2 || (m == -INFINITY && top > m);
         const float mn = rise ? top : m;
         if (i >= 2 && __any_sync(0xffffffffu, rise)) {
           const float al = rise ? ex2_approx(m - mn) : 1.f;  // m = -inf: 0
-          warp_wait(&ctl.pv_done[grp], (cnt - 1) & 1);
+          const int k = (i - 2) & 3;
+          warp_wait(&ctl.pv_done[k], (par >> k & 1) ^ 1);
           tc_fence_after();
 #pragma unroll
           for (int q = 0; q < D / 16; ++q) {
-            float x[16];
+            float o[16];
             uint32_t y[16];
-            tmem_ld16(tO + 16 * q, x);
+            tmem_ld16(tO + 16 * q, o);
             tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(x[e] * al);
+            for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(o[e] * al);
             tmem_st16(tO + 16 * q, y);
           }
           l *= al;
         }
         m = mn;
+        // masked scores: exp2(-inf - sub) = 0
         const float sub = m == -INFINITY ? 0.f : m;
         float sums[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          float x[32];
+        for (int q = 0; q < 2; ++q) {
           uint32_t y[16];
-          tmem_ld32(tS + 32 * q, x);
-          tmem_ld_wait();
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
-            x[e] = ex2_approx(fmaf(x[e], a.scale_log2, -sub));
-            if constexpr (kTail) x[e] = (vis[q] >> e & 1) ? x[e] : 0.f;
-            sums[e & 3] += x[e];
+            x[q][e] = ex2_approx(fmaf(x[q][e], a.scale_log2, -sub));
+            sums[e & 3] += x[q][e];
           }
 #pragma unroll
-          for (int e = 0; e < 16; ++e) y[e] = pack_p(x[2 * e], x[2 * e + 1]);
-          tmem_st16(tS + 16 * q, y);  // over scores already read
+          for (int e = 0; e < 16; ++e) y[e] = pack_p(x[q][2 * e], x[q][2 * e + 1]);
+          tmem_st16(t + 16 * q, y);
         }
         l += (sums[0] + sums[1]) + (sums[2] + sums[3]);
+        tmem_st_wait();
       };
-      for (int i = grp; i < n; i += 2, ++cnt) {
-        const int key0 = (sg.k0 + i) * kTreeKeys;
+      for (int i = grp; i < n; i += 2) {
+        const int key0 = (sg.k0 + i) * kTreeKeys, k = i & 3;
         const bool tail = key0 + kTreeKeys > s.old;
         if (tail) {
-          // V of keys behind the end and non-finite V of new tokens: thread = key
+          // V of keys behind the end and non-finite V of new tokens: two
+          // threads a key, each half of its elements
           const uint32_t f = 2 * (gt0 + i) + 1, st = f % NST;
           warp_wait(&ctl.full[st], (f / NST) & 1);
-          const int key = key0 + r;
-          uint8_t* v = ring + st * SM::kTile + r * 128;
+          const int kr = r & 63, key = key0 + kr;
+          uint8_t* v = ring + st * SM::kTile + kr * 128;
+          auto chunk = [&](int ch) {  // of the thread's D / 16
+            const int c8 = (r >> 6) * (D / 16) + ch;
+            return reinterpret_cast<uint4*>(v + (c8 >> 3) * HB + (((c8 ^ kr) & 7) << 4));
+          };
           if (key >= len) {
 #pragma unroll
-            for (int ch = 0; ch < D / 8; ++ch)
-              *reinterpret_cast<uint4*>(v + (ch >> 3) * HB + (((ch ^ r) & 7) << 4)) =
-                  make_uint4(0, 0, 0, 0);
+            for (int ch = 0; ch < D / 16; ++ch) *chunk(ch) = make_uint4(0, 0, 0, 0);
           } else if (key >= s.old) {
             bool found = false;
 #pragma unroll
-            for (int ch = 0; ch < D / 8; ++ch) {
-              const uint4 w = *reinterpret_cast<const uint4*>(v + (ch >> 3) * HB + (((ch ^ r) & 7) << 4));
+            for (int ch = 0; ch < D / 16; ++ch) {
+              const uint4 w = *chunk(ch);
               found = found || has_nonfinite(w.x) || has_nonfinite(w.y) || has_nonfinite(w.z) ||
                       has_nonfinite(w.w);
             }
             if (found) {
               ctl.poison[seg & 1] = 1;
-              for (int ch = 0; ch < D / 8; ++ch) {
-                uint4* p = reinterpret_cast<uint4*>(v + (ch >> 3) * HB + (((ch ^ r) & 7) << 4));
+              for (int ch = 0; ch < D / 16; ++ch) {
+                uint4* p = chunk(ch);
                 *p = make_uint4(drop_nonfinite(p->x), drop_nonfinite(p->y), drop_nonfinite(p->z),
                                 drop_nonfinite(p->w));
               }
             }
           }
           // what the thread's row sees, before the scores are there
-#pragma unroll
-          for (int q = 0; q < 4; ++q) vis[q] = sees32(a, s, tok, key0 + 32 * q);
+          vis[0] = sees32(a, s, tok, key0);
+          vis[1] = sees32(a, s, tok, key0 + 32);
           fence_proxy_async_smem();
         }
-        warp_wait(&ctl.s_full[grp], cnt & 1);
+        warp_wait(&ctl.s_full[k], par >> k & 1);
         tc_fence_after();
         if (warp_live) {
           if (tail) tile(std::true_type(), i);
           else tile(std::false_type(), i);
-          tmem_st_wait();
         }
+        par ^= 1u << k;
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl.p_ready[grp]);
+        if (lane == 0) mbar_arrive(&ctl.p_ready[k]);
       }
 
       // The two groups' states meet: each leaves (m, l) where its scores were,
       // then takes one half of the head's elements of both O.
-      if (n > grp) warp_wait(&ctl.pv_done[grp], (cnt - 1) & 1);
+      if (n > grp) {
+        const int k = (n - 1 - ((n - 1 - grp) & 1)) & 3;  // the group's last tile
+        warp_wait(&ctl.pv_done[k], (par >> k & 1) ^ 1);
+      }
       tc_fence_after();
-      tmem_st2(tS, __float_as_uint(m), __float_as_uint(l));
+      tmem_st2(tS + grp * kTreeKeys, __float_as_uint(m), __float_as_uint(l));
       tmem_st_wait();
       tc_fence_before();
       bar_sync(1, kTreeSoftmax);
@@ -594,7 +634,7 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
       const int h = row0 + min(r, rows - 1) - tok * a.group;
       const bool poison = ctl.poison[seg & 1] != 0;
       const bool live = r < rows;
-      const int slot = range_begin(c, W, G) >= sg.x ? 0 : 1;
+      const int slot = sg.k0 > 0 || seg == 0 ? 0 : 1;  // a later piece is its CTA's first
       const int64_t prow = ((int64_t)c * 2 + slot) * kTreeRows + r;
 #pragma unroll
       for (int q = 0; q < D / 32; ++q) {  // 16 elements a turn of this group's half
@@ -629,7 +669,7 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
       }
       if (!whole && live && grp == 0) a.ml[prow] = make_float2(M, L);
       if (sg.k0 == 0 && !whole && tid == 0)  // this CTA opens a cut item
-        split = {s.q0, row0, rows, sg.g, slot, owner_of(sg.x + s.nt - 1, W, G)};
+        split = {s.q0, row0, rows, sg.g, slot, owner_of(sg.x + s.nt + kItemCost - 1, W, G)};
       tc_fence_before();
       if (tid == 0) ctl.poison[(seg + 1) & 1] = 0;
       bar_sync(1, kTreeSoftmax);  // both groups are done with O, S and Q
