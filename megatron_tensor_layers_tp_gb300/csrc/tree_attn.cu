@@ -22,16 +22,18 @@
 // piece: that CTA alone pulls every piece (64 KB each at 128 rows), 268 us
 // for prompt chunks instead of @@ us.
 //
-// Roles of the 12 warps:
-//   warp 0     : K and V tiles by TMA into a ring, one box per lane, through
-//                the page table (boxes end where pages end);
-//   warp 1     : one thread issues S = Q K^T into tensor memory;
-//   warps 2, 3 : one thread each issues O += P V of a softmax group, with P read
+// Roles of the 16 warps:
+//   warps 0-3  : K and V tiles by TMA into a ring, through the page table; boxes
+//                end where pages end, and a box costs its warp about 130 cycles
+//                to issue (32 boxes a tile at 8-key pages), so four warps share
+//                a tile's boxes;
+//   warp 4     : one thread issues S = Q K^T into tensor memory;
+//   warps 5, 6 : one thread each issues O += P V of a softmax group, with P read
 //                from tensor memory and V as it lies in the page (the head's
 //                elements contiguous).  Issuing costs about 65 cycles a product
 //                and 80 a commit: one thread for all of them set the pace
 //                (1850-2000 cycles a tile, nothing else busy).
-//   warps 4-7, 8-11: two softmax groups.  They take alternate key tiles, each
+//   warps 8-11, 12-15: two softmax groups.  They take alternate key tiles, each
 //                with its own running maximum, sum and O, so that neither
 //                waits for the other's maxima; the two states meet at the
 //                item's end.  A thread owns a row and holds a tile's 64 scores
@@ -62,8 +64,12 @@
 
 namespace tpk {
 
-constexpr int kTreeThreads = 384;
+constexpr int kTreeThreads = 512;
+constexpr int kTreeLoaders = 4;          // producer warps
 constexpr int kTreeSoftmax = 256;        // threads of the two softmax groups
+// registers of a thread after the hand-over: together no more than the launch
+// brought (checked by the host, since a take-over beyond it would never end)
+constexpr int kTreeRegsOther = 64, kTreeRegsSoftmax = 184;
 constexpr float kRescaleLog2 = 8.f;
 constexpr int kItemCost = 8;             // an item's fixed work in key tiles
 
@@ -80,7 +86,7 @@ struct TreeSmem {
 struct TreeCtl {
   uint64_t full[24], empty[24];
   uint64_t s_full[4], p_ready[4], pv_done[4], q_full, drain;
-  long long warp_sum[12];
+  long long warp_sum[16];
   long long total, u0;
   int b0;
   int poison[2];
@@ -141,13 +147,13 @@ struct SegIter {
         s = seq_info(a, b);
       }
       const int cost = s.nt + kItemCost;
-      const int64_t item = u / cost;
+      const int64_t item = u <= INT32_MAX ? (int64_t)((uint32_t)u / (uint32_t)cost) : u / cost;
       const int at = (int)(u - item * cost);
       const int64_t left = x1 - x;
       const int end = (int)(left < cost - at ? at + left : cost);
       sg.s = s;
       sg.b = b;
-      sg.g = (int)(item / s.qt);
+      sg.g = (uint32_t)item / (uint32_t)s.qt;
       sg.qi = (int)(item - (int64_t)sg.g * s.qt);
       sg.k0 = max(at - kItemCost, 0);
       sg.k1 = max(end - kItemCost, 0);
@@ -251,7 +257,7 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
     tma_prefetch_desc(&a.tmK);
     tma_prefetch_desc(&a.tmV);
   }
-  if (warp == 1) { tmem_alloc(&ctl.tmem, 512); tmem_relinquish(); }
+  if (warp == 4) { tmem_alloc(&ctl.tmem, 512); tmem_relinquish(); }
   pdl_wait();
 
   // This CTA's range: thread t sums the tiles of a run of sequences; the
@@ -313,12 +319,15 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (ok) ok = mbar_wait(bar, parity, a.status);
   };
+  // the softmax warpgroups take over registers that the others do not need
+  if (warp < 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTreeRegsOther));
+  else asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTreeRegsSoftmax));
   auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
     wait(bar, parity);
     __syncwarp();
   };
 
-  if (warp == 0) {
+  if (warp < kTreeLoaders) {
     // ------------------------------------------------------------ K and V
     SegIter it(a, x0, x1, ctl.u0, ctl.b0);
     Seg sg;
@@ -328,8 +337,10 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
     while (ok && it.next(sg)) {
       const int copy = sg.g / a.kv_r, local = sg.g - copy * a.kv_r;
       const int len = sg.s.old + sg.s.T;
-      // lane -> (box, 64-element half)
-      const int box = D == 128 ? lane >> 1 : lane, half = D == 128 ? lane & 1 : 0;
+      // this warp's boxes (of a tile's 64 / R times d / 64): lane j takes
+      // number j * 4 + warp
+      const int y = lane * kTreeLoaders + warp;
+      const int box = D == 128 ? y >> 1 : y, half = D == 128 ? y & 1 : 0;
       // The row of the page table through a window of 64 entries, two a lane:
       // the second half is in flight while the first is used.  (One entry a
       // box and tile, loaded a tile ahead, made the load's latency the tile
@@ -364,8 +375,7 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
           ok = __all_sync(0xffffffffu, ok);
           if (ok) {
             ++n;
-            if (lane == 0) mbar_arrive_expect_tx(&ctl.full[st], here * R * D * 2);
-            __syncwarp();
+            if (warp == 0 && lane == 0) mbar_arrive_expect_tx(&ctl.full[st], here * R * D * 2);
             if (box < here) {
               uint8_t* dst = ring + st * SM::kTile + half * HB + box * R * 128;
               const CUtensorMap* tm = kv ? &a.tmV : &a.tmK;
@@ -382,13 +392,13 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
         if (!mbar_wait(&ctl.full[i % NST], (i / NST) & 1, a.status)) break;
     }
     __syncwarp();
-  } else if (warp < 4) {
+  } else if (warp < 7) {
     // ------------------------------------------------------------ products
     if (lane == 0) {
       SegIter it(a, x0, x1, ctl.u0, ctl.b0);
       Seg sg;
       uint32_t gt = 0;  // key tiles before this segment
-      if (warp == 1) {
+      if (warp == 4) {
         constexpr uint32_t idS = idesc_bf16_f32(kTreeRows, kTreeKeys);
         uint32_t par = 0;   // bit k: products into S buffer k, mod 2
         const uint64_t dq = smem_desc_sw128(sQ), dk0 = smem_desc_sw128(ring);
@@ -415,7 +425,7 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
         }
       } else {
         constexpr uint32_t idO = idesc_bf16_f32_bmn(kTreeRows, D);
-        const int grp = warp - 2;
+        const int grp = warp - 5;
         const uint32_t dO = tmem + 256 + grp * D;
         const uint64_t dv0 = smem_desc_mn_sw128(ring, HB);
         uint32_t par = 0;  // bit k: products with P from S buffer k, mod 2
@@ -443,10 +453,10 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
       mbar_wait(&ctl.drain, 0, a.status);
     }
     __syncwarp();
-  } else if (warp >= 4) {
+  } else if (warp >= 8) {
     // ------------------------------------------------------------ softmax
-    const int grp = (warp - 4) >> 2, quad = warp & 3;
-    const int tid = threadIdx.x - 128;       // 0..255 over both groups
+    const int grp = (warp - 8) >> 2, quad = warp & 3;
+    const int tid = threadIdx.x - 256;       // 0..255 over both groups
     const int r = quad * 32 + lane;          // the thread's row of the tile
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
     const uint32_t tS = tmem + lanes, tO = tmem + lanes + 256 + grp * D;
@@ -636,8 +646,9 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
       const bool live = r < rows;
       const int slot = sg.k0 > 0 || seg == 0 ? 0 : 1;  // a later piece is its CTA's first
       const int64_t prow = ((int64_t)c * 2 + slot) * kTreeRows + r;
-#pragma unroll
-      for (int q = 0; q < D / 32; ++q) {  // 16 elements a turn of this group's half
+#pragma unroll 1
+      for (int q = 0; q < D / 32; ++q) {  // 16 elements a turn of this group's half (rolled: the
+                                          // code runs once an item, from a cold cache)
         const int e0 = grp * (D / 2) + 16 * q;
         float o0[16], o1[16];
         tmem_ld16(tmem + lanes + 256 + e0, o0);
@@ -679,7 +690,7 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
     if (tid == 0) a.splits[c] = split;
   }
   __syncthreads();
-  if (warp == 1) {
+  if (warp == 4) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -728,9 +739,17 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const TreeJoinArgs a) {
 
 template <int D>
 static cudaError_t launch_tree(const TreeAttnArgs& a, cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(tree_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       TreeSmem<D>::kTotal);
-  if (e != cudaSuccess) return e;
+  static const cudaError_t ready = [] {
+    cudaFuncAttributes fa;
+    cudaError_t e = cudaFuncGetAttributes(&fa, tree_attn_kernel<D>);
+    if (e != cudaSuccess) return e;
+    if (fa.numRegs * kTreeThreads <
+        (kTreeThreads - kTreeSoftmax) * kTreeRegsOther + kTreeSoftmax * kTreeRegsSoftmax)
+      return cudaErrorLaunchOutOfResources;
+    return cudaFuncSetAttribute(tree_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                TreeSmem<D>::kTotal);
+  }();
+  if (ready != cudaSuccess) return ready;
   return launch_k(tree_attn_kernel<D>, dim3(a.grid), dim3(kTreeThreads), TreeSmem<D>::kTotal, st, a);
 }
 
