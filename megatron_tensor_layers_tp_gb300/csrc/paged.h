@@ -78,8 +78,9 @@ struct TreeAttnArgs {
   FastDiv div_group;
   float scale_log2;           // log2(e) / sqrt(d)
   int kv_once;                // 1: no sequence has more than one query tile, K and V are read once
+  int loaders;                // warps that share a tile's boxes
   int grid;
-  float* partials;            // [grid][2][128][d]
+  float* partials;            // [grid][2][d / 4][128][4]
   float2* ml;                 // [grid][2][128]
   TreeSplit* splits;          // [grid]
   int* status;
@@ -95,6 +96,7 @@ struct TreeJoinArgs {
 };
 constexpr int kTreeRows = 128;  // query rows (tokens x Q heads of a KV head) of a tile
 constexpr int kTreeKeys = 64;   // keys of a tile
+constexpr int kTreeLoaders = 4;
 cudaError_t launch_tree_attn(const TreeAttnArgs& a, cudaStream_t st);
 // max_rows: no query tile has more rows
 cudaError_t launch_tree_join(const TreeJoinArgs& a, int head_dim, int grid, int max_rows,

@@ -247,6 +247,9 @@ tp_status tp_tree_attention(const tp_model* m, const tp_bf16* q, int64_t ld_q, t
     a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)c.head_dim));
     const int64_t rows = (int64_t)step->max_new * a.group;
     a.kv_once = rows <= kTreeRows;
+    // at most four boxes of a K or V tile a loader warp: 64-key boxes need one
+    // warp, 8-key boxes four (idle loaders would only poll)
+    a.loaders = std::min(kTreeLoaders, cdiv(kTreeKeys / a.box_rows * (c.head_dim / 64), 4));
     a.grid = m->num_sms;
     const StepWs w = step_ws(m);
     uint8_t* base = static_cast<uint8_t*>(ws);

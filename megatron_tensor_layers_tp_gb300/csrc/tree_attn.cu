@@ -25,14 +25,18 @@
 // Roles of the 16 warps:
 //   warps 0-3  : K and V tiles by TMA into a ring, through the page table; boxes
 //                end where pages end, and a box costs its warp about 130 cycles
-//                to issue (32 boxes a tile at 8-key pages), so four warps share
-//                a tile's boxes;
+//                to issue (32 boxes a tile at 8-key pages), so up to four warps
+//                share a tile's boxes;
 //   warp 4     : one thread issues S = Q K^T into tensor memory;
 //   warps 5, 6 : one thread each issues O += P V of a softmax group, with P read
 //                from tensor memory and V as it lies in the page (the head's
 //                elements contiguous).  Issuing costs about 65 cycles a product
 //                and 80 a commit: one thread for all of them set the pace
-//                (1850-2000 cycles a tile, nothing else busy).
+//                (1850-2000 cycles a tile, nothing else busy);
+//   warp 7     : the CTA's parts of items, announced to the other warps two
+//                ahead, and the next item's query tile while this one's softmax
+//                ends.  (Every role finding the parts by itself spilled
+//                registers into the issuing loops: twice the time.);
 //   warps 8-11, 12-15: two softmax groups.  They take alternate key tiles, each
 //                with its own running maximum, sum and O, so that neither
 //                waits for the other's maxima; the two states meet at the
@@ -65,7 +69,6 @@
 namespace tpk {
 
 constexpr int kTreeThreads = 512;
-constexpr int kTreeLoaders = 4;          // producer warps
 constexpr int kTreeSoftmax = 256;        // threads of the two softmax groups
 // registers of a thread after the hand-over: together no more than the launch
 // brought (checked by the host, since a take-over beyond it would never end)
@@ -73,19 +76,31 @@ constexpr int kTreeRegsOther = 64, kTreeRegsSoftmax = 184;
 constexpr float kRescaleLog2 = 8.f;
 constexpr int kItemCost = 8;             // an item's fixed work in key tiles
 
+// One CTA's part of an item: key tiles [k0, k1) of nt of (sequence b, KV head
+// g, query tile qi), the sequence's first row, new tokens and old length.
+// opens: the CTA of the item's last part when this part is the first of
+// several, else -1.  k1 = 0: no more parts.
+struct Seg {
+  int b, g, qi, k0, k1, nt, q0, T, old, opens;
+};
+
 template <int D>
 struct TreeSmem {
   static constexpr int kTile = kTreeKeys * D * 2;    // a K or V tile
-  static constexpr int kStages = D == 128 ? 12 : 24;
-  static constexpr int kRing = kTreeRows * D * 2;     // byte offset of the ring (after Q)
-  static constexpr int kBars = kRing + kStages * kTile;
+  static constexpr int kStages = D == 128 ? 9 : 22;
+  static constexpr int kOut = kTreeRows * D * 2;      // after the query tile: rows of o on their way out
+  static constexpr int kRing = 2 * kOut;
+  static constexpr int kMeet = kRing + kStages * kTile;  // (m, l) of the two groups
+  static constexpr int kBars = kMeet + 2 * kTreeRows * 8;
   static constexpr int kTotal = kBars + 1024 + 1024;  // + alignment of the base
   static_assert(kTotal <= 227 * 1024, "shared memory of one CTA");
 };
 // after the ring
 struct TreeCtl {
   uint64_t full[24], empty[24];
-  uint64_t s_full[4], p_ready[4], pv_done[4], q_full, drain;
+  uint64_t s_full[4], p_ready[4], pv_done[4], q_full, q_free, drain;
+  uint64_t seg_full[4], seg_free[4];
+  Seg seg[4];
   long long warp_sum[16];
   long long total, u0;
   int b0;
@@ -120,15 +135,9 @@ __device__ __forceinline__ int64_t positions(const TreeAttnArgs& a, const SeqInf
   return (int64_t)a.n_kv * s.qt * (s.nt + kItemCost);
 }
 
-// One CTA's part of an item: key tiles [k0, k1) of (sequence b, KV head g,
-// query tile qi); x: the flat position of the item's begin.  A part that lies
-// within the item's fixed cost has no tiles and is passed over: the parts with
-// tiles are those of consecutive CTAs.
-struct Seg {
-  SeqInfo s;
-  int b, g, qi, k0, k1;
-  int64_t x;
-};
+// A CTA's parts in order.  A part that lies within the item's fixed cost has
+// no tiles and is passed over: the parts with tiles are those of consecutive
+// CTAs.
 struct SegIter {
   const TreeAttnArgs& a;
   int64_t x, x1, u;  // flat position, its end, position inside sequence b
@@ -139,11 +148,11 @@ struct SegIter {
       : a(a_), x(x_), x1(x1_), u(u_), b(b_) {
     if (x < x1) s = seq_info(a, b);
   }
-  __device__ __forceinline__ bool next(Seg& sg) {
+  __device__ __forceinline__ Seg next(int64_t W, int G) {
     while (x < x1) {
-      while (u >= positions(a, s)) {  // at most to the last sequence: x < x1 <= total
+      while (u >= positions(a, s)) {  // at most to the last sequence: x < x1 <= W
         u -= positions(a, s);
-        if (++b >= a.n_seqs) return false;
+        ++b;
         s = seq_info(a, b);
       }
       const int cost = s.nt + kItemCost;
@@ -151,24 +160,32 @@ struct SegIter {
       const int at = (int)(u - item * cost);
       const int64_t left = x1 - x;
       const int end = (int)(left < cost - at ? at + left : cost);
-      sg.s = s;
-      sg.b = b;
-      sg.g = (uint32_t)item / (uint32_t)s.qt;
-      sg.qi = (int)(item - (int64_t)sg.g * s.qt);
-      sg.k0 = max(at - kItemCost, 0);
-      sg.k1 = max(end - kItemCost, 0);
-      sg.x = x - at;
+      const int64_t begin = x - at;
       x += end - at;
       u += end - at;
-      if (sg.k1 > sg.k0) return true;
+      if (end <= kItemCost) continue;
+      Seg sg;
+      sg.b = b;
+      sg.g = (uint32_t)item / (uint32_t)s.qt;
+      sg.qi = (int)item - sg.g * s.qt;
+      sg.k0 = max(at - kItemCost, 0);
+      sg.k1 = end - kItemCost;
+      sg.nt = s.nt;
+      sg.q0 = s.q0;
+      sg.T = s.T;
+      sg.old = s.old;
+      sg.opens = sg.k0 == 0 && sg.k1 < s.nt ? owner_of(begin + cost - 1, W, G) : -1;
+      return sg;
     }
-    return false;
+    Seg none;
+    none.k1 = 0;
+    return none;
   }
 };
 
 // 32 bits: which of the keys key0 .. key0 + 31 row `row` (token i of its
 // sequence) sees.
-__device__ __forceinline__ uint32_t sees32(const TreeAttnArgs& a, const SeqInfo& s, int i, int key0) {
+__device__ __forceinline__ uint32_t sees32(const TreeAttnArgs& a, const Seg& s, int i, int key0) {
   const int base = key0 - s.old;  // drafted token of bit 0
   if (base <= -32) return 0xFFFFFFFFu;
   uint32_t m = 0xFFFFFFFFu;
@@ -199,12 +216,13 @@ __device__ __forceinline__ int page_of(const TreeAttnArgs& a, int b, int pg) {
 }
 
 // Infinities and NaN among the V elements e0 .. e0 + 15 of the new tokens that
-// row i sees in keys [key0, key1): added to the row's o.
-__device__ __noinline__ void nonfinite_v(const TreeAttnArgs& a, const SeqInfo& s, int b, int g, int i,
-                                         int key0, int key1, int e0, float (&o)[16]) {
-  for (int j = max(key0, s.old); j < min(key1, s.old + s.T); ++j) {
+// row i sees in the part's keys: added to the row's o.
+__device__ __noinline__ void nonfinite_v(const TreeAttnArgs& a, const Seg& s, int i, int e0,
+                                         float (&o)[16]) {
+  const int g = s.g, end = min(s.k1 * kTreeKeys, s.old + s.T);
+  for (int j = max(s.k0 * kTreeKeys, s.old); j < end; ++j) {
     if (!(sees32(a, s, i, j) & 1)) continue;
-    const int pg = (int)fast_div((uint32_t)j, a.div_page), page = page_of(a, b, pg);
+    const int pg = (int)fast_div((uint32_t)j, a.div_page), page = page_of(a, s.b, pg);
     if (page < 0) continue;
     const uint16_t* v =
         a.v + ((((int64_t)(g / a.kv_r) * a.n_pages + page) * a.kv_r + g % a.kv_r) * a.page_size + j -
@@ -237,7 +255,9 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   uint8_t* sQ = smem;
+  uint8_t* sOut = smem + SM::kOut;
   uint8_t* ring = smem + SM::kRing;
+  float2* meet = reinterpret_cast<float2*>(smem + SM::kMeet);
   TreeCtl& ctl = *reinterpret_cast<TreeCtl*>(smem + SM::kBars);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -250,7 +270,12 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
       mbar_init(&ctl.pv_done[i], 1);
     }
     ctl.poison[0] = ctl.poison[1] = 0;
-    mbar_init(&ctl.q_full, kTreeSoftmax / 32);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&ctl.seg_full[i], 1);
+      mbar_init(&ctl.seg_free[i], a.loaders + 3 + kTreeSoftmax / 32);
+    }
+    mbar_init(&ctl.q_full, 1);
+    mbar_init(&ctl.q_free, 1);
     mbar_init(&ctl.drain, 3);
     fence_barrier_init();
     fence_proxy_async_smem();
@@ -319,190 +344,220 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (ok) ok = mbar_wait(bar, parity, a.status);
   };
-  // the softmax warpgroups take over registers that the others do not need
-  if (warp < 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTreeRegsOther));
-  else asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTreeRegsSoftmax));
   auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
     wait(bar, parity);
     __syncwarp();
   };
 
-  if (warp < kTreeLoaders) {
-    // ------------------------------------------------------------ K and V
-    SegIter it(a, x0, x1, ctl.u0, ctl.b0);
-    Seg sg;
-    const uint64_t pol = policy_evict_first();
-    const int R = a.box_rows, boxes = kTreeKeys / R;
-    uint32_t n = 0;  // ring fills
-    while (ok && it.next(sg)) {
-      const int copy = sg.g / a.kv_r, local = sg.g - copy * a.kv_r;
-      const int len = sg.s.old + sg.s.T;
+  // the next announced part; k1 = 0 when there is none (or the wait ran out)
+  auto fetch = [&](uint32_t seg) -> Seg {
+    wait(&ctl.seg_full[seg & 3], (seg >> 2) & 1);
+    Seg sg = ctl.seg[seg & 3];
+    if (!ok) sg.k1 = 0;
+    return sg;
+  };
+  auto done_with = [&](uint32_t seg) { mbar_arrive(&ctl.seg_free[seg & 3]); };
+
+  // The softmax warpgroups take over registers that the others do not need.
+  if (warp < 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTreeRegsOther));
+    if (warp < a.loaders) {
+      // ------------------------------------------------------------ K and V
+      const uint64_t pol = policy_evict_first();
+      const int R = a.box_rows, boxes = kTreeKeys / R;
       // this warp's boxes (of a tile's 64 / R times d / 64): lane j takes
-      // number j * 4 + warp
-      const int y = lane * kTreeLoaders + warp;
+      // number j * loaders + warp
+      const int y = lane * a.loaders + warp;
       const int box = D == 128 ? y >> 1 : y, half = D == 128 ? y & 1 : 0;
-      // The row of the page table through a window of 64 entries, two a lane:
-      // the second half is in flight while the first is used.  (One entry a
-      // box and tile, loaded a tile ahead, made the load's latency the tile
-      // rate: 1.06 us a tile of 64 keys.)
-      const int32_t* row = a.table + (int64_t)sg.b * a.ld_table;
-      const int last = (int)fast_div((uint32_t)min(len, sg.k1 * kTreeKeys) - 1, a.div_page);
-      auto load = [&](int pg) { return pg <= last ? row[pg] : 0; };
-      int w0 = (int)fast_div((uint32_t)(sg.k0 * kTreeKeys), a.div_page);
-      int win = load(w0 + lane), nxt = load(w0 + 32 + lane);
-      for (int kt = sg.k0; ok && kt < sg.k1; ++kt) {
-        const int here = min(boxes, (len - kt * kTreeKeys + R - 1) / R);
-        const int key = kt * kTreeKeys + min(box, here - 1) * R;  // (spare lanes: the last box)
-        const int pg = (int)fast_div((uint32_t)key, a.div_page);
-        if (__shfl_sync(0xffffffffu, pg, 0) - w0 >= 32) {
-          w0 += 32;
-          win = nxt;
-          nxt = load(w0 + 32 + lane);
-        }
-        const int lo = __shfl_sync(0xffffffffu, win, (pg - w0) & 31);
-        const int hi = __shfl_sync(0xffffffffu, nxt, (pg - w0) & 31);
-        const int page = pg - w0 < 32 ? lo : hi;
-        const int off = key - pg * a.page_size;
-        int z = (copy * a.n_pages + page) * a.kv_r + local;
-        if (page < 0 || page >= a.n_pages) {
-          record_status(a.status, kStatusTableRange);
-          z = a.slices;  // outside the tensor map: zeros
-        }
+      uint32_t n = 0;  // ring fills
+      for (uint32_t seg = 0;; ++seg) {
+        const Seg sg = fetch(seg);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok || sg.k1 == 0) break;
+        const int copy = sg.g / a.kv_r, local = sg.g - copy * a.kv_r;
+        const int len = sg.old + sg.T;
+        // The row of the page table through a window of 64 entries, two a lane:
+        // the second half is in flight while the first is used.
+        const int32_t* row = a.table + (int64_t)sg.b * a.ld_table;
+        const int last = (int)fast_div((uint32_t)min(len, sg.k1 * kTreeKeys) - 1, a.div_page);
+        auto load = [&](int pg) { return pg <= last ? row[pg] : 0; };
+        int w0 = (int)fast_div((uint32_t)(sg.k0 * kTreeKeys), a.div_page);
+        int win = load(w0 + lane), nxt = load(w0 + 32 + lane);
+        for (int kt = sg.k0; ok && kt < sg.k1; ++kt) {
+          const int here = min(boxes, (len - kt * kTreeKeys + R - 1) / R);
+          const int key = kt * kTreeKeys + min(box, here - 1) * R;  // (spare lanes: the last box)
+          const int pg = (int)fast_div((uint32_t)key, a.div_page);
+          const int pg0 = (int)fast_div((uint32_t)(kt * kTreeKeys), a.div_page);
+          if (pg0 - w0 >= 32) {
+            w0 += 32;
+            win = nxt;
+            nxt = load(w0 + 32 + lane);
+          }
+          const int lo = __shfl_sync(0xffffffffu, win, (pg - w0) & 31);
+          const int hi = __shfl_sync(0xffffffffu, nxt, (pg - w0) & 31);
+          const int page = pg - w0 < 32 ? lo : hi;
+          const int off = key - pg * a.page_size;
+          int z = (copy * a.n_pages + page) * a.kv_r + local;
+          if (page < 0 || page >= a.n_pages) {
+            record_status(a.status, kStatusTableRange);
+            z = a.slices;  // outside the tensor map: zeros
+          }
 #pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          const uint32_t st = n % NST;
-          wait(&ctl.empty[st], (n / NST & 1) ^ 1);
-          ok = __all_sync(0xffffffffu, ok);
-          if (ok) {
-            ++n;
-            if (warp == 0 && lane == 0) mbar_arrive_expect_tx(&ctl.full[st], here * R * D * 2);
-            if (box < here) {
-              uint8_t* dst = ring + st * SM::kTile + half * HB + box * R * 128;
-              const CUtensorMap* tm = kv ? &a.tmV : &a.tmK;
-              if (a.kv_once) tma_load_3d(dst, tm, &ctl.full[st], half * 64, off, z, pol);
-              else tma_load_3d_plain(dst, tm, &ctl.full[st], half * 64, off, z);
+          for (int kv = 0; kv < 2; ++kv) {
+            const uint32_t st = n % NST;
+            if (lane == 0) wait(&ctl.empty[st], (n / NST & 1) ^ 1);  // one lane polls
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (ok) {
+              ++n;
+              if (warp == 0 && lane == 0) mbar_arrive_expect_tx(&ctl.full[st], here * R * D * 2);
+              if (box < here) {
+                uint8_t* dst = ring + st * SM::kTile + half * HB + box * R * 128;
+                const CUtensorMap* tm = kv ? &a.tmV : &a.tmK;
+                if (a.kv_once) tma_load_3d(dst, tm, &ctl.full[st], half * 64, off, z, pol);
+                else tma_load_3d_plain(dst, tm, &ctl.full[st], half * 64, off, z);
+              }
             }
           }
         }
+        __syncwarp();
+        if (lane == 0) done_with(seg);
       }
-    }
-    // never leave with copies still landing in shared memory
-    if (lane == 0) {
-      for (uint32_t i = n > NST ? n - NST : 0; i < n; ++i)
-        if (!mbar_wait(&ctl.full[i % NST], (i / NST) & 1, a.status)) break;
-    }
-    __syncwarp();
-  } else if (warp < 7) {
-    // ------------------------------------------------------------ products
-    if (lane == 0) {
+      // never leave with copies still landing in shared memory
+      if (lane == 0) {
+        for (uint32_t i = n > NST ? n - NST : 0; i < n; ++i)
+          if (!mbar_wait(&ctl.full[i % NST], (i / NST) & 1, a.status)) break;
+      }
+      __syncwarp();
+    } else if (warp >= 4 && warp < 7) {
+      // ------------------------------------------------------------ products
+      if (lane == 0) {
+        uint32_t gt = 0;   // key tiles before this part
+        uint32_t par = 0;  // bit k: products with S buffer k, mod 2
+        if (warp == 4) {
+          constexpr uint32_t idS = idesc_bf16_f32(kTreeRows, kTreeKeys);
+          const uint64_t dq = smem_desc_sw128(sQ), dk0 = smem_desc_sw128(ring);
+          for (uint32_t seg = 0;; ++seg) {
+            const Seg sg = fetch(seg);
+            const int n = sg.k1 ? sg.k1 - sg.k0 : 0;
+            if (n == 0) break;
+            done_with(seg);
+            wait(&ctl.q_full, seg & 1);
+            for (int i = 0; i < n; ++i) {  // S buffer i % 4
+              const int k = i & 3;
+              wait(&ctl.pv_done[k], (par >> k & 1) ^ 1);  // P of the buffer's last tile was read
+              par ^= 1u << k;
+              const uint32_t f = 2 * (gt + i), st = f % NST;
+              wait(&ctl.full[st], (f / NST) & 1);
+              if (!ok) break;
+              tc_fence_after();
+              const uint64_t dk = dk0 + st * (SM::kTile >> 4);
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk)
+                tc_mma_f16(tmem + k * kTreeKeys, dq + (kk >> 2) * (HQ >> 4) + (kk & 3) * 2,
+                           dk + (kk >> 2) * (HB >> 4) + (kk & 3) * 2, idS, kk > 0);
+              tc_commit(&ctl.s_full[k]);
+              tc_commit(&ctl.empty[st]);
+            }
+            if (ok) tc_commit(&ctl.q_free);
+            gt += n;
+          }
+        } else {
+          constexpr uint32_t idO = idesc_bf16_f32_bmn(kTreeRows, D);
+          const int grp = warp - 5;
+          const uint32_t dO = tmem + 256 + grp * D;
+          const uint64_t dv0 = smem_desc_mn_sw128(ring, HB);
+          for (uint32_t seg = 0;; ++seg) {
+            const Seg sg = fetch(seg);
+            const int n = sg.k1 ? sg.k1 - sg.k0 : 0;
+            if (n == 0) break;
+            done_with(seg);
+            for (int i = grp; i < n; i += 2) {
+              const int k = i & 3;
+              wait(&ctl.p_ready[k], par >> k & 1);
+              par ^= 1u << k;
+              const uint32_t f = 2 * (gt + i) + 1, st = f % NST;
+              wait(&ctl.full[st], (f / NST) & 1);
+              if (!ok) break;
+              tc_fence_after();
+              const uint64_t dv = dv0 + st * (SM::kTile >> 4);
+#pragma unroll
+              for (int kk = 0; kk < kTreeKeys / 16; ++kk)
+                tc_mma_f16_ta(dO, tmem + k * kTreeKeys + 8 * kk, dv + 128 * kk, idO, i >= 2 || kk > 0);
+              tc_commit(&ctl.pv_done[k]);
+              tc_commit(&ctl.empty[st]);
+            }
+            gt += n;
+          }
+        }
+        tc_commit(&ctl.drain);
+        mbar_wait(&ctl.drain, 0, a.status);
+      }
+      __syncwarp();
+    } else if (warp == 7) {
+      // ------------------------------------------------------------ parts, queries
       SegIter it(a, x0, x1, ctl.u0, ctl.b0);
-      Seg sg;
-      uint32_t gt = 0;  // key tiles before this segment
-      if (warp == 4) {
-        constexpr uint32_t idS = idesc_bf16_f32(kTreeRows, kTreeKeys);
-        uint32_t par = 0;   // bit k: products into S buffer k, mod 2
-        const uint64_t dq = smem_desc_sw128(sQ), dk0 = smem_desc_sw128(ring);
-        for (uint32_t seg = 0; it.next(sg); ++seg) {
-          wait(&ctl.q_full, seg & 1);
-          const int n = sg.k1 - sg.k0;
-          for (int i = 0; i < n; ++i) {  // S buffer i % 4
-            const int k = i & 3;
-            if (i >= 4) wait(&ctl.pv_done[k], (par >> k & 1) ^ 1);  // P of tile i - 4 was read
-            par ^= 1u << k;
-            const uint32_t f = 2 * (gt + i), st = f % NST;
-            wait(&ctl.full[st], (f / NST) & 1);
-            if (!ok) break;
-            tc_fence_after();
-            const uint64_t dk = dk0 + st * (SM::kTile >> 4);
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-              tc_mma_f16(tmem + k * kTreeKeys, dq + (kk >> 2) * (HQ >> 4) + (kk & 3) * 2,
-                         dk + (kk >> 2) * (HB >> 4) + (kk & 3) * 2, idS, kk > 0);
-            tc_commit(&ctl.s_full[k]);
-            tc_commit(&ctl.empty[st]);
-          }
-          gt += n;
+      uint32_t told = 0;
+      bool more = true;
+      auto announce = [&]() {
+        const Seg sg = it.next(W, G);
+        wait(&ctl.seg_free[told & 3], ((told >> 2) & 1) ^ 1);
+        __syncwarp();
+        if (lane == 0) {
+          ctl.seg[told & 3] = sg;
+          mbar_arrive(&ctl.seg_full[told & 3]);
         }
-      } else {
-        constexpr uint32_t idO = idesc_bf16_f32_bmn(kTreeRows, D);
-        const int grp = warp - 5;
-        const uint32_t dO = tmem + 256 + grp * D;
-        const uint64_t dv0 = smem_desc_mn_sw128(ring, HB);
-        uint32_t par = 0;  // bit k: products with P from S buffer k, mod 2
-        while (it.next(sg)) {
-          const int n = sg.k1 - sg.k0;
-          for (int i = grp; i < n; i += 2) {
-            const int k = i & 3;
-            wait(&ctl.p_ready[k], par >> k & 1);
-            par ^= 1u << k;
-            const uint32_t f = 2 * (gt + i) + 1, st = f % NST;
-            wait(&ctl.full[st], (f / NST) & 1);
-            if (!ok) break;
-            tc_fence_after();
-            const uint64_t dv = dv0 + st * (SM::kTile >> 4);
-#pragma unroll
-            for (int kk = 0; kk < kTreeKeys / 16; ++kk)
-              tc_mma_f16_ta(dO, tmem + k * kTreeKeys + 8 * kk, dv + 128 * kk, idO, i >= 2 || kk > 0);
-            tc_commit(&ctl.pv_done[k]);
-            tc_commit(&ctl.empty[st]);
-          }
-          gt += n;
+        __syncwarp();
+        ++told;
+        more = sg.k1 > 0;
+      };
+      announce();
+      if (more) announce();
+      // Query rows of 64 elements (128 bytes), 16-byte chunks swizzled by row.
+      // Rows past the item's are zeros up to the next 32 and undefined behind
+      // (no warp reads their scores).
+      constexpr int kRowStep = 32 / (D / 8);
+      const int ch = lane % (D / 8), r0 = lane / (D / 8);
+      for (uint32_t seg = 0;; ++seg) {
+        const Seg sg = ctl.seg[seg & 3];
+        if (sg.k1 == 0) break;
+        const int row0 = sg.qi * kTreeRows, rows = min(kTreeRows, sg.T * a.group - row0);
+        const int end = (rows + 31) & ~31;
+        if (lane == 0) wait(&ctl.q_free, (seg & 1) ^ 1);
+        __syncwarp();
+#pragma unroll 2
+        for (int rr = r0; rr < end; rr += kRowStep) {
+          const uint32_t dst = smem_u32(sQ + (ch >> 3) * HQ + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4));
+          const int i = (int)fast_div((uint32_t)(row0 + min(rr, rows - 1)), a.div_group);
+          const int h = row0 + min(rr, rows - 1) - i * a.group;
+          cp_async16(dst, a.q + (sg.q0 + i) * a.ld_q + (sg.g * a.group + h) * D + ch * 8,
+                     rr < rows ? 16 : 0);
         }
+        cp_async_wait_all();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl.q_full);
+        if (more) announce();
       }
-      tc_commit(&ctl.drain);
-      mbar_wait(&ctl.drain, 0, a.status);
     }
-    __syncwarp();
-  } else if (warp >= 8) {
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTreeRegsSoftmax));
     // ------------------------------------------------------------ softmax
     const int grp = (warp - 8) >> 2, quad = warp & 3;
     const int tid = threadIdx.x - 256;       // 0..255 over both groups
     const int r = quad * 32 + lane;          // the thread's row of the tile
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
     const uint32_t tS = tmem + lanes, tO = tmem + lanes + 256 + grp * D;
-    SegIter it(a, x0, x1, ctl.u0, ctl.b0);
-    Seg sg;
-    uint32_t seg = 0, gt0 = 0;  // segments, key tiles before this one
-    uint32_t par = 0;           // bit k: tiles taken from S buffer k, mod 2
+    uint32_t gt0 = 0;  // key tiles before this part
+    uint32_t par = 0;  // bit k: tiles taken from S buffer k, mod 2
     TreeSplit split = {0, 0, 0, 0, 0, -1};
-    while (it.next(sg)) {
-      const SeqInfo& s = sg.s;
-      const int row0 = sg.qi * kTreeRows, rows = min(kTreeRows, s.T * a.group - row0);
-      // the query tile: 128-byte rows of 64 elements, 16-byte chunks swizzled
-      // by row; every load is in flight before the first store.  Rows past the
-      // item's are zeros up to the next 32 and undefined behind (no warp reads
-      // their scores).
-      {
-        constexpr int kPer = kTreeRows * (D / 8) / kTreeSoftmax;  // chunks of a thread
-        constexpr int kRowStep = kTreeSoftmax / (D / 8);
-        const int ch = tid % (D / 8), r0 = tid / (D / 8);
-        uint4 val[kPer];
-#pragma unroll
-        for (int y = 0; y < kPer; ++y) {
-          const int rr = r0 + y * kRowStep;
-          val[y] = make_uint4(0, 0, 0, 0);
-          if (rr < rows) {
-            const int i = (int)fast_div((uint32_t)(row0 + rr), a.div_group);
-            const int h = row0 + rr - i * a.group;
-            val[y] = *reinterpret_cast<const uint4*>(a.q + (s.q0 + i) * a.ld_q +
-                                                     (sg.g * a.group + h) * D + ch * 8);
-          }
-        }
-#pragma unroll
-        for (int y = 0; y < kPer; ++y) {
-          const int rr = r0 + y * kRowStep;
-          if (rr < ((rows + 31) & ~31))
-            *reinterpret_cast<uint4*>(sQ + (ch >> 3) * HQ + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4)) =
-                val[y];
-        }
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl.q_full);
-
+    for (uint32_t seg = 0;; ++seg) {
+      const Seg s = fetch(seg);
+      // all of them go on, or none: they meet at named barriers below
+      if (bar_sync_or(1, kTreeSoftmax, s.k1 == 0)) break;
+      const int row0 = s.qi * kTreeRows, rows = min(kTreeRows, s.T * a.group - row0);
       const bool warp_live = quad * 32 < rows;
       const int tok = (int)fast_div((uint32_t)(row0 + min(r, rows - 1)), a.div_group);
-      const int n = sg.k1 - sg.k0, len = s.old + s.T;
+      const int n = s.k1 - s.k0, len = s.old + s.T;
       float m = -INFINITY, l = 0.f;  // in units of log2
       // one tile of the group: scores from tensor memory, P back into it
       uint32_t vis[2];
@@ -563,7 +618,7 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
         tmem_st_wait();
       };
       for (int i = grp; i < n; i += 2) {
-        const int key0 = (sg.k0 + i) * kTreeKeys, k = i & 3;
+        const int key0 = (s.k0 + i) * kTreeKeys, k = i & 3;
         const bool tail = key0 + kTreeKeys > s.old;
         if (tail) {
           // V of keys behind the end and non-finite V of new tokens: two
@@ -613,79 +668,81 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
         if (lane == 0) mbar_arrive(&ctl.p_ready[k]);
       }
 
-      // The two groups' states meet: each leaves (m, l) where its scores were,
-      // then takes one half of the head's elements of both O.
+      // The two groups' states meet, and each takes one half of the head's
+      // elements of both O.
       if (n > grp) {
         const int k = (n - 1 - ((n - 1 - grp) & 1)) & 3;  // the group's last tile
         warp_wait(&ctl.pv_done[k], (par >> k & 1) ^ 1);
       }
-      tc_fence_after();
-      tmem_st2(tS + grp * kTreeKeys, __float_as_uint(m), __float_as_uint(l));
-      tmem_st_wait();
-      tc_fence_before();
+      meet[grp * kTreeRows + r] = make_float2(m, l);
       bar_sync(1, kTreeSoftmax);
       tc_fence_after();
-      float mg[2], lg[2];
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        uint32_t x, y;
-        tmem_ld2(tmem + lanes + q * kTreeKeys, x, y);
-        tmem_ld_wait();
-        mg[q] = __uint_as_float(x);
-        lg[q] = __uint_as_float(y);
-      }
-      const bool two = n > 1;
-      const float M = two ? fmaxf(mg[0], mg[1]) : mg[0];
-      const float w0 = mg[0] == -INFINITY ? 0.f : ex2_approx(mg[0] - M);
-      const float w1 = !two || mg[1] == -INFINITY ? 0.f : ex2_approx(mg[1] - M);
-      const float L = lg[0] * w0 + (two ? lg[1] * w1 : 0.f);
-      const bool whole = sg.k0 == 0 && sg.k1 == s.nt;
-      const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
-      const int h = row0 + min(r, rows - 1) - tok * a.group;
-      const bool poison = ctl.poison[seg & 1] != 0;
+      const bool whole = s.k0 == 0 && s.k1 == s.nt;
       const bool live = r < rows;
-      const int slot = sg.k0 > 0 || seg == 0 ? 0 : 1;  // a later piece is its CTA's first
-      const int64_t prow = ((int64_t)c * 2 + slot) * kTreeRows + r;
+      if (warp_live) {
+        const float2 ml0 = meet[r], ml1 = n > 1 ? meet[kTreeRows + r] : make_float2(-INFINITY, 0.f);
+        const float M = fmaxf(ml0.x, ml1.x);
+        float w0 = ml0.x == -INFINITY ? 0.f : ex2_approx(ml0.x - M);
+        float w1 = ml1.x == -INFINITY ? 0.f : ex2_approx(ml1.x - M);
+        const float L = ml0.y * w0 + ml1.y * w1;
+        const int slot = s.k0 > 0 || seg == 0 ? 0 : 1;  // a later piece is its CTA's first
+        const int64_t piece = (int64_t)c * 2 + slot;
+        if (!whole && live && grp == 0) a.ml[piece * kTreeRows + r] = make_float2(M, L);
+        if (whole) {
+          const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
+          w0 *= inv;
+          w1 *= inv;
+        }
+        const bool poison = ctl.poison[seg & 1] != 0;
 #pragma unroll 1
-      for (int q = 0; q < D / 32; ++q) {  // 16 elements a turn of this group's half (rolled: the
-                                          // code runs once an item, from a cold cache)
-        const int e0 = grp * (D / 2) + 16 * q;
-        float o0[16], o1[16];
-        tmem_ld16(tmem + lanes + 256 + e0, o0);
-        if (two) tmem_ld16(tmem + lanes + 256 + D + e0, o1);
-        tmem_ld_wait();
-        if (live) {
+        for (int q = 0; q < D / 32; ++q) {  // 16 elements a turn
+          const int e0 = grp * (D / 2) + 16 * q;
+          float o0[16], o1[16];
+          tmem_ld16(tmem + lanes + 256 + e0, o0);
+          tmem_ld16(tmem + lanes + 256 + D + e0, o1);
+          tmem_ld_wait();
+          // a state without keys may stand next to anything in tensor memory
 #pragma unroll
-          for (int e = 0; e < 16; ++e) o0[e] = two ? o0[e] * w0 + o1[e] * w1 : o0[e] * w0;
-          if (L == 0.f) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o0[e] = 0.f;
-          }
-          if (poison) nonfinite_v(a, s, sg.b, sg.g, tok, sg.k0 * kTreeKeys, sg.k1 * kTreeKeys, e0, o0);
+          for (int e = 0; e < 16; ++e)
+            o0[e] = (w0 != 0.f ? o0[e] * w0 : 0.f) + (w1 != 0.f ? o1[e] * w1 : 0.f);
+          if (poison && live)
+            nonfinite_v(a, s, tok, e0, o0);
           if (whole) {
+            // through shared memory: rows of o leave as whole lines
             uint32_t y[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = pack_bf16x2(o0[2 * e] * inv, o0[2 * e + 1] * inv);
-            uint4* dst = reinterpret_cast<uint4*>(a.o + (s.q0 + tok) * a.ld_o +
-                                                  (sg.g * a.group + h) * D + e0);
-            dst[0] = make_uint4(y[0], y[1], y[2], y[3]);
-            dst[1] = make_uint4(y[4], y[5], y[6], y[7]);
+            for (int e = 0; e < 8; ++e) y[e] = pack_p(o0[2 * e], o0[2 * e + 1]);
+            uint8_t* row = sOut + r * D * 2;
+            const int c0 = e0 >> 3;
+            *reinterpret_cast<uint4*>(row + ((c0 ^ (r & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+            *reinterpret_cast<uint4*>(row + (((c0 + 1) ^ (r & 7)) << 4)) =
+                make_uint4(y[4], y[5], y[6], y[7]);
           } else {
-            float4* dst = reinterpret_cast<float4*>(a.partials + prow * D + e0);
+            // [4 elements][row]: a warp's stores are contiguous
+            float4* dst = reinterpret_cast<float4*>(a.partials + piece * kTreeRows * D) +
+                          (e0 >> 2) * kTreeRows + r;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              dst[e] = make_float4(o0[4 * e], o0[4 * e + 1], o0[4 * e + 2], o0[4 * e + 3]);
+              dst[e * kTreeRows] = make_float4(o0[4 * e], o0[4 * e + 1], o0[4 * e + 2], o0[4 * e + 3]);
           }
         }
+        if (s.opens >= 0 && tid == 0) split = {s.q0, row0, rows, s.g, slot, s.opens};
       }
-      if (!whole && live && grp == 0) a.ml[prow] = make_float2(M, L);
-      if (sg.k0 == 0 && !whole && tid == 0)  // this CTA opens a cut item
-        split = {s.q0, row0, rows, sg.g, slot, owner_of(sg.x + s.nt + kItemCost - 1, W, G)};
       tc_fence_before();
       if (tid == 0) ctl.poison[(seg + 1) & 1] = 0;
-      bar_sync(1, kTreeSoftmax);  // both groups are done with O, S and Q
+      bar_sync(1, kTreeSoftmax);  // O was read, the rows are in shared memory
+      if (whole) {
+        const int ch = tid % (D / 8);
+        for (int rr = tid / (D / 8); rr < rows; rr += kTreeSoftmax / (D / 8)) {
+          const int i = (int)fast_div((uint32_t)(row0 + rr), a.div_group);
+          const int h = row0 + rr - i * a.group;
+          *reinterpret_cast<uint4*>(a.o + (s.q0 + i) * a.ld_o + (s.g * a.group + h) * D + ch * 8) =
+              *reinterpret_cast<const uint4*>(sOut + rr * D * 2 + ((ch ^ (rr & 7)) << 4));
+        }
+      }
       gt0 += n;
-      ++seg;
+      __syncwarp();
+      if (lane == 0) done_with(seg);
     }
     if (tid == 0) a.splits[c] = split;
   }
@@ -697,43 +754,59 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
 }
 
 // Joins the pieces of the items cut between CTAs, in key order: block (c, y)
-// takes rows [32 y, 32 y + 32) of the item that CTA c opened, a thread 4
-// elements of some rows.  The pieces come from L2: every load of a row's
-// pieces is independent of the others.
+// takes rows [32 y, 32 y + 32) of the item that CTA c opened, lane = row, a
+// warp every eighth group of 4 elements.  The pieces come from L2 as whole
+// lines, every load independent of the others; the rows leave through shared
+// memory as whole lines too.
 template <int D>
 __global__ void __launch_bounds__(256) tree_join_kernel(const TreeJoinArgs a) {
+  __shared__ uint2 out[32][D / 4 + 1];
   pdl_launch_dependents();
   pdl_wait();
   const TreeSplit s = a.splits[blockIdx.x];
-  if (s.last < 0) return;
-  constexpr int kCols = D / 4, kStep = 256 / kCols;
-  const int e = threadIdx.x % kCols * 4, end = min(s.rows, (int)blockIdx.y * 32 + 32);
-  for (int r = blockIdx.y * 32 + threadIdx.x / kCols; r < end; r += kStep) {
-    const int64_t opening = ((int64_t)blockIdx.x * 2 + s.slot) * kTreeRows + r;
-    auto at = [&](int p) {  // the later pieces begin their CTA's range
-      return p == (int)blockIdx.x ? opening : (int64_t)p * 2 * kTreeRows + r;
-    };
-    float M = -INFINITY;
+  const int r0 = blockIdx.y * 32;
+  if (s.last < 0 || r0 >= s.rows) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = r0 + lane;
+  const bool live = r < s.rows;
+  auto piece = [&](int p) {  // the later pieces are their CTA's first
+    return (int64_t)p * 2 + (p == (int)blockIdx.x ? s.slot : 0);
+  };
+  float M = -INFINITY;
 #pragma unroll 8
-    for (int p = blockIdx.x; p <= s.last; ++p) M = fmaxf(M, __ldcg(&a.ml[at(p)]).x);
-    float L = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int p = blockIdx.x; p <= s.last; ++p) {
-      const float2 ml = __ldcg(&a.ml[at(p)]);
-      const float4 y = __ldcg(reinterpret_cast<const float4*>(a.partials + at(p) * D + e));
-      const float w = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
-      L += ml.y * w;
-      o.x += y.x * w;
-      o.y += y.y * w;
-      o.z += y.z * w;
-      o.w += y.w * w;
+  for (int p = blockIdx.x; p <= s.last; ++p)
+    M = fmaxf(M, live ? __ldcg(&a.ml[piece(p) * kTreeRows + r]).x : -INFINITY);
+  constexpr int kPer = D / 32;  // groups of 4 elements of a warp
+  float L = 0.f;
+  float4 o[kPer];
+#pragma unroll
+  for (int q = 0; q < kPer; ++q) o[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int p = blockIdx.x; p <= s.last; ++p) {
+    const int64_t at = piece(p);
+    const float2 ml = live ? __ldcg(&a.ml[at * kTreeRows + r]) : make_float2(-INFINITY, 0.f);
+    const float w = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
+    L += ml.y * w;
+    const float4* src = reinterpret_cast<const float4*>(a.partials + at * kTreeRows * D) + r;
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {
+      const float4 y = live ? __ldcg(src + (warp + 8 * q) * kTreeRows) : make_float4(0.f, 0.f, 0.f, 0.f);
+      o[q].x += y.x * w;
+      o[q].y += y.y * w;
+      o[q].z += y.z * w;
+      o[q].w += y.w * w;
     }
-    const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
-    const int i = (int)fast_div((uint32_t)(s.row0 + r), a.div_group);
-    const int h = s.row0 + r - i * a.group;
-    *reinterpret_cast<uint2*>(a.o + (s.q0 + i) * a.ld_o + (s.g * a.group + h) * D + e) =
-        make_uint2(pack_p(o.x * inv, o.y * inv), pack_p(o.z * inv, o.w * inv));
+  }
+  const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
+#pragma unroll
+  for (int q = 0; q < kPer; ++q)
+    out[lane][warp + 8 * q] =
+        make_uint2(pack_p(o[q].x * inv, o[q].y * inv), pack_p(o[q].z * inv, o[q].w * inv));
+  __syncthreads();
+  const int e = threadIdx.x % (D / 4), end = min(s.rows - r0, 32);
+  for (int rr = threadIdx.x / (D / 4); rr < end; rr += 256 / (D / 4)) {
+    const int i = (int)fast_div((uint32_t)(s.row0 + r0 + rr), a.div_group);
+    const int h = s.row0 + r0 + rr - i * a.group;
+    *reinterpret_cast<uint2*>(a.o + (s.q0 + i) * a.ld_o + (s.g * a.group + h) * D + 4 * e) = out[rr][e];
   }
 }
 
