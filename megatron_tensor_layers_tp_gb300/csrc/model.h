@@ -102,13 +102,13 @@ cudaError_t launch(const tp_model* m, const char* name, cudaStream_t st, F&& f) 
   return cudaEventRecord(b, st);
 }
 
-// 3-D bf16 tensor map (inner K, rows, slices) with a (64, box_rows, 1) box and
-// 128-byte swizzle; reads outside the extents return zeros.
+// 3-D bf16 tensor map (inner K, rows, slices) with a (64, box_rows, box_slices)
+// box and 128-byte swizzle; reads outside the extents return zeros.
 // When the slices sit closer together than the rows (rank shards side by side
 // in one [rows, t*K] buffer), the dimensions are ordered (K, slice, rows) so
 // the strides increase; *slice_mid reports which order was used.
 bool make_tmap(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint64_t slices,
                uint64_t row_stride_bytes, uint64_t slice_stride_bytes, uint32_t box_rows,
-               int* slice_mid = nullptr);
+               int* slice_mid = nullptr, uint32_t box_slices = 1);
 
 }  // namespace tpk

@@ -60,10 +60,10 @@ struct TreeSplit {
 };
 struct TreeAttnArgs {
   CUtensorMap tmK, tmV;       // (d, page_size, copies * n_pages * kv_r), box (64, box_rows, 1)
+  CUtensorMap tmQ;            // (d, n_heads, n_tokens), box (64, group, tile_toks)
+  int tile_toks, tile_rows;   // tokens of a query tile (128 / group), its rows
   int box_rows;               // keys a box brings: a power of two that divides page_size
   int slices;                 // the third extent: coordinates from here on read zeros
-  const uint16_t* q;
-  int64_t ld_q;
   uint16_t* o;
   int64_t ld_o;
   const uint16_t* v;
@@ -78,7 +78,6 @@ struct TreeAttnArgs {
   FastDiv div_group;
   float scale_log2;           // log2(e) / sqrt(d)
   int kv_once;                // 1: no sequence has more than one query tile, K and V are read once
-  int loaders;                // warps that share a tile's boxes
   int grid;
   float* partials;            // [grid][2][d / 4][128][4]
   float2* ml;                 // [grid][2][128]

@@ -210,8 +210,6 @@ tp_status tp_tree_attention(const tp_model* m, const tp_bf16* q, int64_t ld_q, t
       return TP_ERR_WORKSPACE;
     TreeAttnArgs a;
     memset(&a, 0, sizeof(a));
-    a.q = q;
-    a.ld_q = ld_q;
     a.o = o;
     a.ld_o = ld_o;
     a.v = v;
@@ -245,11 +243,12 @@ tp_status tp_tree_attention(const tp_model* m, const tp_bf16* q, int64_t ld_q, t
     a.head_dim = c.head_dim;
     a.div_group = make_fastdiv((uint32_t)a.group);
     a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)c.head_dim));
-    const int64_t rows = (int64_t)step->max_new * a.group;
-    a.kv_once = rows <= kTreeRows;
-    // at most four boxes of a K or V tile a loader warp: 64-key boxes need one
-    // warp, 8-key boxes four (idle loaders would only poll)
-    a.loaders = std::min(kTreeLoaders, cdiv(kTreeKeys / a.box_rows * (c.head_dim / 64), 4));
+    a.tile_toks = kTreeRows / a.group;
+    a.tile_rows = a.tile_toks * a.group;
+    a.kv_once = step->max_new <= a.tile_toks;
+    if (!make_tmap(&a.tmQ, q, d, c.n_heads, step->n_tokens, d * 2, ld_q * 2, a.group, nullptr,
+                   a.tile_toks))
+      return TP_ERR_CUDA;
     a.grid = m->num_sms;
     const StepWs w = step_ws(m);
     uint8_t* base = static_cast<uint8_t*>(ws);
@@ -261,7 +260,7 @@ tp_status tp_tree_attention(const tp_model* m, const tp_bf16* q, int64_t ld_q, t
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     TP_CHECK_CUDA(launch(m, "tree_attn", st, [&] { return launch_tree_attn(a, st); }));
     return cuda_status(launch(m, "tree_join", st, [&] {
-      return launch_tree_join(j, c.head_dim, a.grid, (int)std::min<int64_t>(rows, kTreeRows), st);
+      return launch_tree_join(j, c.head_dim, a.grid, std::min(step->max_new, a.tile_toks) * a.group, st);
     }));
   });
 }

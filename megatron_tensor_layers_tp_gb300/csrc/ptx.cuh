@@ -86,16 +86,6 @@ __device__ __forceinline__ void fence_acq_rel_gpu() {
   asm volatile("fence.acq_rel.gpu;" ::: "memory");
 }
 
-// 16 bytes global -> shared without registers; src_bytes 0 stores zeros (the
-// address must still be valid).
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t src_bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async_wait_all() {
-  asm volatile("cp.async.wait_all;" ::: "memory");
-}
-
 // ---------------------------------------------------------------- TMA
 // Bring `bytes` (a multiple of 16) of global memory at `p` (16-byte aligned)
 // into L2; nothing is written to shared memory and no barrier is involved.

@@ -538,14 +538,14 @@ struct MapUploader {
 // C ABI
 // ============================================================================
 namespace tpk {
-// 3-D bf16 tensor map (inner K, rows, slices) with a (64, box_rows, 1) box and
-// 128-byte swizzle; reads outside the extents return zeros.
+// 3-D bf16 tensor map (inner K, rows, slices) with a (64, box_rows, box_slices)
+// box and 128-byte swizzle; reads outside the extents return zeros.
 // When the slices sit closer together than the rows (rank shards side by side
 // in one [rows, t*K] buffer), the dimensions are ordered (K, slice, rows) so
 // the strides increase; *slice_mid reports which order was used.
 bool make_tmap(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint64_t slices,
                uint64_t row_stride_bytes, uint64_t slice_stride_bytes, uint32_t box_rows,
-               int* slice_mid) {
+               int* slice_mid, uint32_t box_slices) {
   auto enc = get_encoder();
   if (!enc) return false;
   const bool mid = slices > 1 && slice_stride_bytes < row_stride_bytes;
@@ -553,7 +553,7 @@ bool make_tmap(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, 
   if (mid && !slice_mid) return false;
   cuuint64_t dims[3] = {inner, rows, slices};
   cuuint64_t strides[2] = {row_stride_bytes, slice_stride_bytes};
-  cuuint32_t box[3] = {64, box_rows, 1};
+  cuuint32_t box[3] = {64, box_rows, box_slices};
   if (mid) {
     dims[1] = slices; dims[2] = rows;
     strides[0] = slice_stride_bytes; strides[1] = row_stride_bytes;

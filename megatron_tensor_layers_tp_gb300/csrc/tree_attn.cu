@@ -7,8 +7,8 @@
 // sqrt(d) and the running maximum m, in one pass over the keys.
 //
 // Every Q head of a KV head and every new token of a sequence share its keys:
-// they are the rows of 128-row query tiles (row = token * group + head), so K
-// and V are read once for up to 128 / group tokens.  With one tile per
+// they are the rows of query tiles (row = token * group + head, whole tokens, up
+// to 128 rows), so K and V are read once for up to 128 / group tokens.  With one tile per
 // sequence and KV head the cache's bytes bound the kernel: a 64-key tile of K
 // and V (32 KB at d = 128) takes an SM 0.73 us at its share of the memory rate,
 // its two products 0.14 us and its exponentials 0.2 us.
@@ -23,10 +23,10 @@
 // for prompt chunks instead of @@ us.
 //
 // Roles of the 16 warps:
-//   warps 0-3  : K and V tiles by TMA into a ring, through the page table; boxes
-//                end where pages end, and a box costs its warp about 130 cycles
-//                to issue (32 boxes a tile at 8-key pages), so up to four warps
-//                share a tile's boxes;
+//   warps 0-3  : K and V tiles by TMA into a ring, through the page table, each
+//                every fourth tile: boxes end where pages end, a box costs its
+//                warp about 130 cycles to issue (32 boxes a tile at 8-key
+//                pages) and a tile some 1500 in waits and look-ups;
 //   warp 4     : one thread issues S = Q K^T into tensor memory;
 //   warps 5, 6 : one thread each issues O += P V of a softmax group, with P read
 //                from tensor memory and V as it lies in the page (the head's
@@ -75,6 +75,7 @@ constexpr int kTreeSoftmax = 256;        // threads of the two softmax groups
 constexpr int kTreeRegsOther = 64, kTreeRegsSoftmax = 184;
 constexpr float kRescaleLog2 = 8.f;
 constexpr int kItemCost = 8;             // an item's fixed work in key tiles
+constexpr int kMaxGrid = 1024;
 
 // One CTA's part of an item: key tiles [k0, k1) of nt of (sequence b, KV head
 // g, query tile qi), the sequence's first row, new tokens and old length.
@@ -102,7 +103,7 @@ struct TreeCtl {
   uint64_t seg_full[4], seg_free[4];
   Seg seg[4];
   long long warp_sum[16];
-  long long total, u0;
+  long long total, u0, x0, x1;
   int b0;
   int poison[2];
   uint32_t tmem;
@@ -126,13 +127,19 @@ __device__ __forceinline__ SeqInfo seq_info(const TreeAttnArgs& a, int b) {
     record_status(a.status, kStatusTableRange);
     s.T = 0;
   }
-  s.qt = (s.T * a.group + kTreeRows - 1) / kTreeRows;
+  s.qt = (s.T + a.tile_toks - 1) / a.tile_toks;
   s.nt = s.T ? (s.old + s.T + kTreeKeys - 1) / kTreeKeys : 0;
   return s;
 }
 // The flat positions of a sequence: every item's tiles after its fixed cost.
 __device__ __forceinline__ int64_t positions(const TreeAttnArgs& a, const SeqInfo& s) {
   return (int64_t)a.n_kv * s.qt * (s.nt + kItemCost);
+}
+
+// range_begin without a 64-bit division where 32 bits hold the product.
+__device__ __forceinline__ int64_t range_at(int c, int64_t T, int G) {
+  if (T <= 0xFFFFFFFFll / kMaxGrid) return (uint32_t)c * (uint32_t)T / (uint32_t)G;
+  return range_begin(c, T, G);
 }
 
 // A CTA's parts in order.  A part that lies within the item's fixed cost has
@@ -272,13 +279,14 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
     ctl.poison[0] = ctl.poison[1] = 0;
     for (int i = 0; i < 4; ++i) {
       mbar_init(&ctl.seg_full[i], 1);
-      mbar_init(&ctl.seg_free[i], a.loaders + 3 + kTreeSoftmax / 32);
+      mbar_init(&ctl.seg_free[i], kTreeLoaders + 3 + kTreeSoftmax / 32);
     }
     mbar_init(&ctl.q_full, 1);
     mbar_init(&ctl.q_free, 1);
     mbar_init(&ctl.drain, 3);
     fence_barrier_init();
     fence_proxy_async_smem();
+    tma_prefetch_desc(&a.tmQ);
     tma_prefetch_desc(&a.tmK);
     tma_prefetch_desc(&a.tmV);
   }
@@ -318,7 +326,7 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
     }
     long long at = before + incl - sum;
     if (total < G) G = (int)total;
-    const long long x0 = c < G ? range_begin(c, total, G) : total;
+    const long long x0 = c < G ? range_at(c, total, G) : total;
     if (x0 >= at && x0 < at + sum) {
       int b = lo;
       while (true) {
@@ -331,12 +339,16 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
       ctl.b0 = b;
       ctl.u0 = x0 - at;
     }
-    if (threadIdx.x == 0) ctl.total = total;
+    if (threadIdx.x == 0) {
+      ctl.total = total;
+      ctl.x0 = x0;
+      ctl.x1 = c < G ? range_at(c + 1, total, G) : total;
+    }
     __syncthreads();
   }
   const uint32_t tmem = ctl.tmem;
   const int64_t W = ctl.total;
-  const int64_t x0 = c < G ? range_begin(c, W, G) : W, x1 = c < G ? range_begin(c + 1, W, G) : W;
+  const int64_t x0 = ctl.x0, x1 = ctl.x1;
 
   // A wait that runs out is remembered and nothing waits after it: every role
   // then runs to its end without touching the copies or products.
@@ -361,55 +373,50 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
   // The softmax warpgroups take over registers that the others do not need.
   if (warp < 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTreeRegsOther));
-    if (warp < a.loaders) {
+    if (warp < kTreeLoaders) {
       // ------------------------------------------------------------ K and V
       const uint64_t pol = policy_evict_first();
       const int R = a.box_rows, boxes = kTreeKeys / R;
-      // this warp's boxes (of a tile's 64 / R times d / 64): lane j takes
-      // number j * loaders + warp
-      const int y = lane * a.loaders + warp;
-      const int box = D == 128 ? y >> 1 : y, half = D == 128 ? y & 1 : 0;
-      uint32_t n = 0;  // ring fills
+      // lane -> (box, 64-element half)
+      const int box = D == 128 ? lane >> 1 : lane, half = D == 128 ? lane & 1 : 0;
+      uint32_t gt = 0;              // key tiles before this part
+      uint32_t mine[2] = {0, 0};    // this warp's last ring fills + 1 (K, V)
       for (uint32_t seg = 0;; ++seg) {
         const Seg sg = fetch(seg);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok || sg.k1 == 0) break;
         const int copy = sg.g / a.kv_r, local = sg.g - copy * a.kv_r;
-        const int len = sg.old + sg.T;
-        // The row of the page table through a window of 64 entries, two a lane:
-        // the second half is in flight while the first is used.
+        const int len = sg.old + sg.T, n = sg.k1 - sg.k0;
         const int32_t* row = a.table + (int64_t)sg.b * a.ld_table;
         const int last = (int)fast_div((uint32_t)min(len, sg.k1 * kTreeKeys) - 1, a.div_page);
-        auto load = [&](int pg) { return pg <= last ? row[pg] : 0; };
-        int w0 = (int)fast_div((uint32_t)(sg.k0 * kTreeKeys), a.div_page);
-        int win = load(w0 + lane), nxt = load(w0 + 32 + lane);
-        for (int kt = sg.k0; ok && kt < sg.k1; ++kt) {
+        // A tile's page numbers, one a box, loaded two of the warp's tiles
+        // ahead.
+        auto load = [&](int i) {
+          const int pg = (int)fast_div((uint32_t)((sg.k0 + i) * kTreeKeys + box * R), a.div_page);
+          return i < n && box < boxes && pg <= last ? row[pg] : 0;
+        };
+        const int i0 = (warp - gt) & (kTreeLoaders - 1);  // tile gt + i0 is the warp's
+        int page = load(i0), next = load(i0 + kTreeLoaders);
+        for (int i = i0; ok && i < n; i += kTreeLoaders) {
+          const int after = load(i + 2 * kTreeLoaders);
+          const int kt = sg.k0 + i;
           const int here = min(boxes, (len - kt * kTreeKeys + R - 1) / R);
-          const int key = kt * kTreeKeys + min(box, here - 1) * R;  // (spare lanes: the last box)
-          const int pg = (int)fast_div((uint32_t)key, a.div_page);
-          const int pg0 = (int)fast_div((uint32_t)(kt * kTreeKeys), a.div_page);
-          if (pg0 - w0 >= 32) {
-            w0 += 32;
-            win = nxt;
-            nxt = load(w0 + 32 + lane);
-          }
-          const int lo = __shfl_sync(0xffffffffu, win, (pg - w0) & 31);
-          const int hi = __shfl_sync(0xffffffffu, nxt, (pg - w0) & 31);
-          const int page = pg - w0 < 32 ? lo : hi;
-          const int off = key - pg * a.page_size;
+          const int key = kt * kTreeKeys + box * R;
+          const int off = key - (int)fast_div((uint32_t)key, a.div_page) * a.page_size;
           int z = (copy * a.n_pages + page) * a.kv_r + local;
-          if (page < 0 || page >= a.n_pages) {
+          if (box < here && (page < 0 || page >= a.n_pages)) {
             record_status(a.status, kStatusTableRange);
             z = a.slices;  // outside the tensor map: zeros
           }
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv) {
-            const uint32_t st = n % NST;
-            if (lane == 0) wait(&ctl.empty[st], (n / NST & 1) ^ 1);  // one lane polls
+            const uint32_t f = 2 * (gt + i) + kv, st = f % NST;
+            if (lane == 0) wait(&ctl.empty[st], (f / NST & 1) ^ 1);  // one lane polls
             ok = __shfl_sync(0xffffffffu, ok, 0);
             if (ok) {
-              ++n;
-              if (warp == 0 && lane == 0) mbar_arrive_expect_tx(&ctl.full[st], here * R * D * 2);
+              mine[kv] = f + 1;
+              if (lane == 0) mbar_arrive_expect_tx(&ctl.full[st], here * R * D * 2);
+              __syncwarp();
               if (box < here) {
                 uint8_t* dst = ring + st * SM::kTile + half * HB + box * R * 128;
                 const CUtensorMap* tm = kv ? &a.tmV : &a.tmK;
@@ -418,14 +425,23 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
               }
             }
           }
+          page = next;
+          next = after;
         }
+        gt += n;
         __syncwarp();
         if (lane == 0) done_with(seg);
       }
-      // never leave with copies still landing in shared memory
+      // Never leave with copies still landing in shared memory.  A fill whose
+      // slot is filled again later (by another warp) landed before that.
       if (lane == 0) {
-        for (uint32_t i = n > NST ? n - NST : 0; i < n; ++i)
-          if (!mbar_wait(&ctl.full[i % NST], (i / NST) & 1, a.status)) break;
+        for (uint32_t back = 0; back < NST; back += 2 * kTreeLoaders)
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv) {
+            const uint32_t f = mine[kv] - 1 - back;
+            if (mine[kv] > back && (!ok || f + NST >= 2 * gt))
+              mbar_wait(&ctl.full[f % NST], (f / NST) & 1, a.status);
+          }
       }
       __syncwarp();
     } else if (warp >= 4 && warp < 7) {
@@ -512,32 +528,29 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
       };
       announce();
       if (more) announce();
-      // Query rows of 64 elements (128 bytes), 16-byte chunks swizzled by row.
-      // Rows past the item's are zeros up to the next 32 and undefined behind
-      // (no warp reads their scores).
-      constexpr int kRowStep = 32 / (D / 8);
-      const int ch = lane % (D / 8), r0 = lane / (D / 8);
+      // A query tile is a box of the group's heads and its tokens.  (Rows
+      // behind the item's hold other tokens or zeros; nothing reads their o.)
+      uint32_t asked = 0;
       for (uint32_t seg = 0;; ++seg) {
         const Seg sg = ctl.seg[seg & 3];
         if (sg.k1 == 0) break;
-        const int row0 = sg.qi * kTreeRows, rows = min(kTreeRows, sg.T * a.group - row0);
-        const int end = (rows + 31) & ~31;
-        if (lane == 0) wait(&ctl.q_free, (seg & 1) ^ 1);
-        __syncwarp();
-#pragma unroll 2
-        for (int rr = r0; rr < end; rr += kRowStep) {
-          const uint32_t dst = smem_u32(sQ + (ch >> 3) * HQ + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4));
-          const int i = (int)fast_div((uint32_t)(row0 + min(rr, rows - 1)), a.div_group);
-          const int h = row0 + min(rr, rows - 1) - i * a.group;
-          cp_async16(dst, a.q + (sg.q0 + i) * a.ld_q + (sg.g * a.group + h) * D + ch * 8,
-                     rr < rows ? 16 : 0);
+        if (lane == 0) {
+          wait(&ctl.q_free, (seg & 1) ^ 1);
+          if (ok) {
+            ++asked;
+            mbar_arrive_expect_tx(&ctl.q_full, a.tile_rows * D * 2);
+#pragma unroll
+            for (int h = 0; h < D / 64; ++h)
+              tma_load_3d_plain(sQ + h * HQ, &a.tmQ, &ctl.q_full, h * 64, sg.g * a.group,
+                                sg.q0 + sg.qi * a.tile_toks);
+          }
         }
-        cp_async_wait_all();
-        fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl.q_full);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
         if (more) announce();
       }
+      if (lane == 0 && asked) mbar_wait(&ctl.q_full, (asked - 1) & 1, a.status);  // landed
+      __syncwarp();
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTreeRegsSoftmax));
@@ -554,7 +567,7 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
       const Seg s = fetch(seg);
       // all of them go on, or none: they meet at named barriers below
       if (bar_sync_or(1, kTreeSoftmax, s.k1 == 0)) break;
-      const int row0 = s.qi * kTreeRows, rows = min(kTreeRows, s.T * a.group - row0);
+      const int row0 = s.qi * a.tile_rows, rows = min(a.tile_rows, s.T * a.group - row0);
       const bool warp_live = quad * 32 < rows;
       const int tok = (int)fast_div((uint32_t)(row0 + min(r, rows - 1)), a.div_group);
       const int n = s.k1 - s.k0, len = s.old + s.T;
