@@ -127,6 +127,6 @@ struct LogitsArgs {
   const int32_t* allowed_row;
   int* status;
 };
-cudaError_t launch_process_logits(const LogitsArgs& a, cudaStream_t st);
+cudaError_t launch_process_logits(const LogitsArgs& a, int num_sms, cudaStream_t st);
 
 }  // namespace tpk

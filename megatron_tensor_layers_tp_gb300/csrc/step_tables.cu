@@ -10,8 +10,11 @@
 //
 // The work is a few bytes a token: latency bounds it.  Every CTA therefore
 // repeats the prefix sums (up to 8192 sequences: 96 KB of shared memory)
-// instead of handing them over through memory, and then fills its own 2048
-// tokens and its own sequences' pages.  The ring's new state is written by
+// instead of handing them over through memory, and then fills its own 512
+// tokens and its own sequences' pages.  A token's path is a walk over parents,
+// up to 256 dependent steps: they are staged in shared memory first (512
+// sequences of up to 64 drafted tokens: 17 us with the walk in global memory
+// and 2048 tokens a CTA, @@ us so).  The ring's new state is written by
 // the last CTA to finish (a ticket), since the others read the old one, which
 // may be the same two words.
 #include <cuda_bf16.h>
@@ -24,7 +27,7 @@
 namespace tpk {
 
 constexpr int kTabThreads = 512;
-constexpr int kTabTokens = 2048;  // tokens of one CTA
+constexpr int kTabTokens = 512;  // tokens of one CTA, one a thread
 
 struct Scan3 {
   long long t, p, u;
@@ -58,6 +61,7 @@ __device__ __forceinline__ Scan3 block_scan3(Scan3 v, Scan3* warp_sums, Scan3* t
 __global__ void __launch_bounds__(kTabThreads) step_tables_kernel(const StepTablesArgs a) {
   extern __shared__ int32_t sm[];
   __shared__ Scan3 warp_sums[kTabThreads / 32];
+  __shared__ int32_t parents[kMaxTreeTokens + kTabTokens];
   const int n = a.n_seqs, tid = threadIdx.x;
   int32_t* qs = sm;             // [n + 1] first token
   int32_t* pop = qs + n + 1;    // [n] first page taken
@@ -110,6 +114,11 @@ __global__ void __launch_bounds__(kTabThreads) step_tables_kernel(const StepTabl
   // this CTA's tokens
   const int t0 = blockIdx.x * kTabTokens;
   const int t1 = min(a.n_tokens, t0 + kTabTokens);
+  const int p0 = max(0, t0 - kMaxTreeTokens);  // a path stays within its sequence's 256 tokens
+  if (a.parents) {
+    for (int t = p0 + tid; t < t1; t += kTabThreads) parents[t - p0] = a.parents[t];
+    __syncthreads();
+  }
   for (int t = t0 + tid; t < t1; t += kTabThreads) {
     int slot = -1, position = 0, seq = -1;
     uint64_t m[kMaxTreeWords] = {0, 0, 0, 0};
@@ -134,7 +143,7 @@ __global__ void __launch_bounds__(kTabThreads) step_tables_kernel(const StepTabl
 #pragma unroll
           for (int w = 0; w < kMaxTreeWords; ++w)
             if ((p >> 6) == w) m[w] |= 1ull << (p & 63);
-          const int q = a.parents[q0 + p];
+          const int q = parents[q0 + p - p0];
           if (q < -1 || q >= p) record_status(a.status, kStatusTableRange);
           if (q < 0 || q >= p) break;
           p = q;

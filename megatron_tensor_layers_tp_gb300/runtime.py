@@ -75,6 +75,8 @@ class Batch:
 def _check(t: torch.Tensor, name: str, dtype, shape, device, rows: bool = False) -> None:
     """Raises ValueError unless t is a tensor on `device` of that dtype and shape (None: any
     size), contiguous; with `rows`, a matrix whose rows are contiguous (any row stride)."""
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return
     if t.dtype != dtype or t.device != device:
         raise ValueError(f"{name}: {dtype} on {device} expected, got {t.dtype} on {t.device}")
     if len(t.shape) != len(shape) or any(w is not None and g != w for g, w in zip(t.shape, shape)):
@@ -459,6 +461,13 @@ class TPModel:
             self.step_ws = ws
         return self.step_ws
 
+    def _stream(self, stream) -> int:
+        """As _stream; the current stream is looked up by the device's number, which takes a
+        tenth of the time that finding the current device out takes."""
+        if stream is None:
+            return torch.cuda.current_stream(self.device.index).cuda_stream
+        return _stream(stream)
+
     def _out(self, shape, dtype, stream) -> torch.Tensor:
         """An output buffer that belongs to the stream the call runs on."""
         if stream is None:
@@ -480,7 +489,7 @@ class TPModel:
         if ws is None:
             ws = self.ensure_step_workspace(step.n_seqs, step.max_new, stream)
         B.check(B.tp_step_tables(self.handle, pages.c, step.c, ws.data_ptr(), ws.numel(),
-                                 _stream(stream)), "tp_step_tables")
+                                 self._stream(stream)), "tp_step_tables")
         return step
 
     def cache_append(self, qkv: torch.Tensor, positions: torch.Tensor, slots: torch.Tensor,
@@ -505,7 +514,7 @@ class TPModel:
         B.check(B.tp_cache_append(self.handle, qkv.data_ptr(), M * qkv.shape[2], M,
                                   positions.data_ptr(), slots.data_ptr(), pages.c, k.data_ptr(),
                                   v.data_ptr(), _ptr(q), 0 if q is None else _ld(q),
-                                  _stream(stream)), "tp_cache_append")
+                                  self._stream(stream)), "tp_cache_append")
         return q
 
     def tree_attention(self, q: torch.Tensor, step: Step, pages: PageTable, k: torch.Tensor,
@@ -531,7 +540,7 @@ class TPModel:
             ws = self.ensure_step_workspace(step.n_seqs, step.max_new, stream)
         B.check(B.tp_tree_attention(self.handle, q.data_ptr(), _ld(q), out.data_ptr(), _ld(out),
                                     pages.c, step.c, k.data_ptr(), v.data_ptr(), ws.data_ptr(),
-                                    ws.numel(), _stream(stream)), "tp_tree_attention")
+                                    ws.numel(), self._stream(stream)), "tp_tree_attention")
         return out
 
     def _check_pool(self, t: torch.Tensor, name: str, pages: PageTable) -> None:
@@ -562,7 +571,7 @@ class TPModel:
             _check(out, "out", out.dtype, (S, V), self.device, rows=True)
         B.check(B.tp_process_logits(self.handle, logits.data_ptr(), _ld(logits), S, rules.c,
                                     out.data_ptr(), _ld(out), int(out.dtype == torch.float32),
-                                    _stream(stream)), "tp_process_logits")
+                                    self._stream(stream)), "tp_process_logits")
         return out
 
     def capture_forward(self, ids: torch.Tensor, batch: Batch, h: torch.Tensor,
