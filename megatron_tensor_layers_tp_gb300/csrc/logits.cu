@@ -5,30 +5,43 @@
 // allowed: -infinity.  Counts come from the request's text and the drafted
 // tokens on the row's path.
 //
-// Memory-bound: 2 bytes in, 2 or 4 out and a mask bit a token.  A row's
-// vocabulary is cut into slices, one CTA each, 16 tokens a thread.  A thread
-// first puts its logits and mask bits in flight; meanwhile the CTA reads the
-// request's text and marks what it touches of the slice in shared memory
-// (integer atomics: their order does not matter): 16 bits a token, or 32 where
-// a text is long enough to overflow them.  Almost all marks are zero, so the
-// rules cost one 16-byte shared load for eight tokens.  The biases sit in a
-// slice-sized array that is neither cleared nor read except where a mark says
-// so.
+// Memory-bound: 2 bytes in, 2 or 4 out and a mask bit a token.  The vocabulary
+// is cut into slices; a CTA takes one slice of some consecutive rows, the next
+// row's logits, mask bits and path in flight while it works on this one.  A
+// slice is every so-manieth block of 64 tokens: frequent tokens have
+// neighbouring numbers, and runs of the vocabulary would give one CTA all of
+// them (50 us instead of 47 for the rows below).
 //
-// Slices of 8192 tokens (512 threads, four CTAs an SM) keep the repeated
-// reading of the text small; with too few rows to fill the GPU that way,
-// slices of 2048 (128 threads): one row of 128256 logits @@ us instead of @@.
+// What a request's text, biases and drafted path touch of a slice is little.
+// The CTA marks it in shared memory (integer atomics: their order does not
+// matter; 16 bits a token, or 32 where a text is long enough to overflow them)
+// and lists it: once for as many rows as belong to the same request, a row's
+// path added and taken out again.  All tokens then stream through as copies
+// with the mask applied, a few instructions each, and the listed ones are
+// written over with the rules applied, one thread each, while their lines are
+// still in the caches.
+//
+// 256 rows (16 trees) of 152064 logits, texts of 1500 tokens, 300 biases, bf16:
+// 47 us, 3.4 TB/s; the stream alone would take 32.  Measured before: the rules
+// applied in the stream, a slice a CTA: 110 us; the touched tokens in a second
+// kernel behind the stream: 55 us, since their lines come from memory again.
+// 64 rows of 128256 with texts of 4096 tokens, fp32: 23 us, 2.2 TB/s; there the
+// text's way into the marks (some 4 us a CTA) binds.
+//
+// Slices have 4096 tokens, 8192 where texts are long (their reading is repeated
+// for every slice: 23 us instead of 33 at 4096 tokens, but 65 instead of 47 at
+// 1500), 2048 where there are too few rows to fill the GPU.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "paged.h"
 #include "ptx.cuh"
 
 namespace tpk {
-
-constexpr int kLogPer = 16;  // tokens of a thread
 
 // Marks of a token: bit 0 = in the prompt, bit 1 = has a bias, the rest = times
 // written by the model.
@@ -36,276 +49,381 @@ constexpr uint32_t kMarkPrompt = 1, kMarkBias = 2, kMarkWritten = 4;
 // the longest text (and path) whose counts fit 16-bit marks
 constexpr int64_t kNarrowText = (1 << 14) - 1;
 
+// The slice's marks; add and set return what the token had before.
 template <bool kWide>
 struct Marks {
   uint32_t* w;
-  __device__ __forceinline__ void add(int v, uint32_t x) {
-    if constexpr (kWide) atomicAdd(w + v, x);
-    else atomicAdd(w + (v >> 1), x << (16 * (v & 1)));
+  __device__ __forceinline__ uint32_t add(int v, uint32_t x) {
+    if constexpr (kWide) return atomicAdd(w + v, x);
+    else return atomicAdd(w + (v >> 1), x << (16 * (v & 1))) >> (16 * (v & 1)) & 0xFFFF;
   }
-  __device__ __forceinline__ void set(int v, uint32_t x) {
-    if constexpr (kWide) atomicOr(w + v, x);
-    else atomicOr(w + (v >> 1), x << (16 * (v & 1)));
+  __device__ __forceinline__ uint32_t set(int v, uint32_t x) {
+    if constexpr (kWide) return atomicOr(w + v, x);
+    else return atomicOr(w + (v >> 1), x << (16 * (v & 1))) >> (16 * (v & 1)) & 0xFFFF;
   }
   __device__ __forceinline__ uint32_t get(int v) const {
     if constexpr (kWide) return w[v];
     else return (w[v >> 1] >> (16 * (v & 1))) & 0xFFFF;
   }
-  // any mark among tokens v .. v + 7 (v a multiple of 8)
-  __device__ __forceinline__ bool any8(int v) const {
-    const uint4* p = reinterpret_cast<const uint4*>(w + (kWide ? v : v >> 1));
-    uint4 a = p[0];
-    if constexpr (kWide) {
-      const uint4 b = p[1];
-      a.x |= b.x; a.y |= b.y; a.z |= b.z; a.w |= b.w;
-    }
-    return (a.x | a.y | a.z | a.w) != 0;
-  }
 };
 
-// One request's numbers for the rules on a single logit.
-struct Rules {
-  float rep, freq, pres;
+// A thread's part of a row: its logits, which of them are allowed, and a token
+// of the row's drafted path (-1: none).
+template <int kPer>
+struct RowPart {
+  uint4 x[kPer / 8];
+  uint32_t ok;
+  int path;
 };
-__device__ __forceinline__ float apply_rules(float x, uint32_t mark, const float* bias,
-                                             const Rules& r) {
-  const uint32_t n = mark / kMarkWritten;
-  if (n || (mark & kMarkPrompt)) x = x > 0.f ? x / r.rep : x * r.rep;
-  if (n) x = x - r.freq * (float)n - r.pres;
-  if (mark & kMarkBias) x += *bias;
-  return x;
+
+// What a row's indices say, looked up once by the CTA: its request (-1: left
+// alone), its grammar row (-1: none, -2: nothing is allowed), its path's first
+// token and length.
+struct RowInfo {
+  int r, m, q0, T;
+};
+constexpr int kLogRows = 16;  // rows of a CTA, at most
+
+// Two logits with those not allowed made -infinity (0xFF80).
+__device__ __forceinline__ uint32_t allow2(uint32_t w, uint32_t ok) {
+  if (!(ok & 1)) w = (w & 0xFFFF0000u) | 0xFF80u;
+  if (!(ok & 2)) w = (w & 0x0000FFFFu) | 0xFF800000u;
+  return w;
 }
 
-template <int kThreads, bool kWide>
-__global__ void __launch_bounds__(kThreads) process_logits_kernel(const LogitsArgs a, int slices) {
-  constexpr int kSlice = kThreads * kLogPer;
-  extern __shared__ __align__(16) uint32_t sm[];
-  Marks<kWide> marks{sm};
-  float* bias = reinterpret_cast<float*>(sm + (kWide ? kSlice : kSlice / 2));  // with a.bias_start
+template <int kThreads, int kPer, bool kWide>
+struct LogitsSmem {
+  static constexpr int kSlice = kThreads * kPer;
+  static constexpr int kMarks = 16 + kLogRows * sizeof(RowInfo);  // after the count and the rows
+  static constexpr int kList = kMarks + kSlice * (kWide ? 4 : 2);
+  static constexpr int kRaw = kList + kSlice * 2;
+  static constexpr int kBias = kRaw + kSlice * 2;
+  static constexpr int bytes(bool bias) { return kBias + (bias ? kSlice * 4 : 0); }
+};
+
+template <int kThreads, int kPer, bool kWide>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) process_logits_kernel(const LogitsArgs a, int slices, FastDiv div_slices,
+                                                                  int rows) {
+  using SM = LogitsSmem<kThreads, kPer, kWide>;
+  constexpr int kSlice = SM::kSlice;
+  extern __shared__ __align__(16) uint8_t smem[];
+  int* listed = reinterpret_cast<int*>(smem);  // tokens in the list
+  RowInfo* info = reinterpret_cast<RowInfo*>(smem + 16);
+  Marks<kWide> marks{reinterpret_cast<uint32_t*>(smem + SM::kMarks)};
+  uint16_t* list = reinterpret_cast<uint16_t*>(smem + SM::kList);
+  uint16_t* raw = reinterpret_cast<uint16_t*>(smem + SM::kRaw);  // the listed tokens' logits
+  float* bias = reinterpret_cast<float*>(smem + SM::kBias);      // with a.bias_start
   pdl_launch_dependents();
   pdl_wait();
-  const int row = blockIdx.x / slices, slice = blockIdx.x - row * slices;
-  const int v0 = slice * kSlice, n = min(kSlice, a.vocab - v0);
+  const int group = blockIdx.x / slices, slice = blockIdx.x - group * slices;
   const int tid = threadIdx.x;
-  const uint16_t* in = a.logits + row * a.ld + v0;
-  uint8_t* out = static_cast<uint8_t*>(a.out) + (row * a.ld_out + v0) * (a.out_fp32 ? 4 : 2);
+  // place i of the slice <-> token
+  auto token = [&](int i) { return ((i >> 6) * slices + slice) * 64 + (i & 63); };
+  auto place = [&](int id) {  // -1: not a token of the slice
+    if ((uint32_t)id >= (uint32_t)a.vocab) return -1;
+    const int block = id >> 6, turn = (int)fast_div((uint32_t)block, div_slices);
+    return block - turn * slices == slice ? turn * 64 + (id & 63) : -1;
+  };
+  const int row0 = group * rows, row1 = (int)min((int64_t)row0 + rows, (int64_t)a.S);
+  auto in_of = [&](int row) { return a.logits + row * a.ld; };
+  auto out_of = [&](int row) {
+    return static_cast<uint8_t*>(a.out) + row * a.ld_out * (a.out_fp32 ? 4 : 2);
+  };
+  auto mask_of = [&](int m) {
+    return reinterpret_cast<const uint8_t*>(a.allowed + m * a.ld_allowed);
+  };
 
-  // The thread's tokens: two runs of 8 where the rows allow 16-byte accesses,
-  // else 16 single ones a CTA's width apart.
-  const bool vec = ((reinterpret_cast<uintptr_t>(in) | reinterpret_cast<uintptr_t>(out)) & 15) == 0;
-  uint4 x[2];
-  uint32_t ok = 0xFFFFFFFFu;  // bit i: token i of the thread is allowed
-  const int m = a.allowed ? (a.allowed_row ? a.allowed_row[row] : row) : -1;
-  const uint8_t* mask = m >= 0 && m < a.n_allowed
-                            ? reinterpret_cast<const uint8_t*>(a.allowed + m * a.ld_allowed) + v0 / 8
-                            : nullptr;
-  const bool bad_mask = a.allowed && (m < -1 || m >= a.n_allowed);
-  if (bad_mask) ok = 0;
-  if (vec) {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int i = (j * kThreads + tid) * 8;
-      if (i + 8 <= n) {
-        x[j] = *reinterpret_cast<const uint4*>(in + i);
-      } else {
-        uint16_t e[8];
-#pragma unroll
-        for (int q = 0; q < 8; ++q) e[q] = i + q < n ? in[i + q] : 0;
-        x[j] = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
-      }
-      if (mask && i < n) ok &= ~(0xFFu << (8 * j)) | (uint32_t)mask[i / 8] << (8 * j);
-    }
-  } else {
-    uint16_t e[kLogPer];
-#pragma unroll
-    for (int j = 0; j < kLogPer; ++j) {
-      const int i = j * kThreads + tid;
-      e[j] = i < n ? in[i] : 0;
-      if (mask && i < n && !(mask[i >> 3] >> (i & 7) & 1)) ok &= ~(1u << j);
-    }
-    x[0] = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
-    x[1] = make_uint4(e[8] | e[9] << 16, e[10] | e[11] << 16, e[12] | e[13] << 16, e[14] | e[15] << 16);
-  }
-
-  const int r = a.row_req ? a.row_req[row] : row;
-  if (r < 0 || r >= a.n_reqs) {
-    if (r != -1 && tid == 0) record_status(a.status, kStatusTableRange);
-    return;
-  }
-  if (bad_mask && tid == 0) record_status(a.status, kStatusTableRange);
-  const Rules ru = {a.repetition ? a.repetition[r] : 1.f, a.frequency ? a.frequency[r] : 0.f,
-                    a.presence ? a.presence[r] : 0.f};
-  const bool marked = a.history || a.draft_tokens || a.bias_start;
-  if (marked) {
-    for (int i = tid; i < (kWide ? kSlice : kSlice / 2) / 4; i += kThreads)
-      reinterpret_cast<uint4*>(sm)[i] = make_uint4(0, 0, 0, 0);
-    __syncthreads();
-  }
-  if (a.history) {
-    const int len = a.history_lens[r], pl = a.prompt_lens ? a.prompt_lens[r] : 0;
-    const int len_c = (int)min((int64_t)max(len, 0), a.ld_history), pl_c = min(max(pl, 0), len_c);
-    if ((len != len_c || pl != pl_c) && tid == 0) record_status(a.status, kStatusTableRange);
-    const int32_t* h = a.history + r * a.ld_history;
-#pragma unroll 4
-    for (int i = tid; i < len_c; i += kThreads) {
-      const uint32_t v = (uint32_t)h[i] - (uint32_t)v0;  // (a foreign id becomes a large one)
-      if (v < (uint32_t)n) {
-        if (i < pl_c) marks.set(v, kMarkPrompt);
-        else marks.add(v, kMarkWritten);
-      }
-    }
-  }
-  if (a.draft_tokens) {
-    const int q0 = a.q_start[r];
-    const int64_t T = (int64_t)a.q_start[r + 1] - q0;
-    if (q0 < 0 || T < 0 || q0 + T > a.S) {
-      if (tid == 0) record_status(a.status, kStatusTableRange);
+  // token t of the row's drafted path that lies in the slice, or -1
+  auto path_token = [&](int row, const RowInfo& w, int t) {
+    if (t >= w.T || !((a.tree_mask[(int64_t)row * a.tree_words + (t >> 6)] >> (t & 63)) & 1)) return -1;
+    return place(a.draft_tokens[w.q0 + t]);
+  };
+  if (tid < row1 - row0) {
+    const int row = row0 + tid;
+    RowInfo w;
+    w.r = a.row_req ? a.row_req[row] : row;
+    w.m = a.allowed ? (a.allowed_row ? a.allowed_row[row] : row) : -1;
+    w.q0 = w.T = 0;
+    bool bad = false;
+    if (w.r < 0 || w.r >= a.n_reqs) {
+      bad = w.r != -1;
+      w.r = -1;
     } else {
-      for (int t = tid; t < min((int)T, 64 * a.tree_words); t += kThreads)
-        if ((a.tree_mask[(int64_t)row * a.tree_words + (t >> 6)] >> (t & 63)) & 1) {
-          const uint32_t v = (uint32_t)a.draft_tokens[q0 + t] - (uint32_t)v0;
-          if (v < (uint32_t)n) marks.add(v, kMarkWritten);
+      if (a.allowed && (w.m < -1 || w.m >= a.n_allowed)) {
+        bad = true;
+        w.m = -2;
+      }
+      if (a.draft_tokens) {
+        const int q0 = a.q_start[w.r];
+        const int64_t T = (int64_t)a.q_start[w.r + 1] - q0;
+        if (q0 < 0 || T < 0 || q0 + T > a.S) {
+          bad = true;
+        } else {
+          w.q0 = q0;
+          w.T = (int)min(T, (int64_t)64 * a.tree_words);
         }
+      }
     }
+    if (bad && slice == 0) record_status(a.status, kStatusTableRange);
+    info[tid] = w;
   }
-  if (a.bias_start) {
-    const int b0 = a.bias_start[r];
-    int b1 = a.bias_start[r + 1];
-    if (b0 < 0 || b1 < b0 || b1 > a.n_biases) {
-      if (tid == 0) record_status(a.status, kStatusTableRange);
-      b1 = b0;
-    }
-    // Entries of tokens named once need no order.  How often a token is named
-    // is counted in its place in the bias array.
-    int* named = reinterpret_cast<int*>(bias);
-    bool any = false;
-    for (int i = b0 + tid; i < b1; i += kThreads) {
-      const uint32_t v = (uint32_t)a.bias_ids[i] - (uint32_t)v0;
-      if (v < (uint32_t)n) {
-        named[v] = 0;
-        any = true;
+  __syncthreads();
+
+  // The thread's tokens: runs of 8 where the rows allow 16-byte accesses, else
+  // single ones a CTA's width apart.
+  auto vec_row = [&](int row) {
+    return ((reinterpret_cast<uintptr_t>(in_of(row)) | reinterpret_cast<uintptr_t>(out_of(row))) & 15) == 0;
+  };
+  auto fetch = [&](int row) {
+    RowPart<kPer> p;
+    const RowInfo w = info[row - row0];
+    const uint16_t* in = in_of(row);
+    p.ok = w.m == -2 ? 0 : 0xFFFFFFFFu;  // bit i: token i of the thread is allowed
+    const uint8_t* mask = w.m >= 0 ? mask_of(w.m) : nullptr;
+    p.path = -1;
+    if (a.draft_tokens) p.path = path_token(row, w, tid);
+    if (vec_row(row)) {
+#pragma unroll
+      for (int j = 0; j < kPer / 8; ++j) {
+        const int v = token((j * kThreads + tid) * 8);
+        if (v + 8 <= a.vocab) p.x[j] = *reinterpret_cast<const uint4*>(in + v);
+        if (mask && v < a.vocab) p.ok &= ~(0xFFu << (8 * j)) | (uint32_t)mask[v / 8] << (8 * j);
+      }
+    } else {
+      uint32_t* x2 = reinterpret_cast<uint32_t*>(p.x);
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const int v = token(j * kThreads + tid);
+        const uint32_t e = v < a.vocab ? in[v] : 0;
+        x2[j / 2] = j & 1 ? x2[j / 2] | e << 16 : e;
+        if (mask && v < a.vocab && !(mask[v >> 3] >> (v & 7) & 1)) p.ok &= ~(1u << j);
       }
     }
-    if (__syncthreads_or(any)) {
+    return p;
+  };
+  auto enlist = [&](int v, uint32_t before) {
+    if (before == 0) list[atomicAdd(listed, 1)] = (uint16_t)v;
+  };
+
+  // Marks and list of request r's text and biases in the slice; starts and ends
+  // with the CTA's threads together.
+  auto mark_request = [&](int r) {
+    __syncthreads();
+    for (int i = tid; i < kSlice * (kWide ? 4 : 2) / 16; i += kThreads)
+      reinterpret_cast<uint4*>(smem + SM::kMarks)[i] = make_uint4(0, 0, 0, 0);
+    if (tid == 0) *listed = 0;
+    __syncthreads();
+    if (a.history) {
+      const int len = a.history_lens[r], pl = a.prompt_lens ? a.prompt_lens[r] : 0;
+      const int len_c = (int)min((int64_t)max(len, 0), a.ld_history), pl_c = min(max(pl, 0), len_c);
+      if ((len != len_c || pl != pl_c) && tid == 0) record_status(a.status, kStatusTableRange);
+      const int32_t* h = a.history + r * a.ld_history;
+      auto mark = [&](int i, int id) {
+        const int v = place(id);
+        if (v >= 0) enlist(v, i < pl_c ? marks.set(v, kMarkPrompt) : marks.add(v, kMarkWritten));
+      };
+      const int quads = (reinterpret_cast<uintptr_t>(h) & 15) ? 0 : len_c / 4;
+#pragma unroll 4
+      for (int i = tid; i < quads; i += kThreads) {
+        const int4 id = reinterpret_cast<const int4*>(h)[i];
+        mark(4 * i, id.x);
+        mark(4 * i + 1, id.y);
+        mark(4 * i + 2, id.z);
+        mark(4 * i + 3, id.w);
+      }
+      for (int i = 4 * quads + tid; i < len_c; i += kThreads) mark(i, h[i]);
+    }
+    if (a.bias_start) {
+      const int b0 = a.bias_start[r];
+      int b1 = a.bias_start[r + 1];
+      if (b0 < 0 || b1 < b0 || b1 > a.n_biases) {
+        if (tid == 0) record_status(a.status, kStatusTableRange);
+        b1 = b0;
+      }
+      // Entries of tokens named once need no order.  How often a token is named
+      // is counted in its place in the bias array.
+      int* named = reinterpret_cast<int*>(bias);
+      bool any = false;
       for (int i = b0 + tid; i < b1; i += kThreads) {
-        const uint32_t v = (uint32_t)a.bias_ids[i] - (uint32_t)v0;
-        if (v < (uint32_t)n) {
-          atomicAdd(named + v, 1);
-          marks.set(v, kMarkBias);
+        const int v = place(a.bias_ids[i]);
+        if (v >= 0) {
+          named[v] = 0;
+          any = true;
         }
       }
-      __syncthreads();
-      bool again = false;
-      for (int i = b0 + tid; i < b1; i += kThreads) {
-        const uint32_t v = (uint32_t)a.bias_ids[i] - (uint32_t)v0;
-        if (v < (uint32_t)n) {
-          if (named[v] == 1) bias[v] = a.bias_values[i];  // no other entry looks at it
-          else again = true;
-        }
-      }
-      if (__syncthreads_or(again)) {
-        // Some token is named more than once: the list anew, in order, by one
-        // warp, entries of the same token among its 32 added in order too.
+      if (__syncthreads_or(any)) {
         for (int i = b0 + tid; i < b1; i += kThreads) {
-          const uint32_t v = (uint32_t)a.bias_ids[i] - (uint32_t)v0;
-          if (v < (uint32_t)n) bias[v] = 0.f;
+          const int v = place(a.bias_ids[i]);
+          if (v >= 0) {
+            atomicAdd(named + v, 1);
+            enlist(v, marks.set(v, kMarkBias));
+          }
         }
         __syncthreads();
-        if (tid < 32) {
-          for (int base = b0; base < b1; base += 32) {
-            const int i = base + tid;
-            const uint32_t v = i < b1 ? (uint32_t)a.bias_ids[i] - (uint32_t)v0 : 0xFFFFFFFFu;
-            const bool here = v < (uint32_t)n;
-            const float y = here ? a.bias_values[i] : 0.f;
-            const unsigned same = __match_any_sync(0xffffffffu, here ? (int)v : -1 - tid);
-            const bool lead = here && (same & ((1u << tid) - 1)) == 0;
-            float s = lead ? bias[v] : 0.f;
-            for (int j = 0; j < 32; ++j) {
-              const float z = __shfl_sync(0xffffffffu, y, j);
-              if (same >> j & 1) s += z;
+        bool again = false;
+        for (int i = b0 + tid; i < b1; i += kThreads) {
+          const int v = place(a.bias_ids[i]);
+          if (v >= 0) {
+            if (named[v] == 1) bias[v] = a.bias_values[i];  // no other entry looks at it
+            else again = true;
+          }
+        }
+        if (__syncthreads_or(again)) {
+          // Some token is named more than once: the list anew, in order, by one
+          // warp, entries of the same token among its 32 added in order too.
+          for (int i = b0 + tid; i < b1; i += kThreads) {
+            const int v = place(a.bias_ids[i]);
+            if (v >= 0) bias[v] = 0.f;
+          }
+          __syncthreads();
+          if (tid < 32) {
+            for (int base = b0; base < b1; base += 32) {
+              const int i = base + tid;
+              const int v = i < b1 ? place(a.bias_ids[i]) : -1;
+              const bool here = v >= 0;
+              const float y = here ? a.bias_values[i] : 0.f;
+              const unsigned same = __match_any_sync(0xffffffffu, here ? v : -1 - tid);
+              const bool lead = here && (same & ((1u << tid) - 1)) == 0;
+              float s = lead ? bias[v] : 0.f;
+              for (int j = 0; j < 32; ++j) {
+                const float z = __shfl_sync(0xffffffffu, y, j);
+                if (same >> j & 1) s += z;
+              }
+              if (lead) bias[v] = s;
+              __syncwarp();
             }
-            if (lead) bias[v] = s;
-            __syncwarp();
           }
         }
       }
     }
-  }
-  if (marked) __syncthreads();
+    __syncthreads();
+  };
 
-  if (vec) {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int i = (j * kThreads + tid) * 8;
-      if (i >= n) break;
-      const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
-      float f[8];
-#pragma unroll
-      for (int q = 0; q < 8; ++q)
-        f[q] = __uint_as_float(q & 1 ? w[q >> 1] & 0xFFFF0000u : w[q >> 1] << 16);
-      if (marked && marks.any8(i)) {
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const uint32_t mk = marks.get(i + q);
-          if (mk) f[q] = apply_rules(f[q], mk, bias + i + q, ru);
-        }
+  const bool in_place = a.out == a.logits;
+  const bool marked = a.history || a.draft_tokens || a.bias_start;
+  RowPart<kPer> next = fetch(row0);
+  int made = -1, own = 0;  // the request whose marks are there; its listed tokens
+  float rep = 1.f, freq = 0.f, pres = 0.f;
+  for (int row = row0; row < row1; ++row) {
+    const RowPart<kPer> p = next;
+    const RowInfo w = info[row - row0];
+    if (row + 1 < row1) next = fetch(row + 1);
+    if (w.r < 0) continue;
+    // (paths have up to 256 tokens: two a thread where a CTA has 128)
+    int far = -1;
+    if (marked) {
+      if (w.r != made) {
+        if (a.repetition) rep = a.repetition[w.r];
+        if (a.frequency) freq = a.frequency[w.r];
+        if (a.presence) pres = a.presence[w.r];
+        mark_request(w.r);
+        made = w.r;
+        own = *listed;
+        __syncthreads();  // own was read
       }
-#pragma unroll
-      for (int q = 0; q < 8; ++q) f[q] = ok >> (8 * j + q) & 1 ? f[q] : -INFINITY;
-      if (i + 8 <= n) {
-        if (a.out_fp32) {
-          float4* o = reinterpret_cast<float4*>(out) + i / 4;
-          o[0] = make_float4(f[0], f[1], f[2], f[3]);
-          o[1] = make_float4(f[4], f[5], f[6], f[7]);
-        } else {
-          reinterpret_cast<uint4*>(out)[i / 8] =
-              make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                         pack_bf16x2(f[6], f[7]));
-        }
-      } else {
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-          if (i + q < n) {
-            if (a.out_fp32) reinterpret_cast<float*>(out)[i + q] = f[q];
-            else reinterpret_cast<uint16_t*>(out)[i + q] = f_to_bf16(f[q]);
-          }
+      if (a.draft_tokens) {
+        if (kThreads < kMaxTreeTokens) far = path_token(row, w, tid + kThreads);
+        if (p.path >= 0) enlist(p.path, marks.add(p.path, kMarkWritten));
+        if (far >= 0) enlist(far, marks.add(far, kMarkWritten));
+      }
+      if (in_place) {
+        __syncthreads();
+        const int many = *listed;
+        for (int i = tid; i < many; i += kThreads) raw[i] = in_of(row)[token(list[i])];
+        __syncthreads();  // before the stream writes over them
       }
     }
-  } else {
-    const uint32_t w[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
+
+    uint8_t* out = out_of(row);
+    if (vec_row(row)) {
 #pragma unroll
-    for (int j = 0; j < kLogPer; ++j) {
-      const int i = j * kThreads + tid;
-      if (i >= n) break;
-      float f = __uint_as_float(j & 1 ? w[j >> 1] & 0xFFFF0000u : w[j >> 1] << 16);
-      const uint32_t mk = marked ? marks.get(i) : 0;
-      if (mk) f = apply_rules(f, mk, bias + i, ru);
-      if (!(ok >> j & 1)) f = -INFINITY;
-      if (a.out_fp32) reinterpret_cast<float*>(out)[i] = f;
-      else reinterpret_cast<uint16_t*>(out)[i] = f_to_bf16(f);
+      for (int j = 0; j < kPer / 8; ++j) {
+        const int v = token((j * kThreads + tid) * 8);
+        if (v >= a.vocab) break;
+        const uint32_t ok = p.ok >> (8 * j);
+        if (v + 8 <= a.vocab) {
+          const uint32_t e[4] = {allow2(p.x[j].x, ok), allow2(p.x[j].y, ok >> 2),
+                                 allow2(p.x[j].z, ok >> 4), allow2(p.x[j].w, ok >> 6)};
+          if (a.out_fp32) {
+            uint4* o = reinterpret_cast<uint4*>(out) + v / 4;
+            o[0] = make_uint4(e[0] << 16, e[0] & 0xFFFF0000u, e[1] << 16, e[1] & 0xFFFF0000u);
+            o[1] = make_uint4(e[2] << 16, e[2] & 0xFFFF0000u, e[3] << 16, e[3] & 0xFFFF0000u);
+          } else {
+            reinterpret_cast<uint4*>(out)[v / 8] = make_uint4(e[0], e[1], e[2], e[3]);
+          }
+        } else {  // the row's last tokens
+          for (int q = 0; v + q < a.vocab; ++q) {
+            const uint32_t e = ok >> q & 1 ? in_of(row)[v + q] : 0xFF80u;
+            if (a.out_fp32) reinterpret_cast<uint32_t*>(out)[v + q] = e << 16;
+            else reinterpret_cast<uint16_t*>(out)[v + q] = (uint16_t)e;
+          }
+        }
+      }
+    } else {
+      const uint32_t* x2 = reinterpret_cast<const uint32_t*>(p.x);
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const int v = token(j * kThreads + tid);
+        if (v >= a.vocab) break;
+        const uint32_t e = p.ok >> j & 1 ? (j & 1 ? x2[j / 2] >> 16 : x2[j / 2] & 0xFFFF) : 0xFF80u;
+        if (a.out_fp32) reinterpret_cast<uint32_t*>(out)[v] = e << 16;
+        else reinterpret_cast<uint16_t*>(out)[v] = (uint16_t)e;
+      }
+    }
+
+    if (marked) {
+      __syncthreads();  // the stream is through, the list complete
+      const int many = *listed;
+      const uint16_t* in = in_of(row);
+      const uint8_t* mask = w.m >= 0 ? mask_of(w.m) : nullptr;
+      for (int i = tid; i < many; i += kThreads) {
+        const int at = list[i], v = token(at);
+        const uint32_t mk = marks.get(at), times = mk / kMarkWritten;
+        float x = bf16_to_f(in_place ? raw[i] : in[v]);
+        if (times || (mk & kMarkPrompt)) x = x > 0.f ? x / rep : x * rep;
+        if (times) x = x - freq * (float)times - pres;
+        if (mk & kMarkBias) x += bias[at];
+        if (w.m == -2 || (mask && !(mask[v >> 3] >> (v & 7) & 1))) x = -INFINITY;
+        if (a.out_fp32) reinterpret_cast<float*>(out)[v] = x;
+        else reinterpret_cast<uint16_t*>(out)[v] = f_to_bf16(x);
+      }
+      if (a.draft_tokens && row + 1 < row1) {
+        __syncthreads();
+        if (p.path >= 0) marks.add(p.path, 0u - kMarkWritten);
+        if (far >= 0) marks.add(far, 0u - kMarkWritten);
+        if (tid == 0) *listed = own;
+        __syncthreads();
+      }
     }
   }
 }
 
-template <int kThreads, bool kWide>
-static cudaError_t launch_logits(const LogitsArgs& a, cudaStream_t st) {
-  constexpr int kSlice = kThreads * kLogPer;
-  const int smem = kSlice * (kWide ? 4 : 2) + (a.bias_start ? kSlice * 4 : 0);
+template <int kThreads, int kPer, bool kWide>
+static cudaError_t launch_logits(const LogitsArgs& a, int num_sms, cudaStream_t st) {
+  using SM = LogitsSmem<kThreads, kPer, kWide>;
+  const int smem = SM::bytes(a.bias_start != nullptr);
   if (smem > 48 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(process_logits_kernel<kThreads, kWide>,
+    cudaError_t e = cudaFuncSetAttribute(process_logits_kernel<kThreads, kPer, kWide>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
   }
-  const int slices = (a.vocab + kSlice - 1) / kSlice;
-  return launch_k(process_logits_kernel<kThreads, kWide>, dim3((unsigned)((int64_t)a.S * slices)),
-                  dim3(kThreads), smem, st, a, slices);
+  // as many rows a CTA as leave four CTAs an SM
+  const int slices = (a.vocab + SM::kSlice - 1) / SM::kSlice;
+  const int64_t parts = (int64_t)a.S * slices;
+  const int rows = (int)std::max<int64_t>(1, std::min<int64_t>(kLogRows, parts / (4 * num_sms)));
+  const int64_t ctas = (int64_t)((a.S + rows - 1) / rows) * slices;
+  return launch_k(process_logits_kernel<kThreads, kPer, kWide>, dim3((unsigned)ctas), dim3(kThreads),
+                  smem, st, a, slices, make_fastdiv((uint32_t)slices), rows);
 }
 
 cudaError_t launch_process_logits(const LogitsArgs& a, int num_sms, cudaStream_t st) {
   const bool wide = a.history && a.ld_history + kMaxTreeTokens > kNarrowText;
-  if ((int64_t)a.S * ((a.vocab + 8191) / 8192) >= num_sms)
-    return wide ? launch_logits<512, true>(a, st) : launch_logits<512, false>(a, st);
-  return wide ? launch_logits<128, true>(a, st) : launch_logits<128, false>(a, st);
+  if ((int64_t)a.S * ((a.vocab + 4095) / 4096) < num_sms)
+    return wide ? launch_logits<128, 16, true>(a, num_sms, st)
+                : launch_logits<128, 16, false>(a, num_sms, st);
+  if (!a.history || a.ld_history < 2048) return launch_logits<256, 16, false>(a, num_sms, st);
+  return wide ? launch_logits<256, 32, true>(a, num_sms, st)
+              : launch_logits<256, 32, false>(a, num_sms, st);
 }
 
 }  // namespace tpk

@@ -325,8 +325,8 @@ tp_status tp_process_logits(const tp_model* m, const tp_bf16* logits, int64_t ld
     a.allowed_row = r.allowed_row;
     a.status = m->status;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return cuda_status(launch(m, "process_logits", st, [&] {
-      return launch_process_logits(a, m->num_sms, st); }));
+    return cuda_status(
+        launch(m, "process_logits", st, [&] { return launch_process_logits(a, m->num_sms, st); }));
   });
 }
 
