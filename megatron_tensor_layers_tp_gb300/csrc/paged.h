@@ -52,12 +52,6 @@ struct CacheAppendArgs {
 };
 cudaError_t launch_cache_append(const CacheAppendArgs& a, cudaStream_t st);
 
-// An item cut between CTAs, as the CTA that opened it leaves it: its first
-// row (token q0, row row0 of the sequence's), rows, KV head, the slot of the
-// CTA's piece and the CTA of the last piece (-1: no item was cut).
-struct TreeSplit {
-  int q0, row0, rows, g, slot, last;
-};
 struct TreeAttnArgs {
   CUtensorMap tmK, tmV;       // (d, page_size, copies * n_pages * kv_r), box (64, box_rows, 1)
   CUtensorMap tmQ;            // (d, n_heads, n_tokens), box (64, group, tile_toks)
@@ -81,25 +75,14 @@ struct TreeAttnArgs {
   int grid;
   float* partials;            // [grid][2][d / 4][128][4]
   float2* ml;                 // [grid][2][128]
-  TreeSplit* splits;          // [grid]
+  int* tickets;               // [n_seqs][n_kv][q_tiles_max], zero on entry and exit
+  int q_tiles_max;            // query tiles of max_new tokens
   int* status;
-};
-struct TreeJoinArgs {
-  const float* partials;
-  const float2* ml;
-  const TreeSplit* splits;
-  uint16_t* o;
-  int64_t ld_o;
-  int group;
-  FastDiv div_group;
 };
 constexpr int kTreeRows = 128;  // query rows (tokens x Q heads of a KV head) of a tile
 constexpr int kTreeKeys = 64;   // keys of a tile
 constexpr int kTreeLoaders = 4;
 cudaError_t launch_tree_attn(const TreeAttnArgs& a, cudaStream_t st);
-// max_rows: no query tile has more rows
-cudaError_t launch_tree_join(const TreeJoinArgs& a, int head_dim, int grid, int max_rows,
-                             cudaStream_t st);
 
 struct LogitsArgs {
   const uint16_t* logits;

@@ -49,16 +49,22 @@ bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
   return x < y + (uintptr_t)b_bytes && y < x + (uintptr_t)a_bytes;
 }
 
-// Workspace regions: the step tables' ticket, then tree attention's pieces,
-// their (m, l) and the list of cut items.
+// Tokens of a query tile, and query tiles of n new tokens.
+int tile_tokens(const tp_model* m) { return kTreeRows / (m->cfg.n_heads / m->cfg.n_kv_heads); }
+int query_tiles(const tp_model* m, int n) { return cdiv(n, tile_tokens(m)); }
+
+// Workspace regions: the step tables' ticket, then tree attention's tickets,
+// pieces and their (m, l).  (Steps of more new tokens than tree attention
+// takes, prompts, only use the first.)
 struct StepWs {
-  size_t splits, ml, partials, total;
+  size_t tickets, ml, partials, total;
 };
-StepWs step_ws(const tp_model* m) {
+StepWs step_ws(const tp_model* m, int n_seqs, int max_new) {
   StepWs w;
   const size_t pieces = (size_t)m->num_sms * 2 * kTreeRows;
-  w.splits = kStepTicketBytes;
-  w.ml = align_up(w.splits + m->num_sms * sizeof(TreeSplit), 256);
+  const int tiles = query_tiles(m, std::min(max_new, kMaxTreeTokens));
+  w.tickets = kStepTicketBytes;
+  w.ml = align_up(w.tickets + (size_t)n_seqs * m->cfg.n_kv_heads * tiles * sizeof(int), 256);
   w.partials = align_up(w.ml + pieces * sizeof(float2), 256);
   w.total = w.partials + pieces * m->cfg.head_dim * sizeof(float);
   return w;
@@ -75,7 +81,7 @@ extern "C" {
 
 size_t tp_step_workspace_bytes(const tp_model* m, int32_t n_seqs, int32_t max_new) {
   if (!m || n_seqs < 1 || n_seqs > kMaxStepSeqs || max_new < 0) return 0;
-  return step_ws(m).total;
+  return step_ws(m, n_seqs, max_new).total;
 }
 
 tp_status tp_step_tables(const tp_model* m, const tp_pages_t* pages, const tp_step_t* step,
@@ -243,25 +249,22 @@ tp_status tp_tree_attention(const tp_model* m, const tp_bf16* q, int64_t ld_q, t
     a.head_dim = c.head_dim;
     a.div_group = make_fastdiv((uint32_t)a.group);
     a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)c.head_dim));
-    a.tile_toks = kTreeRows / a.group;
+    a.tile_toks = tile_tokens(m);
     a.tile_rows = a.tile_toks * a.group;
     a.kv_once = step->max_new <= a.tile_toks;
     if (!make_tmap(&a.tmQ, q, d, c.n_heads, step->n_tokens, d * 2, ld_q * 2, a.group, nullptr,
                    a.tile_toks))
       return TP_ERR_CUDA;
     a.grid = m->num_sms;
-    const StepWs w = step_ws(m);
+    const StepWs w = step_ws(m, step->n_seqs, step->max_new);
     uint8_t* base = static_cast<uint8_t*>(ws);
-    a.splits = reinterpret_cast<TreeSplit*>(base + w.splits);
+    a.tickets = reinterpret_cast<int*>(base + w.tickets);
+    a.q_tiles_max = query_tiles(m, step->max_new);
     a.ml = reinterpret_cast<float2*>(base + w.ml);
     a.partials = reinterpret_cast<float*>(base + w.partials);
     a.status = m->status;
-    const TreeJoinArgs j = {a.partials, a.ml, a.splits, o, ld_o, a.group, a.div_group};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    TP_CHECK_CUDA(launch(m, "tree_attn", st, [&] { return launch_tree_attn(a, st); }));
-    return cuda_status(launch(m, "tree_join", st, [&] {
-      return launch_tree_join(j, c.head_dim, a.grid, std::min(step->max_new, a.tile_toks) * a.group, st);
-    }));
+    return cuda_status(launch(m, "tree_attn", st, [&] { return launch_tree_attn(a, st); }));
   });
 }
 

@@ -17,10 +17,11 @@
 // item's fixed work counted as kItemCost tiles more, split evenly over one CTA
 // per SM.  A CTA finds its range from the lengths on
 // the GPU, so a captured launch follows them.  An item cut between CTAs leaves
-// unnormalised fp32 pieces, and a second small kernel joins them in key order
-// (deterministic).  Measured against the join by the last CTA to finish a
-// piece: that CTA alone pulls every piece (64 KB each at 128 rows), 268 us
-// for prompt chunks instead of @@ us.
+// unnormalised fp32 pieces, and the last CTA to finish one (a ticket, no
+// waiting) joins them in key order: deterministic.  The pieces lie [4 elements]
+// [row], so that lane = row reads and writes whole lines with every load in
+// flight (a second kernel for the join cost 3-5 us a call; the join with rows
+// of pieces and loads one after another, 50).
 //
 // Roles of the 16 warps:
 //   warps 0-3  : K and V tiles by TMA into a ring, through the page table, each
@@ -78,11 +79,11 @@ constexpr int kItemCost = 8;             // an item's fixed work in key tiles
 constexpr int kMaxGrid = 1024;
 
 // One CTA's part of an item: key tiles [k0, k1) of nt of (sequence b, KV head
-// g, query tile qi), the sequence's first row, new tokens and old length.
-// opens: the CTA of the item's last part when this part is the first of
-// several, else -1.  k1 = 0: no more parts.
+// g, query tile qi), the sequence's first row, new tokens and old length; of an
+// item cut between CTAs, the first and last CTA that have a part, and where in
+// its two piece slots the first has it.  k1 = 0: no more parts.
 struct Seg {
-  int b, g, qi, k0, k1, nt, q0, T, old, opens;
+  int b, g, qi, k0, k1, nt, q0, T, old, first, last, slot;
 };
 
 template <int D>
@@ -106,6 +107,7 @@ struct TreeCtl {
   long long total, u0, x0, x1;
   int b0;
   int poison[2];
+  int last;
   uint32_t tmem;
 };
 static_assert(sizeof(TreeCtl) <= 1024, "control block");
@@ -181,7 +183,11 @@ struct SegIter {
       sg.q0 = s.q0;
       sg.T = s.T;
       sg.old = s.old;
-      sg.opens = sg.k0 == 0 && sg.k1 < s.nt ? owner_of(begin + cost - 1, W, G) : -1;
+      if (sg.k1 - sg.k0 < s.nt) {
+        sg.first = owner_of(begin + kItemCost, W, G);
+        sg.last = owner_of(begin + cost - 1, W, G);
+        sg.slot = range_at(sg.first, W, G) < begin ? 1 : 0;  // after the end of another item
+      }
       return sg;
     }
     Seg none;
@@ -251,6 +257,58 @@ __device__ __forceinline__ uint32_t drop_nonfinite(uint32_t x) {
   if ((x & 0x7F80u) == 0x7F80u) x &= 0xFFFF0000u;
   if ((x & 0x7F800000u) == 0x7F800000u) x &= 0x0000FFFFu;
   return x;
+}
+
+// Joins the pieces of an item, in key order, into the rows of o in shared
+// memory.  Eight warps share the blocks of 32 rows: lane = row, and a warp takes
+// groups of 4 elements, eight at a time, with the loads of two pieces in flight.
+// (Not inlined: the softmax loops stay together in the instruction cache.)
+template <int D>
+__device__ __noinline__ void join_pieces(const TreeAttnArgs& a, const Seg& s, int rows, int w, int lane,
+                                         uint8_t* sOut) {
+  const int blocks = (rows + 31) >> 5;
+  auto piece = [&](int p) { return (int64_t)p * 2 + (p == s.first ? s.slot : 0); };
+  constexpr int kPer = 8, kTurns = D / 4 / kPer;  // groups at a time; turns of a block
+  for (int t = w; t < blocks * kTurns; t += 8) {
+    const int r = (t % blocks) * 32 + lane, g0 = t / blocks * kPer;
+    const bool on = r < rows;
+    float M = -INFINITY, L = 0.f;
+    float4 o[kPer];
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) o[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+    // (the running maximum: one round of loads a piece, not two)
+#pragma unroll 2
+    for (int p = s.first; p <= s.last; ++p) {
+      const int64_t at = piece(p);
+      const float2 ml = on ? __ldcg(&a.ml[at * kTreeRows + r]) : make_float2(-INFINITY, 0.f);
+      const float4* src = reinterpret_cast<const float4*>(a.partials + at * kTreeRows * D) + r;
+      float4 y[kPer];
+#pragma unroll
+      for (int q = 0; q < kPer; ++q)
+        y[q] = on ? __ldcg(src + (g0 + q) * kTreeRows) : make_float4(0.f, 0.f, 0.f, 0.f);
+      const float Mn = fmaxf(M, ml.x);
+      const float u = M == -INFINITY ? 0.f : ex2_approx(M - Mn);
+      const float v = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - Mn);
+      M = Mn;
+      L = L * u + ml.y * v;
+#pragma unroll
+      for (int q = 0; q < kPer; ++q) {
+        o[q].x = o[q].x * u + y[q].x * v;
+        o[q].y = o[q].y * u + y[q].y * v;
+        o[q].z = o[q].z * u + y[q].z * v;
+        o[q].w = o[q].w * u + y[q].w * v;
+      }
+    }
+    const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
+    if (on) {
+#pragma unroll
+      for (int q = 0; q < kPer; q += 2)  // the 16-byte chunks of a row are swizzled by row
+        *reinterpret_cast<uint4*>(sOut + r * D * 2 + ((((g0 + q) >> 1) ^ (r & 7)) << 4)) =
+            make_uint4(pack_p(o[q].x * inv, o[q].y * inv), pack_p(o[q].z * inv, o[q].w * inv),
+                       pack_p(o[q + 1].x * inv, o[q + 1].y * inv),
+                       pack_p(o[q + 1].z * inv, o[q + 1].w * inv));
+    }
+  }
 }
 
 template <int D>
@@ -562,7 +620,6 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
     const uint32_t tS = tmem + lanes, tO = tmem + lanes + 256 + grp * D;
     uint32_t gt0 = 0;  // key tiles before this part
     uint32_t par = 0;  // bit k: tiles taken from S buffer k, mod 2
-    TreeSplit split = {0, 0, 0, 0, 0, -1};
     for (uint32_t seg = 0;; ++seg) {
       const Seg s = fetch(seg);
       // all of them go on, or none: they meet at named barriers below
@@ -698,8 +755,7 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
         float w0 = ml0.x == -INFINITY ? 0.f : ex2_approx(ml0.x - M);
         float w1 = ml1.x == -INFINITY ? 0.f : ex2_approx(ml1.x - M);
         const float L = ml0.y * w0 + ml1.y * w1;
-        const int slot = s.k0 > 0 || seg == 0 ? 0 : 1;  // a later piece is its CTA's first
-        const int64_t piece = (int64_t)c * 2 + slot;
+        const int64_t piece = (int64_t)c * 2 + (!whole && c == s.first ? s.slot : 0);
         if (!whole && live && grp == 0) a.ml[piece * kTreeRows + r] = make_float2(M, L);
         if (whole) {
           const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
@@ -739,12 +795,28 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
               dst[e * kTreeRows] = make_float4(o0[4 * e], o0[4 * e + 1], o0[4 * e + 2], o0[4 * e + 3]);
           }
         }
-        if (s.opens >= 0 && tid == 0) split = {s.q0, row0, rows, s.g, slot, s.opens};
       }
       tc_fence_before();
       if (tid == 0) ctl.poison[(seg + 1) & 1] = 0;
-      bar_sync(1, kTreeSoftmax);  // O was read, the rows are in shared memory
-      if (whole) {
+      bar_sync(1, kTreeSoftmax);  // O was read; the rows are in shared memory, or the pieces written
+      bool finish = whole;
+      if (!whole) {
+        if (tid == 0) {
+          fence_acq_rel_gpu();
+          int* ticket = a.tickets + ((int64_t)s.b * a.n_kv + s.g) * a.q_tiles_max + s.qi;
+          const bool last = atomicAdd(ticket, 1) == s.last - s.first;
+          if (last) *ticket = 0;
+          fence_acq_rel_gpu();
+          ctl.last = last;
+        }
+        bar_sync(1, kTreeSoftmax);
+        finish = ctl.last != 0;
+        if (finish) {
+          join_pieces<D>(a, s, rows, tid >> 5, lane, sOut);
+          bar_sync(1, kTreeSoftmax);
+        }
+      }
+      if (finish) {
         const int ch = tid % (D / 8);
         for (int rr = tid / (D / 8); rr < rows; rr += kTreeSoftmax / (D / 8)) {
           const int i = (int)fast_div((uint32_t)(row0 + rr), a.div_group);
@@ -757,69 +829,11 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
       __syncwarp();
       if (lane == 0) done_with(seg);
     }
-    if (tid == 0) a.splits[c] = split;
   }
   __syncthreads();
   if (warp == 4) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
-  }
-}
-
-// Joins the pieces of the items cut between CTAs, in key order: block (c, y)
-// takes rows [32 y, 32 y + 32) of the item that CTA c opened, lane = row, a
-// warp every eighth group of 4 elements.  The pieces come from L2 as whole
-// lines, every load independent of the others; the rows leave through shared
-// memory as whole lines too.
-template <int D>
-__global__ void __launch_bounds__(256) tree_join_kernel(const TreeJoinArgs a) {
-  __shared__ uint2 out[32][D / 4 + 1];
-  pdl_launch_dependents();
-  pdl_wait();
-  const TreeSplit s = a.splits[blockIdx.x];
-  const int r0 = blockIdx.y * 32;
-  if (s.last < 0 || r0 >= s.rows) return;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = r0 + lane;
-  const bool live = r < s.rows;
-  auto piece = [&](int p) {  // the later pieces are their CTA's first
-    return (int64_t)p * 2 + (p == (int)blockIdx.x ? s.slot : 0);
-  };
-  float M = -INFINITY;
-#pragma unroll 8
-  for (int p = blockIdx.x; p <= s.last; ++p)
-    M = fmaxf(M, live ? __ldcg(&a.ml[piece(p) * kTreeRows + r]).x : -INFINITY);
-  constexpr int kPer = D / 32;  // groups of 4 elements of a warp
-  float L = 0.f;
-  float4 o[kPer];
-#pragma unroll
-  for (int q = 0; q < kPer; ++q) o[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int p = blockIdx.x; p <= s.last; ++p) {
-    const int64_t at = piece(p);
-    const float2 ml = live ? __ldcg(&a.ml[at * kTreeRows + r]) : make_float2(-INFINITY, 0.f);
-    const float w = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
-    L += ml.y * w;
-    const float4* src = reinterpret_cast<const float4*>(a.partials + at * kTreeRows * D) + r;
-#pragma unroll
-    for (int q = 0; q < kPer; ++q) {
-      const float4 y = live ? __ldcg(src + (warp + 8 * q) * kTreeRows) : make_float4(0.f, 0.f, 0.f, 0.f);
-      o[q].x += y.x * w;
-      o[q].y += y.y * w;
-      o[q].z += y.z * w;
-      o[q].w += y.w * w;
-    }
-  }
-  const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
-#pragma unroll
-  for (int q = 0; q < kPer; ++q)
-    out[lane][warp + 8 * q] =
-        make_uint2(pack_p(o[q].x * inv, o[q].y * inv), pack_p(o[q].z * inv, o[q].w * inv));
-  __syncthreads();
-  const int e = threadIdx.x % (D / 4), end = min(s.rows - r0, 32);
-  for (int rr = threadIdx.x / (D / 4); rr < end; rr += 256 / (D / 4)) {
-    const int i = (int)fast_div((uint32_t)(s.row0 + r0 + rr), a.div_group);
-    const int h = s.row0 + r0 + rr - i * a.group;
-    *reinterpret_cast<uint2*>(a.o + (s.q0 + i) * a.ld_o + (s.g * a.group + h) * D + 4 * e) = out[rr][e];
   }
 }
 
@@ -841,13 +855,6 @@ static cudaError_t launch_tree(const TreeAttnArgs& a, cudaStream_t st) {
 
 cudaError_t launch_tree_attn(const TreeAttnArgs& a, cudaStream_t st) {
   return a.head_dim == 128 ? launch_tree<128>(a, st) : launch_tree<64>(a, st);
-}
-
-cudaError_t launch_tree_join(const TreeJoinArgs& a, int head_dim, int grid, int max_rows,
-                             cudaStream_t st) {
-  const dim3 g(grid, (max_rows + 31) / 32);
-  return head_dim == 128 ? launch_k(tree_join_kernel<128>, g, dim3(256), 0, st, a)
-                         : launch_k(tree_join_kernel<64>, g, dim3(256), 0, st, a);
 }
 
 }  // namespace tpk
