@@ -644,46 +644,54 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
           for (int e = 0; e < 64; ++e)
             x[e >> 5][e & 31] = (vis[e >> 5] >> (e & 31) & 1) ? x[e >> 5][e & 31] : -INFINITY;
         }
-        float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        // The probabilities relative to the maximum so far, before the tile's
+        // own maximum is known: most tiles do not raise it by 2^8, and neither
+        // chain then waits for the other.
+        float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, sums[4];
+        uint32_t y[2][16];
+        auto probabilities = [&](float sub) {
 #pragma unroll
-        for (int e = 0; e < 64; ++e) tops[e & 3] = fmaxf(tops[e & 3], x[e >> 5][e & 31]);
-        const float top =
-            fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * a.scale_log2;
-        const bool rise = top > m + kRescaleLog2 || (m == -INFINITY && top > m);
-        const float mn = rise ? top : m;
-        if (i >= 2 && __any_sync(0xffffffffu, rise)) {
-          const float al = rise ? ex2_approx(m - mn) : 1.f;  // m = -inf: 0
-          const int k = (i - 2) & 3;
-          warp_wait(&ctl.pv_done[k], (par >> k & 1) ^ 1);
-          tc_fence_after();
-#pragma unroll
-          for (int q = 0; q < D / 16; ++q) {
-            float o[16];
-            uint32_t y[16];
-            tmem_ld16(tO + 16 * q, o);
-            tmem_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(o[e] * al);
-            tmem_st16(tO + 16 * q, y);
-          }
-          l *= al;
-        }
-        m = mn;
-        // masked scores: exp2(-inf - sub) = 0
-        const float sub = m == -INFINITY ? 0.f : m;
-        float sums[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          uint32_t y[16];
+          for (int q = 0; q < 4; ++q) sums[q] = 0.f;
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
-            x[q][e] = ex2_approx(fmaf(x[q][e], a.scale_log2, -sub));
-            sums[e & 3] += x[q][e];
+            const float p0 = ex2_approx(fmaf(x[e >> 4][2 * (e & 15)], a.scale_log2, -sub));
+            const float p1 = ex2_approx(fmaf(x[e >> 4][2 * (e & 15) + 1], a.scale_log2, -sub));
+            sums[e & 3] += p0 + p1;
+            y[e >> 4][e & 15] = pack_p(p0, p1);
           }
+        };
+        probabilities(m);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) y[e] = pack_p(x[q][2 * e], x[q][2 * e + 1]);
-          tmem_st16(t + 16 * q, y);
+        for (int e = 0; e < 32; ++e)
+          tops[e & 3] = fmaxf(tops[e & 3], fmaxf(x[e >> 4][2 * (e & 15)], x[e >> 4][2 * (e & 15) + 1]));
+        const float top =
+            fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * a.scale_log2;
+        const bool rise = top > m + kRescaleLog2 || m == -INFINITY;
+        if (__any_sync(0xffffffffu, rise)) {
+          const float mn = rise ? top : m;
+          if (i >= 2) {
+            const float al = rise && top > m ? ex2_approx(m - mn) : 1.f;  // m = -inf: 0
+            const int k = (i - 2) & 3;
+            warp_wait(&ctl.pv_done[k], (par >> k & 1) ^ 1);
+            tc_fence_after();
+#pragma unroll 1
+            for (int q = 0; q < D / 16; ++q) {
+              float o[16];
+              uint32_t z[16];
+              tmem_ld16(tO + 16 * q, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) z[e] = __float_as_uint(o[e] * al);
+              tmem_st16(tO + 16 * q, z);
+            }
+            l *= al;
+          }
+          m = mn;
+          // masked scores: exp2(-inf - sub) = 0
+          probabilities(m == -INFINITY ? 0.f : m);
         }
+        tmem_st16(t, y[0]);
+        tmem_st16(t + 16, y[1]);
         l += (sums[0] + sums[1]) + (sums[2] + sums[3]);
         tmem_st_wait();
       };
