@@ -282,6 +282,11 @@ class TPModel:
         self.max_tokens = 0
         self.ws = None
         self.device = torch.device("cuda", torch.cuda.current_device())
+        # sizes the paged calls check against (reading a ctypes field takes its time)
+        self._ranks, self._qkv_cols = cfg.attn_tp, self.qkv_rows()
+        self._width = cfg.n_heads * cfg.head_dim
+        self._copies, self._kv_heads, self._dim = cfg.kv_copies, cfg.kv_heads_per_rank, cfg.head_dim
+        self._vocab = cfg.vocab
         self.step_ws = None
         self._old_step_ws = []
         self.ensure_workspace(max_tokens, stream)
@@ -462,10 +467,10 @@ class TPModel:
         return self.step_ws
 
     def _stream(self, stream) -> int:
-        """As _stream; the current stream is looked up by the device's number, which takes a
-        tenth of the time that finding the current device out takes."""
+        """As _stream, without building a stream object (the call's own kernels take 2 to 5 us,
+        torch.cuda.current_stream up to 4)."""
         if stream is None:
-            return torch.cuda.current_stream(self.device.index).cuda_stream
+            return torch._C._cuda_getCurrentRawStream(self.device.index)
         return _stream(stream)
 
     def _out(self, shape, dtype, stream) -> torch.Tensor:
@@ -499,19 +504,18 @@ class TPModel:
         """RoPE and the new K/V rows into their slots; returns the rotated queries
         [M, n_heads*d] (into q when given; None with want_q False).  qkv: column_linear's
         output [ranks, M, N_r]."""
-        c = self.cfg
         M = qkv.shape[1]
         dev = self.device
-        _check(qkv, "qkv", torch.bfloat16, (c.attn_tp, M, self.qkv_rows()), dev)
+        _check(qkv, "qkv", torch.bfloat16, (self._ranks, M, self._qkv_cols), dev)
         _check(positions, "positions", torch.int32, (M,), dev)
         _check(slots, "slots", torch.int32, (M,), dev)
         self._check_pool(k, "k", pages)
         self._check_pool(v, "v", pages)
         if q is not None:
-            _check(q, "q", torch.bfloat16, (M, c.n_heads * c.head_dim), dev, rows=True)
+            _check(q, "q", torch.bfloat16, (M, self._width), dev, rows=True)
         elif want_q:
-            q = self._out((M, c.n_heads * c.head_dim), torch.bfloat16, stream)
-        B.check(B.tp_cache_append(self.handle, qkv.data_ptr(), M * qkv.shape[2], M,
+            q = self._out((M, self._width), torch.bfloat16, stream)
+        B.check(B.tp_cache_append(self.handle, qkv.data_ptr(), M * self._qkv_cols, M,
                                   positions.data_ptr(), slots.data_ptr(), pages.c, k.data_ptr(),
                                   v.data_ptr(), _ptr(q), 0 if q is None else _ld(q),
                                   self._stream(stream)), "tp_cache_append")
@@ -522,9 +526,8 @@ class TPModel:
                        ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         """Attention of the step's tokens over the paged cache; q, out [n_tokens, n_heads*d].
         Padding rows of out are not written (undefined in a buffer allocated here)."""
-        c = self.cfg
         t = pages.table
-        shape = (step.n_tokens, c.n_heads * c.head_dim)
+        shape = (step.n_tokens, self._width)
         _check(q, "q", torch.bfloat16, shape, self.device, rows=True)
         if step.q_start is None or t is None or t.shape[0] < step.n_seqs or \
                 t.device != self.device or step.old_lens.device != self.device:
@@ -544,9 +547,8 @@ class TPModel:
         return out
 
     def _check_pool(self, t: torch.Tensor, name: str, pages: PageTable) -> None:
-        c = self.cfg
-        _check(t, name, torch.bfloat16, (c.kv_copies, pages.n_pages, c.kv_heads_per_rank,
-                                         pages.page_size, c.head_dim), self.device)
+        _check(t, name, torch.bfloat16, (self._copies, pages.n_pages, self._kv_heads,
+                                         pages.page_size, self._dim), self.device)
 
     def process_logits(self, logits: torch.Tensor, rules: LogitRules,
                        out: Optional[torch.Tensor] = None, dtype=torch.float32,
@@ -554,7 +556,7 @@ class TPModel:
         """Penalties, biases and grammar masks on bf16 logits [S, vocab]; the result in a new
         tensor of `dtype` (float32 or bfloat16), or in `out`, which may be `logits` itself.
         Rows with row_req -1 are not written (undefined in a tensor allocated here)."""
-        S, V = logits.shape[0], self.cfg.vocab
+        S, V = logits.shape[0], self._vocab
         _check(logits, "logits", torch.bfloat16, (S, V), self.device, rows=True)
         n = rules.c.n_reqs if rules.n_rows is None else rules.n_rows
         if n != S:
