@@ -53,20 +53,22 @@ bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
 int tile_tokens(const tp_model* m) { return kTreeRows / (m->cfg.n_heads / m->cfg.n_kv_heads); }
 int query_tiles(const tp_model* m, int n) { return cdiv(n, tile_tokens(m)); }
 
-// Workspace regions: the step tables' ticket, then tree attention's tickets,
-// pieces and their (m, l).  (Steps of more new tokens than tree attention
-// takes, prompts, only use the first.)
+// Workspace regions: the step tables' ticket, then tree attention's (m, l),
+// pieces and tickets.  (Steps of more new tokens than tree attention takes,
+// prompts, only use the first.)  The tickets, whose number is the step's, lie
+// last: a workspace also serves smaller steps, and what one step writes must
+// not lie where another expects tickets of zero.
 struct StepWs {
-  size_t tickets, ml, partials, total;
+  size_t ml, partials, tickets, total;
 };
 StepWs step_ws(const tp_model* m, int n_seqs, int max_new) {
   StepWs w;
   const size_t pieces = (size_t)m->num_sms * 2 * kTreeRows;
   const int tiles = query_tiles(m, std::min(max_new, kMaxTreeTokens));
-  w.tickets = kStepTicketBytes;
-  w.ml = align_up(w.tickets + (size_t)n_seqs * m->cfg.n_kv_heads * tiles * sizeof(int), 256);
+  w.ml = kStepTicketBytes;
   w.partials = align_up(w.ml + pieces * sizeof(float2), 256);
-  w.total = w.partials + pieces * m->cfg.head_dim * sizeof(float);
+  w.tickets = align_up(w.partials + pieces * m->cfg.head_dim * sizeof(float), 256);
+  w.total = w.tickets + (size_t)n_seqs * m->cfg.n_kv_heads * tiles * sizeof(int);
   return w;
 }
 

@@ -1078,6 +1078,20 @@ def test_two_graphs_with_a_workspace_each():
     assert m.check_device() == 0
 
 
+def test_one_workspace_for_steps_of_different_sizes():
+    """Pieces of a small step lie where no larger step keeps its tickets."""
+    rng = np.random.default_rng(92)
+    m = model(16, 8, 64, 2)
+    ws = m.step_workspace(300, 80)
+    small = attn_case(rng, m, [5001], [80], 64)
+    large = attn_case(rng, m, rng.integers(100, 900, 300).tolist(), [1] * 300, 16)
+    for c, pick in ((small, 13), (large, 3), (small, 13)):
+        out = torch.full_like(c["q"], 3.0)
+        m.tree_attention(c["q"], c["step"], c["pages"], c["k"], c["v"], out=out, ws=ws)
+        check_attn(m, c, out, rows=lambda b, i: (b + i) % pick == 0)
+    assert m.check_device() == 0
+
+
 def test_workspace_does_not_grow_inside_a_capture():
     m = TPModel(make_config(512, 8, 2, 64, 256, 100, 0, 2, max_positions=64), [], max_tokens=1)
     g = torch.cuda.CUDAGraph()
