@@ -523,7 +523,7 @@ typedef struct {
  * are padding.  A sequence not in use has old = new = 0. */
 typedef struct {
   int32_t n_seqs;              /* 1..8192 */
-  int32_t n_tokens;
+  int32_t n_tokens;            /* 0..2^30 */
   int32_t max_new;             /* host: no T_b is larger */
   int32_t max_ctx;             /* host: no length is larger; lengths end at 2^30 */
   int32_t tree_words;          /* 64-bit words of a tree mask row (with tree_mask) */

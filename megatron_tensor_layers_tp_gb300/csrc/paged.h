@@ -14,7 +14,7 @@ namespace tpk {
 constexpr int kMaxStepSeqs = 8192;   // the step tables keep three words a sequence in shared memory
 constexpr int kMaxTreeTokens = 256;  // new tokens a sequence with tree masks, and in tree attention
 constexpr int kMaxTreeWords = kMaxTreeTokens / 64;
-constexpr int kMaxLength = 1 << 30;  // tokens of a sequence
+constexpr int kMaxLength = 1 << 30;  // tokens of a sequence, rows of a step
 constexpr int kMaxVocab = 1 << 30;   // logits of a row
 constexpr size_t kStepTicketBytes = 256;  // the step tables' part of the workspace
 

@@ -100,7 +100,7 @@ tp_status tp_step_tables(const tp_model* m, const tp_pages_t* pages, const tp_st
     if (step->n_tokens > 0 && (!step->slots || !step->positions || !step->token_seq))
       return TP_ERR_ARG;
     if (step->tree_mask && step->tree_words < 1) return TP_ERR_ARG;
-    if (step->n_seqs > kMaxStepSeqs ||
+    if (step->n_seqs > kMaxStepSeqs || step->n_tokens > kMaxLength ||
         ((step->tree_mask || step->parents) && step->max_new > kMaxTreeTokens) ||
         (step->tree_mask &&
          (step->tree_words > kMaxTreeWords || step->max_new > 64 * step->tree_words)))
@@ -203,7 +203,7 @@ tp_status tp_tree_attention(const tp_model* m, const tp_bf16* q, int64_t ld_q, t
         pages->ld_table < 1 || !pages->table || !step->old_lens || !step->q_start)
       return TP_ERR_ARG;
     if (step->tree_mask && step->tree_words < 1) return TP_ERR_ARG;
-    if (step->n_seqs > kMaxStepSeqs || step->max_new > kMaxTreeTokens ||
+    if (step->n_seqs > kMaxStepSeqs || step->n_tokens > kMaxLength || step->max_new > kMaxTreeTokens ||
         (step->tree_mask &&
          (step->tree_words > kMaxTreeWords || step->max_new > 64 * step->tree_words)))
       return TP_ERR_UNSUPPORTED;

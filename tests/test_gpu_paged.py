@@ -14,6 +14,8 @@ fp32 by 2^-24):
 - logits: at most six fp32 roundings of terms whose magnitudes add up to m:
   6 * 2^-24 m, and 2^-8 |x| more for a bf16 result.
 """
+import threading
+
 import numpy as np
 import pytest
 
@@ -842,6 +844,7 @@ def test_refusals_of_the_c_calls():
         assert attn(**kw) == ARG, kw
     for kw in (dict(pages=dict(page_size=12)), dict(pages=dict(page_size=65544)),
                dict(pages=dict(n_pages=2**28)), dict(step=dict(n_seqs=8193)), dict(step=dict(max_new=257)),
+               dict(step=dict(n_tokens=2**30 + 1)),
                dict(step=dict(max_new=65)), dict(step=dict(tree_words=5))):
         assert attn(**kw) == UNS, kw
     for kw in (dict(w=0), dict(w=ws.data_ptr() + 8), dict(wb=ws.numel() - 1)):
@@ -864,7 +867,7 @@ def test_refusals_of_the_c_calls():
                  "n_seqs"):
         assert tables(step_={name: 0}) == ARG, name
     for kw in (dict(max_new=65), dict(max_new=257, tree_words=5), dict(n_seqs=8193),
-               dict(tree_mask=0, max_new=300)):
+               dict(tree_mask=0, max_new=300), dict(n_tokens=2**30 + 1)):
         assert tables(step_=kw) == UNS, kw
     assert tables(w=0) == WS and tables(wb=8) == WS
 
@@ -907,7 +910,12 @@ def test_refusals_of_the_c_calls():
                dict(allowed=p, n_allowed=3, ld_allowed=31), dict(allowed=p, n_allowed=2, ld_allowed=32),
                dict(allowed=p, allowed_row=p, ld_allowed=32)):
         assert logits(**kw) == ARG, kw
-    assert m.check_device() == 0
+    big = TPModel(make_config(512, 8, 2, 64, 256, 2**30 + 2, 0, 2, max_positions=8), [], max_tokens=1)
+    r = B.tp_logit_rules_t()
+    r.n_reqs = 1
+    far = x.data_ptr() + 2**40  # (refused before anything looks at it)
+    assert B.tp_process_logits(big.handle, x.data_ptr(), 2**30 + 2, 1, r, far, 2**30 + 2, 1, 0) == UNS
+    assert m.check_device() == 0 and big.check_device() == 0
 
 
 # ---------------------------------------------------------------------------
@@ -1048,6 +1056,50 @@ def test_speculative_steps_match_one_token_at_a_time():
         assert pages.free_state.tolist()[1] == n_pages - used
         assert m.check_device() == 0
     assert min(len(x) for x in text) > 3
+
+
+def test_threads_with_steps_of_different_sizes():
+    """Four host threads, a stream and a workspace each, steps and rules of different sizes."""
+    rng = np.random.default_rng(93)
+    m = model(8, 2, 64, 2, 32003)
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                c, rules = cases[i]
+                x = torch.zeros((300, 32003), dtype=torch.bfloat16, device="cuda")
+                words = 0
+                for _ in range(20):
+                    pages = PageTable(c["page"], i32(c["table"]), i32(c["ring"]),
+                                      i32([c["first"], c["count"]]))
+                    step = Step.alloc(len(c["old"]), c["n_tokens"], c["max_new"], c["max_ctx"],
+                                      i32(c["old"]), i32(c["new"]), i32(c["parents"]), words)
+                    ws = m.step_workspace(len(c["old"]), c["max_new"])
+                    m.step_tables(pages, step, ws=ws)
+                    m.process_logits(x, rules, dtype=torch.bfloat16)
+                    torch.cuda.current_stream().synchronize()
+                    check_tables(c, words, pages, step)
+        except Exception as e:  # noqa: BLE001 (handed to the test)
+            failed.append((i, repr(e)))
+
+    cases = []
+    for i, n in enumerate((8000, 3600, 5000, 40)):
+        c = tables_case(rng, n, 3, 16, 40, True, 0.2)
+        hist = torch.zeros((300, 2100 + i), dtype=torch.int32, device="cuda")
+        kw = dict(history=hist, history_lens=torch.zeros(300, dtype=torch.int32, device="cuda"))
+        if i % 2:
+            kw.update(bias_start=i32([0] * 301), bias_ids=i32([0]), bias_values=torch.ones(1).cuda())
+        cases.append((c, LogitRules(**kw)))
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
+    assert m.check_device() == 0
 
 
 def test_two_graphs_with_a_workspace_each():
