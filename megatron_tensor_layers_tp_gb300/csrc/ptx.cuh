@@ -55,6 +55,22 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
+// Two at once, their latencies overlapped: bit 0 and bit 1.
+__device__ __forceinline__ uint32_t mbar_try_wait2(uint64_t* bar0, uint32_t parity0, uint64_t* bar1,
+                                                   uint32_t parity1) {
+  uint32_t a, b;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%2], %3;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 q, [%4], %5;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "selp.u32 %1, 2, 0, q;\n\t}"
+      : "=r"(a), "=r"(b)
+      : "r"(smem_u32(bar0)), "r"(parity0), "r"(smem_u32(bar1)), "r"(parity1)
+      : "memory");
+  return a | b;
+}
+
 // Waits until the phase with the given parity has completed.  Returns false
 // (and records a timeout in *status) once about kWaitLimitCycles SM cycles
 // (~2 s at the GB300 clock) have passed; the cycle counter is read only every

@@ -17,9 +17,9 @@
 //
 // Measured: one token behind 700 old ones, 32 heads of 128 over 8 KV heads:
 // 16 us; 16 trees of 8-32 tokens behind 150-2048, 40 heads over 8 (80 MB): 40 us;
-// 64 trees of 2-8 tokens behind 1500-4096, 32 heads over 8 (740 MB): 127 us,
-// 5.8 TB/s; 6 chunks of 100-256 tokens behind up to 8000, 32 heads of 64 over 4
-// (36 GFLOP): 134 us.
+// 64 trees of 2-8 tokens behind 1500-4096, 32 heads over 8 (740 MB): 123 us,
+// 6.0 TB/s; 6 chunks of 100-256 tokens behind up to 8000, 32 heads of 64 over 4
+// (36 GFLOP): 109 us.
 //
 // Work is the flat sequence of (sequence, KV head, query tile, key tile), an
 // item's fixed work counted as kItemCost tiles more, split evenly over one CTA
@@ -31,22 +31,24 @@
 // flight (a second kernel for the join cost 3-5 us a call; the join with rows
 // of pieces and loads one after another, 50).
 //
-// Roles of the 16 warps:
-//   warps 0-3  : K and V tiles by TMA into a ring, through the page table, each
-//                every fourth tile: boxes end where pages end, a box costs its
-//                warp about 130 cycles to issue (32 boxes a tile at 8-key
-//                pages) and a tile some 1500 in waits and look-ups;
-//   warp 4     : one thread issues S = Q K^T into tensor memory;
-//   warps 5, 6 : one thread each issues O += P V of a softmax group, with P read
-//                from tensor memory and V as it lies in the page (the head's
-//                elements contiguous).  Issuing costs about 65 cycles a product
-//                and 80 a commit: one thread for all of them set the pace
-//                (1850-2000 cycles a tile, nothing else busy);
-//   warp 7     : the CTA's parts of items, announced to the other warps two
+// Roles of the 20 warps:
+//   warps 0-3  : K and V tiles by TMA into rings, through the page table, each
+//                every other tile of a group: boxes end where pages end, a box
+//                costs its warp about 130 cycles to issue (32 boxes a tile at
+//                8-key pages) and a tile some 1500 in waits and look-ups;
+//   warps 4, 5 : one thread each issues S = Q K^T of a softmax group into tensor
+//                memory;
+//   warps 6, 7 : one thread each issues O += P V of a group, with P read from
+//                tensor memory and V as it lies in the page (the head's elements
+//                contiguous).  Issuing costs about 65 cycles a product, 80 a
+//                commit and 100-150 a wait: one thread for all products set the
+//                pace (1850-2000 cycles a tile, nothing else busy), and so did
+//                one for both groups' S (1300; the chunks below 134 us, not 109);
+//   warp 8     : the CTA's parts of items, announced to the other warps two
 //                ahead, and the next item's query tile while this one's softmax
 //                ends.  (Every role finding the parts by itself spilled
 //                registers into the issuing loops: twice the time.);
-//   warps 8-11, 12-15: two softmax groups.  They take alternate key tiles, each
+//   warps 12-15, 16-19: two softmax groups.  They take alternate key tiles, each
 //                with its own running maximum, sum and O, so that neither
 //                waits for the other's maxima; the two states meet at the
 //                item's end.  A thread owns a row and holds a tile's 64 scores
@@ -54,7 +56,9 @@
 // Each group has two S buffers: the products of its next tile run while it
 // works on this one.  Measured with 128-key tiles and one buffer a group, the
 // chain scores -> exponentials -> P V -> next scores left the SM waiting: an
-// 8000-key chunk of 64-element heads took 172 us instead of 134.
+// 8000-key chunk of 64-element heads took 172 us instead of 134.  Two warpgroups
+// a group, each with half of a tile's keys: 159 instead of 134, the issuing
+// threads waiting longer for their turns.
 // P overwrites S in place (bf16, half the columns).  O is rescaled only when a
 // row's maximum rose by more than 2^8 since its last rescaling: the sums are
 // relative to the older maximum until then, which is exact algebra and keeps
@@ -77,11 +81,12 @@
 
 namespace tpk {
 
-constexpr int kTreeThreads = 512;
-constexpr int kTreeSoftmax = 256;        // threads of the two softmax groups
+constexpr int kTreeThreads = 640;
+constexpr int kTreeSoftmax = 256;        // threads of the two softmax groups, the last ones
+constexpr int kTreeFirst = kTreeThreads - kTreeSoftmax;
 // registers of a thread after the hand-over: together no more than the launch
 // brought (checked by the host, since a take-over beyond it would never end)
-constexpr int kTreeRegsOther = 64, kTreeRegsSoftmax = 184;
+constexpr int kTreeRegsOther = 56, kTreeRegsSoftmax = 152;
 constexpr float kRescaleLog2 = 8.f;
 constexpr int kItemCost = 8;             // an item's fixed work in key tiles
 constexpr int kMaxGrid = 1024;
@@ -97,21 +102,21 @@ struct Seg {
 template <int D>
 struct TreeSmem {
   static constexpr int kTile = kTreeKeys * D * 2;    // a K or V tile
-  static constexpr int kStages = D == 128 ? 9 : 22;
+  static constexpr int kDepth = D == 128 ? 2 : 5;     // tiles of each of the four rings
   static constexpr int kOut = kTreeRows * D * 2;      // after the query tile: rows of o on their way out
   static constexpr int kRing = 2 * kOut;
-  static constexpr int kMeet = kRing + kStages * kTile;  // (m, l) of the two groups
+  static constexpr int kMeet = kRing + 4 * kDepth * kTile;  // (m, l) of the two groups
   static constexpr int kBars = kMeet + 2 * kTreeRows * 8;
   static constexpr int kTotal = kBars + 1024 + 1024;  // + alignment of the base
   static_assert(kTotal <= 227 * 1024, "shared memory of one CTA");
 };
 // after the ring
 struct TreeCtl {
-  uint64_t full[24], empty[24];
+  uint64_t full[20], empty[20];
   uint64_t s_full[4], p_ready[4], pv_done[4], q_full, q_free, drain;
   uint64_t seg_full[4], seg_free[4];
   Seg seg[4];
-  long long warp_sum[16];
+  long long warp_sum[kTreeThreads / 32];
   long long total, u0, x0, x1;
   int b0;
   int poison[2];
@@ -323,7 +328,10 @@ template <int D>
 __global__ void __launch_bounds__(kTreeThreads, 1)
 tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
   using SM = TreeSmem<D>;
-  constexpr int NST = SM::kStages;
+  // Rings: K and V of each softmax group, (2 * group + (V: 1)) * R on.  Each has
+  // one consumer, so that whoever waits for a fill has itself consumed the one
+  // before it in that place: a parity then tells the two apart.
+  constexpr int R = SM::kDepth;
   constexpr int HB = kTreeKeys * 128, HQ = kTreeRows * 128;  // bytes of 64 elements of a K/V, Q tile
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -336,7 +344,7 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
 
   pdl_launch_dependents();
   if (threadIdx.x == 0) {
-    for (int i = 0; i < NST; ++i) { mbar_init(&ctl.full[i], 1); mbar_init(&ctl.empty[i], 1); }
+    for (int i = 0; i < 4 * R; ++i) { mbar_init(&ctl.full[i], 1); mbar_init(&ctl.empty[i], 1); }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&ctl.s_full[i], 1);
       mbar_init(&ctl.p_ready[i], 4);
@@ -345,11 +353,11 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
     ctl.poison[0] = ctl.poison[1] = 0;
     for (int i = 0; i < 4; ++i) {
       mbar_init(&ctl.seg_full[i], 1);
-      mbar_init(&ctl.seg_free[i], kTreeLoaders + 3 + kTreeSoftmax / 32);
+      mbar_init(&ctl.seg_free[i], kTreeLoaders + 4 + kTreeSoftmax / 32);
     }
     mbar_init(&ctl.q_full, 1);
-    mbar_init(&ctl.q_free, 1);
-    mbar_init(&ctl.drain, 3);
+    mbar_init(&ctl.q_free, 2);
+    mbar_init(&ctl.drain, 4);
     fence_barrier_init();
     fence_proxy_async_smem();
     tma_prefetch_desc(&a.tmQ);
@@ -422,6 +430,12 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (ok) ok = mbar_wait(bar, parity, a.status);
   };
+  auto wait2 = [&](uint64_t* bar0, uint32_t parity0, uint64_t* bar1, uint32_t parity1) {
+    if (!ok) return;
+    const uint32_t got = mbar_try_wait2(bar0, parity0, bar1, parity1);
+    if (!(got & 1)) ok = mbar_wait(bar0, parity0, a.status);
+    if (!(got & 2)) wait(bar1, parity1);
+  };
   auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
     wait(bar, parity);
     __syncwarp();
@@ -437,16 +451,17 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
   auto done_with = [&](uint32_t seg) { mbar_arrive(&ctl.seg_free[seg & 3]); };
 
   // The softmax warpgroups take over registers that the others do not need.
-  if (warp < 8) {
+  if (warp < kTreeFirst / 32) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTreeRegsOther));
     if (warp < kTreeLoaders) {
       // ------------------------------------------------------------ K and V
       const uint64_t pol = policy_evict_first();
-      const int R = a.box_rows, boxes = kTreeKeys / R;
+      const int rows = a.box_rows, boxes = kTreeKeys / rows;
       // lane -> (box, 64-element half)
       const int box = D == 128 ? lane >> 1 : lane, half = D == 128 ? lane & 1 : 0;
-      uint32_t gt = 0;              // key tiles before this part
-      uint32_t mine[2] = {0, 0};    // this warp's last ring fills + 1 (K, V)
+      const int grp = warp & 1, turn = warp >> 1;  // every other tile of a group is the warp's
+      uint32_t gj = 0;              // the group's tiles before this part
+      uint32_t mine[2] = {0, 0};    // this warp's last fills + 1 (K, V)
       for (uint32_t seg = 0;; ++seg) {
         const Seg sg = fetch(seg);
         ok = __all_sync(0xffffffffu, ok);
@@ -458,33 +473,34 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
         // A tile's page numbers, one a box, loaded two of the warp's tiles
         // ahead.
         auto load = [&](int i) {
-          const int pg = (int)fast_div((uint32_t)((sg.k0 + i) * kTreeKeys + box * R), a.div_page);
+          const int pg = (int)fast_div((uint32_t)((sg.k0 + i) * kTreeKeys + box * rows), a.div_page);
           return i < n && box < boxes && pg <= last ? row[pg] : 0;
         };
-        const int i0 = (warp - gt) & (kTreeLoaders - 1);  // tile gt + i0 is the warp's
-        int page = load(i0), next = load(i0 + kTreeLoaders);
-        for (int i = i0; ok && i < n; i += kTreeLoaders) {
-          const int after = load(i + 2 * kTreeLoaders);
+        const int i0 = grp + 2 * ((turn - gj) & 1);
+        int page = load(i0), next = load(i0 + 4);
+        for (int i = i0; ok && i < n; i += 4) {
+          const int after = load(i + 8);
           const int kt = sg.k0 + i;
-          const int here = min(boxes, (len - kt * kTreeKeys + R - 1) / R);
-          const int key = kt * kTreeKeys + box * R;
+          const int here = min(boxes, (len - kt * kTreeKeys + rows - 1) / rows);
+          const int key = kt * kTreeKeys + box * rows;
           const int off = key - (int)fast_div((uint32_t)key, a.div_page) * a.page_size;
           int z = (copy * a.n_pages + page) * a.kv_r + local;
           if (box < here && (page < 0 || page >= a.n_pages)) {
             record_status(a.status, kStatusTableRange);
             z = a.slices;  // outside the tensor map: zeros
           }
+          const uint32_t j = gj + (i >> 1);
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv) {
-            const uint32_t f = 2 * (gt + i) + kv, st = f % NST;
-            if (lane == 0) wait(&ctl.empty[st], (f / NST & 1) ^ 1);  // one lane polls
+            const uint32_t st = (2 * grp + kv) * R + j % R;
+            if (lane == 0) wait(&ctl.empty[st], (j / R & 1) ^ 1);  // one lane polls
             ok = __shfl_sync(0xffffffffu, ok, 0);
             if (ok) {
-              mine[kv] = f + 1;
-              if (lane == 0) mbar_arrive_expect_tx(&ctl.full[st], here * R * D * 2);
+              mine[kv] = j + 1;
+              if (lane == 0) mbar_arrive_expect_tx(&ctl.full[st], here * rows * D * 2);
               __syncwarp();
               if (box < here) {
-                uint8_t* dst = ring + st * SM::kTile + half * HB + box * R * 128;
+                uint8_t* dst = ring + st * SM::kTile + half * HB + box * rows * 128;
                 const CUtensorMap* tm = kv ? &a.tmV : &a.tmK;
                 if (a.kv_once) tma_load_3d(dst, tm, &ctl.full[st], half * 64, off, z, pol);
                 else tma_load_3d_plain(dst, tm, &ctl.full[st], half * 64, off, z);
@@ -494,42 +510,45 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
           page = next;
           next = after;
         }
-        gt += n;
+        gj += (n - grp + 1) >> 1;
         __syncwarp();
         if (lane == 0) done_with(seg);
       }
-      // Never leave with copies still landing in shared memory.  A fill whose
-      // slot is filled again later (by another warp) landed before that.
+      // Never leave with copies still landing in shared memory.  (A fill that
+      // another, perhaps another warp's, follows in its place landed before
+      // that.)
       if (lane == 0) {
-        for (uint32_t back = 0; back < NST; back += 2 * kTreeLoaders)
+        for (uint32_t back = 0; back < R; back += 2)
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv) {
-            const uint32_t f = mine[kv] - 1 - back;
-            if (mine[kv] > back && (!ok || f + NST >= 2 * gt))
-              mbar_wait(&ctl.full[f % NST], (f / NST) & 1, a.status);
+            const uint32_t j = mine[kv] - 1 - back;
+            if (mine[kv] > back && (!ok || j + R >= gj))
+              mbar_wait(&ctl.full[(2 * grp + kv) * R + j % R], j / R & 1, a.status);
           }
       }
       __syncwarp();
-    } else if (warp >= 4 && warp < 7) {
+    } else if (warp >= 4 && warp < 8) {
       // ------------------------------------------------------------ products
       if (lane == 0) {
-        uint32_t gt = 0;   // key tiles before this part
         uint32_t par = 0;  // bit k: products with S buffer k, mod 2
-        if (warp == 4) {
+        uint32_t st = 0, ph = 0;  // the next tile's place in its ring, and parity
+        const int grp = warp & 1;
+        if (warp < 6) {
           constexpr uint32_t idS = idesc_bf16_f32(kTreeRows, kTreeKeys);
-          const uint64_t dq = smem_desc_sw128(sQ), dk0 = smem_desc_sw128(ring);
+          const uint64_t dq = smem_desc_sw128(sQ);
+          const uint64_t dk0 = smem_desc_sw128(ring + 2 * grp * R * SM::kTile);
+          uint64_t *full = ctl.full + 2 * grp * R, *empty = ctl.empty + 2 * grp * R;
           for (uint32_t seg = 0;; ++seg) {
             const Seg sg = fetch(seg);
             const int n = sg.k1 ? sg.k1 - sg.k0 : 0;
             if (n == 0) break;
             done_with(seg);
             wait(&ctl.q_full, seg & 1);
-            for (int i = 0; i < n; ++i) {  // S buffer i % 4
+            for (int i = grp; i < n; i += 2) {  // S buffer i % 4
               const int k = i & 3;
-              wait(&ctl.pv_done[k], (par >> k & 1) ^ 1);  // P of the buffer's last tile was read
+              // P of the buffer's last tile was read, K is there
+              wait2(&ctl.pv_done[k], (par >> k & 1) ^ 1, &full[st], ph);
               par ^= 1u << k;
-              const uint32_t f = 2 * (gt + i), st = f % NST;
-              wait(&ctl.full[st], (f / NST) & 1);
               if (!ok) break;
               tc_fence_after();
               const uint64_t dk = dk0 + st * (SM::kTile >> 4);
@@ -538,16 +557,16 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
                 tc_mma_f16(tmem + k * kTreeKeys, dq + (kk >> 2) * (HQ >> 4) + (kk & 3) * 2,
                            dk + (kk >> 2) * (HB >> 4) + (kk & 3) * 2, idS, kk > 0);
               tc_commit(&ctl.s_full[k]);
-              tc_commit(&ctl.empty[st]);
+              tc_commit(&empty[st]);
+              if (++st == R) { st = 0; ph ^= 1; }
             }
             if (ok) tc_commit(&ctl.q_free);
-            gt += n;
           }
         } else {
           constexpr uint32_t idO = idesc_bf16_f32_bmn(kTreeRows, D);
-          const int grp = warp - 5;
           const uint32_t dO = tmem + 256 + grp * D;
-          const uint64_t dv0 = smem_desc_mn_sw128(ring, HB);
+          const uint64_t dv0 = smem_desc_mn_sw128(ring + (2 * grp + 1) * R * SM::kTile, HB);
+          uint64_t *full = ctl.full + (2 * grp + 1) * R, *empty = ctl.empty + (2 * grp + 1) * R;
           for (uint32_t seg = 0;; ++seg) {
             const Seg sg = fetch(seg);
             const int n = sg.k1 ? sg.k1 - sg.k0 : 0;
@@ -555,10 +574,8 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
             done_with(seg);
             for (int i = grp; i < n; i += 2) {
               const int k = i & 3;
-              wait(&ctl.p_ready[k], par >> k & 1);
+              wait2(&ctl.p_ready[k], par >> k & 1, &full[st], ph);
               par ^= 1u << k;
-              const uint32_t f = 2 * (gt + i) + 1, st = f % NST;
-              wait(&ctl.full[st], (f / NST) & 1);
               if (!ok) break;
               tc_fence_after();
               const uint64_t dv = dv0 + st * (SM::kTile >> 4);
@@ -566,16 +583,16 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
               for (int kk = 0; kk < kTreeKeys / 16; ++kk)
                 tc_mma_f16_ta(dO, tmem + k * kTreeKeys + 8 * kk, dv + 128 * kk, idO, i >= 2 || kk > 0);
               tc_commit(&ctl.pv_done[k]);
-              tc_commit(&ctl.empty[st]);
+              tc_commit(&empty[st]);
+              if (++st == R) { st = 0; ph ^= 1; }
             }
-            gt += n;
           }
         }
         tc_commit(&ctl.drain);
         mbar_wait(&ctl.drain, 0, a.status);
       }
       __syncwarp();
-    } else if (warp == 7) {
+    } else if (warp == 8) {
       // ------------------------------------------------------------ parts, queries
       SegIter it(a, x0, x1, ctl.u0, ctl.b0);
       uint32_t told = 0;
@@ -621,12 +638,12 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTreeRegsSoftmax));
     // ------------------------------------------------------------ softmax
-    const int grp = (warp - 8) >> 2, quad = warp & 3;
-    const int tid = threadIdx.x - 256;       // 0..255 over both groups
+    const int grp = (warp - kTreeFirst / 32) >> 2, quad = warp & 3;
+    const int tid = threadIdx.x - kTreeFirst;       // 0..255 over both groups
     const int r = quad * 32 + lane;          // the thread's row of the tile
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
     const uint32_t tS = tmem + lanes, tO = tmem + lanes + 256 + grp * D;
-    uint32_t gt0 = 0;  // key tiles before this part
+    uint32_t gj = 0;   // the group's tiles before this part
     uint32_t par = 0;  // bit k: tiles taken from S buffer k, mod 2
     for (uint32_t seg = 0;; ++seg) {
       const Seg s = fetch(seg);
@@ -706,11 +723,15 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
       for (int i = grp; i < n; i += 2) {
         const int key0 = (s.k0 + i) * kTreeKeys, k = i & 3;
         const bool tail = key0 + kTreeKeys > s.old;
+        // (Scores first: with them, the fill before this one in V's place was
+        // consumed.)
+        warp_wait(&ctl.s_full[k], par >> k & 1);
+        tc_fence_after();
         if (tail) {
           // V of keys behind the end and non-finite V of new tokens: two
           // threads a key, each half of its elements
-          const uint32_t f = 2 * (gt0 + i) + 1, st = f % NST;
-          warp_wait(&ctl.full[st], (f / NST) & 1);
+          const uint32_t j = gj + (i >> 1), st = (2 * grp + 1) * R + j % R;
+          warp_wait(&ctl.full[st], j / R & 1);
           const int kr = r & 63, key = key0 + kr;
           uint8_t* v = ring + st * SM::kTile + kr * 128;
           auto chunk = [&](int ch) {  // of the thread's D / 16
@@ -742,8 +763,6 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
           vis[1] = sees32(a, s, tok, key0 + 32);
           fence_proxy_async_smem();
         }
-        warp_wait(&ctl.s_full[k], par >> k & 1);
-        tc_fence_after();
         if (warp_live) {
           if (tail) tile(std::true_type(), i);
           else tile(std::false_type(), i);
@@ -841,7 +860,7 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
               *reinterpret_cast<const uint4*>(sOut + rr * D * 2 + ((ch ^ (rr & 7)) << 4));
         }
       }
-      gt0 += n;
+      gj += (n - grp + 1) >> 1;
       __syncwarp();
       if (lane == 0) done_with(seg);
     }
