@@ -86,9 +86,9 @@ constexpr int kTreeSoftmax = 256;        // threads of the two softmax groups, t
 constexpr int kTreeFirst = kTreeThreads - kTreeSoftmax;
 // registers of a thread after the hand-over: together no more than the launch
 // brought (checked by the host, since a take-over beyond it would never end)
-constexpr int kTreeRegsOther = 56, kTreeRegsSoftmax = 152;
+constexpr int kTreeRegsOther = 64, kTreeRegsSoftmax = 144;
 constexpr float kRescaleLog2 = 8.f;
-constexpr int kItemCost = 8;             // an item's fixed work in key tiles
+constexpr int kItemCost = 12;             // an item's fixed work in key tiles
 constexpr int kMaxGrid = 1024;
 
 // One CTA's part of an item: key tiles [k0, k1) of nt of (sequence b, KV head
@@ -103,6 +103,9 @@ template <int D>
 struct TreeSmem {
   static constexpr int kTile = kTreeKeys * D * 2;    // a K or V tile
   static constexpr int kDepth = D == 128 ? 2 : 5;     // tiles of each of the four rings
+  // S buffers of a group: as many as tensor memory's 512 columns hold beside O
+  static constexpr int kBufs = (512 / 2 - D) / kTreeKeys < 3 ? (512 / 2 - D) / kTreeKeys : 3;
+  static_assert(kBufs <= kDepth, "a tile's scores imply that the fill before its V was consumed");
   static constexpr int kOut = kTreeRows * D * 2;      // after the query tile: rows of o on their way out
   static constexpr int kRing = 2 * kOut;
   static constexpr int kMeet = kRing + 4 * kDepth * kTile;  // (m, l) of the two groups
@@ -113,7 +116,7 @@ struct TreeSmem {
 // after the ring
 struct TreeCtl {
   uint64_t full[20], empty[20];
-  uint64_t s_full[4], p_ready[4], pv_done[4], q_full, q_free, drain;
+  uint64_t s_full[6], p_ready[6], pv_done[6], q_full, q_free, drain;  // [group][S buffer]
   uint64_t seg_full[4], seg_free[4];
   Seg seg[4];
   long long warp_sum[kTreeThreads / 32];
@@ -241,10 +244,10 @@ __device__ __forceinline__ int page_of(const TreeAttnArgs& a, int b, int pg) {
   return -1;
 }
 
-// Infinities and NaN among the V elements e0 .. e0 + 15 of the new tokens that
+// Infinities and NaN among the V elements e0 .. e0 + 31 of the new tokens that
 // row i sees in the part's keys: added to the row's o.
 __device__ __noinline__ void nonfinite_v(const TreeAttnArgs& a, const Seg& s, int i, int e0,
-                                         float (&o)[16]) {
+                                         float (&o)[32]) {
   const int g = s.g, end = min(s.k1 * kTreeKeys, s.old + s.T);
   for (int j = max(s.k0 * kTreeKeys, s.old); j < end; ++j) {
     if (!(sees32(a, s, i, j) & 1)) continue;
@@ -253,9 +256,29 @@ __device__ __noinline__ void nonfinite_v(const TreeAttnArgs& a, const Seg& s, in
     const uint16_t* v =
         a.v + ((((int64_t)(g / a.kv_r) * a.n_pages + page) * a.kv_r + g % a.kv_r) * a.page_size + j -
                pg * a.page_size) * a.head_dim + e0;
-    for (int e = 0; e < 16; ++e)
+    for (int e = 0; e < 32; ++e)
       if ((v[e] & 0x7F80) == 0x7F80) o[e] += bf16_to_f(v[e]);
   }
+}
+
+// Two fp32 operations an instruction.
+__device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z, d;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, x, y, z;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y), "f"(z.x), "f"(z.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 x, float2 y) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, d;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 d, x, y;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+  return d;
 }
 
 __device__ __forceinline__ uint32_t pack_p(float lo, float hi) {
@@ -263,8 +286,10 @@ __device__ __forceinline__ uint32_t pack_p(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-__device__ __forceinline__ bool has_nonfinite(uint32_t x) {
-  return (x & 0x7F80u) == 0x7F80u || (x & 0x7F800000u) == 0x7F800000u;
+// Bits 15 and 31: whether the bf16 in that half is an infinity or NaN (an
+// exponent of ones and one more carries into the sign's place).
+__device__ __forceinline__ uint32_t nonfinite2(uint32_t x) {
+  return (x & 0x7F807F80u) + 0x00800080u;
 }
 __device__ __forceinline__ uint32_t drop_nonfinite(uint32_t x) {
   if ((x & 0x7F80u) == 0x7F80u) x &= 0xFFFF0000u;
@@ -332,6 +357,7 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
   // one consumer, so that whoever waits for a fill has itself consumed the one
   // before it in that place: a parity then tells the two apart.
   constexpr int R = SM::kDepth;
+  constexpr int NB = SM::kBufs, kColO = 2 * NB * kTreeKeys;  // tensor memory: S buffers, then O
   constexpr int HB = kTreeKeys * 128, HQ = kTreeRows * 128;  // bytes of 64 elements of a K/V, Q tile
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -345,7 +371,7 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
   pdl_launch_dependents();
   if (threadIdx.x == 0) {
     for (int i = 0; i < 4 * R; ++i) { mbar_init(&ctl.full[i], 1); mbar_init(&ctl.empty[i], 1); }
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2 * SM::kBufs; ++i) {
       mbar_init(&ctl.s_full[i], 1);
       mbar_init(&ctl.p_ready[i], 4);
       mbar_init(&ctl.pv_done[i], 1);
@@ -530,7 +556,7 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
     } else if (warp >= 4 && warp < 8) {
       // ------------------------------------------------------------ products
       if (lane == 0) {
-        uint32_t par = 0;  // bit k: products with S buffer k, mod 2
+        uint32_t kb = 0, kp = 0;  // the next tile's S buffer (of the group's), and parity
         uint32_t st = 0, ph = 0;  // the next tile's place in its ring, and parity
         const int grp = warp & 1;
         if (warp < 6) {
@@ -544,11 +570,10 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
             if (n == 0) break;
             done_with(seg);
             wait(&ctl.q_full, seg & 1);
-            for (int i = grp; i < n; i += 2) {  // S buffer i % 4
-              const int k = i & 3;
+            for (int i = grp; i < n; i += 2) {
+              const int k = grp * NB + kb;
               // P of the buffer's last tile was read, K is there
-              wait2(&ctl.pv_done[k], (par >> k & 1) ^ 1, &full[st], ph);
-              par ^= 1u << k;
+              wait2(&ctl.pv_done[k], kp ^ 1, &full[st], ph);
               if (!ok) break;
               tc_fence_after();
               const uint64_t dk = dk0 + st * (SM::kTile >> 4);
@@ -559,12 +584,13 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
               tc_commit(&ctl.s_full[k]);
               tc_commit(&empty[st]);
               if (++st == R) { st = 0; ph ^= 1; }
+              if (++kb == NB) { kb = 0; kp ^= 1; }
             }
             if (ok) tc_commit(&ctl.q_free);
           }
         } else {
           constexpr uint32_t idO = idesc_bf16_f32_bmn(kTreeRows, D);
-          const uint32_t dO = tmem + 256 + grp * D;
+          const uint32_t dO = tmem + kColO + grp * D;
           const uint64_t dv0 = smem_desc_mn_sw128(ring + (2 * grp + 1) * R * SM::kTile, HB);
           uint64_t *full = ctl.full + (2 * grp + 1) * R, *empty = ctl.empty + (2 * grp + 1) * R;
           for (uint32_t seg = 0;; ++seg) {
@@ -573,9 +599,8 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
             if (n == 0) break;
             done_with(seg);
             for (int i = grp; i < n; i += 2) {
-              const int k = i & 3;
-              wait2(&ctl.p_ready[k], par >> k & 1, &full[st], ph);
-              par ^= 1u << k;
+              const int k = grp * NB + kb;
+              wait2(&ctl.p_ready[k], kp, &full[st], ph);
               if (!ok) break;
               tc_fence_after();
               const uint64_t dv = dv0 + st * (SM::kTile >> 4);
@@ -585,6 +610,7 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
               tc_commit(&ctl.pv_done[k]);
               tc_commit(&empty[st]);
               if (++st == R) { st = 0; ph ^= 1; }
+              if (++kb == NB) { kb = 0; kp ^= 1; }
             }
           }
         }
@@ -642,9 +668,13 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
     const int tid = threadIdx.x - kTreeFirst;       // 0..255 over both groups
     const int r = quad * 32 + lane;          // the thread's row of the tile
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-    const uint32_t tS = tmem + lanes, tO = tmem + lanes + 256 + grp * D;
+    const uint32_t tS = tmem + lanes, tO = tmem + lanes + kColO + grp * D;
     uint32_t gj = 0;   // the group's tiles before this part
-    uint32_t par = 0;  // bit k: tiles taken from S buffer k, mod 2
+    uint32_t kb = 0, kp = 0;  // the next tile's S buffer (of the group's), and parity
+    // waits for the products with P of the group's last tile
+    auto wait_pv = [&]() {
+      warp_wait(&ctl.pv_done[grp * NB + (kb ? kb - 1 : NB - 1)], kb ? kp : kp ^ 1);
+    };
     for (uint32_t seg = 0;; ++seg) {
       const Seg s = fetch(seg);
       // all of them go on, or none: they meet at named barriers below
@@ -659,36 +689,47 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
       // tile i: scores from tensor memory, P back into it
       auto tile = [&](auto tail_tag, int i) {
         constexpr bool kTail = decltype(tail_tag)::value;
-        const uint32_t t = tS + (i & 3) * kTreeKeys;
+        const uint32_t t = tS + (grp * NB + kb) * kTreeKeys;
+        // Two halves of 32 keys: one's scores arrive while the other's are worked on.
         float x[2][32];
-        tmem_ld32(t, x[0]);
-        tmem_ld32(t + 32, x[1]);
-        tmem_ld_wait();
-        if constexpr (kTail) {
+        auto mask = [&](int h) {
+          if constexpr (kTail) {
 #pragma unroll
-          for (int e = 0; e < 64; ++e)
-            x[e >> 5][e & 31] = (vis[e >> 5] >> (e & 31) & 1) ? x[e >> 5][e & 31] : -INFINITY;
-        }
+            for (int e = 0; e < 32; ++e) x[h][e] = (vis[h] >> e & 1) ? x[h][e] : -INFINITY;
+          }
+        };
+        float2 sums[2];
+        auto probabilities = [&](int h, float sub) {
+          uint32_t y[16];
+          const float2 scale = make_float2(a.scale_log2, a.scale_log2), minus = make_float2(-sub, -sub);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float2 z = fma2(make_float2(x[h][2 * e], x[h][2 * e + 1]), scale, minus);
+            const float2 p = make_float2(ex2_approx(z.x), ex2_approx(z.y));
+            sums[e & 1] = add2(sums[e & 1], p);
+            y[e] = pack_p(p.x, p.y);
+          }
+          tmem_st16(t + 16 * h, y);
+        };
         // The probabilities relative to the maximum so far, before the tile's
         // own maximum is known: most tiles do not raise it by 2^8, and neither
         // chain then waits for the other.
-        float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, sums[4];
-        uint32_t y[2][16];
-        auto probabilities = [&](float sub) {
+        sums[0] = sums[1] = make_float2(0.f, 0.f);
+        tmem_ld32(t, x[0]);
+        tmem_ld32(t + 32, x[1]);
+        tmem_ld_wait32(x[0]);
+        mask(0);
+        probabilities(0, m);
+        float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int q = 0; q < 4; ++q) sums[q] = 0.f;
+        for (int e = 0; e < 16; ++e)
+          tops[e & 3] = fmaxf(tops[e & 3], fmaxf(x[0][2 * e], x[0][2 * e + 1]));
+        tmem_ld_wait32(x[1]);
+        mask(1);
+        probabilities(1, m);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const float p0 = ex2_approx(fmaf(x[e >> 4][2 * (e & 15)], a.scale_log2, -sub));
-            const float p1 = ex2_approx(fmaf(x[e >> 4][2 * (e & 15) + 1], a.scale_log2, -sub));
-            sums[e & 3] += p0 + p1;
-            y[e >> 4][e & 15] = pack_p(p0, p1);
-          }
-        };
-        probabilities(m);
-#pragma unroll
-        for (int e = 0; e < 32; ++e)
-          tops[e & 3] = fmaxf(tops[e & 3], fmaxf(x[e >> 4][2 * (e & 15)], x[e >> 4][2 * (e & 15) + 1]));
+        for (int e = 0; e < 16; ++e)
+          tops[e & 3] = fmaxf(tops[e & 3], fmaxf(x[1][2 * e], x[1][2 * e + 1]));
         const float top =
             fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * a.scale_log2;
         const bool rise = top > m + kRescaleLog2 || m == -INFINITY;
@@ -696,8 +737,7 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
           const float mn = rise ? top : m;
           if (i >= 2) {
             const float al = rise && top > m ? ex2_approx(m - mn) : 1.f;  // m = -inf: 0
-            const int k = (i - 2) & 3;
-            warp_wait(&ctl.pv_done[k], (par >> k & 1) ^ 1);
+            wait_pv();
             tc_fence_after();
 #pragma unroll 1
             for (int q = 0; q < D / 16; ++q) {
@@ -713,19 +753,20 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
           }
           m = mn;
           // masked scores: exp2(-inf - sub) = 0
-          probabilities(m == -INFINITY ? 0.f : m);
+          const float sub = m == -INFINITY ? 0.f : m;
+          sums[0] = sums[1] = make_float2(0.f, 0.f);
+          probabilities(0, sub);
+          probabilities(1, sub);
         }
-        tmem_st16(t, y[0]);
-        tmem_st16(t + 16, y[1]);
-        l += (sums[0] + sums[1]) + (sums[2] + sums[3]);
+        l += (sums[0].x + sums[0].y) + (sums[1].x + sums[1].y);
         tmem_st_wait();
       };
       for (int i = grp; i < n; i += 2) {
-        const int key0 = (s.k0 + i) * kTreeKeys, k = i & 3;
+        const int key0 = (s.k0 + i) * kTreeKeys, k = grp * NB + kb;
         const bool tail = key0 + kTreeKeys > s.old;
         // (Scores first: with them, the fill before this one in V's place was
         // consumed.)
-        warp_wait(&ctl.s_full[k], par >> k & 1);
+        warp_wait(&ctl.s_full[k], kp);
         tc_fence_after();
         if (tail) {
           // V of keys behind the end and non-finite V of new tokens: two
@@ -742,14 +783,13 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
 #pragma unroll
             for (int ch = 0; ch < D / 16; ++ch) *chunk(ch) = make_uint4(0, 0, 0, 0);
           } else if (key >= s.old) {
-            bool found = false;
+            uint32_t found = 0;
 #pragma unroll
             for (int ch = 0; ch < D / 16; ++ch) {
               const uint4 w = *chunk(ch);
-              found = found || has_nonfinite(w.x) || has_nonfinite(w.y) || has_nonfinite(w.z) ||
-                      has_nonfinite(w.w);
+              found |= nonfinite2(w.x) | nonfinite2(w.y) | nonfinite2(w.z) | nonfinite2(w.w);
             }
-            if (found) {
+            if (found & 0x80008000u) {
               ctl.poison[seg & 1] = 1;
               for (int ch = 0; ch < D / 16; ++ch) {
                 uint4* p = chunk(ch);
@@ -758,7 +798,6 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
               }
             }
           }
-          // what the thread's row sees, before the scores are there
           vis[0] = sees32(a, s, tok, key0);
           vis[1] = sees32(a, s, tok, key0 + 32);
           fence_proxy_async_smem();
@@ -767,7 +806,7 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
           if (tail) tile(std::true_type(), i);
           else tile(std::false_type(), i);
         }
-        par ^= 1u << k;
+        if (++kb == NB) { kb = 0; kp ^= 1; }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl.p_ready[k]);
@@ -775,10 +814,7 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
 
       // The two groups' states meet, and each takes one half of the head's
       // elements of both O.
-      if (n > grp) {
-        const int k = (n - 1 - ((n - 1 - grp) & 1)) & 3;  // the group's last tile
-        warp_wait(&ctl.pv_done[k], (par >> k & 1) ^ 1);
-      }
+      if (n > grp) wait_pv();
       meet[grp * kTreeRows + r] = make_float2(m, l);
       bar_sync(1, kTreeSoftmax);
       tc_fence_after();
@@ -799,34 +835,31 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
         }
         const bool poison = ctl.poison[seg & 1] != 0;
 #pragma unroll 1
-        for (int q = 0; q < D / 32; ++q) {  // 16 elements a turn
-          const int e0 = grp * (D / 2) + 16 * q;
-          float o0[16], o1[16];
-          tmem_ld16(tmem + lanes + 256 + e0, o0);
-          tmem_ld16(tmem + lanes + 256 + D + e0, o1);
-          tmem_ld_wait();
+        for (int q = 0; q < D / 64; ++q) {  // 32 elements a turn
+          const int e0 = grp * (D / 2) + 32 * q;
+          float o0[32], o1[32];
+          tmem_ld32(tmem + lanes + kColO + e0, o0);
+          tmem_ld32(tmem + lanes + kColO + D + e0, o1);
+          tmem_ld_wait32(o0);
+          tmem_ld_wait32(o1);
           // a state without keys may stand next to anything in tensor memory
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
+          for (int e = 0; e < 32; ++e)
             o0[e] = (w0 != 0.f ? o0[e] * w0 : 0.f) + (w1 != 0.f ? o1[e] * w1 : 0.f);
-          if (poison && live)
-            nonfinite_v(a, s, tok, e0, o0);
+          if (poison && live) nonfinite_v(a, s, tok, e0, o0);
           if (whole) {
             // through shared memory: rows of o leave as whole lines
-            uint32_t y[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = pack_p(o0[2 * e], o0[2 * e + 1]);
-            uint8_t* row = sOut + r * D * 2;
-            const int c0 = e0 >> 3;
-            *reinterpret_cast<uint4*>(row + ((c0 ^ (r & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
-            *reinterpret_cast<uint4*>(row + (((c0 + 1) ^ (r & 7)) << 4)) =
-                make_uint4(y[4], y[5], y[6], y[7]);
+            for (int e = 0; e < 32; e += 8)
+              *reinterpret_cast<uint4*>(sOut + r * D * 2 + ((((e0 + e) >> 3) ^ (r & 7)) << 4)) =
+                  make_uint4(pack_p(o0[e], o0[e + 1]), pack_p(o0[e + 2], o0[e + 3]),
+                             pack_p(o0[e + 4], o0[e + 5]), pack_p(o0[e + 6], o0[e + 7]));
           } else {
             // [4 elements][row]: a warp's stores are contiguous
             float4* dst = reinterpret_cast<float4*>(a.partials + piece * kTreeRows * D) +
                           (e0 >> 2) * kTreeRows + r;
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
+            for (int e = 0; e < 8; ++e)
               dst[e * kTreeRows] = make_float4(o0[4 * e], o0[4 * e + 1], o0[4 * e + 2], o0[4 * e + 3]);
           }
         }
