@@ -299,14 +299,13 @@ __device__ __forceinline__ uint32_t drop_nonfinite(uint32_t x) {
 
 // Joins the pieces of an item, in key order, into the rows of o in shared
 // memory.  Eight warps share the blocks of 32 rows: lane = row, and a warp takes
-// groups of 4 elements, eight at a time, with the loads of two pieces in flight.
+// kPer groups of 4 elements at a time, with the loads of kBatch pieces in flight.
 // (Not inlined: the softmax loops stay together in the instruction cache.)
-template <int D>
+template <int D, int kPer, int kBatch>
 __device__ __noinline__ void join_pieces(const TreeAttnArgs& a, const Seg& s, int rows, int w, int lane,
                                          uint8_t* sOut) {
   const int blocks = (rows + 31) >> 5;
-  auto piece = [&](int p) { return (int64_t)p * 2 + (p == s.first ? s.slot : 0); };
-  constexpr int kPer = 8, kTurns = D / 4 / kPer;  // groups at a time; turns of a block
+  constexpr int kTurns = D / 4 / kPer;  // turns of a block
   for (int t = w; t < blocks * kTurns; t += 8) {
     const int r = (t % blocks) * 32 + lane, g0 = t / blocks * kPer;
     const bool on = r < rows;
@@ -314,37 +313,47 @@ __device__ __noinline__ void join_pieces(const TreeAttnArgs& a, const Seg& s, in
     float4 o[kPer];
 #pragma unroll
     for (int q = 0; q < kPer; ++q) o[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-    // (the running maximum: one round of loads a piece, not two)
-#pragma unroll 2
-    for (int p = s.first; p <= s.last; ++p) {
-      const int64_t at = piece(p);
-      const float2 ml = on ? __ldcg(&a.ml[at * kTreeRows + r]) : make_float2(-INFINITY, 0.f);
-      const float4* src = reinterpret_cast<const float4*>(a.partials + at * kTreeRows * D) + r;
-      float4 y[kPer];
+    for (int p0 = s.first; p0 <= s.last; p0 += kBatch) {
+      float2 ml[kBatch];
+      float4 y[kBatch][kPer];
 #pragma unroll
-      for (int q = 0; q < kPer; ++q)
-        y[q] = on ? __ldcg(src + (g0 + q) * kTreeRows) : make_float4(0.f, 0.f, 0.f, 0.f);
-      const float Mn = fmaxf(M, ml.x);
+      for (int b = 0; b < kBatch; ++b) {
+        const int64_t at = (int64_t)(p0 + b) * 2 + (p0 + b == s.first ? s.slot : 0);
+        const bool here = on && p0 + b <= s.last;
+        const float4* src = reinterpret_cast<const float4*>(a.partials + at * kTreeRows * D) + r;
+        ml[b] = here ? __ldcg(&a.ml[at * kTreeRows + r]) : make_float2(-INFINITY, 0.f);
+#pragma unroll
+        for (int q = 0; q < kPer; ++q)
+          y[b][q] = here ? __ldcg(src + (g0 + q) * kTreeRows) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      float Mn = M;
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) Mn = fmaxf(Mn, ml[b].x);
       const float u = M == -INFINITY ? 0.f : ex2_approx(M - Mn);
-      const float v = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - Mn);
       M = Mn;
-      L = L * u + ml.y * v;
+      L *= u;
 #pragma unroll
-      for (int q = 0; q < kPer; ++q) {
-        o[q].x = o[q].x * u + y[q].x * v;
-        o[q].y = o[q].y * u + y[q].y * v;
-        o[q].z = o[q].z * u + y[q].z * v;
-        o[q].w = o[q].w * u + y[q].w * v;
+      for (int q = 0; q < kPer; ++q) o[q] = make_float4(o[q].x * u, o[q].y * u, o[q].z * u, o[q].w * u);
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const float v = ml[b].x == -INFINITY ? 0.f : ex2_approx(ml[b].x - Mn);
+        L += ml[b].y * v;
+#pragma unroll
+        for (int q = 0; q < kPer; ++q) {
+          o[q].x += y[b][q].x * v;
+          o[q].y += y[b][q].y * v;
+          o[q].z += y[b][q].z * v;
+          o[q].w += y[b][q].w * v;
+        }
       }
     }
     const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
     if (on) {
+      uint2* dst = reinterpret_cast<uint2*>(sOut + r * D * 2);
 #pragma unroll
-      for (int q = 0; q < kPer; q += 2)  // the 16-byte chunks of a row are swizzled by row
-        *reinterpret_cast<uint4*>(sOut + r * D * 2 + ((((g0 + q) >> 1) ^ (r & 7)) << 4)) =
-            make_uint4(pack_p(o[q].x * inv, o[q].y * inv), pack_p(o[q].z * inv, o[q].w * inv),
-                       pack_p(o[q + 1].x * inv, o[q + 1].y * inv),
-                       pack_p(o[q + 1].z * inv, o[q + 1].w * inv));
+      for (int q = 0; q < kPer; ++q)  // the 16-byte chunks of a row are swizzled by row
+        dst[((((g0 + q) >> 1) ^ (r & 7)) << 1) + ((g0 + q) & 1)] =
+            make_uint2(pack_p(o[q].x * inv, o[q].y * inv), pack_p(o[q].z * inv, o[q].w * inv));
     }
   }
 }
@@ -880,7 +889,12 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
         bar_sync(1, kTreeSoftmax);
         finish = ctl.last != 0;
         if (finish) {
-          join_pieces<D>(a, s, rows, tid >> 5, lane, sOut);
+          // Few rows, as single tokens have, are cut finer, so that every warp has
+          // some, and mostly lie in more pieces (14.2 us for one token behind 700
+          // instead of 15.7 with the other; that one 38 us for the trees above,
+          // not 40).
+          if (rows <= 32) join_pieces<D, 4, 4>(a, s, rows, tid >> 5, lane, sOut);
+          else join_pieces<D, 8, 2>(a, s, rows, tid >> 5, lane, sOut);
           bar_sync(1, kTreeSoftmax);
         }
       }
