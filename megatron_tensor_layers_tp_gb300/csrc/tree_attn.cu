@@ -12,24 +12,27 @@
 // one tile per sequence and KV head the cache's bytes bound the kernel: a
 // 64-key tile of K and V (32 KB at d = 128) takes an SM 0.73 us at its share of
 // the memory rate, its two products 0.14 us and its exponentials 0.2 us.  With
-// many tiles the softmax threads do: their 128 x 64 scores take about as long
-// as the memory would.
+// many tiles (chunks) the round trip of a tile does: scores -> probabilities ->
+// P V -> the buffer's next scores, 0.4-0.5 us a tile over all buffers.  Short
+// calls are bound by what a part of an item costs besides its tiles (about 5 us:
+// the first copies, the groups' meeting, the pieces) and by the join (1.5-3 us).
 //
 // Measured: one token behind 700 old ones, 32 heads of 128 over 8 KV heads:
-// 16 us; 16 trees of 8-32 tokens behind 150-2048, 40 heads over 8 (80 MB): 40 us;
-// 64 trees of 2-8 tokens behind 1500-4096, 32 heads over 8 (740 MB): 123 us,
-// 6.0 TB/s; 6 chunks of 100-256 tokens behind up to 8000, 32 heads of 64 over 4
-// (36 GFLOP): 109 us.
+// 14 us; 16 trees of 8-32 tokens behind 150-2048, 40 heads over 8 (80 MB): 38 us;
+// 64 trees of 2-8 tokens behind 1500-4096, 32 heads over 8 (740 MB): 120 us,
+// 6.1 TB/s; 6 chunks of 100-256 tokens behind up to 8000, 32 heads of 64 over 4
+// (64 GFLOP in whole tiles): 99 us, 650 TFLOP/s.
 //
 // Work is the flat sequence of (sequence, KV head, query tile, key tile), an
 // item's fixed work counted as kItemCost tiles more, split evenly over one CTA
 // per SM.  A CTA finds its range from the lengths on the GPU, so a captured
-// launch follows them.  An item cut between CTAs leaves
-// unnormalised fp32 pieces, and the last CTA to finish one (a ticket, no
-// waiting) joins them in key order: deterministic.  The pieces lie [4 elements]
-// [row], so that lane = row reads and writes whole lines with every load in
-// flight (a second kernel for the join cost 3-5 us a call; the join with rows
-// of pieces and loads one after another, 50).
+// launch follows them.  An item cut between CTAs leaves unnormalised fp32
+// pieces, and the last CTA to finish one (a ticket, no waiting) joins them in
+// key order: deterministic.  The pieces lie [4 elements][row], so that lane =
+// row reads and writes whole lines with every load in flight (a second kernel
+// for the join cost 3-5 us a call; the join with rows of pieces and loads one
+// after another, 50; joined rows straight into o instead of through shared
+// memory, 3).
 //
 // Roles of the 20 warps:
 //   warps 0-3  : K and V tiles by TMA into rings, through the page table, each
@@ -43,7 +46,7 @@
 //                contiguous).  Issuing costs about 65 cycles a product, 80 a
 //                commit and 100-150 a wait: one thread for all products set the
 //                pace (1850-2000 cycles a tile, nothing else busy), and so did
-//                one for both groups' S (1300; the chunks below 134 us, not 109);
+//                one for both groups' S (1300; the chunks above 134 us instead of 109);
 //   warp 8     : the CTA's parts of items, announced to the other warps two
 //                ahead, and the next item's query tile while this one's softmax
 //                ends.  (Every role finding the parts by itself spilled
@@ -53,12 +56,11 @@
 //                waits for the other's maxima; the two states meet at the
 //                item's end.  A thread owns a row and holds a tile's 64 scores
 //                in registers.
-// Each group has two S buffers: the products of its next tile run while it
-// works on this one.  Measured with 128-key tiles and one buffer a group, the
-// chain scores -> exponentials -> P V -> next scores left the SM waiting: an
-// 8000-key chunk of 64-element heads took 172 us instead of 134.  Two warpgroups
-// a group, each with half of a tile's keys: 159 instead of 134, the issuing
-// threads waiting longer for their turns.
+// Each group has two S buffers, three where tensor memory holds them (heads of
+// 64): the products of its next tiles run while it works on this one.  (One
+// buffer and 128-key tiles: 172 us for the chunks when two took 134; two instead
+// of three: 113, not 110.  Two warpgroups a group, each with half of a tile's
+// keys: 159 when one took 134, the issuing threads waiting for their turns.)
 // P overwrites S in place (bf16, half the columns).  O is rescaled only when a
 // row's maximum rose by more than 2^8 since its last rescaling: the sums are
 // relative to the older maximum until then, which is exact algebra and keeps
@@ -88,7 +90,9 @@ constexpr int kTreeFirst = kTreeThreads - kTreeSoftmax;
 // brought (checked by the host, since a take-over beyond it would never end)
 constexpr int kTreeRegsOther = 64, kTreeRegsSoftmax = 144;
 constexpr float kRescaleLog2 = 8.f;
-constexpr int kItemCost = 12;             // an item's fixed work in key tiles
+// An item's fixed work in key tiles (the chunks: 105 us with 8, 99 with 12 and
+// 16; 64 long sequences: 119, 120, 122).
+constexpr int kItemCost = 12;
 constexpr int kMaxGrid = 1024;
 
 // One CTA's part of an item: key tiles [k0, k1) of nt of (sequence b, KV head
