@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) process_logits_kern
     bool bad = false;
     if (w.r < 0 || w.r >= a.n_reqs) {
       bad = w.r != -1;
-      w.r = -1;
+      w.r = w.m = -1;  // nothing of the row is looked up
     } else {
       if (a.allowed && (w.m < -1 || w.m >= a.n_allowed)) {
         bad = true;

@@ -814,6 +814,27 @@ def test_process_logits_bad_indices():
     assert m.check_device() == 0
 
 
+@pytest.mark.parametrize("rows", [4, 400])
+def test_process_logits_rows_left_alone_are_not_looked_up(rows):
+    """A padding row's other indices may hold anything."""
+    rng = np.random.default_rng(55)
+    V = 40000
+    m = model(8, 2, 64, 2, V)
+    x = bf16(rng, rows, V)
+    req = np.where(np.arange(rows) % 2, -1, 0)
+    which = np.where(req < 0, 2**30, 0)
+    allowed = torch.full((1, R.ceil_div(V, 32)), -1, dtype=torch.int32, device="cuda")
+    rules = LogitRules(row_req=i32(req), n_reqs=1, allowed=allowed, allowed_row=i32(which),
+                       presence=torch.ones(1).cuda(), history=i32([[7, 9]]), history_lens=i32([2]))
+    out = torch.full((rows, V), 3.0, device="cuda")
+    m.process_logits(x, rules, out=out)
+    assert torch.all(out[1::2] == 3.0)
+    want = x[0::2].float()
+    want[:, [7, 9]] -= 1.0
+    assert torch.equal(out[0::2], want)
+    assert m.check_device() == 0
+
+
 # ---------------------------------------------------------------------------
 # refusals
 # ---------------------------------------------------------------------------
