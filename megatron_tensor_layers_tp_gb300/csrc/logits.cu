@@ -234,11 +234,10 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) process_logits_kern
       for (int i = 4 * quads + tid; i < len_c; i += kThreads) mark(i, h[i]);
     }
     if (a.bias_start) {
-      const int b0 = a.bias_start[r];
-      int b1 = a.bias_start[r + 1];
+      int b0 = a.bias_start[r], b1 = a.bias_start[r + 1];
       if (b0 < 0 || b1 < b0 || b1 > a.n_biases) {
         if (tid == 0) record_status(a.status, kStatusTableRange);
-        b1 = b0;
+        b0 = b1 = 0;  // (counting on from any b0 could overflow)
       }
       // Entries of tokens named once need no order.  How often a token is named
       // is counted in its place in the bias array.

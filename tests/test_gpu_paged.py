@@ -814,6 +814,40 @@ def test_process_logits_bad_indices():
     assert m.check_device() == 0
 
 
+@pytest.mark.parametrize("start", [[2**31 - 1, 2**31 - 1], [2**31 - 1, 3], [-(2**31), 2**31 - 1], [0, 2**31 - 1]])
+def test_process_logits_bias_ranges_outside(start):
+    rng = np.random.default_rng(56)
+    m = model(8, 2, 64, 2)
+    x = bf16(rng, 1, 1000)
+    rules = LogitRules(n_reqs=1, bias_start=i32(start), bias_ids=i32([1, 2, 3]),
+                       bias_values=torch.ones(3).cuda())
+    got = m.process_logits(x, rules)
+    bad = start[0] < 0 or start[1] < start[0] or start[1] > 3
+    assert m.check_device() == (TABLE_RANGE if bad else 0)
+    assert torch.equal(got, x.float())
+
+
+@pytest.mark.parametrize("n", [40, 300, 700, 2000])
+def test_process_logits_many_biases(n):
+    """More biases than a CTA's threads keep, tokens named once and several times."""
+    rng = np.random.default_rng(57)
+    V = 40000
+    m = model(8, 2, 64, 2, V)
+    x = bf16(rng, 2, V)
+    ids = rng.integers(0, V, (2, n))
+    ids[1, n // 2:] = ids[1, :n - n // 2]
+    vals = rng.standard_normal((2, n)).astype(np.float32)
+    rules = LogitRules(n_reqs=2, bias_start=i32([0, n, 2 * n]), bias_ids=i32(ids.reshape(-1)),
+                       bias_values=torch.from_numpy(vals.reshape(-1)).cuda())
+    got = m.process_logits(x, rules).cpu().numpy()
+    for r in range(2):
+        add = np.zeros(V, dtype=np.float32)
+        for i, y in zip(ids[r], vals[r]):
+            add[i] += y  # in the list's order, as documented
+        assert np.array_equal(got[r], x[r].float().cpu().numpy() + add)
+    assert m.check_device() == 0
+
+
 @pytest.mark.parametrize("rows", [4, 400])
 def test_process_logits_rows_left_alone_are_not_looked_up(rows):
     """A padding row's other indices may hold anything."""
