@@ -249,9 +249,10 @@ __device__ __forceinline__ int page_of(const TreeAttnArgs& a, int b, int pg) {
 }
 
 // Infinities and NaN among the V elements e0 .. e0 + 31 of the new tokens that
-// row i sees in the part's keys: added to the row's o.
+// row i sees in the part's keys: what they add to the row's o.
 __device__ __noinline__ void nonfinite_v(const TreeAttnArgs& a, const Seg& s, int i, int e0,
                                          float (&o)[32]) {
+  for (int e = 0; e < 32; ++e) o[e] = 0.f;
   const int g = s.g, end = min(s.k1 * kTreeKeys, s.old + s.T);
   for (int j = max(s.k0 * kTreeKeys, s.old); j < end; ++j) {
     if (!(sees32(a, s, i, j) & 1)) continue;
@@ -859,7 +860,12 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
 #pragma unroll
           for (int e = 0; e < 32; ++e)
             o0[e] = (w0 != 0.f ? o0[e] * w0 : 0.f) + (w1 != 0.f ? o1[e] * w1 : 0.f);
-          if (poison && live) nonfinite_v(a, s, tok, e0, o0);
+          if (poison && live) {
+            float add[32];  // (its own array: o0 stays in registers)
+            nonfinite_v(a, s, tok, e0, add);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o0[e] += add[e];
+          }
           if (whole) {
             // through shared memory: rows of o leave as whole lines
 #pragma unroll
