@@ -14,14 +14,14 @@
 // the memory rate, its two products 0.14 us and its exponentials 0.2 us.  With
 // many tiles (chunks) the round trip of a tile does: scores -> probabilities ->
 // P V -> the buffer's next scores, 0.4-0.5 us a tile over all buffers.  Short
-// calls are bound by what a part of an item costs besides its tiles (about 5 us:
+// calls are bound by what a part of an item costs besides its tiles (4-5 us:
 // the first copies, the groups' meeting, the pieces) and by the join (1.5-3 us).
 //
 // Measured: one token behind 700 old ones, 32 heads of 128 over 8 KV heads:
-// 14 us; 16 trees of 8-32 tokens behind 150-2048, 40 heads over 8 (80 MB): 38 us;
+// 14 us; 16 trees of 8-32 tokens behind 150-2048, 40 heads over 8 (80 MB): 36 us;
 // 64 trees of 2-8 tokens behind 1500-4096, 32 heads over 8 (740 MB): 120 us,
 // 6.1 TB/s; 6 chunks of 100-256 tokens behind up to 8000, 32 heads of 64 over 4
-// (64 GFLOP in whole tiles): 99 us, 650 TFLOP/s.
+// (64 GFLOP in whole tiles): 96 us, 670 TFLOP/s.
 //
 // Work is the flat sequence of (sequence, KV head, query tile, key tile), an
 // item's fixed work counted as kItemCost tiles more, split evenly over one CTA
@@ -847,6 +847,7 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
           w0 *= inv;
           w1 *= inv;
         }
+        const uint32_t keep0 = w0 != 0.f ? ~0u : 0u, keep1 = w1 != 0.f ? ~0u : 0u;
         const bool poison = ctl.poison[seg & 1] != 0;
 #pragma unroll 1
         for (int q = 0; q < D / 64; ++q) {  // 32 elements a turn
@@ -859,10 +860,11 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
           // a state without keys may stand next to anything in tensor memory
 #pragma unroll
           for (int e = 0; e < 32; ++e)
-            o0[e] = (w0 != 0.f ? o0[e] * w0 : 0.f) + (w1 != 0.f ? o1[e] * w1 : 0.f);
+            o0[e] = fmaf(__uint_as_float(__float_as_uint(o0[e]) & keep0), w0,
+                         __uint_as_float(__float_as_uint(o1[e]) & keep1) * w1);
           if (poison && live) {
             float add[32];  // (its own array: o0 stays in registers)
-            nonfinite_v(a, s, tok, e0, add);
+            nonfinite_v(a, ctl.seg[seg & 3], tok, e0, add);
 #pragma unroll
             for (int e = 0; e < 32; ++e) o0[e] += add[e];
           }
@@ -903,8 +905,8 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
           // some, and mostly lie in more pieces (14.2 us for one token behind 700
           // instead of 15.7 with the other; that one 38 us for the trees above,
           // not 40).
-          if (rows <= 32) join_pieces<D, 4, 4>(a, s, rows, tid >> 5, lane, sOut);
-          else join_pieces<D, 8, 2>(a, s, rows, tid >> 5, lane, sOut);
+          if (rows <= 32) join_pieces<D, 4, 4>(a, ctl.seg[seg & 3], rows, tid >> 5, lane, sOut);
+          else join_pieces<D, 8, 2>(a, ctl.seg[seg & 3], rows, tid >> 5, lane, sOut);
           bar_sync(1, kTreeSoftmax);
         }
       }
