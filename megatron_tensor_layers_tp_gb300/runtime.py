@@ -288,6 +288,7 @@ class TPModel:
         self._copies, self._kv_heads, self._dim = cfg.kv_copies, cfg.kv_heads_per_rank, cfg.head_dim
         self._vocab = cfg.vocab
         self.step_ws = None
+        self._step_cover = (0, -1)  # sequences and new tokens that it is large enough for
         self._old_step_ws = []
         self.ensure_workspace(max_tokens, stream)
 
@@ -456,6 +457,8 @@ class TPModel:
 
     def ensure_step_workspace(self, n_seqs: int, max_new: int, stream=None) -> torch.Tensor:
         """The model's own step workspace, grown when too small (not inside a graph capture)."""
+        if 0 < n_seqs <= self._step_cover[0] and 0 <= max_new <= self._step_cover[1]:
+            return self.step_ws
         n = B.tp_step_workspace_bytes(self.handle, n_seqs, max_new)
         if self.step_ws is None or self.step_ws.numel() < n or n == 0:
             if torch.cuda.is_current_stream_capturing():
@@ -464,6 +467,7 @@ class TPModel:
             if self.step_ws is not None:
                 self._old_step_ws.append(self.step_ws)  # captured graphs may still use it
             self.step_ws = ws
+            self._step_cover = (n_seqs, max_new)
         return self.step_ws
 
     def _stream(self, stream) -> int:
@@ -509,8 +513,7 @@ class TPModel:
         _check(qkv, "qkv", torch.bfloat16, (self._ranks, M, self._qkv_cols), dev)
         _check(positions, "positions", torch.int32, (M,), dev)
         _check(slots, "slots", torch.int32, (M,), dev)
-        self._check_pool(k, "k", pages)
-        self._check_pool(v, "v", pages)
+        self._check_pools(k, v, pages)
         if q is not None:
             _check(q, "q", torch.bfloat16, (M, self._width), dev, rows=True)
         elif want_q:
@@ -533,8 +536,7 @@ class TPModel:
                 t.device != self.device or step.old_lens.device != self.device:
             raise ValueError("tree_attention needs q_start and a table row for every sequence, on "
                              "the model's device")
-        self._check_pool(k, "k", pages)
-        self._check_pool(v, "v", pages)
+        self._check_pools(k, v, pages)
         if out is None:
             out = self._out(shape, torch.bfloat16, stream)
         else:
@@ -546,9 +548,10 @@ class TPModel:
                                     ws.numel(), self._stream(stream)), "tp_tree_attention")
         return out
 
-    def _check_pool(self, t: torch.Tensor, name: str, pages: PageTable) -> None:
-        _check(t, name, torch.bfloat16, (self._copies, pages.n_pages, self._kv_heads,
-                                         pages.page_size, self._dim), self.device)
+    def _check_pools(self, k: torch.Tensor, v: torch.Tensor, pages: PageTable) -> None:
+        shape = (self._copies, pages.n_pages, self._kv_heads, pages.page_size, self._dim)
+        _check(k, "k", torch.bfloat16, shape, self.device)
+        _check(v, "v", torch.bfloat16, shape, self.device)
 
     def process_logits(self, logits: torch.Tensor, rules: LogitRules,
                        out: Optional[torch.Tensor] = None, dtype=torch.float32,

@@ -1211,6 +1211,11 @@ def test_workspace_does_not_grow_inside_a_capture():
         m.step_workspace(8193, 4)
     first = m.ensure_step_workspace(4, 4)
     assert m.ensure_step_workspace(1, 1) is first
+    larger = m.ensure_step_workspace(8000, 256)
+    assert larger is not first and larger.numel() == B.tp_step_workspace_bytes(m.handle, 8000, 256)
+    assert m.ensure_step_workspace(8000, 256) is larger and m.ensure_step_workspace(2, 7) is larger
+    with pytest.raises(ValueError):
+        m.ensure_step_workspace(0, 4)
 
 
 def test_counters_and_profile_names():
