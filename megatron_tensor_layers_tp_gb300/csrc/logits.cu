@@ -13,23 +13,25 @@
 // them (50 us instead of 47 for the rows below).
 //
 // What a request's text, biases and drafted path touch of a slice is little.
-// The CTA marks it in shared memory (integer atomics: their order does not
-// matter; 16 bits a token, or 32 where a text is long enough to overflow them)
-// and lists it: once for as many rows as belong to the same request, a row's
-// path added and taken out again.  All tokens then stream through as copies
-// with the mask applied, a few instructions each, and the listed ones are
-// written over with the rules applied, one thread each, while their lines are
-// still in the caches.
+// All tokens stream through first, as copies with the mask applied, a few
+// instructions each.  Meanwhile the CTA marks the touched tokens in shared memory
+// (integer atomics: their order does not matter; 16 bits a token, or 32 where a
+// text is long enough to overflow them) and lists them: once for as many rows as
+// belong to the same request, a row's path added and taken out again.  The listed
+// ones are then written over with the rules applied, one thread each, while their
+// lines are still in the caches.  (In place the copies change only what is not
+// allowed, so the listed tokens' logits are still there.)
 //
 // 256 rows (16 trees) of 152064 logits, texts of 1500 tokens, 300 biases, bf16:
-// 47 us, 3.4 TB/s; the stream alone would take 32.  Measured before: the rules
-// applied in the stream, a slice a CTA: 110 us; the touched tokens in a second
-// kernel behind the stream: 55 us, since their lines come from memory again.
-// 64 rows of 128256 with texts of 4096 tokens, fp32: 23 us, 2.2 TB/s; there the
-// text's way into the marks (some 4 us a CTA) binds.
+// 45.5 us, 3.5 TB/s; the stream alone takes 29.  Measured before: marks before the
+// stream: 47; the rules applied in the stream, a slice a CTA: 110 us; the touched
+// tokens in a second kernel behind the stream: 55 us, since their lines come from
+// memory again; rows through shared memory by asynchronous copies, three ahead: 63.
+// 64 rows of 128256 with texts of 4096 tokens, fp32: 21 us, 2.3 TB/s (the stream
+// alone 10.5); there the text's way into the marks binds.
 //
 // Slices have 4096 tokens, 8192 where texts are long (their reading is repeated
-// for every slice: 23 us instead of 33 at 4096 tokens, but 65 instead of 47 at
+// for every slice: 21 us instead of 30 at 4096 tokens, but 65 instead of 47 at
 // 1500), 2048 where there are too few rows to fill the GPU.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -96,8 +98,7 @@ struct LogitsSmem {
   static constexpr int kSlice = kThreads * kPer;
   static constexpr int kMarks = 16 + kLogRows * sizeof(RowInfo);  // after the count and the rows
   static constexpr int kList = kMarks + kSlice * (kWide ? 4 : 2);
-  static constexpr int kRaw = kList + kSlice * 2;
-  static constexpr int kBias = kRaw + kSlice * 2;
+  static constexpr int kBias = kList + kSlice * 2;
   static constexpr int bytes(bool bias) { return kBias + (bias ? kSlice * 4 : 0); }
 };
 
@@ -111,7 +112,6 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) process_logits_kern
   RowInfo* info = reinterpret_cast<RowInfo*>(smem + 16);
   Marks<kWide> marks{reinterpret_cast<uint32_t*>(smem + SM::kMarks)};
   uint16_t* list = reinterpret_cast<uint16_t*>(smem + SM::kList);
-  uint16_t* raw = reinterpret_cast<uint16_t*>(smem + SM::kRaw);  // the listed tokens' logits
   float* bias = reinterpret_cast<float*>(smem + SM::kBias);      // with a.bias_start
   pdl_launch_dependents();
   pdl_wait();
@@ -223,13 +223,22 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) process_logits_kern
         if (v >= 0) enlist(v, i < pl_c ? marks.set(v, kMarkPrompt) : marks.add(v, kMarkWritten));
       };
       const int quads = (reinterpret_cast<uintptr_t>(h) & 15) ? 0 : len_c / 4;
-#pragma unroll 4
-      for (int i = tid; i < quads; i += kThreads) {
-        const int4 id = reinterpret_cast<const int4*>(h)[i];
-        mark(4 * i, id.x);
-        mark(4 * i + 1, id.y);
-        mark(4 * i + 2, id.z);
-        mark(4 * i + 3, id.w);
+      // Few tokens of a text lie in the slice: the thread finds which of its 16
+      // do, and then marks those alone (their ids once more, from L1), instead of
+      // taking part in its neighbours' marks 16 times.
+      for (int i0 = tid; i0 < quads; i0 += 4 * kThreads) {
+        uint32_t in_slice = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int i = i0 + k * kThreads;
+          const int4 id = i < quads ? reinterpret_cast<const int4*>(h)[i] : make_int4(-1, -1, -1, -1);
+          in_slice |= (uint32_t)((place(id.x) >= 0) | (place(id.y) >= 0) << 1 | (place(id.z) >= 0) << 2 |
+                                 (place(id.w) >= 0) << 3) << (4 * k);
+        }
+        for (; in_slice; in_slice &= in_slice - 1) {
+          const int e = __ffs(in_slice) - 1, i = 4 * (i0 + (e >> 2) * kThreads) + (e & 3);
+          mark(i, h[i]);
+        }
       }
       for (int i = 4 * quads + tid; i < len_c; i += kThreads) mark(i, h[i]);
     }
@@ -298,7 +307,6 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) process_logits_kern
     __syncthreads();
   };
 
-  const bool in_place = a.out == a.logits;
   const bool marked = a.history || a.draft_tokens || a.bias_start;
   RowPart<kPer> next = fetch(row0);
   int made = -1, own = 0;  // the request whose marks are there; its listed tokens
@@ -308,31 +316,6 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) process_logits_kern
     const RowInfo w = info[row - row0];
     if (row + 1 < row1) next = fetch(row + 1);
     if (w.r < 0) continue;
-    // (paths have up to 256 tokens: two a thread where a CTA has 128)
-    int far = -1;
-    if (marked) {
-      if (w.r != made) {
-        if (a.repetition) rep = a.repetition[w.r];
-        if (a.frequency) freq = a.frequency[w.r];
-        if (a.presence) pres = a.presence[w.r];
-        mark_request(w.r);
-        made = w.r;
-        own = *listed;
-        __syncthreads();  // own was read
-      }
-      if (a.draft_tokens) {
-        if (kThreads < kMaxTreeTokens) far = path_token(row, w, tid + kThreads);
-        if (p.path >= 0) enlist(p.path, marks.add(p.path, kMarkWritten));
-        if (far >= 0) enlist(far, marks.add(far, kMarkWritten));
-      }
-      if (in_place) {
-        __syncthreads();
-        const int many = *listed;
-        for (int i = tid; i < many; i += kThreads) raw[i] = in_of(row)[token(list[i])];
-        __syncthreads();  // before the stream writes over them
-      }
-    }
-
     uint8_t* out = out_of(row);
     if (vec_row(row)) {
 #pragma unroll
@@ -371,6 +354,21 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) process_logits_kern
     }
 
     if (marked) {
+      if (w.r != made) {
+        if (a.repetition) rep = a.repetition[w.r];
+        if (a.frequency) freq = a.frequency[w.r];
+        if (a.presence) pres = a.presence[w.r];
+        mark_request(w.r);
+        made = w.r;
+        own = *listed;
+        __syncthreads();  // own was read
+      }
+      int far = -1;  // (paths have up to 256 tokens: two a thread where a CTA has 128)
+      if (a.draft_tokens) {
+        if (kThreads < kMaxTreeTokens) far = path_token(row, w, tid + kThreads);
+        if (p.path >= 0) enlist(p.path, marks.add(p.path, kMarkWritten));
+        if (far >= 0) enlist(far, marks.add(far, kMarkWritten));
+      }
       __syncthreads();  // the stream is through, the list complete
       const int many = *listed;
       const uint16_t* in = in_of(row);
@@ -378,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) process_logits_kern
       for (int i = tid; i < many; i += kThreads) {
         const int at = list[i], v = token(at);
         const uint32_t mk = marks.get(at), times = mk / kMarkWritten;
-        float x = bf16_to_f(in_place ? raw[i] : in[v]);
+        float x = bf16_to_f(in[v]);  // (in place: as it was where it is allowed)
         if (times || (mk & kMarkPrompt)) x = x > 0.f ? x / rep : x * rep;
         if (times) x = x - freq * (float)times - pres;
         if (mk & kMarkBias) x += bias[at];
