@@ -8,11 +8,16 @@
 // loads and stores, both members of eight pairs in one thread), keeps the
 // eight rotation factors of its chunk in registers and walks over the heads,
 // two at a time.  V heads are the same two chunks, copied.  The rows' loads do
-// not depend on the token's position and slot and are issued first; the CTA
-// has as many threads as deal the heads out evenly.  8191 rows of 40 + 8 heads
-// of 128 (200 MB): 38 us, 5.2 TB/s (40.5 us with 256 threads and the position
-// first; 60 us with a CTA walking over tokens, the next row's loads ahead of
-// this one's stores; 40-74 us with fewer registers and more threads an SM).
+// not depend on the token's position and slot and are issued first; the CTA has
+// as many threads, up to 256 or 128, as deal the heads out evenly.
+//
+// While the rows fit the GPU at once, 256 threads take a row fastest (8 rows of
+// 32 + 16 heads of 128: 1.9 us, 2.3 with 128); beyond that smaller CTAs, more of
+// them on an SM and out of step with one another, keep the memory busier: 8191
+// rows of 40 + 8 heads of 128 (200 MB): 33.4 us, 6.0 TB/s, with 128 threads, 38.1
+// with 256 (64: the same); of 32 + 16 heads of 64: 18.9 and 25.8.  Measured
+// before: 60 us with a CTA walking over tokens, the next row's loads ahead of
+// this one's stores; 40-74 us with fewer registers and more threads an SM.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -22,7 +27,6 @@
 
 namespace tpk {
 
-constexpr int kAppThreads = 256;  // at most
 
 __device__ __forceinline__ void rotate8(uint4& lo, uint4& hi, const float2 (&cs)[8]) {
   uint32_t a[4] = {lo.x, lo.y, lo.z, lo.w}, b[4] = {hi.x, hi.y, hi.z, hi.w};
@@ -38,7 +42,8 @@ __device__ __forceinline__ void rotate8(uint4& lo, uint4& hi, const float2 (&cs)
   hi = make_uint4(b[0], b[1], b[2], b[3]);
 }
 
-__global__ void __launch_bounds__(kAppThreads) cache_append_kernel(const CacheAppendArgs a) {
+template <int kThreads>  // at most
+__global__ void __launch_bounds__(kThreads) cache_append_kernel(const CacheAppendArgs a) {
   pdl_launch_dependents();
   pdl_wait();
   const int token = blockIdx.x, d = a.head_dim, half = d / 2;
@@ -115,11 +120,16 @@ __global__ void __launch_bounds__(kAppThreads) cache_append_kernel(const CacheAp
   }
 }
 
-cudaError_t launch_cache_append(const CacheAppendArgs& a, cudaStream_t st) {
+template <int kThreads>
+static cudaError_t launch_append(const CacheAppendArgs& a, cudaStream_t st) {
   const int chunks = a.head_dim / 16, heads = (a.q ? a.n_heads : 0) + 2 * a.n_kv;
-  const int turns = (heads * chunks + kAppThreads - 1) / kAppThreads;
+  const int turns = (heads * chunks + kThreads - 1) / kThreads;
   const int lanes = (heads + turns - 1) / turns;  // heads at a time
-  return launch_k(cache_append_kernel, dim3(a.M), dim3(lanes * chunks), 0, st, a);
+  return launch_k(cache_append_kernel<kThreads>, dim3(a.M), dim3(lanes * chunks), 0, st, a);
+}
+
+cudaError_t launch_cache_append(const CacheAppendArgs& a, int num_sms, cudaStream_t st) {
+  return a.M > 4 * num_sms ? launch_append<128>(a, st) : launch_append<256>(a, st);
 }
 
 }  // namespace tpk

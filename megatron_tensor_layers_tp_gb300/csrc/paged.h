@@ -52,7 +52,7 @@ struct CacheAppendArgs {
   int max_positions;
   int* status;
 };
-cudaError_t launch_cache_append(const CacheAppendArgs& a, cudaStream_t st);
+cudaError_t launch_cache_append(const CacheAppendArgs& a, int num_sms, cudaStream_t st);
 
 struct TreeAttnArgs {
   CUtensorMap tmK, tmV;       // (d, page_size, copies * n_pages * kv_r), box (64, box_rows, 1)

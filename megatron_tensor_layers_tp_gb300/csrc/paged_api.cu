@@ -188,7 +188,8 @@ tp_status tp_cache_append(const tp_model* m, const tp_bf16* qkv, int64_t rank_st
     a.max_positions = c.max_positions;
     a.status = m->status;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return cuda_status(launch(m, "cache_append", st, [&] { return launch_cache_append(a, st); }));
+    return cuda_status(
+        launch(m, "cache_append", st, [&] { return launch_cache_append(a, m->num_sms, st); }));
   });
 }
 

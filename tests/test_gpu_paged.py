@@ -265,7 +265,7 @@ def near(got, ref, mag):
 
 
 @pytest.mark.parametrize("heads", HEADS)
-@pytest.mark.parametrize("M,page", [(1, 8), (7, 24), (301, 64)])
+@pytest.mark.parametrize("M,page", [(1, 8), (7, 24), (301, 64), (1003, 16)])
 def test_cache_append(heads, M, page):
     h, kv, d, t, dp = heads
     rng = np.random.default_rng(M + h)
