@@ -21,14 +21,16 @@
 // 14 us; 16 trees of 8-32 tokens behind 150-2048, 40 heads over 8 (80 MB): 36 us;
 // 64 trees of 2-8 tokens behind 1500-4096, 32 heads over 8 (740 MB): 120 us,
 // 6.1 TB/s; 6 chunks of 100-256 tokens behind up to 8000, 32 heads of 64 over 4
-// (64 GFLOP in whole tiles): 96 us, 670 TFLOP/s.
+// (64 GFLOP in whole tiles): 93 us, 690 TFLOP/s.
 //
 // Work is the flat sequence of (sequence, KV head, query tile, key tile), an
 // item's fixed work counted as kItemCost tiles more, split evenly over one CTA
 // per SM.  A CTA finds its range from the lengths on the GPU, so a captured
 // launch follows them.  An item cut between CTAs leaves unnormalised fp32
 // pieces, and the last CTA to finish one (a ticket, no waiting) joins them in
-// key order: deterministic.  The pieces lie [4 elements][row], so that lane =
+// key order: deterministic.  Where all others are there before it begins to write
+// its own, it keeps that in registers (the chunks 93 us instead of 96), by the same
+// operations in the same order.  The pieces lie [4 elements][row], so that lane =
 // row reads and writes whole lines with every load in flight (a second kernel
 // for the join cost 3-5 us a call; the join with rows of pieces and loads one
 // after another, 50; joined rows straight into o instead of through shared
@@ -94,6 +96,7 @@ constexpr float kRescaleLog2 = 8.f;
 // 16; 64 long sequences: 119, 120, 122).
 constexpr int kItemCost = 12;
 constexpr int kMaxGrid = 1024;
+constexpr int kFewRows = 32;             // rows whose pieces are joined in finer cuts
 
 // One CTA's part of an item: key tiles [k0, k1) of nt of (sequence b, KV head
 // g, query tile qi), the sequence's first row, new tokens and old length; of an
@@ -286,6 +289,12 @@ __device__ __forceinline__ float2 add2(float2 x, float2 y) {
   return d;
 }
 
+__device__ __forceinline__ int ld_acquire(const int* p) {
+  int v;
+  asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(__cvta_generic_to_global(p)) : "memory");
+  return v;
+}
+
 __device__ __forceinline__ uint32_t pack_p(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
@@ -336,20 +345,19 @@ __device__ __noinline__ void join_pieces(const TreeAttnArgs& a, const Seg& s, in
       for (int b = 0; b < kBatch; ++b) Mn = fmaxf(Mn, ml[b].x);
       const float u = M == -INFINITY ? 0.f : ex2_approx(M - Mn);
       M = Mn;
-      L *= u;
+      L = __fmul_rn(L, u);
 #pragma unroll
-      for (int q = 0; q < kPer; ++q) o[q] = make_float4(o[q].x * u, o[q].y * u, o[q].z * u, o[q].w * u);
+      for (int q = 0; q < kPer; ++q)
+        o[q] = make_float4(__fmul_rn(o[q].x, u), __fmul_rn(o[q].y, u), __fmul_rn(o[q].z, u),
+                           __fmul_rn(o[q].w, u));
 #pragma unroll
       for (int b = 0; b < kBatch; ++b) {
         const float v = ml[b].x == -INFINITY ? 0.f : ex2_approx(ml[b].x - Mn);
-        L += ml[b].y * v;
+        L = __fmaf_rn(ml[b].y, v, L);
 #pragma unroll
-        for (int q = 0; q < kPer; ++q) {
-          o[q].x += y[b][q].x * v;
-          o[q].y += y[b][q].y * v;
-          o[q].z += y[b][q].z * v;
-          o[q].w += y[b][q].w * v;
-        }
+        for (int q = 0; q < kPer; ++q)
+          o[q] = make_float4(__fmaf_rn(y[b][q].x, v, o[q].x), __fmaf_rn(y[b][q].y, v, o[q].y),
+                             __fmaf_rn(y[b][q].z, v, o[q].z), __fmaf_rn(y[b][q].w, v, o[q].w));
       }
     }
     const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
@@ -826,13 +834,24 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
         if (lane == 0) mbar_arrive(&ctl.p_ready[k]);
       }
 
+      // Of a cut item, whether every other piece is there already: this one then
+      // need not be written.
+      const bool whole = s.k0 == 0 && s.k1 == s.nt;
+      int* ticket = a.tickets + ((int64_t)s.b * a.n_kv + s.g) * a.q_tiles_max + s.qi;
+      if (tid == 0) {
+        ctl.last = 0;
+        if (!whole && rows > kFewRows && ld_acquire(ticket) == s.last - s.first) {
+          *ticket = 0;
+          ctl.last = 1;
+        }
+      }
       // The two groups' states meet, and each takes one half of the head's
       // elements of both O.
       if (n > grp) wait_pv();
       meet[grp * kTreeRows + r] = make_float2(m, l);
       bar_sync(1, kTreeSoftmax);
       tc_fence_after();
-      const bool whole = s.k0 == 0 && s.k1 == s.nt;
+      const bool joins = ctl.last != 0;
       const bool live = r < rows;
       if (warp_live) {
         const float2 ml0 = meet[r], ml1 = n > 1 ? meet[kTreeRows + r] : make_float2(-INFINITY, 0.f);
@@ -841,7 +860,7 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
         float w1 = ml1.x == -INFINITY ? 0.f : ex2_approx(ml1.x - M);
         const float L = ml0.y * w0 + ml1.y * w1;
         const int64_t piece = (int64_t)c * 2 + (!whole && c == s.first ? s.slot : 0);
-        if (!whole && live && grp == 0) a.ml[piece * kTreeRows + r] = make_float2(M, L);
+        if (!whole && !joins && live && grp == 0) a.ml[piece * kTreeRows + r] = make_float2(M, L);
         if (whole) {
           const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
           w0 *= inv;
@@ -868,7 +887,60 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
 #pragma unroll
             for (int e = 0; e < 32; ++e) o0[e] += add[e];
           }
-          if (whole) {
+          if (joins) {
+            // the other pieces and this one, in the order and with the operations
+            // of join_pieces
+#pragma unroll
+            for (int h = 0; h < 32; h += 16) {
+              float Mr = -INFINITY, Lr = 0.f, acc[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) acc[e] = 0.f;
+              for (int p0 = s.first; p0 <= s.last; p0 += 2) {
+                float2 pml[2];
+                float4 y[2][4];
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                  const int64_t at = (int64_t)(p0 + b) * 2 + (p0 + b == s.first ? s.slot : 0);
+                  const bool here = live && p0 + b <= s.last && p0 + b != c;
+                  const float4* src = reinterpret_cast<const float4*>(a.partials + at * kTreeRows * D) +
+                                      ((e0 + h) >> 2) * kTreeRows + r;
+                  pml[b] = here ? __ldcg(&a.ml[at * kTreeRows + r]) : make_float2(-INFINITY, 0.f);
+#pragma unroll
+                  for (int q = 0; q < 4; ++q)
+                    y[b][q] = here ? __ldcg(src + q * kTreeRows) : make_float4(0.f, 0.f, 0.f, 0.f);
+                  if (p0 + b == c) {
+                    pml[b] = make_float2(M, L);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                      y[b][q] = make_float4(o0[h + 4 * q], o0[h + 4 * q + 1], o0[h + 4 * q + 2],
+                                            o0[h + 4 * q + 3]);
+                  }
+                }
+                const float Mn = fmaxf(fmaxf(Mr, pml[0].x), pml[1].x);
+                const float u = Mr == -INFINITY ? 0.f : ex2_approx(Mr - Mn);
+                Mr = Mn;
+                Lr = __fmul_rn(Lr, u);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) acc[e] = __fmul_rn(acc[e], u);
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                  const float v = pml[b].x == -INFINITY ? 0.f : ex2_approx(pml[b].x - Mn);
+                  Lr = __fmaf_rn(pml[b].y, v, Lr);
+#pragma unroll
+                  for (int q = 0; q < 4; ++q) {
+                    acc[4 * q] = __fmaf_rn(y[b][q].x, v, acc[4 * q]);
+                    acc[4 * q + 1] = __fmaf_rn(y[b][q].y, v, acc[4 * q + 1]);
+                    acc[4 * q + 2] = __fmaf_rn(y[b][q].z, v, acc[4 * q + 2]);
+                    acc[4 * q + 3] = __fmaf_rn(y[b][q].w, v, acc[4 * q + 3]);
+                  }
+                }
+              }
+              const float inv = Lr > 0.f || Lr != Lr ? 1.f / Lr : 0.f;
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o0[h + e] = acc[e] * inv;
+            }
+          }
+          if (whole || joins) {
             // through shared memory: rows of o leave as whole lines
 #pragma unroll
             for (int e = 0; e < 32; e += 8)
@@ -888,11 +960,10 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
       tc_fence_before();
       if (tid == 0) ctl.poison[(seg + 1) & 1] = 0;
       bar_sync(1, kTreeSoftmax);  // O was read; the rows are in shared memory, or the pieces written
-      bool finish = whole;
-      if (!whole) {
+      bool finish = whole || joins;
+      if (!finish) {
         if (tid == 0) {
           fence_acq_rel_gpu();
-          int* ticket = a.tickets + ((int64_t)s.b * a.n_kv + s.g) * a.q_tiles_max + s.qi;
           const bool last = atomicAdd(ticket, 1) == s.last - s.first;
           if (last) *ticket = 0;
           fence_acq_rel_gpu();
@@ -905,7 +976,7 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
           // some, and mostly lie in more pieces (14.2 us for one token behind 700
           // instead of 15.7 with the other; that one 38 us for the trees above,
           // not 40).
-          if (rows <= 32) join_pieces<D, 4, 4>(a, ctl.seg[seg & 3], rows, tid >> 5, lane, sOut);
+          if (rows <= kFewRows) join_pieces<D, 4, 4>(a, ctl.seg[seg & 3], rows, tid >> 5, lane, sOut);
           else join_pieces<D, 8, 2>(a, ctl.seg[seg & 3], rows, tid >> 5, lane, sOut);
           bar_sync(1, kTreeSoftmax);
         }
