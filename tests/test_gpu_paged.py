@@ -814,6 +814,25 @@ def test_process_logits_bad_indices():
     assert m.check_device() == 0
 
 
+@pytest.mark.parametrize("V,reqs,nodes,history", [(1000, 3, 5, 40), (8192, 40, 1, 300), (32000, 90, 1, 2500),
+                                                  (32000, 12, 16, 700), (20008, 7, 20, 20000)])
+def test_process_logits_in_place_aligned(V, reqs, nodes, history):
+    rng = np.random.default_rng(V + nodes)
+    m = model(vocab=V)
+    c = logits_case(rng, V, reqs, nodes, history=history, biases=20)
+    x = bf16(rng, c["S"], V, scale=4.0)
+    ref, mag = logits_reference(c, f64(x))
+    live = c["row_req"] >= 0
+    rules = rules_of(c)
+    apart = m.process_logits(x, rules, dtype=torch.bfloat16)
+    y = x.clone()
+    m.process_logits(y, rules, out=y)
+    check_logits(f64(y)[live], ref[live], mag[live], True)
+    rows = torch.from_numpy(live).cuda()
+    assert torch.equal(y[rows], apart[rows]) and torch.equal(y[~rows], x[~rows])
+    assert m.check_device() == 0
+
+
 @pytest.mark.parametrize("start", [[2**31 - 1, 2**31 - 1], [2**31 - 1, 3], [-(2**31), 2**31 - 1], [0, 2**31 - 1]])
 def test_process_logits_bias_ranges_outside(start):
     rng = np.random.default_rng(56)
