@@ -251,6 +251,8 @@ class LogitRules:
         c.n_biases = 0 if bias_ids is None else bias_ids.numel()
         c.n_allowed = 0 if allowed is None else allowed.shape[0]
         c.ld_allowed = 0 if allowed is None else _ld(allowed)
+        # tokens that a grammar row has bits for (rows may lie further apart than they are long)
+        self._allowed_tokens = None if allowed is None else 32 * allowed.shape[1]
 
 
 class TPModel:
@@ -566,6 +568,9 @@ class TPModel:
             raise ValueError(f"the rules are for {n} rows, not {S}")
         if rules.device is not None and rules.device != self.device:
             raise ValueError("the rules' tensors are on another device")
+        if rules._allowed_tokens is not None and rules._allowed_tokens < V:
+            raise ValueError(f"allowed: {rules._allowed_tokens // 32} words a row do not cover "
+                             f"{V} tokens")
         if out is None:
             if dtype not in (torch.float32, torch.bfloat16):
                 raise ValueError("dtype: float32 or bfloat16 expected")

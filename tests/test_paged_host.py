@@ -11,7 +11,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 import megatron_tensor_layers_tp_gb300.binding as B  # noqa: E402
-from megatron_tensor_layers_tp_gb300.runtime import LogitRules, PageTable, Step  # noqa: E402
+from megatron_tensor_layers_tp_gb300.runtime import LogitRules, PageTable, Step, TPModel  # noqa: E402
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
@@ -96,3 +96,27 @@ def test_logit_rules_checks():
                 dict(allowed=ints(4, 9).long()), dict(history=ints(5, 2).t(), history_lens=ints(2))):
         with pytest.raises(ValueError):
             LogitRules(**bad)
+
+
+class Host:
+    """What the paged wrappers read of a model, on the CPU: their checks come before the C call,
+    which refuses the missing handle with another error."""
+    handle, device = None, torch.device("cpu")
+    _vocab = 100
+
+    def _out(self, shape, dtype, stream):
+        return torch.empty(shape, dtype=dtype)
+
+    def _stream(self, stream):
+        return 0
+
+
+def test_allowed_words_must_cover_the_vocabulary():
+    """A view of fewer words than the vocabulary needs, in rows that lie as far apart as it needs:
+    its last row would be read behind its end."""
+    logits = torch.zeros((3, 100), dtype=torch.bfloat16)
+    for allowed in (ints(11).as_strided((3, 3), (4, 1)), ints(3, 8)[:, :1], ints(3, 3)):
+        with pytest.raises(ValueError, match="allowed"):
+            TPModel.process_logits(Host(), logits, LogitRules(allowed=allowed))
+    with pytest.raises(B.TPError):  # as many as it needs: on to the call
+        TPModel.process_logits(Host(), logits, LogitRules(allowed=ints(3, 4)))
