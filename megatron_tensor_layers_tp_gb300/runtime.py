@@ -472,6 +472,12 @@ class TPModel:
             self._step_cover = (n_seqs, max_new)
         return self.step_ws
 
+    def _ws_args(self, ws: torch.Tensor):
+        """Address and bytes of a step workspace."""
+        if ws.device != self.device or not ws.is_contiguous():
+            raise ValueError("the workspace has to be contiguous, on the model's device")
+        return ws.data_ptr(), ws.nbytes
+
     def _stream(self, stream) -> int:
         """As _stream, without building a stream object (the call's own kernels take 2 to 5 us,
         torch.cuda.current_stream up to 4)."""
@@ -499,7 +505,7 @@ class TPModel:
             raise ValueError("the page table has too few rows, or the tables are on another device")
         if ws is None:
             ws = self.ensure_step_workspace(step.n_seqs, step.max_new, stream)
-        B.check(B.tp_step_tables(self.handle, pages.c, step.c, ws.data_ptr(), ws.numel(),
+        B.check(B.tp_step_tables(self.handle, pages.c, step.c, *self._ws_args(ws),
                                  self._stream(stream)), "tp_step_tables")
         return step
 
@@ -546,8 +552,8 @@ class TPModel:
         if ws is None:
             ws = self.ensure_step_workspace(step.n_seqs, step.max_new, stream)
         B.check(B.tp_tree_attention(self.handle, q.data_ptr(), _ld(q), out.data_ptr(), _ld(out),
-                                    pages.c, step.c, k.data_ptr(), v.data_ptr(), ws.data_ptr(),
-                                    ws.numel(), self._stream(stream)), "tp_tree_attention")
+                                    pages.c, step.c, k.data_ptr(), v.data_ptr(),
+                                    *self._ws_args(ws), self._stream(stream)), "tp_tree_attention")
         return out
 
     def _check_pools(self, k: torch.Tensor, v: torch.Tensor, pages: PageTable) -> None:

@@ -102,7 +102,8 @@ class Host:
     """What the paged wrappers read of a model, on the CPU: their checks come before the C call,
     which refuses the missing handle with another error."""
     handle, device = None, torch.device("cpu")
-    _vocab = 100
+    _vocab, _width, _copies, _kv_heads, _dim = 100, 512, 1, 2, 64
+    _check_pools, _ws_args = TPModel._check_pools, getattr(TPModel, "_ws_args", None)
 
     def _out(self, shape, dtype, stream):
         return torch.empty(shape, dtype=dtype)
@@ -120,3 +121,20 @@ def test_allowed_words_must_cover_the_vocabulary():
             TPModel.process_logits(Host(), logits, LogitRules(allowed=allowed))
     with pytest.raises(B.TPError):  # as many as it needs: on to the call
         TPModel.process_logits(Host(), logits, LogitRules(allowed=ints(3, 4)))
+
+
+def test_workspaces_that_are_refused():
+    """A workspace on another device, or one whose bytes are not one run: its size in bytes would
+    not be what the kernels may write."""
+    pages, step = PageTable.alloc(2, 9, 8, 32, device="cpu"), Step.alloc(2, 4, 4, 32, device="cpu")
+    q = torch.zeros((4, 512), dtype=torch.bfloat16)
+    k = torch.zeros((1, 9, 2, 8, 64), dtype=torch.bfloat16)
+    calls = (lambda ws: TPModel.step_tables(Host(), pages, step, ws=ws),
+             lambda ws: TPModel.tree_attention(Host(), q, step, pages, k, k, ws=ws))
+    for call in calls:
+        for ws in (torch.empty(512, dtype=torch.uint8, device="meta"),
+                   torch.empty(1024, dtype=torch.uint8)[::2]):
+            with pytest.raises(ValueError, match="workspace"):
+                call(ws)
+        with pytest.raises(B.TPError):  # on to the call
+            call(torch.empty(512, dtype=torch.uint8))
