@@ -565,9 +565,11 @@ size_t tp_step_workspace_bytes(const tp_model* m, int32_t n_seqs, int32_t max_ne
  * Errors on the device (TP_ERR_TABLE_RANGE): a length below 0, above max_ctx
  * or above ld_table * page_size, more than max_new new tokens in a sequence
  * or n_tokens in all, fewer free pages than needed, a ring state outside the
- * ring.  Then no page moves (free_next = free_state), q_start is all 0 and
- * every row is padding.  A parent not below its token counts as -1, and a
- * page number outside [0, n_pages) gives slot -1, each with that status. */
+ * ring, a page number outside [0, n_pages) among those that a shrinking
+ * sequence returns.  Then no page moves (free_next = free_state), q_start is
+ * all 0 and every row is padding.  A parent not below its token counts as -1,
+ * and a page number outside [0, n_pages) under a new token gives slot -1, each
+ * with that status. */
 tp_status tp_step_tables(const tp_model* m, const tp_pages_t* pages, const tp_step_t* step,
                          void* ws, size_t ws_bytes, void* stream);
 

@@ -232,6 +232,44 @@ def test_step_tables_bad_parent_and_bad_page():
     assert step.slots.tolist()[10:13] == [-1, -1, -1] and min(step.slots.tolist()[:10]) >= 0
 
 
+@pytest.mark.parametrize("value", [-1, "n_pages", 2**31 - 1, -2**31])
+@pytest.mark.parametrize("n_seqs,which", [(5, 1), (600, 599)])
+def test_step_tables_bad_page_given_back(n_seqs, which, value):
+    """A page number outside the cache in a row that shrinks must not get into the ring: nothing
+    moves, in every CTA's part of the step, and the step goes through once the row is mended."""
+    rng = np.random.default_rng(6)
+    m = model()
+    for at in (0, 2):  # of the three pages that it gives back
+        c = tables_case(rng, n_seqs, 9, 8, 60, True, 0.2)
+        c["old"][which], c["new"][which] = 30, 7
+        have = [R.ceil_div(int(o), 8) for o in c["old"]]
+        n = len(c["ring"]) + 4  # room for that sequence's pages, whatever it held before
+        perm = rng.permutation(n)
+        table, used = -7 * np.ones_like(c["table"]), 0
+        for b, h in enumerate(have):
+            table[b, :h] = perm[used:used + h]
+            used += h
+        c["table"], c["count"] = table, n - used
+        c["ring"], c["first"] = np.roll(np.concatenate([perm[used:], -9 * np.ones(used, dtype=np.int64)]), 11), 11
+        sizes = np.maximum(c["new"] - c["old"], 0)
+        c["n_tokens"] = int(sizes.sum()) + 3
+        c["parents"] = sum((R.random_tree(rng, int(s)) for s in sizes), []) + [-1] * 3
+        c["max_ctx"] = int(max(c["old"].max(), c["new"].max()))
+        good, bad = dict(c), dict(c, table=table.copy())
+        bad["table"][which, 1 + at] = n if value == "n_pages" else value
+        for in_place in (False, True):
+            pages, step = run_tables(m, bad, 1, in_place)
+            assert m.check_device() == TABLE_RANGE
+            assert pages.table.tolist() == bad["table"].tolist()
+            assert pages.free_ring.tolist() == bad["ring"].tolist()
+            assert pages.free_next.tolist() == [bad["first"], bad["count"]]
+            assert not step.q_start.any() and not step.tree_mask.any() and not step.positions.any()
+            assert step.slots.tolist() == [-1] * bad["n_tokens"] == step.token_seq.tolist()
+        pages, step = run_tables(m, good, 1)
+        check_tables(good, 1, pages, step)
+        assert m.check_device() == 0
+
+
 # ---------------------------------------------------------------------------
 # append
 # ---------------------------------------------------------------------------

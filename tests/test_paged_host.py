@@ -103,7 +103,7 @@ class Host:
     which refuses the missing handle with another error."""
     handle, device = None, torch.device("cpu")
     _vocab, _width, _copies, _kv_heads, _dim = 100, 512, 1, 2, 64
-    _check_pools, _ws_args = TPModel._check_pools, getattr(TPModel, "_ws_args", None)
+    _check_pools, _ws_args = TPModel._check_pools, TPModel._ws_args
 
     def _out(self, shape, dtype, stream):
         return torch.empty(shape, dtype=dtype)
