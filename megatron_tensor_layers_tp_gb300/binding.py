@@ -63,6 +63,10 @@ class tp_kernel_time_t(Structure):
     _fields_ = [("name", ctypes.c_char * 24), ("launches", c_int64), ("total_ms", ctypes.c_double)]
 
 
+MAX_STEP_SEQS = 8192    # sequences of a step
+MAX_TREE_TOKENS = 256   # new tokens a sequence in tree attention
+
+
 class tp_pages_t(Structure):
     _fields_ = [("n_pages", c_int32), ("page_size", c_int32), ("ld_table", c_int32)] + \
                [(n, c_void_p) for n in ("table", "free_ring", "free_state", "free_next")]

@@ -290,7 +290,7 @@ class TPModel:
         self._copies, self._kv_heads, self._dim = cfg.kv_copies, cfg.kv_heads_per_rank, cfg.head_dim
         self._vocab = cfg.vocab
         self.step_ws = None
-        self._step_cover = (0, -1)  # sequences and new tokens that it is large enough for
+        self._step_cover = 0  # sequences that it is large enough for
         self._old_step_ws = []
         self.ensure_workspace(max_tokens, stream)
 
@@ -458,19 +458,22 @@ class TPModel:
         return ws
 
     def ensure_step_workspace(self, n_seqs: int, max_new: int, stream=None) -> torch.Tensor:
-        """The model's own step workspace, grown when too small (not inside a graph capture)."""
-        if 0 < n_seqs <= self._step_cover[0] and 0 <= max_new <= self._step_cover[1]:
+        """The model's own step workspace, grown when too small (not inside a graph capture).
+        Nearly all of it is the same for every step (20 MB with heads of 128; a sequence adds some
+        hundred bytes) and the earlier ones are kept, since captured graphs may still use them: it
+        is made for any number of new tokens and 1024 sequences, and at least doubled."""
+        if 0 < n_seqs <= self._step_cover and max_new >= 0:
             return self.step_ws
-        n = B.tp_step_workspace_bytes(self.handle, n_seqs, max_new)
-        if self.step_ws is None or self.step_ws.numel() < n or n == 0:
-            if torch.cuda.is_current_stream_capturing():
-                raise RuntimeError("call ensure_step_workspace before the graph capture")
-            ws = self.step_workspace(n_seqs, max_new, stream)
-            if self.step_ws is not None:
-                self._old_step_ws.append(self.step_ws)  # captured graphs may still use it
-            self.step_ws = ws
-            self._step_cover = (n_seqs, max_new)
-        return self.step_ws
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("call ensure_step_workspace before the graph capture")
+        if n_seqs > 0 and max_new >= 0:  # (else step_workspace refuses them)
+            n_seqs = max(n_seqs, min(max(1024, 2 * self._step_cover), B.MAX_STEP_SEQS))
+            max_new = max(max_new, B.MAX_TREE_TOKENS)  # more take no more
+        ws = self.step_workspace(n_seqs, max_new, stream)
+        if self.step_ws is not None:
+            self._old_step_ws.append(self.step_ws)
+        self.step_ws, self._step_cover = ws, n_seqs
+        return ws
 
     def _ws_args(self, ws: torch.Tensor):
         """Address and bytes of a step workspace."""

@@ -1275,6 +1275,25 @@ def test_workspace_does_not_grow_inside_a_capture():
         m.ensure_step_workspace(0, 4)
 
 
+def test_workspaces_held_while_a_batch_grows():
+    """A batch that grows by one sequence a step, up to the most a step has: a handful of
+    workspaces, and a capture after the first step needs no new one."""
+    m = TPModel(make_config(512, 8, 2, 64, 256, 100, 0, 2, max_positions=64), [], max_tokens=1)
+    for n in list(range(1, 600)) + [1000, 2000, 5000, 8192]:
+        ws = m.ensure_step_workspace(n, 1 + n % 300)
+        assert ws.numel() >= B.tp_step_workspace_bytes(m.handle, n, 1 + n % 300)
+        if n == 599:
+            assert not m._old_step_ws
+    held = [m.step_ws] + m._old_step_ws
+    most = B.tp_step_workspace_bytes(m.handle, 8192, 256)
+    assert len(held) <= 4 and sum(w.numel() for w in held) <= 4 * most
+    assert m.ensure_step_workspace(1, 9000) is m.step_ws is ws
+    assert not any(w.any() for w in held)
+    for bad in ((8193, 4), (0, 4), (-1, 4), (4, -1)):
+        with pytest.raises(ValueError):
+            m.ensure_step_workspace(*bad)
+
+
 def test_counters_and_profile_names():
     rng = np.random.default_rng(91)
     m = model(8, 2, 64, 2)
