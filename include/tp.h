@@ -601,7 +601,8 @@ tp_status tp_cache_append(const tp_model* m, const tp_bf16* qkv, int64_t rank_st
  * 1/sqrt(d), one rounding of the output.  The result does not depend on what
  * cache slots hold that the row does not see, infinities and NaN included.
  *   q, o  : [n_tokens, n_heads*d], row strides ld_q, ld_o (multiples of 8);
- *           they must not overlap.  Padding rows of o are not written.
+ *           o must overlap neither q nor the cache.  Padding rows of o are not
+ *           written.
  *   pages : n_pages, page_size, ld_table and table are used
  *   step  : n_seqs, n_tokens, max_new (<= 256), max_ctx (>= every old + T),
  *           old_lens, q_start, tree_mask and tree_words are used; the

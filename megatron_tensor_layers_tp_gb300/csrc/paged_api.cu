@@ -79,6 +79,11 @@ int64_t span_bytes(int64_t rows, int64_t ld, int64_t cols, int elem) {
   return ((rows - 1) * ld + cols) * elem;
 }
 
+// Bytes of a layer's K or V pages.
+int64_t cache_bytes(const tp_config_t& c, const tp_pages_t* p) {
+  return (int64_t)c.n_kv_heads * p->n_pages * p->page_size * c.head_dim * 2;
+}
+
 }  // namespace
 
 extern "C" {
@@ -155,8 +160,7 @@ tp_status tp_cache_append(const tp_model* m, const tp_bf16* qkv, int64_t rank_st
       return TP_ERR_ARG;
     if (q && (!aligned16(q) || ld_q % 8 || ld_q < nhd)) return TP_ERR_ARG;
     const int64_t in = ((c.attn_tp - 1) * rank_stride + (int64_t)M * n_r) * 2;
-    const int64_t cache =
-        (int64_t)c.n_kv_heads * pages->n_pages * pages->page_size * c.head_dim * 2;
+    const int64_t cache = cache_bytes(c, pages);
     const int64_t out = q ? span_bytes(M, ld_q, nhd, 2) : 0;
     if (overlap(k, cache, v, cache) || overlap(qkv, in, k, cache) || overlap(qkv, in, v, cache) ||
         (q && (overlap(q, out, qkv, in) || overlap(q, out, k, cache) || overlap(q, out, v, cache))))
@@ -212,9 +216,14 @@ tp_status tp_tree_attention(const tp_model* m, const tp_bf16* q, int64_t ld_q, t
     const tp_config_t& c = m->cfg;
     const int nhd = c.n_heads * c.head_dim;
     if (!q || !o || !k || !v || !aligned16(q) || !aligned16(o) || !aligned16(k) || !aligned16(v) ||
-        ld_q % 8 || ld_o % 8 || ld_q < nhd || ld_o < nhd ||
-        overlap(q, span_bytes(step->n_tokens, ld_q, nhd, 2), o,
-                span_bytes(step->n_tokens, ld_o, nhd, 2)))
+        ld_q % 8 || ld_o % 8 || ld_q < nhd || ld_o < nhd)
+      return TP_ERR_ARG;
+    const uint64_t slices =
+        (uint64_t)c.kv_copies * pages->n_pages * c.kv_heads_per_rank, d = c.head_dim;
+    if (slices >= INT32_MAX) return TP_ERR_UNSUPPORTED;  // a tensor map coordinate
+    const int64_t cache = cache_bytes(c, pages), out = span_bytes(step->n_tokens, ld_o, nhd, 2);
+    if (overlap(q, span_bytes(step->n_tokens, ld_q, nhd, 2), o, out) || overlap(o, out, k, cache) ||
+        overlap(o, out, v, cache))
       return TP_ERR_ARG;
     if (!ws || !aligned16(ws) ||
         ws_bytes < tp_step_workspace_bytes(m, step->n_seqs, step->max_new))
@@ -227,9 +236,6 @@ tp_status tp_tree_attention(const tp_model* m, const tp_bf16* q, int64_t ld_q, t
     // boxes of as many keys as divide the page (and the key tile)
     a.box_rows = 8;
     while (a.box_rows < kTreeKeys && pages->page_size % (2 * a.box_rows) == 0) a.box_rows *= 2;
-    const uint64_t slices =
-        (uint64_t)c.kv_copies * pages->n_pages * c.kv_heads_per_rank, d = c.head_dim;
-    if (slices >= INT32_MAX) return TP_ERR_UNSUPPORTED;  // a tensor map coordinate
     a.slices = (int)slices;
     if (!make_tmap(&a.tmK, k, d, pages->page_size, slices, d * 2, pages->page_size * d * 2, a.box_rows) ||
         !make_tmap(&a.tmV, v, d, pages->page_size, slices, d * 2, pages->page_size * d * 2, a.box_rows))

@@ -1033,6 +1033,26 @@ def test_refusals_of_the_c_calls():
 # ---------------------------------------------------------------------------
 # streams, graphs, the run together
 # ---------------------------------------------------------------------------
+def test_tree_attention_output_in_the_cache_is_refused():
+    """o in one buffer with the pages, from the first bytes of K to the last of V."""
+    rng = np.random.default_rng(61)
+    m = model(8, 2, 64, 2)
+    c = attn_case(rng, m, [20], [3], 8, pad=0)
+    ref = m.tree_attention(c["q"], c["step"], c["pages"], c["k"], c["v"])
+    n, row = c["k"].numel(), 3 * 512
+    buf = torch.zeros(2 * n + 2 * row, dtype=torch.bfloat16, device="cuda")
+    k, v = buf[row:row + n].view_as(c["k"]), buf[row + n:row + 2 * n].view_as(c["v"])
+    k.copy_(c["k"])
+    v.copy_(c["v"])
+    for at in (8, row, row + n - 8, row + n, row + 2 * n - row, row + 2 * n - 8):
+        with pytest.raises(B.TPError, match="TP_ERR_ARG"):
+            m.tree_attention(c["q"], c["step"], c["pages"], k, v, out=buf[at:at + row].view(3, 512))
+    for at in (0, row + 2 * n):  # next to the cache
+        out = buf[at:at + row].view(3, 512)
+        m.tree_attention(c["q"], c["step"], c["pages"], k, v, out=out)
+        assert torch.equal(out, ref)
+
+
 def test_calls_on_another_stream():
     rng = np.random.default_rng(70)
     m = model(8, 2, 64, 2)
