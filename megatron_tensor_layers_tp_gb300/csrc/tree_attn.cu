@@ -705,8 +705,10 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
       const bool warp_live = quad * 32 < rows;
       const int tok = (int)fast_div((uint32_t)(row0 + min(r, rows - 1)), a.div_group);
       const int n = s.k1 - s.k0, len = s.old + s.T;
-      float m = -INFINITY, l = 0.f;  // in units of log2
-      // one tile of the group: scores from tensor memory, P back into it
+      // The running maximum (in units of log2) and sum.  Rows behind the item's hold
+      // other queries, or anything: a maximum that no score exceeds keeps them out of
+      // the vote on rescaling.  (NaN there took one token behind 20000 from 25 to 29 us.)
+      float m = r < rows ? -INFINITY : INFINITY, l = 0.f;
       uint32_t vis[2];
       // tile i: scores from tensor memory, P back into it
       auto tile = [&](auto tail_tag, int i) {
