@@ -453,6 +453,19 @@ def test_tree_attention(heads, ctx, T, page, tree):
     assert m.check_device() == 0
 
 
+@pytest.mark.parametrize("heads", [(16, 2, 64, 8, 2), (8, 4, 128, 4, 4), (8, 2, 64, 4, 2)])
+def test_tree_attention_with_dp_attention(heads):
+    """The heads sharded over t / attn_dp ranks: fewer cache copies, more heads in each."""
+    h, kv, d, t, dp = heads
+    rng = np.random.default_rng(h + t)
+    m = model(h, kv, d, t, attn_dp=dp)
+    c = attn_case(rng, m, [0, 40, 300], [3, 1, 17], 24)
+    assert c["k"].shape[0] == min(t // dp, kv)
+    out = m.tree_attention(c["q"], c["step"], c["pages"], c["k"], c["v"])
+    check_attn(m, c, out)
+    assert m.check_device() == 0
+
+
 @pytest.mark.parametrize("heads", [(32, 8, 128, 8), (32, 4, 64, 2)])
 def test_tree_attention_full_trees(heads):
     """256 drafted tokens (many query tiles) next to a single one, long and short contexts."""
@@ -1220,6 +1233,70 @@ def test_speculative_steps_match_one_token_at_a_time():
         assert pages.free_state.tolist()[1] == n_pages - used
         assert m.check_device() == 0
     assert min(len(x) for x in text) > 3
+
+
+@pytest.mark.parametrize("t", [1, 4])
+def test_a_whole_layer_over_pages_with_trained_norms(t):
+    """The chain of calls of a paged layer (the unfolded shards, since its norm weights are not 1;
+    SiLU(gate) * up by the caller), a prompt chunk and then single tokens, against the layer in
+    64 bits; without the unfolded shards column_linear refuses."""
+    rng = np.random.default_rng(82)
+    shape, inter, page = dict(hidden=512, heads=8, kv=2, dim=64), 256, 8
+    w = weights(rng, shape)
+    w["attn_norm"], w["mlp_norm"] = (1 + bf16(rng, 512, scale=0.3) for _ in range(2))
+    cfg = make_config(512, 8, 2, 64, inter, 100, 1, t, max_positions=512, plain_column_shards=1)
+    m = TPModel(cfg, [w], max_tokens=64)
+    folded = TPModel(make_config(512, 8, 2, 64, inter, 100, 1, t, max_positions=512), [w], max_tokens=64)
+    with pytest.raises(B.TPError, match="TP_ERR_UNSUPPORTED"):
+        folded.column_linear(0, B.TP_QKV, bf16(rng, 3, 512))
+    n, prompt = 2, [37, 5]
+    pages = PageTable.alloc(n, 40, page, 100)
+    k, v = m.alloc_pages(40, page), m.alloc_pages(40, page)
+    k.fill_(float("nan"))
+    v.fill_(float("nan"))
+    x = [bf16(rng, p + 2, 512) for p in prompt]
+
+    W = {a: f64(w[a]) for a in w}
+
+    def norm(h, g):
+        return h / np.sqrt((h**2).mean(-1, keepdims=True) + cfg.rms_eps) * g
+
+    def layer(h):  # one sequence in 64 bits
+        L = len(h)
+        u = norm(h, W["attn_norm"])
+        q = R.rotate((u @ W["wq"].T).reshape(L, 8, 64), np.arange(L), cfg.rope_theta)
+        kk = R.rotate((u @ W["wk"].T).reshape(L, 2, 64), np.arange(L), cfg.rope_theta)
+        vv = (u @ W["wv"].T).reshape(L, 2, 64)
+        o = np.stack([np.concatenate([R.attention_row(q[i, j], kk[:, j // 4], vv[:, j // 4], np.arange(L) <= i)[0]
+                                      for j in range(8)]) for i in range(L)])
+        h = h + o @ W["wo"].T
+        u = norm(h, W["mlp_norm"])
+        gate, up = u @ W["wg"].T, u @ W["wu"].T
+        return h + (gate / (1 + np.exp(-gate)) * up) @ W["wd"].T
+
+    ref = [layer(f64(y)) for y in x]
+    lens = [0] * n
+    for sizes in (prompt, [1, 1], [1, 1]):
+        new = [a + b for a, b in zip(lens, sizes)]
+        M = sum(sizes)
+        step = Step.alloc(n, M, max(sizes), 100, i32(lens), i32(new))
+        h = torch.cat([y[a:b] for y, a, b in zip(x, lens, new)])
+        m.step_tables(pages, step)
+        qkv = m.column_linear(0, B.TP_QKV, m.rmsnorm(h, w["attn_norm"]))
+        q = m.cache_append(qkv, step.positions, step.slots, pages, k, v)
+        o = m.tree_attention(q, step, pages, k, v)
+        h = m.row_linear_reduce(0, B.TP_O, o, residual=h)
+        gate, up = m.column_linear(0, B.TP_GATE_UP, m.rmsnorm(h, w["mlp_norm"])).float().chunk(2, dim=2)
+        a = (torch.nn.functional.silu(gate) * up).bfloat16()  # [t, M, inter / t]
+        got = f64(m.row_linear_reduce(0, B.TP_DOWN, a.transpose(0, 1).reshape(M, inter), residual=h))
+        at = 0
+        for b in range(n):
+            want = ref[b][lens[b]:new[b]]
+            # bf16 storage of every tensor on the way: the layer tests' bound
+            assert np.abs(got[at:at + sizes[b]] - want).max() <= 2e-2 * np.abs(want).max()
+            at += sizes[b]
+        lens = new
+    assert m.check_device() == 0
 
 
 def test_threads_with_steps_of_different_sizes():
