@@ -482,13 +482,18 @@ tp_status tp_selftest_wait_timeout(tp_model* m, int32_t milliseconds, void* stre
  * Paged KV cache, drafted trees and logit rules (no counterpart on the pages'
  * forward; the calls a serving loop makes around it).  One verification step:
  *   tp_step_tables    -> slots, positions and tree masks of the drafted tokens
- *   per layer: tp_column_linear(TP_QKV) -> tp_cache_append -> tp_tree_attention
- *              -> tp_row_linear_reduce(TP_O) ...
- *   tp_lm_head_gather -> tp_process_logits, and the caller accepts a path
+ *   per layer: tp_rmsnorm -> tp_column_linear(TP_QKV) -> tp_cache_append ->
+ *              tp_tree_attention -> tp_row_linear_reduce(TP_O) -> tp_rmsnorm ->
+ *              tp_column_linear(TP_GATE_UP) -> SiLU(gate) * up, by the caller ->
+ *              tp_row_linear_reduce(TP_DOWN)
+ *   tp_rmsnorm -> tp_lm_head_gather -> tp_process_logits, and the caller accepts
+ *   a path
  *   tp_cache_append of the kept qkv rows, the accepted path's rows at the
  *   sequence's first slots of the step and slot -1 elsewhere; tp_step_tables
  *   with the shorter lengths returns the pages no longer needed.
  * A single new token is a tree of one; a prompt chunk is a chain.
+ * tp_column_linear needs the unfolded shards: cfg->plain_column_shards = 1, unless
+ * every norm weight is 1 (see tp_load_shards).
  *
  * Cache (per layer, caller-owned, bf16): K or V of copy c, page p, KV head g
  * (local to the copy), offset x in the page, element e lives at
@@ -620,7 +625,10 @@ tp_status tp_tree_attention(const tp_model* m, const tp_bf16* q, int64_t ld_q, t
 
 /* What tp_process_logits applies.  Row s of the logits belongs to request
  * row_req[s] (NULL: request s); a row with row_req -1 is left as it was.
- * A pointer that is NULL leaves its rule out. */
+ * A pointer that is NULL leaves its rule out.  The kernel is chosen by S /
+ * n_reqs (rows of a request) and ld_history (the texts' lengths are on the GPU):
+ * requests without rows, and room for 2048 ids or more where texts are short, cost
+ * time (up to 2.4 times that of exact sizes), not results. */
 typedef struct {
   int32_t n_reqs;
   const int32_t* row_req;        /* [S] */

@@ -30,9 +30,17 @@
 // 64 rows of 128256 with texts of 4096 tokens, fp32: 21 us, 2.3 TB/s (the stream
 // alone 10.5); there the text's way into the marks binds.
 //
-// Slices have 4096 tokens, 8192 where texts are long (their reading is repeated
-// for every slice: 21 us instead of 30 at 4096 tokens, but 65 instead of 47 at
-// 1500), 2048 where there are too few rows to fill the GPU.
+// Slices have 4096 tokens; 2048 where there are too few rows to fill the GPU; 8192
+// where the text buffer's rows have room for 2048 ids or more, since every slice
+// reads the whole text.  That room stands in for the texts' lengths, which only the
+// GPU knows.  Measured at texts of 300, 1500, 4000, 8000 ids (us, 8192 against 4096
+// tokens a slice):
+//   64 rows of as many requests, fp32        16.8 18.3 21.1 28.9   20.4 22.0 24.8 34.3
+//   200 rows of as many requests, bf16       35.2 38.5 45.2 65.1   48.4 54.6 63.5 89.4
+//   32 trees of 4, grammar                   22.4 23.1 25.1 32.1   27.0 27.9 30.0 36.4
+//   16 trees of 16, grammar and 300 biases   81.0 81.4 84.0 103    44.8 45.5 47.1 51.5
+// So the last kind pays for a buffer with that much room, whatever its texts are
+// (16-bit marks, and 32-bit ones from 16128 ids on: 64 at 32768).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -410,7 +418,9 @@ static cudaError_t launch_logits(const LogitsArgs& a, int num_sms, cudaStream_t 
   // request's, and if possible a whole fraction of them: rows of another request
   // have to wait for marks of their own (64 requests of one row and 1500 tokens:
   // 27 us with one row a CTA, 33 with three; 8 trees of 16 and 1500 tokens: 35
-  // with four, 41 with six).
+  // with four, 41 with six).  A request's rows are taken to be S / n_reqs: requests
+  // without rows make that too few, and marks are made again for every row (the
+  // trees above among 512 requests: 111 us instead of 46).
   const int slices = (a.vocab + SM::kSlice - 1) / SM::kSlice;
   const int64_t parts = (int64_t)a.S * slices;
   int rows = (int)std::max<int64_t>(1, std::min<int64_t>(kLogRows, parts / (4 * num_sms)));

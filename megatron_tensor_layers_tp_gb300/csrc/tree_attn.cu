@@ -59,11 +59,16 @@
 //                item's end.  A thread owns a row and holds a tile's 64 scores
 //                in registers.
 // Each group has two S buffers, three where tensor memory holds them (heads of
-// 64): the products of its next tiles run while it works on this one.  (One
-// buffer and 128-key tiles: 172 us for the chunks when two took 134; two instead
-// of three: 113, not 110.  Two warpgroups a group, each with half of a tile's
-// keys: 159 when one took 134, the issuing threads waiting for their turns.)
-// P overwrites S in place (bf16, half the columns).  O is rescaled only when a
+// 64): the products of its next tiles run while it works on this one.  (Two
+// instead of three: 113 us for 8000-key chunks, not 110.  Measured before each
+// group's scores had an issuing thread of their own, when the chunks took 134:
+// one buffer and 128-key tiles 172; two warpgroups a group, each with half of a
+// tile's keys, 159.)
+// P overwrites S in place, rounded to bf16: the product with V takes both of its
+// operands in one 16-bit type, and V is bf16.  That moves o by at most 2^-8 of
+// sum p |v|; measured, the error against 64 bits is 0.0023 of the output's norm
+// instead of 0.0017 with the output's own rounding alone.  The sums take p
+// before its rounding, in fp32.  O is rescaled only when a
 // row's maximum rose by more than 2^8 since its last rescaling: the sums are
 // relative to the older maximum until then, which is exact algebra and keeps
 // every p below 2^8.
@@ -92,11 +97,17 @@ constexpr int kTreeFirst = kTreeThreads - kTreeSoftmax;
 // brought (checked by the host, since a take-over beyond it would never end)
 constexpr int kTreeRegsOther = 64, kTreeRegsSoftmax = 144;
 constexpr float kRescaleLog2 = 8.f;
-// An item's fixed work in key tiles (the chunks: 105 us with 8, 99 with 12 and
-// 16; 64 long sequences: 119, 120, 122).
+// An item's fixed work in key tiles.  With 8, 12, 16, 24: the chunks above 95.8,
+// 93.6, 93.4, 95.1 us, with heads of 128 (24-key pages) 144.6, 145.1, 146.3, 148.5;
+// 64 long sequences 119.7, 120.5, 122.0, 125.1; one token behind 700 14.5, 14.2,
+// 13.6, 13.3; 32 single tokens behind 1000 38.3, 36.9, 36.2, 35.6.
 constexpr int kItemCost = 12;
 constexpr int kMaxGrid = 1024;
-constexpr int kFewRows = 32;             // rows whose pieces are joined in finer cuts
+// Up to so many rows of an item its pieces are joined in finer cuts (16, 32, 48, 64
+// rows of one sequence behind 4000 tokens: 16.6, 17.4, 21.7, 21.9 us so, 17.7,
+// 19.1, 20.4, 20.6 in wider ones; of 16 sequences behind 1100: 25.9, 26.3, 27.5,
+// 27.6 and 26.8, 26.9, 27.2, 26.9; heads of 128).
+constexpr int kFewRows = 32;
 
 // One CTA's part of an item: key tiles [k0, k1) of nt of (sequence b, KV head
 // g, query tile qi), the sequence's first row, new tokens and old length; of an
@@ -975,9 +986,7 @@ tree_attn_kernel(const __grid_constant__ TreeAttnArgs a) {
         finish = ctl.last != 0;
         if (finish) {
           // Few rows, as single tokens have, are cut finer, so that every warp has
-          // some, and mostly lie in more pieces (14.2 us for one token behind 700
-          // instead of 15.7 with the other; that one 38 us for the trees above,
-          // not 40).
+          // some, and mostly lie in more pieces.
           if (rows <= kFewRows) join_pieces<D, 4, 4>(a, ctl.seg[seg & 3], rows, tid >> 5, lane, sOut);
           else join_pieces<D, 8, 2>(a, ctl.seg[seg & 3], rows, tid >> 5, lane, sOut);
           bar_sync(1, kTreeSoftmax);
