@@ -362,7 +362,7 @@ def _plain_compact(s):
     holders = torch.zeros(N, dtype=torch.long, device=DEV).index_add(0, table[there], torch.ones_like(table[there]))
     held = holders > 0
     used, page = held.sum(), torch.arange(N, device=DEV)
-    movers, holes = (held & (page >= used)).nonzero()[:, 0], (~held & (page < used)).nonzero()[:, 0]
+    movers, holes = (held & (page >= used)).nonzero()[:, 0].flip(0), (~held & (page < used)).nonzero()[:, 0]
     name = page.clone()
     name[movers] = holes
     s["table_out"].copy_(torch.where(there, name[table], s["table_out"].long()))
