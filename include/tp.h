@@ -519,6 +519,9 @@ typedef struct {
                                   free_state itself.  With another buffer the
                                   call proposes: repeated with the same
                                   free_state it gives the same tables. */
+  int32_t* holders;            /* [n_pages] or NULL (no two rows share a page): the rows
+                                  that hold each page, written by tp_fork_pages and
+                                  tp_compact_pages.  Of free pages: any number below 2. */
 } tp_pages_t;
 
 /* One step of n_seqs sequences: sequence b goes from old_lens[b] to
@@ -571,7 +574,9 @@ size_t tp_step_workspace_bytes(const tp_model* m, int32_t n_seqs, int32_t max_ne
  * or above ld_table * page_size, more than max_new new tokens in a sequence
  * or n_tokens in all, fewer free pages than needed, a ring state outside the
  * ring, a page number outside [0, n_pages) among those that a shrinking
- * sequence returns.  Then no page moves (free_next = free_state), q_start is
+ * sequence returns; with holders, a page of several rows among those, or as the
+ * page that a growing sequence's first new token goes to (tp_fork_pages shortens
+ * rows that share pages).  Then no page moves (free_next = free_state), q_start is
  * all 0 and every row is padding.  A parent not below its token counts as -1,
  * and a page number outside [0, n_pages) under a new token gives slot -1, each
  * with that status. */
@@ -686,6 +691,139 @@ typedef struct {
 tp_status tp_process_logits(const tp_model* m, const tp_bf16* logits, int64_t ld_logits,
                             int32_t S, const tp_logit_rules_t* rules, void* out, int64_t ld_out,
                             int32_t out_fp32, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Beam search over the paged cache (no counterpart on the pages).  Beam w of
+ * request r is row r*width + w of every call: of the logits, the texts, the page
+ * table and the step.  One step of all requests, after the logits:
+ *   tp_beam_select   -> the next beams: parent rows, tokens, scores
+ *   tp_beam_advance  -> the texts that tp_process_logits reads
+ *   tp_fork_pages    -> the page table of the next beams, pages shared
+ *   tp_copy_pages    -> the pages that several beams go on writing to, all layers
+ *   tp_step_tables   -> with tokens as the ids of the next forward
+ * Any other sharing of pages goes through tp_fork_pages too: several answers to
+ * one prompt, a prefix kept in a row of its own, a row that ends. */
+
+/* A selection's sizes, inputs and outputs.  Beams are rows as above. */
+typedef struct {
+  int32_t n_reqs;              /* 1..8192 */
+  int32_t width;               /* W: beams of a request, 1..32 */
+  int32_t n_cands;             /* K: candidates of a request, W..64 */
+  int32_t n_ends;              /* 0..8 */
+  const int32_t* ends;         /* [n_ends]: the ids that end a text */
+  const float* scores;         /* [n_reqs*W]: log-probabilities of the texts so far; a row
+                                  whose score is not finite is not in use */
+  float* cand_scores;          /* [n_reqs*K], best first; -infinity behind the last */
+  int32_t* cand_rows;          /* [n_reqs*K]: the row that is continued, or -1 */
+  int32_t* cand_tokens;        /* [n_reqs*K]: its next token, or -1 */
+  float* next_scores;          /* [n_reqs*W]; may be scores itself */
+  int32_t* parents;            /* [n_reqs*W]: the row that the next beam continues, or -1 */
+  int32_t* tokens;             /* [n_reqs*W]: its token; 0 where there is no parent */
+} tp_beams_t;
+
+/* Workspace bytes of tp_beam_select for up to n_reqs requests of these sizes (0 for
+ * sizes outside its limits).  Zero-filled once, shared and renewed as
+ * tp_step_workspace_bytes has it. */
+size_t tp_beam_workspace_bytes(const tp_model* m, int32_t n_reqs, int32_t width,
+                               int32_t n_cands);
+
+/* Selection over beams and vocabulary.  A request's candidates are the K best of
+ * its W * vocab continuations by
+ *   scores[row] + logit - log(sum over the row of exp(logit)),
+ * in order; equal ones by row, by logit, then by token.  The order is that of the unrounded
+ * values: the sum of exponentials in fp32 from the row's largest logit on, the rest in
+ * 64 bits, one rounding to fp32.  -infinity and NaN are never chosen and add nothing,
+ * +infinity counts as the largest fp32 number.  A row that allows nothing has no
+ * continuations.  The next beams are the first W candidates whose token is none of
+ * ends: K = W * (1 + n_ends) candidates always hold that many, where there are.
+ *   logits : [n_reqs*W, vocab] bf16, or fp32 with fp32 = 1 (what tp_lm_head_gather and
+ *            tp_process_logits write), row stride ld_logits >= vocab.  Rows not in use
+ *            are not read.
+ * Outputs overlap neither the inputs (but next_scores) nor each other.  vocab up to 2^30
+ * (TP_ERR_UNSUPPORTED above).  Deterministic. */
+tp_status tp_beam_select(const tp_model* m, const void* logits, int64_t ld_logits, int32_t fp32,
+                         const tp_beams_t* beams, void* ws, size_t ws_bytes, void* stream);
+
+/* The beams' texts: row b of out becomes row parents[b] of history, its lens[parents[b]]
+ * ids, and tokens[b] behind them; lens_out[b] their number.  With parent -1 the text is
+ * empty.  Ids behind a text are not written.
+ *   history, out   : [n_rows, ...] row strides ld_history, ld_out; texts may be as long
+ *                    as these.  They must not overlap (two buffers in turns).
+ *   lens, lens_out : [n_rows], not overlapping
+ * Errors on the device (TP_ERR_TABLE_RANGE): a parent outside [-1, n_rows) counts as -1,
+ * a length is cut to [0, min(ld_history, ld_out)], and where out has no room for the
+ * token the text is kept without it. */
+tp_status tp_beam_advance(const tp_model* m, int32_t n_rows, const int32_t* parents,
+                          const int32_t* tokens, const int32_t* history, int64_t ld_history,
+                          const int32_t* lens, int32_t* out, int64_t ld_out, int32_t* lens_out,
+                          void* stream);
+
+/* Workspace bytes of tp_fork_pages and tp_compact_pages for caches of up to n_pages
+ * pages (0 for sizes outside the limits).  As tp_step_workspace_bytes, apart from it. */
+size_t tp_share_workspace_bytes(const tp_model* m, int32_t n_pages);
+
+/* A fork of the page table: row b goes on as the first keep_lens[b] tokens of row
+ * src[b]. */
+typedef struct {
+  int32_t n_seqs;              /* 1..8192: every row that holds pages */
+  int32_t max_ctx;             /* host: no length is larger */
+  const int32_t* old_lens;     /* [n_seqs]: tokens of each row */
+  const int32_t* src;          /* [n_seqs]: the row that row b continues; -1: none */
+  const int32_t* keep_lens;    /* [n_seqs], or NULL: all of them */
+  int32_t* table;              /* [n_seqs][ld_table]: the new table, of the same row
+                                  length; another buffer than pages->table */
+  int32_t* new_lens;           /* [n_seqs]; another buffer than old_lens */
+  int32_t* moves;              /* [n_seqs][3]: page, new page, tokens (see tp_copy_pages) */
+  int32_t* n_moves;            /* [1] */
+} tp_fork_t;
+
+/* Forks, shortens and frees rows of the page table at once.  Full pages are shared.
+ * A page that a row goes on writing to (its last one, unless it is full) belongs to it
+ * alone: of the rows that hold it, the first keeps it if it is no other row's full page;
+ * the others take a page from the ring's front, rows in order, and a move of the tokens
+ * kept in it.  Pages that no row holds any more go behind the ring's end, by number
+ * (usable from the next call on).  Columns behind a row's pages are not written.
+ *   pages : table, free_ring and free_state are read, free_ring, free_next and (when not
+ *           NULL) holders written.  As with tp_step_tables a free_next of its own makes
+ *           the call a proposal.
+ * tp_copy_pages with the moves brings the new pages up to date; the next tp_step_tables
+ * takes new table and lengths.  Errors on the device (TP_ERR_TABLE_RANGE): a length below
+ * 0, above max_ctx or above ld_table * page_size, a source outside [-1, n_seqs), keep_lens
+ * outside [0, old_lens[src]], a page number outside [0, n_pages) in a row, fewer free pages
+ * than needed, a ring state outside the ring.  Then the new table and lengths are the old
+ * ones, nothing is moved, free_next = free_state and holders stays. */
+tp_status tp_fork_pages(const tp_model* m, const tp_pages_t* pages, const tp_fork_t* fork,
+                        void* ws, size_t ws_bytes, void* stream);
+
+/* Makes the pages in use the first ones of the cache.  With U pages held by rows, each
+ * held page from U on moves into a free page below U: the highest to the lowest, the next
+ * to the next.
+ *   lens  : [n_seqs] (1..8192: every row that holds pages); max_ctx as in tp_fork_t
+ *   to    : its table, free_ring, free_next and (when not NULL) holders are written, each
+ *           in a buffer of its own or that of pages; n_pages, page_size and ld_table
+ *           are those of pages.  The ring becomes 0, 1, 2, ... with the pages from U on
+ *           free.  Columns behind a row's pages are not written.
+ *   moves : [max_moves][3] with max_moves >= n_pages / 2, n_moves [1]; for tp_copy_pages
+ *           (whole pages)
+ * Afterwards n_pages could be made U.  Errors on the device (TP_ERR_TABLE_RANGE): a length
+ * or a page number out of bounds as for tp_fork_pages.  Then table, ring and state are
+ * those of pages and nothing is moved. */
+tp_status tp_compact_pages(const tp_model* m, const tp_pages_t* pages, const tp_pages_t* to,
+                           int32_t n_seqs, int32_t max_ctx, const int32_t* lens,
+                           int32_t* moves, int32_t max_moves, int32_t* n_moves, void* ws,
+                           size_t ws_bytes, void* stream);
+
+/* Copies pages of the cache, in every layer at once: for each move (page, new page,
+ * tokens) the first `tokens` tokens of every head's K and V.
+ *   moves   : [max_moves][3]; n_moves [1] on the device says how many there are
+ *   k, v    : HOST arrays [n_layers] of the layers' caches (read during the call only),
+ *             16-byte aligned, no two of them overlapping; pages gives n_pages and page_size
+ * No page may be both read and written by the moves, nor written twice.  Errors on the
+ * device (TP_ERR_TABLE_RANGE): a move with a page outside [0, n_pages) or tokens outside
+ * [0, page_size] is left out, n_moves is cut to [0, max_moves]. */
+tp_status tp_copy_pages(const tp_model* m, const tp_pages_t* pages, const int32_t* moves,
+                        const int32_t* n_moves, int32_t max_moves, int32_t n_layers,
+                        tp_bf16* const* k, tp_bf16* const* v, void* stream);
 
 const char* tp_strerror(tp_status s);
 

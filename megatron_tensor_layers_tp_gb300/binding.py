@@ -65,11 +65,12 @@ class tp_kernel_time_t(Structure):
 
 MAX_STEP_SEQS = 8192    # sequences of a step
 MAX_TREE_TOKENS = 256   # new tokens a sequence in tree attention
+MAX_BEAM_CANDS = 64     # candidates of a request in beam selection
 
 
 class tp_pages_t(Structure):
     _fields_ = [("n_pages", c_int32), ("page_size", c_int32), ("ld_table", c_int32)] + \
-               [(n, c_void_p) for n in ("table", "free_ring", "free_state", "free_next")]
+               [(n, c_void_p) for n in ("table", "free_ring", "free_state", "free_next", "holders")]
 
 
 class tp_step_t(Structure):
@@ -86,6 +87,18 @@ class tp_logit_rules_t(Structure):
                 ("tree_words", c_int32), ("n_biases", c_int32), ("bias_start", c_void_p),
                 ("bias_ids", c_void_p), ("bias_values", c_void_p), ("n_allowed", c_int32),
                 ("ld_allowed", c_int64), ("allowed", c_void_p), ("allowed_row", c_void_p)]
+
+
+class tp_beams_t(Structure):
+    _fields_ = [(n, c_int32) for n in ("n_reqs", "width", "n_cands", "n_ends")] + \
+               [(n, c_void_p) for n in ("ends", "scores", "cand_scores", "cand_rows", "cand_tokens",
+                                        "next_scores", "parents", "tokens")]
+
+
+class tp_fork_t(Structure):
+    _fields_ = [("n_seqs", c_int32), ("max_ctx", c_int32)] + \
+               [(n, c_void_p) for n in ("old_lens", "src", "keep_lens", "table", "new_lens", "moves",
+                                        "n_moves")]
 
 
 class TPError(RuntimeError):
@@ -147,6 +160,19 @@ _SIGS = {
     "tp_process_logits": (c_int32, [c_void_p, c_void_p, c_int64, c_int32,
                                     POINTER(tp_logit_rules_t), c_void_p, c_int64, c_int32,
                                     c_void_p]),
+    "tp_beam_workspace_bytes": (c_size_t, [c_void_p, c_int32, c_int32, c_int32]),
+    "tp_beam_select": (c_int32, [c_void_p, c_void_p, c_int64, c_int32, POINTER(tp_beams_t), c_void_p,
+                                 c_size_t, c_void_p]),
+    "tp_beam_advance": (c_int32, [c_void_p, c_int32, c_void_p, c_void_p, c_void_p, c_int64, c_void_p,
+                                  c_void_p, c_int64, c_void_p, c_void_p]),
+    "tp_share_workspace_bytes": (c_size_t, [c_void_p, c_int32]),
+    "tp_fork_pages": (c_int32, [c_void_p, POINTER(tp_pages_t), POINTER(tp_fork_t), c_void_p, c_size_t,
+                                c_void_p]),
+    "tp_compact_pages": (c_int32, [c_void_p, POINTER(tp_pages_t), POINTER(tp_pages_t), c_int32, c_int32,
+                                   c_void_p, c_void_p, c_int32, c_void_p, c_void_p, c_size_t,
+                                   c_void_p]),
+    "tp_copy_pages": (c_int32, [c_void_p, POINTER(tp_pages_t), c_void_p, c_void_p, c_int32, c_int32,
+                                POINTER(c_void_p), POINTER(c_void_p), c_void_p]),
     "tp_get_stats": (c_int32, [c_void_p, POINTER(tp_stats_t)]),
     "tp_reset_stats": (None, [c_void_p]),
     "tp_check_device": (c_int32, [c_void_p, c_void_p]),
@@ -336,6 +362,41 @@ def tp_process_logits(model, logits, ld_logits, S, rules: tp_logit_rules_t, out,
                       stream) -> int:
     return lib().tp_process_logits(model, logits, ld_logits, S, ctypes.byref(rules), out, ld_out,
                                    out_fp32, stream)
+
+
+def tp_beam_workspace_bytes(model, n_reqs: int, width: int, n_cands: int) -> int:
+    return lib().tp_beam_workspace_bytes(model, n_reqs, width, n_cands)
+
+
+def tp_beam_select(model, logits, ld_logits, fp32, beams: tp_beams_t, ws, ws_bytes, stream) -> int:
+    return lib().tp_beam_select(model, logits, ld_logits, fp32, ctypes.byref(beams), ws, ws_bytes,
+                                stream)
+
+
+def tp_beam_advance(model, n_rows, parents, tokens, history, ld_history, lens, out, ld_out, lens_out,
+                    stream) -> int:
+    return lib().tp_beam_advance(model, n_rows, parents, tokens, history, ld_history, lens, out, ld_out,
+                                 lens_out, stream)
+
+
+def tp_share_workspace_bytes(model, n_pages: int) -> int:
+    return lib().tp_share_workspace_bytes(model, n_pages)
+
+
+def tp_fork_pages(model, pages: tp_pages_t, fork: tp_fork_t, ws, ws_bytes, stream) -> int:
+    return lib().tp_fork_pages(model, ctypes.byref(pages), ctypes.byref(fork), ws, ws_bytes, stream)
+
+
+def tp_compact_pages(model, pages: tp_pages_t, to: tp_pages_t, n_seqs, max_ctx, lens, moves, max_moves,
+                     n_moves, ws, ws_bytes, stream) -> int:
+    return lib().tp_compact_pages(model, ctypes.byref(pages), ctypes.byref(to), n_seqs, max_ctx, lens,
+                                  moves, max_moves, n_moves, ws, ws_bytes, stream)
+
+
+def tp_copy_pages(model, pages: tp_pages_t, moves, n_moves, max_moves, n_layers, k, v, stream) -> int:
+    """k, v: ctypes arrays of the layers' addresses (in host memory)."""
+    return lib().tp_copy_pages(model, ctypes.byref(pages), moves, n_moves, max_moves, n_layers, k, v,
+                               stream)
 
 
 def tp_get_stats(model) -> tp_stats_t:

@@ -25,7 +25,7 @@ N_EPI = 8
 def _units():
     units = []
     for name in ("small", "attention", "tp_api", "no_alloc", "step_tables", "cache_append",
-                 "tree_attn", "logits", "paged_api"):
+                 "tree_attn", "logits", "beam", "share", "copy_pages", "paged_api"):
         units.append((os.path.join(CSRC, name + ".cu"), os.path.join(BUILD, name + ".o"), []))
     for e in range(N_EPI):
         units.append((os.path.join(CSRC, "gemm_inst.cu"), os.path.join(BUILD, f"gemm_epi{e}.o"),

@@ -26,6 +26,7 @@ struct StepTablesArgs {
   int32_t* free_ring;
   const int32_t* free_state;
   int32_t* free_next;
+  const int32_t* holders;     // null: no page is shared
   int n_seqs, n_tokens, max_new, cap;  // cap: no length is larger
   int tree_words;
   const int32_t *old_lens, *new_lens, *parents;
@@ -113,5 +114,103 @@ struct LogitsArgs {
   int* status;
 };
 cudaError_t launch_process_logits(const LogitsArgs& a, int num_sms, cudaStream_t st);
+
+constexpr int kMaxBeams = 32;      // of a request
+constexpr int kMaxBeamCands = 64;  // of a request
+constexpr int kMaxEnds = 8;
+
+// The K best logits of a part of a row, in order: (ordered value << 32) | ~token, 0 where
+// there are fewer; and its sum of exponentials, from its largest logit on.
+struct BeamPart {
+  double sum;
+  float top;
+};
+struct BeamSelectArgs {
+  const void* logits;
+  int64_t ld;
+  int fp32, vocab;
+  int n_reqs, width, n_cands, n_ends;
+  const int32_t* ends;
+  const float* scores;
+  float* cand_scores;
+  int32_t *cand_rows, *cand_tokens;
+  float* next_scores;
+  int32_t *parents, *tokens;
+  int parts, part_chunks;     // parts of a row, chunks of a part
+  FastDiv div_parts, div_width;
+  BeamPart* sums;             // [rows][parts]
+  unsigned long long* lists;  // [rows][parts][n_cands]
+  int* tickets;               // [n_reqs], zero on entry and exit
+};
+// The most parts that up to `rows` rows are cut into, all together.
+int64_t beam_parts_all(int64_t rows, int num_sms);
+cudaError_t launch_beam_select(BeamSelectArgs a, int num_sms, cudaStream_t st);
+
+struct BeamAdvanceArgs {
+  int n_rows;
+  const int32_t *parents, *tokens, *history;
+  int64_t ld, ld_out;
+  const int32_t* lens;
+  int32_t *out, *lens_out;
+  int* status;
+};
+cudaError_t launch_beam_advance(const BeamAdvanceArgs& a, int num_sms, cudaStream_t st);
+
+// What the fork and the compaction keep of a page in the workspace.
+struct PageNote {
+  uint32_t refs;   // rows that hold it; fork: before (<< 16) and after, as a full page.  Zero between calls
+  uint32_t first;  // fork: n_seqs - the first row that goes on writing to it.  Zero between calls
+  int32_t move;    // compaction: of a page that moves, its move and its rows
+  int32_t rows;
+};
+constexpr int kShareCtas = 1024;  // CTAs at most
+struct ShareHeader {              // zero between calls, but for counts
+  unsigned arrived[4];            // CTAs at each barrier
+  unsigned done, bad;
+  int32_t counts[2][kShareCtas];
+};
+constexpr size_t kShareNotes = 16384;  // where the notes begin in the workspace
+
+struct ForkArgs {
+  int n_pages, ld_table, page_size;
+  FastDiv div_page;
+  const int32_t* table;
+  int32_t* free_ring;
+  const int32_t* free_state;
+  int32_t *free_next, *holders;
+  int n_seqs, cap;
+  const int32_t *old_lens, *src, *keep_lens;
+  int32_t *table_out, *new_lens, *moves, *n_moves;
+  ShareHeader* head;
+  PageNote* notes;
+  int* status;
+};
+cudaError_t launch_fork_pages(const ForkArgs& a, int num_sms, cudaStream_t st);
+
+struct CompactArgs {
+  int n_pages, ld_table, page_size;
+  FastDiv div_page;
+  const int32_t *table, *ring, *free_state;
+  int32_t *table_out, *ring_out, *free_next, *holders;
+  int n_seqs, cap;
+  const int32_t* lens;
+  int32_t *moves, *n_moves;
+  ShareHeader* head;
+  PageNote* notes;
+  int* status;
+};
+cudaError_t launch_compact_pages(const CompactArgs& a, int num_sms, cudaStream_t st);
+
+constexpr int kCopyLayers = 128;  // of a launch
+struct CopyPagesArgs {
+  int n_pages, page_size, max_moves;
+  int row;                    // 16-byte words of a token's head
+  int copies, kv_r, layers;
+  FastDiv div_heads, div_kv;  // by copies * kv_r, by kv_r
+  const int32_t *moves, *n_moves;
+  int* status;
+  uint4* pools[2 * kCopyLayers];
+};
+cudaError_t launch_copy_pages(const CopyPagesArgs& a, int num_sms, cudaStream_t st);
 
 }  // namespace tpk

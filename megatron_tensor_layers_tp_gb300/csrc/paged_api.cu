@@ -41,14 +41,22 @@ tp_status check_pages(const tp_pages_t* p) {
 
 // The longest sequence a table row and the caller's bound allow (the kernels
 // round lengths up to key tiles and pages in 32 bits).
-int length_cap(const tp_pages_t* p, const tp_step_t* s) {
-  return (int)std::min({(int64_t)s->max_ctx, (int64_t)p->ld_table * p->page_size,
+int length_cap(const tp_pages_t* p, int32_t max_ctx) {
+  return (int)std::min({(int64_t)max_ctx, (int64_t)p->ld_table * p->page_size,
                         (int64_t)kMaxLength});
 }
 
 bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return x < y + (uintptr_t)b_bytes && y < x + (uintptr_t)a_bytes;
+}
+
+struct Span {
+  const void* p;
+  int64_t bytes;
+};
+bool overlap(const Span& a, const Span& b) {
+  return a.bytes > 0 && b.bytes > 0 && overlap(a.p, a.bytes, b.p, b.bytes);
 }
 
 // Tokens of a query tile, and query tiles of n new tokens.
@@ -71,6 +79,25 @@ StepWs step_ws(const tp_model* m, int n_seqs, int max_new) {
   w.partials = align_up(w.ml + pieces * sizeof(float2), 256);
   w.tickets = align_up(w.partials + pieces * m->cfg.head_dim * sizeof(float), 256);
   w.total = w.tickets + (size_t)n_seqs * m->cfg.n_kv_heads * tiles * sizeof(int);
+  return w;
+}
+
+// The selection's limits; its workspace: the requests' tickets (first, and as many for
+// every call, since what one call writes must not lie where another expects zeros), then
+// sums and lists of the rows' parts.
+bool beam_sizes(int n_reqs, int width, int n_cands) {
+  return n_reqs >= 1 && n_reqs <= kMaxStepSeqs && width >= 1 && width <= kMaxBeams &&
+         n_cands >= width && n_cands <= kMaxBeamCands;
+}
+struct BeamWs {
+  size_t sums, lists, total;
+};
+BeamWs beam_ws(const tp_model* m, int n_reqs, int width, int n_cands) {
+  const size_t parts = beam_parts_all((int64_t)n_reqs * width, m->num_sms);
+  BeamWs w;
+  w.sums = kMaxStepSeqs * sizeof(int);
+  w.lists = align_up(w.sums + parts * sizeof(BeamPart), 256);
+  w.total = w.lists + parts * n_cands * sizeof(unsigned long long);
   return w;
 }
 
@@ -123,10 +150,11 @@ tp_status tp_step_tables(const tp_model* m, const tp_pages_t* pages, const tp_st
     a.free_ring = pages->free_ring;
     a.free_state = pages->free_state;
     a.free_next = pages->free_next;
+    a.holders = pages->holders;
     a.n_seqs = step->n_seqs;
     a.n_tokens = step->n_tokens;
     a.max_new = step->max_new;
-    a.cap = length_cap(pages, step);
+    a.cap = length_cap(pages, step->max_ctx);
     a.tree_words = step->tree_words;
     a.old_lens = step->old_lens;
     a.new_lens = step->new_lens;
@@ -248,7 +276,7 @@ tp_status tp_tree_attention(const tp_model* m, const tp_bf16* q, int64_t ld_q, t
     a.n_seqs = step->n_seqs;
     a.n_tokens = step->n_tokens;
     a.max_new = step->max_new;
-    a.cap = length_cap(pages, step);
+    a.cap = length_cap(pages, step->max_ctx);
     a.old_lens = step->old_lens;
     a.q_start = step->q_start;
     a.tree_mask = step->tree_mask;
@@ -341,6 +369,252 @@ tp_status tp_process_logits(const tp_model* m, const tp_bf16* logits, int64_t ld
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     return cuda_status(
         launch(m, "process_logits", st, [&] { return launch_process_logits(a, m->num_sms, st); }));
+  });
+}
+
+size_t tp_beam_workspace_bytes(const tp_model* m, int32_t n_reqs, int32_t width,
+                               int32_t n_cands) {
+  if (!m || !beam_sizes(n_reqs, width, n_cands)) return 0;
+  return beam_ws(m, n_reqs, width, n_cands).total;
+}
+
+tp_status tp_beam_select(const tp_model* m, const void* logits, int64_t ld_logits, int32_t fp32,
+                         const tp_beams_t* beams, void* ws, size_t ws_bytes, void* stream) {
+  return guarded(m, [&]() -> tp_status {
+    if (!beams || fp32 < 0 || fp32 > 1) return TP_ERR_ARG;
+    const tp_beams_t& b = *beams;
+    const int V = m->cfg.vocab;
+    const uintptr_t elem = fp32 ? 4 : 2;
+    if (b.n_reqs < 1 || b.width < 1 || b.n_cands < b.width || b.n_ends < 0 || V < 1 || !logits ||
+        reinterpret_cast<uintptr_t>(logits) % elem || ld_logits < V || (b.n_ends > 0 && !b.ends) ||
+        !b.scores || !b.cand_scores || !b.cand_rows || !b.cand_tokens || !b.next_scores ||
+        !b.parents || !b.tokens)
+      return TP_ERR_ARG;
+    if (!beam_sizes(b.n_reqs, b.width, b.n_cands) || b.n_ends > kMaxEnds || V > kMaxVocab)
+      return TP_ERR_UNSUPPORTED;
+    const int64_t rows = (int64_t)b.n_reqs * b.width, cands = (int64_t)b.n_reqs * b.n_cands;
+    const Span out[6] = {{b.cand_scores, cands * 4}, {b.cand_rows, cands * 4}, {b.cand_tokens, cands * 4},
+                         {b.next_scores, rows * 4}, {b.parents, rows * 4}, {b.tokens, rows * 4}};
+    const Span in[3] = {{logits, span_bytes(rows, ld_logits, V, (int)elem)}, {b.ends, b.n_ends * 4},
+                        {b.scores, rows * 4}};
+    for (int i = 0; i < 6; ++i) {
+      for (int j = 0; j < i; ++j)
+        if (overlap(out[i], out[j])) return TP_ERR_ARG;
+      for (int j = 0; j < 3; ++j)
+        if (overlap(out[i], in[j]) && !(i == 3 && j == 2 && out[i].p == in[j].p)) return TP_ERR_ARG;
+    }
+    const BeamWs w = beam_ws(m, b.n_reqs, b.width, b.n_cands);
+    if (!ws || !aligned16(ws) || ws_bytes < w.total) return TP_ERR_WORKSPACE;
+    BeamSelectArgs a;
+    memset(&a, 0, sizeof(a));
+    a.logits = logits;
+    a.ld = ld_logits;
+    a.fp32 = fp32;
+    a.vocab = V;
+    a.n_reqs = b.n_reqs;
+    a.width = b.width;
+    a.n_cands = b.n_cands;
+    a.n_ends = b.n_ends;
+    a.ends = b.ends;
+    a.scores = b.scores;
+    a.cand_scores = b.cand_scores;
+    a.cand_rows = b.cand_rows;
+    a.cand_tokens = b.cand_tokens;
+    a.next_scores = b.next_scores;
+    a.parents = b.parents;
+    a.tokens = b.tokens;
+    uint8_t* base = static_cast<uint8_t*>(ws);
+    a.tickets = reinterpret_cast<int*>(base);
+    a.sums = reinterpret_cast<BeamPart*>(base + w.sums);
+    a.lists = reinterpret_cast<unsigned long long*>(base + w.lists);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return cuda_status(
+        launch(m, "beam_select", st, [&] { return launch_beam_select(a, m->num_sms, st); }));
+  });
+}
+
+tp_status tp_beam_advance(const tp_model* m, int32_t n_rows, const int32_t* parents,
+                          const int32_t* tokens, const int32_t* history, int64_t ld_history,
+                          const int32_t* lens, int32_t* out, int64_t ld_out, int32_t* lens_out,
+                          void* stream) {
+  return guarded(m, [&]() -> tp_status {
+    if (n_rows < 0) return TP_ERR_ARG;
+    if (n_rows == 0) return TP_OK;
+    if (!parents || !tokens || !history || !lens || !out || !lens_out || ld_history < 1 || ld_out < 1)
+      return TP_ERR_ARG;
+    if (std::min(ld_history, ld_out) > kMaxLength || n_rows > kMaxLength) return TP_ERR_UNSUPPORTED;
+    const Span text{history, n_rows * ld_history * 4}, to{out, n_rows * ld_out * 4};
+    const Span words[4] = {{parents, n_rows * 4ll}, {tokens, n_rows * 4ll}, {lens, n_rows * 4ll},
+                           {lens_out, n_rows * 4ll}};
+    if (overlap(text, to) || overlap(text, words[3])) return TP_ERR_ARG;
+    for (int i = 0; i < 4; ++i)
+      if (overlap(to, words[i]) || (i < 3 && overlap(words[3], words[i]))) return TP_ERR_ARG;
+    BeamAdvanceArgs a;
+    memset(&a, 0, sizeof(a));
+    a.n_rows = n_rows;
+    a.parents = parents;
+    a.tokens = tokens;
+    a.history = history;
+    a.ld = ld_history;
+    a.ld_out = ld_out;
+    a.lens = lens;
+    a.out = out;
+    a.lens_out = lens_out;
+    a.status = m->status;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return cuda_status(
+        launch(m, "beam_advance", st, [&] { return launch_beam_advance(a, m->num_sms, st); }));
+  });
+}
+
+size_t tp_share_workspace_bytes(const tp_model* m, int32_t n_pages) {
+  if (!m || n_pages < 1 || n_pages > INT32_MAX / 8) return 0;
+  return kShareNotes + (size_t)n_pages * sizeof(PageNote);
+}
+
+tp_status tp_fork_pages(const tp_model* m, const tp_pages_t* pages, const tp_fork_t* fork,
+                        void* ws, size_t ws_bytes, void* stream) {
+  return guarded(m, [&]() -> tp_status {
+    tp_status s = check_pages(pages);
+    if (s != TP_OK) return s;
+    if (!fork || fork->n_seqs < 1 || fork->max_ctx < 0 || pages->ld_table < 1 || !pages->table ||
+        !pages->free_ring || !pages->free_state || !pages->free_next || !fork->old_lens || !fork->src ||
+        !fork->table || !fork->new_lens || !fork->moves || !fork->n_moves)
+      return TP_ERR_ARG;
+    if (fork->n_seqs > kMaxStepSeqs) return TP_ERR_UNSUPPORTED;
+    const int64_t n = fork->n_seqs, table = n * pages->ld_table * 4;
+    const Span out[7] = {{fork->table, table}, {fork->new_lens, n * 4}, {fork->moves, n * 12},
+                         {fork->n_moves, 4}, {pages->free_ring, pages->n_pages * 4ll},
+                         {pages->free_next, 8}, {pages->holders, pages->holders ? pages->n_pages * 4ll : 0}};
+    const Span in[5] = {{pages->table, table}, {fork->old_lens, n * 4}, {fork->src, n * 4},
+                        {fork->keep_lens, fork->keep_lens ? n * 4 : 0}, {pages->free_state, 8}};
+    for (int i = 0; i < 7; ++i) {
+      for (int j = 0; j < i; ++j)
+        if (overlap(out[i], out[j])) return TP_ERR_ARG;
+      for (int j = 0; j < 5; ++j)
+        if (overlap(out[i], in[j]) && !(i == 5 && j == 4 && out[i].p == in[j].p)) return TP_ERR_ARG;
+    }
+    if (!ws || !aligned16(ws) || ws_bytes < tp_share_workspace_bytes(m, pages->n_pages))
+      return TP_ERR_WORKSPACE;
+    ForkArgs a;
+    memset(&a, 0, sizeof(a));
+    a.n_pages = pages->n_pages;
+    a.ld_table = pages->ld_table;
+    a.page_size = pages->page_size;
+    a.div_page = make_fastdiv((uint32_t)pages->page_size);
+    a.table = pages->table;
+    a.free_ring = pages->free_ring;
+    a.free_state = pages->free_state;
+    a.free_next = pages->free_next;
+    a.holders = pages->holders;
+    a.n_seqs = fork->n_seqs;
+    a.cap = length_cap(pages, fork->max_ctx);
+    a.old_lens = fork->old_lens;
+    a.src = fork->src;
+    a.keep_lens = fork->keep_lens;
+    a.table_out = fork->table;
+    a.new_lens = fork->new_lens;
+    a.moves = fork->moves;
+    a.n_moves = fork->n_moves;
+    a.head = static_cast<ShareHeader*>(ws);
+    a.notes = reinterpret_cast<PageNote*>(static_cast<uint8_t*>(ws) + kShareNotes);
+    a.status = m->status;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return cuda_status(
+        launch(m, "fork_pages", st, [&] { return launch_fork_pages(a, m->num_sms, st); }));
+  });
+}
+
+tp_status tp_compact_pages(const tp_model* m, const tp_pages_t* pages, const tp_pages_t* to,
+                           int32_t n_seqs, int32_t max_ctx, const int32_t* lens,
+                           int32_t* moves, int32_t max_moves, int32_t* n_moves, void* ws,
+                           size_t ws_bytes, void* stream) {
+  return guarded(m, [&]() -> tp_status {
+    tp_status s = check_pages(pages);
+    if (s != TP_OK) return s;
+    if (!to || n_seqs < 1 || max_ctx < 0 || pages->ld_table < 1 || !pages->table || !pages->free_ring ||
+        !pages->free_state || to->n_pages != pages->n_pages || to->page_size != pages->page_size ||
+        to->ld_table != pages->ld_table || !to->table || !to->free_ring || !to->free_next || !lens ||
+        (!moves && max_moves > 0) || !n_moves || max_moves < pages->n_pages / 2)
+      return TP_ERR_ARG;
+    if (n_seqs > kMaxStepSeqs) return TP_ERR_UNSUPPORTED;
+    const int64_t n = n_seqs, table = n * pages->ld_table * 4, ring = pages->n_pages * 4ll;
+    // (in and out of the same index may be the same buffer)
+    const Span out[6] = {{to->table, table}, {to->free_ring, ring}, {to->free_next, 8},
+                         {to->holders, to->holders ? ring : 0}, {moves, max_moves * 12ll}, {n_moves, 4}};
+    const Span in[4] = {{pages->table, table}, {pages->free_ring, ring}, {pages->free_state, 8},
+                        {lens, n * 4}};
+    for (int i = 0; i < 6; ++i) {
+      for (int j = 0; j < i; ++j)
+        if (overlap(out[i], out[j])) return TP_ERR_ARG;
+      for (int j = 0; j < 4; ++j)
+        if (overlap(out[i], in[j]) && !(i == j && i < 3 && out[i].p == in[j].p)) return TP_ERR_ARG;
+    }
+    if (!ws || !aligned16(ws) || ws_bytes < tp_share_workspace_bytes(m, pages->n_pages))
+      return TP_ERR_WORKSPACE;
+    CompactArgs a;
+    memset(&a, 0, sizeof(a));
+    a.n_pages = pages->n_pages;
+    a.ld_table = pages->ld_table;
+    a.page_size = pages->page_size;
+    a.div_page = make_fastdiv((uint32_t)pages->page_size);
+    a.table = pages->table;
+    a.ring = pages->free_ring;
+    a.free_state = pages->free_state;
+    a.table_out = to->table;
+    a.ring_out = to->free_ring;
+    a.free_next = to->free_next;
+    a.holders = to->holders;
+    a.n_seqs = n_seqs;
+    a.cap = length_cap(pages, max_ctx);
+    a.lens = lens;
+    a.moves = moves;
+    a.n_moves = n_moves;
+    a.head = static_cast<ShareHeader*>(ws);
+    a.notes = reinterpret_cast<PageNote*>(static_cast<uint8_t*>(ws) + kShareNotes);
+    a.status = m->status;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return cuda_status(
+        launch(m, "compact_pages", st, [&] { return launch_compact_pages(a, m->num_sms, st); }));
+  });
+}
+
+tp_status tp_copy_pages(const tp_model* m, const tp_pages_t* pages, const int32_t* moves,
+                        const int32_t* n_moves, int32_t max_moves, int32_t n_layers,
+                        tp_bf16* const* k, tp_bf16* const* v, void* stream) {
+  return guarded(m, [&]() -> tp_status {
+    tp_status s = check_pages(pages);
+    if (s != TP_OK) return s;
+    if (max_moves < 0 || n_layers < 0) return TP_ERR_ARG;
+    if (max_moves == 0 || n_layers == 0) return TP_OK;
+    if (!moves || !n_moves || !k || !v) return TP_ERR_ARG;
+    for (int i = 0; i < n_layers; ++i)
+      if (!k[i] || !v[i] || !aligned16(k[i]) || !aligned16(v[i])) return TP_ERR_ARG;
+    CopyPagesArgs a;
+    memset(&a, 0, sizeof(a));
+    a.n_pages = pages->n_pages;
+    a.page_size = pages->page_size;
+    a.max_moves = max_moves;
+    a.row = m->cfg.head_dim / 8;
+    a.copies = m->cfg.kv_copies;
+    a.kv_r = m->cfg.kv_heads_per_rank;
+    a.div_kv = make_fastdiv((uint32_t)a.kv_r);
+    a.div_heads = make_fastdiv((uint32_t)(a.copies * a.kv_r));
+    a.moves = moves;
+    a.n_moves = n_moves;
+    a.status = m->status;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    for (int first = 0; first < n_layers; first += kCopyLayers) {
+      a.layers = std::min(n_layers - first, kCopyLayers);
+      for (int i = 0; i < a.layers; ++i) {
+        a.pools[2 * i] = reinterpret_cast<uint4*>(k[first + i]);
+        a.pools[2 * i + 1] = reinterpret_cast<uint4*>(v[first + i]);
+      }
+      s = cuda_status(
+          launch(m, "copy_pages", st, [&] { return launch_copy_pages(a, m->num_sms, st); }));
+      if (s != TP_OK) return s;
+    }
+    return TP_OK;
   });
 }
 

@@ -61,10 +61,11 @@ __device__ __forceinline__ Scan3 block_scan3(Scan3 v, Scan3* warp_sums, Scan3* t
 }
 
 // Whether a page that the warp's sequences give back has a number outside the
-// cache: `gone` pages of the lane's sequence, from `row` on.  Four sequences at
+// cache, or other rows that hold it: `gone` pages of the lane's sequence, from `row` on.  Four sequences at
 // a time, lane = page, eight look-ups in flight.  (Not inlined: steps that only
 // grow do not fetch it.)
-__device__ __noinline__ bool returns_bad_page(const int32_t* row, int gone, int n_pages) {
+__device__ __noinline__ bool returns_bad_page(const int32_t* row, int gone, int n_pages,
+                                              const int32_t* holders) {
   const int lane = threadIdx.x & 31;
   bool bad = false;
   for (unsigned left = __ballot_sync(0xffffffffu, gone > 0); left;) {
@@ -88,7 +89,11 @@ __device__ __noinline__ bool returns_bad_page(const int32_t* row, int gone, int 
         page[k] = i < many[k >> 1] ? src[k >> 1][i] : 0;
       }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) bad |= (uint32_t)page[k] >= (uint32_t)n_pages;
+      for (int k = 0; k < 8; ++k) {
+        const bool out = (uint32_t)page[k] >= (uint32_t)n_pages;
+        const bool mine = j + 32 * (k & 1) < many[k >> 1];
+        bad |= out || (holders && mine && holders[page[k]] > 1);
+      }
     }
   }
   return bad;
@@ -121,13 +126,18 @@ __global__ void __launch_bounds__(kTabThreads) step_tables_kernel(const StepTabl
         v.t = max(w - o, 0);
         v.p = max(want - have, 0);
         v.u = max(have - want, 0);
+        if (a.holders && w > o && o < have * a.page_size) {
+          // the first new token goes to the sequence's last page
+          const int page = row[(int64_t)b * a.ld_table + have - 1];
+          if ((uint32_t)page < (uint32_t)a.n_pages && a.holders[page] > 1) bad = true;
+        }
         row += (int64_t)b * a.ld_table + want;
       }
     }
     // A page number outside the cache in a row that shrinks must not get into
-    // the ring.  Every CTA looks at all pages given back (this launch writes none
+    // the ring, nor a page that other rows hold.  Every CTA looks at all pages given back (this launch writes none
     // of them), so that all come to the same verdict without waiting for others.
-    if (__any_sync(0xffffffffu, v.u > 0) && returns_bad_page(row, (int)v.u, a.n_pages)) bad = true;
+    if (__any_sync(0xffffffffu, v.u > 0) && returns_bad_page(row, (int)v.u, a.n_pages, a.holders)) bad = true;
     Scan3 total;
     const Scan3 e = block_scan3(v, warp_sums, &total);
     if (b < n) {

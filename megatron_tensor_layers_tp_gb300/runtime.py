@@ -98,14 +98,16 @@ class PageTable:
 
     table [rows, ld] int32, free_ring [n_pages] int32 and free_state [2] int32 (first, count) as
     the C ABI wants them; free_next (default: free_state itself) receives the ring's state after
-    step_tables.  For cache_append alone page_size and n_pages suffice, for tree_attention also
+    step_tables.  holders [n_pages] int32 is needed where rows share pages (fork_pages).  For
+    cache_append and copy_pages alone page_size and n_pages suffice, for tree_attention also
     the table.  The tensors' addresses are kept: refresh their contents, not the objects.
     """
 
     def __init__(self, page_size: int, table: Optional[torch.Tensor] = None,
                  free_ring: Optional[torch.Tensor] = None,
                  free_state: Optional[torch.Tensor] = None,
-                 free_next: Optional[torch.Tensor] = None, n_pages: Optional[int] = None):
+                 free_next: Optional[torch.Tensor] = None, n_pages: Optional[int] = None,
+                 holders: Optional[torch.Tensor] = None):
         if n_pages is None:
             if free_ring is None:
                 raise ValueError("n_pages or free_ring is needed")
@@ -120,23 +122,35 @@ class PageTable:
             _check(free_ring, "free_ring", torch.int32, (n_pages,), table.device)
             _check(free_state, "free_state", torch.int32, (2,), table.device)
             _check(free_next, "free_next", torch.int32, (2,), table.device)
+        if holders is not None:
+            if table is None:
+                raise ValueError("holders come with a table")
+            _check(holders, "holders", torch.int32, (n_pages,), table.device)
         self.page_size, self.n_pages = page_size, n_pages
         self.table, self.free_ring = table, free_ring
-        self.free_state, self.free_next = free_state, free_next
+        self.free_state, self.free_next, self.holders = free_state, free_next, holders
         c = self.c = B.tp_pages_t()
         c.n_pages, c.page_size = n_pages, page_size
         c.ld_table = 0 if table is None else table.shape[1]
         c.table, c.free_ring = _ptr(table), _ptr(free_ring)
         c.free_state, c.free_next = _ptr(free_state), _ptr(free_next)
+        c.holders = _ptr(holders)
 
     @classmethod
     def alloc(cls, n_seqs: int, n_pages: int, page_size: int, max_len: int,
-              device="cuda") -> "PageTable":
-        """An empty table for n_seqs sequences of up to max_len tokens; every page is free."""
+              device="cuda", shared: bool = False) -> "PageTable":
+        """An empty table for n_seqs sequences of up to max_len tokens; every page is free.  With
+        shared, fork_pages can let its rows share pages."""
         ld = max(1, -(-max_len // page_size))
         return cls(page_size, torch.zeros((n_seqs, ld), dtype=torch.int32, device=device),
                    torch.arange(n_pages, dtype=torch.int32, device=device),
-                   torch.tensor([0, n_pages], dtype=torch.int32, device=device))
+                   torch.tensor([0, n_pages], dtype=torch.int32, device=device),
+                   holders=torch.zeros(n_pages, dtype=torch.int32, device=device) if shared else None)
+
+    def with_table(self, table: torch.Tensor) -> "PageTable":
+        """The same pages, ring and ring state behind another table: what a fork writes to."""
+        return PageTable(self.page_size, table, self.free_ring, self.free_state, self.free_next,
+                         self.n_pages, self.holders)
 
 
 class Step:
@@ -255,6 +269,136 @@ class LogitRules:
         self._allowed_tokens = None if allowed is None else 32 * allowed.shape[1]
 
 
+class Beams:
+    """A beam selection's sizes, inputs and outputs (see tp_beams_t).
+
+    Inputs: scores [n_reqs*width] float32 (not finite: the row is not in use), ends [n] int32 (ids
+    that end a text).  Outputs, written by beam_select: cand_scores, cand_rows, cand_tokens [n_reqs,
+    n_cands], next_scores (which may be scores itself), parents and tokens [n_reqs*width].
+    """
+
+    def __init__(self, n_reqs: int, width: int, n_cands: int, scores: torch.Tensor,
+                 cand_scores: torch.Tensor, cand_rows: torch.Tensor, cand_tokens: torch.Tensor,
+                 next_scores: torch.Tensor, parents: torch.Tensor, tokens: torch.Tensor,
+                 ends: Optional[torch.Tensor] = None):
+        dev, rows, cands = scores.device, (n_reqs * width,), (n_reqs, n_cands)
+        for name, t, dtype, shape in (
+                ("scores", scores, torch.float32, rows), ("next_scores", next_scores, torch.float32, rows),
+                ("parents", parents, torch.int32, rows), ("tokens", tokens, torch.int32, rows),
+                ("cand_scores", cand_scores, torch.float32, cands),
+                ("cand_rows", cand_rows, torch.int32, cands),
+                ("cand_tokens", cand_tokens, torch.int32, cands)):
+            _check(t, name, dtype, shape, dev)
+        if ends is not None:
+            _check(ends, "ends", torch.int32, (None,), dev)
+        self.n_reqs, self.width, self.n_cands, self.ends = n_reqs, width, n_cands, ends
+        self.scores, self.next_scores, self.parents, self.tokens = scores, next_scores, parents, tokens
+        self.cand_scores, self.cand_rows, self.cand_tokens = cand_scores, cand_rows, cand_tokens
+        self.sizes = (n_reqs, width, n_cands)
+        c = self.c = B.tp_beams_t()
+        c.n_reqs, c.width, c.n_cands = n_reqs, width, n_cands
+        c.n_ends = 0 if ends is None else ends.numel()
+        for name in ("ends", "scores", "cand_scores", "cand_rows", "cand_tokens", "next_scores",
+                     "parents", "tokens"):
+            setattr(c, name, _ptr(getattr(self, name)))
+
+    @classmethod
+    def alloc(cls, n_reqs: int, width: int, n_cands: Optional[int] = None,
+              ends: Optional[torch.Tensor] = None, scores: Optional[torch.Tensor] = None,
+              in_place: bool = False, device="cuda") -> "Beams":
+        """With its outputs allocated.  n_cands: by default enough for every next beam to be found,
+        width * (1 + ends), up to 64.  scores: by default those of a first step, one beam a request
+        in use.  in_place: next_scores is scores."""
+        if n_cands is None:
+            n_cands = min(width * (1 + (0 if ends is None else ends.numel())), B.MAX_BEAM_CANDS)
+        if scores is None:
+            scores = torch.full((n_reqs, width), -float("inf"), device=device)
+            scores[:, 0] = 0
+            scores = scores.flatten()
+
+        def ints(*shape):
+            return torch.zeros(shape, dtype=torch.int32, device=scores.device)
+        return cls(n_reqs, width, n_cands, scores,
+                   torch.zeros((n_reqs, n_cands), dtype=torch.float32, device=scores.device),
+                   ints(n_reqs, n_cands), ints(n_reqs, n_cands),
+                   scores if in_place else torch.zeros_like(scores), ints(n_reqs * width),
+                   ints(n_reqs * width), ends)
+
+
+class PageMoves:
+    """Moves of pages: table [most, 3] int32 (page, new page, tokens) and their count [1] int32, on
+    the GPU (see tp_copy_pages)."""
+
+    def __init__(self, table: torch.Tensor, count: torch.Tensor):
+        _check(table, "table", torch.int32, (None, 3), table.device)
+        _check(count, "count", torch.int32, (1,), table.device)
+        self.table, self.count, self.most = table, count, table.shape[0]
+        self._ptrs = (_ptr(table), _ptr(count))
+
+    @classmethod
+    def alloc(cls, most: int, device="cuda") -> "PageMoves":
+        return cls(torch.zeros((most, 3), dtype=torch.int32, device=device),
+                   torch.zeros(1, dtype=torch.int32, device=device))
+
+
+class PageFork:
+    """A fork of a page table (see tp_fork_t): row b goes on as the first keep_lens[b] tokens
+    (None: all) of row src[b] (-1: none).
+
+    old_lens, src, keep_lens [n_seqs] int32.  fork_pages fills table (of the page table's shape, in
+    another buffer), new_lens and moves (room for n_seqs).
+    """
+
+    def __init__(self, max_ctx: int, old_lens: torch.Tensor, src: torch.Tensor,
+                 keep_lens: Optional[torch.Tensor], table: torch.Tensor, new_lens: torch.Tensor,
+                 moves: PageMoves):
+        n, dev = old_lens.numel(), old_lens.device
+        for name, t in (("old_lens", old_lens), ("src", src), ("keep_lens", keep_lens),
+                        ("new_lens", new_lens)):
+            if t is not None:
+                _check(t, name, torch.int32, (n,), dev)
+        _check(table, "table", torch.int32, (None, None), dev)
+        if moves.most < n or moves.table.device != dev:
+            raise ValueError(f"moves: room for {n} on {dev} expected")
+        self.n_seqs, self.max_ctx = n, max_ctx
+        self.old_lens, self.src, self.keep_lens = old_lens, src, keep_lens
+        self.table, self.new_lens, self.moves = table, new_lens, moves
+        c = self.c = B.tp_fork_t()
+        c.n_seqs, c.max_ctx = n, max_ctx
+        c.old_lens, c.src, c.keep_lens = _ptr(old_lens), _ptr(src), _ptr(keep_lens)
+        c.table, c.new_lens = _ptr(table), _ptr(new_lens)
+        c.moves, c.n_moves = moves._ptrs
+
+    @classmethod
+    def alloc(cls, pages: PageTable, max_ctx: int, old_lens: torch.Tensor, src: torch.Tensor,
+              keep_lens: Optional[torch.Tensor] = None,
+              table: Optional[torch.Tensor] = None) -> "PageFork":
+        """With its outputs (the table too, unless it is given) allocated."""
+        return cls(max_ctx, old_lens, src, keep_lens,
+                   torch.zeros_like(pages.table) if table is None else table,
+                   torch.zeros_like(old_lens), PageMoves.alloc(old_lens.numel(), old_lens.device))
+
+
+class LayerPages:
+    """The K and V pages of every layer (alloc_pages's), for copy_pages.  Their addresses are
+    kept."""
+
+    def __init__(self, k: Sequence[torch.Tensor], v: Sequence[torch.Tensor]):
+        if len(k) != len(v):
+            raise ValueError("as many layers of K as of V are needed")
+        self.k, self.v, self.n_layers = list(k), list(v), len(k)
+        self.shape, self.device = (k[0].shape, k[0].device) if self.n_layers else (None, None)
+        ends = []
+        for i, t in enumerate(self.k + self.v):
+            _check(t, f"layer {i % self.n_layers}", torch.bfloat16, self.shape, self.device)
+            ends.append((t.data_ptr(), t.data_ptr() + t.nbytes))
+        ends.sort()
+        if any(a[1] > b[0] for a, b in zip(ends, ends[1:])):
+            raise ValueError("the layers' pages must not overlap")
+        self._k = (ctypes.c_void_p * max(1, self.n_layers))(*[t.data_ptr() for t in self.k])
+        self._v = (ctypes.c_void_p * max(1, self.n_layers))(*[t.data_ptr() for t in self.v])
+
+
 class TPModel:
     """Owns one tp_model (the t ranks' shards) plus a workspace."""
 
@@ -292,6 +436,7 @@ class TPModel:
         self.step_ws = None
         self._step_cover = 0  # sequences that it is large enough for
         self._old_step_ws = []
+        self._own_ws = {}  # kind -> (workspaces, the last of them in use; the last call's sizes)
         self.ensure_workspace(max_tokens, stream)
 
     # ------------------------------------------------------------------ utils
@@ -592,6 +737,143 @@ class TPModel:
                                     out.data_ptr(), _ld(out), int(out.dtype == torch.float32),
                                     self._stream(stream)), "tp_process_logits")
         return out
+
+    # ------------------------------------------------------- beams, shared pages
+    def beam_workspace(self, n_reqs: int, width: int, n_cands: int, stream=None) -> torch.Tensor:
+        """A workspace for beam_select on up to n_reqs requests of these sizes.  Calls that may
+        overlap on the GPU need one each; the others can share the model's own."""
+        return self._workspace(B.tp_beam_workspace_bytes(self.handle, n_reqs, width, n_cands),
+                               f"{n_reqs} requests of {width} beams, {n_cands} candidates", stream)
+
+    def share_workspace(self, n_pages: int, stream=None) -> torch.Tensor:
+        """A workspace for fork_pages and compact_pages on up to n_pages pages, as
+        beam_workspace."""
+        return self._workspace(B.tp_share_workspace_bytes(self.handle, n_pages),
+                               f"{n_pages} pages", stream)
+
+    def _workspace(self, n: int, what: str, stream) -> torch.Tensor:
+        if n == 0:
+            raise ValueError(f"{what}: outside limits")
+        ws = self._out((n,), torch.uint8, stream)
+        B.tp_workspace_init(ws.data_ptr(), n, _stream(stream))
+        return ws
+
+    def ensure_beam_workspace(self, n_reqs: int, width: int, n_cands: int, stream=None):
+        """The model's own workspace of beam_select, at least doubled when too small (not inside a
+        graph capture; the earlier ones are kept, since captured graphs may still use them)."""
+        return self._ensure("beam", (n_reqs, width, n_cands), B.tp_beam_workspace_bytes, stream)
+
+    def ensure_share_workspace(self, n_pages: int, stream=None):
+        """The model's own workspace of fork_pages and compact_pages, as ensure_beam_workspace."""
+        return self._ensure("share", (n_pages,), B.tp_share_workspace_bytes, stream)
+
+    def _ensure(self, kind: str, sizes, size, stream) -> torch.Tensor:
+        held, last = self._own_ws.setdefault(kind, ([], [None]))
+        if last[0] == sizes:
+            return held[-1]
+        n = size(self.handle, *sizes)
+        if n == 0 or not held or held[-1].numel() < n:
+            if torch.cuda.is_current_stream_capturing():
+                raise RuntimeError(f"call ensure_{kind}_workspace before the graph capture")
+            most = 2 * held[-1].numel() if n and held else 0
+            held.append(self._workspace(max(n, most), f"{kind} of {sizes}", stream))
+        last[0] = sizes
+        return held[-1]
+
+    def beam_select(self, logits: torch.Tensor, beams: Beams, ws: Optional[torch.Tensor] = None,
+                    stream=None) -> Beams:
+        """The best continuations of every request's beams; logits [n_reqs*width, vocab] bf16 or
+        float32."""
+        dtype = logits.dtype
+        if dtype is not torch.bfloat16 and dtype is not torch.float32:
+            raise ValueError("logits: float32 or bfloat16 expected")
+        _check(logits, "logits", dtype, (beams.n_reqs * beams.width, self._vocab), self.device, rows=True)
+        if beams.scores.device != self.device:
+            raise ValueError("the beams' tensors are on another device")
+        if ws is None:
+            ws = self.ensure_beam_workspace(*beams.sizes, stream)
+        B.check(B.tp_beam_select(self.handle, logits.data_ptr(), _ld(logits),
+                                 int(dtype is torch.float32), beams.c, *self._ws_args(ws),
+                                 self._stream(stream)), "tp_beam_select")
+        return beams
+
+    def beam_advance(self, parents: torch.Tensor, tokens: torch.Tensor, history: torch.Tensor,
+                     lens: torch.Tensor, out: Optional[torch.Tensor] = None,
+                     lens_out: Optional[torch.Tensor] = None, stream=None):
+        """Row b of out becomes row parents[b] of history [rows, room] and tokens[b] behind it.
+        Returns (out, lens_out); ids of out behind a text are not written (undefined in a buffer
+        allocated here)."""
+        n, dev, i32 = parents.shape[0], self.device, torch.int32
+        _check(parents, "parents", i32, (n,), dev)
+        _check(tokens, "tokens", i32, (n,), dev)
+        _check(lens, "lens", i32, (n,), dev)
+        _check(history, "history", i32, (n, None), dev, rows=True)
+        if out is None:
+            out = self._out(history.shape, i32, stream)
+        else:
+            _check(out, "out", i32, (n, None), dev, rows=True)
+        if lens_out is None:
+            lens_out = self._out((n,), i32, stream)
+        else:
+            _check(lens_out, "lens_out", i32, (n,), dev)
+        B.check(B.tp_beam_advance(self.handle, n, parents.data_ptr(), tokens.data_ptr(),
+                                  history.data_ptr(), _ld(history), lens.data_ptr(), out.data_ptr(),
+                                  _ld(out), lens_out.data_ptr(), self._stream(stream)),
+                "tp_beam_advance")
+        return out, lens_out
+
+    def fork_pages(self, pages: PageTable, fork: PageFork, ws: Optional[torch.Tensor] = None,
+                   stream=None) -> PageFork:
+        """The page table behind the fork's sources, pages shared; fork.moves goes to copy_pages.
+        pages.with_table(fork.table) is the page table from here on."""
+        t = pages.table
+        if t is None or pages.free_ring is None:
+            raise ValueError("fork_pages needs a page table with its ring")
+        if t.shape[0] < fork.n_seqs or fork.table.shape[0] < fork.n_seqs or \
+                fork.table.shape[1] != t.shape[1] or t.device != self.device or \
+                fork.table.device != self.device:
+            raise ValueError("the page tables differ in row length, have too few rows, or are on "
+                             "another device")
+        if ws is None:
+            ws = self.ensure_share_workspace(pages.n_pages, stream)
+        B.check(B.tp_fork_pages(self.handle, pages.c, fork.c, *self._ws_args(ws),
+                                self._stream(stream)), "tp_fork_pages")
+        return fork
+
+    def compact_pages(self, pages: PageTable, lens: torch.Tensor, max_ctx: int, moves: PageMoves,
+                      out: Optional[PageTable] = None, ws: Optional[torch.Tensor] = None,
+                      stream=None) -> PageTable:
+        """Renames the pages in use to the first ones; moves (room for n_pages // 2) goes to
+        copy_pages.  Written to `out` (None: pages itself), whose tensors may be those of pages."""
+        out = pages if out is None else out
+        n = lens.numel()
+        _check(lens, "lens", torch.int32, (n,), self.device)
+        for p in (pages, out):
+            if p.table is None or p.free_ring is None or p.table.shape[0] < n or p.table.device != self.device:
+                raise ValueError("compact_pages needs page tables with their rings and a row for every "
+                                 "length, on the model's device")
+        if moves.table.device != self.device:
+            raise ValueError("the moves are on another device")
+        if ws is None:
+            ws = self.ensure_share_workspace(pages.n_pages, stream)
+        table, count = moves._ptrs
+        B.check(B.tp_compact_pages(self.handle, pages.c, out.c, n, max_ctx, lens.data_ptr(), table,
+                                   moves.most, count, *self._ws_args(ws), self._stream(stream)),
+                "tp_compact_pages")
+        return out
+
+    def copy_pages(self, moves: PageMoves, pages: PageTable, layers: LayerPages, stream=None) -> None:
+        """Copies the moves' pages in every layer's K and V."""
+        if moves.table.device != self.device:
+            raise ValueError("the moves are on another device")
+        if layers.n_layers:
+            shape = (self._copies, pages.n_pages, self._kv_heads, pages.page_size, self._dim)
+            if layers.shape != shape or layers.device != self.device:
+                raise ValueError(f"layers: pages of shape {shape} on {self.device} expected, got "
+                                 f"{tuple(layers.shape)} on {layers.device}")
+        table, count = moves._ptrs
+        B.check(B.tp_copy_pages(self.handle, pages.c, table, count, moves.most, layers.n_layers,
+                                layers._k, layers._v, self._stream(stream)), "tp_copy_pages")
 
     def capture_forward(self, ids: torch.Tensor, batch: Batch, h: torch.Tensor,
                         logits: torch.Tensor, stream, fused: bool = True,
