@@ -5,17 +5,26 @@
 // and the K best logits come out of one pass; a row is cut into parts, and the
 // last CTA of a request's parts joins their sums and lists.
 //
-// The K best: a chunk of the part at a time in registers.  The K-th largest of
-// 128 maxima (two threads each) of the first chunk bounds the K-th largest
-// logit from below; what passes the bound goes to a buffer in shared memory, and
-// the buffer, when it has many, is ranked by counting and cut to K, which
-// raises the bound.  Later chunks' tokens have higher numbers, so that only
-// what is larger than the bound can still count.  A chunk from which more passes
-// than the buffer holds (rising or equal logits) is taken one logit of each
-// thread at a time.
+// The pass is bound by memory: 16 KB of a part at a time come by bulk copies into a
+// ring in shared memory, and a thread takes 16-byte words of them into registers.
+// The warps run through the ring without waiting for each other.
+// The K best: a thread leaves the largest logit of each chunk in shared memory.
+// Behind the last chunk the K-th largest of 128 maxima (two threads each) bounds the
+// K-th largest logit from below, and the logits of the few cells (a thread's of a
+// chunk) that reach the bound are read once more, from L2: what passes is ranked by
+// counting.  Where more passes than the buffer holds (equal logits) the cells are gone
+// through a warp a cell, and ranked in between.
+//
+// Sums: of 2^(x log2(e) - r), r the thread's largest x log2(e) so far, rounded to a whole
+// number, so that sums are brought to one r exactly; added in fp32 (at most V / 256
+// of them), the threads' sums as whole multiples of 2^-32, whose order does not
+// matter: equal rows get equal sums.  What log2(e) in fp32 (c) is off by cancels, as x
+// counts from M in the same units: M c - r.  Rows with NaN, and those whose largest
+// logit is beyond 2^20, are summed once more, from M on.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <float.h>
+#include <limits.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -28,9 +37,13 @@ namespace tpk {
 
 constexpr int kSelThreads = 256, kSelWarps = kSelThreads / 32;
 constexpr int kSelVecs = 4;         // 16-byte words of a thread in a chunk
-constexpr int kSelBuffer = 512;     // keys that may pass a bound
-constexpr int kSelRank = 192;       // from so many on they are ranked
-constexpr int kSelLists = 512;      // parts of a request, at most
+constexpr int kSelStages = 4;       // chunks in the ring
+constexpr int kSelCells = 24;       // of a thread: its largest logits, each of so many chunks
+constexpr int kSelChunkBytes = kSelThreads * kSelVecs * 16;
+constexpr int kSelStageBytes = kSelChunkBytes + 128;  // (rows off 16-byte boundaries take a word more)
+constexpr int kSelBuffer = 2 * kSelThreads - kMaxBeamCands;  // keys that may pass a bound
+constexpr int kSelKeys = 2048;      // of a request's lists, at most
+constexpr int kSelSmall = 32;       // so many are ranked without a bound
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Bits whose order as whole numbers is that of the values (-0 as 0).
@@ -41,164 +54,259 @@ __device__ __forceinline__ uint32_t ordered(float x) {
 __device__ __forceinline__ float of_ordered(uint32_t o) {
   return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
 }
+__device__ __forceinline__ unsigned long long ordered(double x) {
+  const long long b = __double_as_longlong(x);
+  return (unsigned long long)(b ^ (b >> 63 | (long long)0x8000000000000000ull));
+}
 // Larger for larger logits, among equal ones for lower tokens; never 0.
 __device__ __forceinline__ unsigned long long key_of(float x, int token) {
   return (unsigned long long)ordered(fminf(x, FLT_MAX)) << 32 | (uint32_t)~token;
 }
 
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, d;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 d, x, y;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z, d;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, x, y, z;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {  // (NaN falls out)
+  uint32_t d;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+constexpr float kFar = 1048576.f;  // logits beyond are summed from the largest on
+__device__ __forceinline__ bool is_far(float top) { return !(fabsf(top) <= kFar); }
+// r of a largest logit: whole, and exact in fp32
+__device__ __forceinline__ float power_of(float top) {
+  return rintf(fminf(fmaxf(top, -kFar), kFar) * kLog2e);
+}
+
+// log of s * 2^-32, s >= 1, to 10^-8: with s = 2^k m, 2/3 < m <= 4/3 and
+// z = (m - 1) / (m + 1), it is k log 2 + 2 (z + z^3 / 3 + z^5 / 5 + ...); z in two fp32
+// numbers, the powers from its first.  (log in 64 bits took 2900 cycles instead of about
+// 300, on the path of every request.)
+__device__ __forceinline__ double log_fixed(unsigned long long s) {
+  const int lead = __clzll((long long)s);
+  const unsigned long long x = s << lead;
+  float m = (float)(uint32_t)(x >> 40) * 0x1p-23f;             // in [1, 2), exact
+  float ml = (float)(uint32_t)(x >> 8 & 0xFFFFFFFFu) * 0x1p-55f;  // the bits behind
+  int k = 31 - lead;
+  if (m > 1.3333333f) {
+    m *= 0.5f;
+    ml *= 0.5f;
+    ++k;
+  }
+  const float a = m - 1.f, b = m + 1.f, bl = m - (b - 1.f) + ml;
+  const float z = a / b;
+  const float zl = (fmaf(-z, b, a) + ml - z * bl) / b;
+  const float y = z * z;
+  float p = 1.f / 13.f;
+  p = fmaf(p, y, 1.f / 11.f);
+  p = fmaf(p, y, 1.f / 9.f);
+  p = fmaf(p, y, 1.f / 7.f);
+  p = fmaf(p, y, 1.f / 5.f);
+  p = fmaf(p, y, 1.f / 3.f);
+  return fma((double)k, 0.693147180559945309417, (double)(2.f * z)) + (double)(2.f * fmaf(z * y, p, zl));
+}
+
 struct SelectSmem {
-  unsigned long long keys[kSelBuffer + kMaxBeamCands];  // the best so far, then the buffer
-  float group[kSelThreads / 2];
-  float bound;
-  int many, valid;   // keys in the buffer; before the first that found no room
+  unsigned long long keys[kSelBuffer + kMaxBeamCands + 2];  // the best so far, then the buffer
+  __align__(16) uint16_t cell[kSelThreads][kSelCells];  // bf16, rounded up
+  uint64_t full[kSelStages], empty[kSelStages];
+  int many;  // keys in the buffer
+  int hits;  // cells that reach the bound
   int last;
-  float warp_top[kSelWarps];
-  double warp_sum[kSelWarps];
-  // the join of a request's parts
-  double row_top[kMaxBeams], row_log[kMaxBeams], row_score[kMaxBeams];
-  double value[kSelWarps][kMaxBeamCands];
-  unsigned long long key[kSelWarps][kMaxBeamCands];
-  int row[kSelWarps][kMaxBeamCands];
-  int found[kSelWarps];
+  __align__(16) uint32_t pair[kSelThreads / 2];
+  uint32_t bound;  // largest logits of two threads; of them the K-th largest
+  uint32_t warp_top[kSelWarps];
+  int warp_power[kSelWarps];
+  unsigned long long warp_sum[kSelWarps];
+};
+struct JoinSmem {  // lies in the ring
+  unsigned long long key[kSelKeys];    // of the lists
+  union {
+    struct {
+      float below[kSelKeys], near[kSelKeys];  // their values' parts: from the row's largest logit on; the row's
+    };
+    unsigned long long value[kSelKeys];  // of those that may be among the K best, bits in order
+  };
+  uint16_t entry[kSelKeys];            // these
+  int many;
+  uint32_t warp_bound[kSelWarps];
+  double row_top[kMaxBeams], row_rest[kMaxBeams];  // largest logit; score - log of the sum
+  float row_near[kMaxBeams];
   int best_row[kMaxBeamCands], best_token[kMaxBeamCands];
   float best_score[kMaxBeamCands];
 };
+constexpr int kSelRingBytes =
+    kSelStages * kSelStageBytes > (int)sizeof(JoinSmem) ? kSelStages * kSelStageBytes : (int)sizeof(JoinSmem);
+
+// How many threads count for one of m keys.
+__device__ __forceinline__ int threads_a_key(int m) { return m <= 32 ? 8 : m <= 64 ? 4 : m <= 128 ? 2 : 1; }
 
 // Ranks the keys, `best` sorted ones and n more, and keeps the K best: their
 // number.  All threads, together; the keys are visible on entry and exit.
-__device__ __forceinline__ int rank_keys(SelectSmem& sm, int best, int n, int K) {
-  const int m = best + n, tid = threadIdx.x;
-  constexpr int kMost = (kSelBuffer + kMaxBeamCands + kSelThreads - 1) / kSelThreads;
+__device__ __noinline__ int rank_keys(SelectSmem& sm, int best, int n, int K) {
+  const int m = best + n, tid = threadIdx.x, T = threads_a_key(m);
+  constexpr int kMost = (kSelBuffer + kMaxBeamCands) / kSelThreads;
   unsigned long long key[kMost];
   int rank[kMost];
 #pragma unroll
   for (int i = 0; i < kMost; ++i) {
-    const int at = tid + i * kSelThreads;
-    if (at >= m) break;
-    key[i] = sm.keys[at];
+    const int at = tid / T + i * kSelThreads;
+    key[i] = at < m ? sm.keys[at] : 0;
+    rank[i] = K;
+    if (i * kSelThreads >= m) break;
     int r = 0;
-    for (int j = 0; j < m; ++j) r += sm.keys[j] > key[i];
-    rank[i] = r;
+#pragma unroll 4
+    for (int j = tid & (T - 1); j < m; j += T) r += sm.keys[j] > key[i];
+    for (int q = 1; q < T; q <<= 1) r += __shfl_xor_sync(0xffffffffu, r, q);
+    if (at < m && (tid & (T - 1)) == 0) rank[i] = r;
   }
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kMost; ++i) {
-    if (tid + i * kSelThreads >= m) break;
+  for (int i = 0; i < kMost; ++i)
     if (rank[i] < K) sm.keys[rank[i]] = key[i];
-  }
   if (tid == 0) sm.many = 0;
   __syncthreads();
   return min(m, K);
 }
 
-// A continuation: its value, row of the request and key; no row: none.
-struct Candidate {
-  double value;
-  unsigned long long key;
-  int row;
-};
-// The better value, equal ones by row, logit (different logits of a row can have the
-// same value in 64 bits) and token.
-__device__ __forceinline__ bool before(const Candidate& a, const Candidate& b) {
-  if (a.value != b.value) return a.value > b.value;
-  return a.row != b.row ? a.row < b.row : a.key > b.key;
-}
-
-// The request's parts joined: its candidates and next beams.
-__device__ void join_request(const BeamSelectArgs& a, SelectSmem& sm, int req) {
+// The request's parts joined: its candidates and next beams.  All keys of its lists
+// get their values in fp32, off by at most kNear of their parts; the least of the warps'
+// ceil(K / 8)-th largest lane maxima bounds the K-th value from below, and what may reach
+// it gets its value in 64 bits (of which the GPU does few at a time) and is ranked by
+// counting.
+constexpr float kNear = 0x1p-21f;
+__device__ void join_request(const BeamSelectArgs& a, JoinSmem& sm, int req) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int W = a.width, K = a.n_cands, lists = W * a.parts;
+  const int W = a.width, K = a.n_cands, per_row = a.parts * K, N = W * per_row;
   const int row0 = req * W;
-  for (int w = warp; w < W; w += kSelWarps) {
-    const float score = a.scores[row0 + w];
-    const BeamPart* p = a.sums + (int64_t)(row0 + w) * a.parts;
-    const bool used = isfinite(score);
-    float top = -FLT_MAX;
-    if (used)
-      for (int i = lane; i < a.parts; i += 32) top = fmaxf(top, p[i].top);
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    double sum = 0.;
-    if (used)
-      for (int i = lane; i < a.parts; i += 32) sum += p[i].sum * exp((double)p[i].top - (double)top);
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) {
-      sm.row_top[w] = top;
-      sm.row_log[w] = log(sum);
-      sm.row_score[w] = used ? (double)score : -INFINITY;
-    }
-  }
-  __syncthreads();
-
-  // Each warp takes every eighth list, a lane up to two of them, and draws the
-  // best head K times.
-  constexpr int kOwn = kSelLists / kSelThreads;
-  Candidate own[kOwn];
-  int next[kOwn];
-  auto head = [&](int i) {
-    own[i] = {-INFINITY, 0, kMaxBeams};  // none: behind all others
-    const int l = warp + kSelWarps * (lane + 32 * i);
-    if (l >= lists || next[i] >= K) return;
-    const int w = l / a.parts;
-    if (sm.row_score[w] == -INFINITY) return;
-    const unsigned long long key = a.lists[((int64_t)row0 * a.parts + l) * K + next[i]];
-    if (key == 0) return;
-    own[i] = {((double)of_ordered((uint32_t)(key >> 32)) - sm.row_top[w] - sm.row_log[w]) + sm.row_score[w], key, w};
+  const unsigned long long* keys = a.lists + (int64_t)row0 * per_row;
+  // (the first keys of the thread are on their way while the rows' sums are joined)
+  unsigned long long key[4];
+  auto fetch = [&](int e0) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) key[i] = e0 + i * kSelThreads < N ? keys[e0 + i * kSelThreads] : 0;
   };
-#pragma unroll
-  for (int i = 0; i < kOwn; ++i) {
-    next[i] = 0;
-    head(i);
-  }
-  int n = 0;
-  for (; n < K; ++n) {
-    Candidate c = own[0];
-#pragma unroll
-    for (int i = 1; i < kOwn; ++i)
-      if (before(own[i], c)) c = own[i];
-    for (int o = 16; o; o >>= 1) {
-      const Candidate d = {__shfl_xor_sync(0xffffffffu, c.value, o), __shfl_xor_sync(0xffffffffu, c.key, o),
-                           __shfl_xor_sync(0xffffffffu, c.row, o)};
-      if (before(d, c)) c = d;
+  fetch(tid);
+  const int end = warp == 0 && lane < a.n_ends ? a.ends[lane] : -1;
+  if (tid == 0) sm.many = 0;
+  // A row a group of as many lanes as it has parts (up to 32, a power of two).
+  const int group = a.parts > 16 ? 32 : a.parts > 8 ? 16 : a.parts > 4 ? 8 : a.parts > 2 ? 4 : a.parts;
+  const int of_row = tid & (group - 1);
+  for (int w0 = 0; w0 < W; w0 += kSelThreads / group) {
+    const int w = w0 + tid / group;
+    const float score = w < W ? a.scores[row0 + w] : -INFINITY;
+    const BeamPart* p = a.sums + (int64_t)(row0 + min(w, W - 1)) * a.parts;
+    const BeamPart own = of_row < a.parts ? p[of_row] : BeamPart{0, -INFINITY, INT_MIN};
+    // the largest logit and power; parts far below the row's largest logit add nothing
+    // (what stands for a row not in use may be anything)
+    float top = own.top;
+    for (int i = of_row + 32; i < a.parts; i += 32) top = fmaxf(top, p[i].top);
+    for (int q = 1; q < group; q <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, q));
+    const bool far = is_far(top);
+    int r = is_far(own.top) ? INT_MIN : own.power;
+    for (int i = of_row + 32; i < a.parts; i += 32)
+      if (!is_far(p[i].top)) r = max(r, p[i].power);
+    for (int q = 1; q < group; q <<= 1) r = max(r, __shfl_xor_sync(0xffffffffu, r, q));
+    unsigned long long sum = 0;
+    for (int i = of_row; i < a.parts; i += 32) {
+      const BeamPart x = i == of_row ? own : p[i];
+      if (far && x.sum) sum += (unsigned long long)((double)x.sum * (double)ex2_approx((x.top - top) * kLog2e));
+      if (!far && !is_far(x.top)) sum += x.sum >> min(max(r - x.power, 0), 63);
     }
-    if (c.row == kMaxBeams) break;
-    if (lane == 0) {
-      sm.value[warp][n] = c.value;
-      sm.key[warp][n] = c.key;
-      sm.row[warp][n] = c.row;
+    for (int q = 1; q < group; q <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, q);
+    if (of_row == 0 && w < W) {
+      double log = log_fixed(max(sum, 1ull));  // of the sum, from the largest logit on
+      if (!far) log += 0.693147180559945309417 * ((double)r - (double)top * (double)kLog2e);
+      sm.row_top[w] = top;
+      sm.row_rest[w] = isfinite(score) ? (double)score - log : -INFINITY;
+      sm.row_near[w] = (float)sm.row_rest[w];
     }
-#pragma unroll
-    for (int i = 0; i < kOwn; ++i)
-      if (own[i].row == c.row && own[i].key == c.key) {
-        ++next[i];
-        head(i);
-      }
   }
-  if (lane == 0) sm.found[warp] = n;
   __syncthreads();
 
-  // A candidate's place: those before it in every warp's list.
-  auto listed = [&](int q, int i) { return Candidate{sm.value[q][i], sm.key[q][i], sm.row[q][i]}; };
-  int all = 0;
-  for (int q = 0; q < kSelWarps; ++q) all += sm.found[q];
-  all = min(all, K);
-  for (int e = tid; e < kSelWarps * kMaxBeamCands; e += kSelThreads) {
-    const int q = e / kMaxBeamCands, i = e % kMaxBeamCands;
-    if (i >= sm.found[q]) continue;
-    const Candidate c = listed(q, i);
-    int place = i;
-    for (int p = 0; p < kSelWarps; ++p) {
-      if (p == q) continue;
-      int lo = 0, hi = sm.found[p];
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (before(listed(p, mid), c)) lo = mid + 1; else hi = mid;
-      }
-      place += lo;
+  for (int e0 = tid; e0 < N; e0 += 4 * kSelThreads) {
+    if (e0 != tid) fetch(e0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int e = e0 + i * kSelThreads;
+      if (e >= N) break;
+      const int w = (int)fast_div((uint32_t)e, a.div_row_keys);
+      const float x = of_ordered((uint32_t)(key[i] >> 32));
+      sm.key[e] = key[i];
+      // (-infinity: none)
+      sm.below[e] = x - sm.row_top[w], sm.near[e] = key[i] ? sm.row_near[w] : -INFINITY;
     }
-    if (place < K) {
-      sm.best_row[place] = row0 + c.row;
-      sm.best_token[place] = (int)~(uint32_t)c.key;
-      sm.best_score[place] = (float)c.value;
+  }
+  __syncthreads();
+  auto value = [&](int e, float side) { return sm.below[e] + sm.near[e] + side * (fabsf(sm.below[e]) + fabsf(sm.near[e])); };
+  uint32_t bound = ordered(-INFINITY) + 1;
+  if (N > kSelSmall) {
+    // a warp takes every eighth key, each lane's at another depth of its list
+    float most = -INFINITY;
+    for (int e0 = lane * kSelWarps; e0 < N; e0 += kSelThreads) {
+      const int e = e0 + ((lane + warp) & (kSelWarps - 1));
+      if (e < N && sm.near[e] > -INFINITY) most = fmaxf(most, value(e, -kNear));
+    }
+    uint32_t o = ordered(most), v = 0;
+    for (int r = 0; r < (K + kSelWarps - 1) / kSelWarps; ++r) {
+      v = __reduce_max_sync(0xffffffffu, o);
+      const unsigned m = __ballot_sync(0xffffffffu, o == v);
+      if (lane == __ffs(m) - 1) o = 0;
+    }
+    if (lane == 0) sm.warp_bound[warp] = v;
+    __syncthreads();
+    v = sm.warp_bound[0];
+#pragma unroll
+    for (int q = 1; q < kSelWarps; ++q) v = min(v, sm.warp_bound[q]);
+    bound = max(v, bound);
+  }
+  for (int e = tid; e < N; e += kSelThreads)
+    if (sm.near[e] > -INFINITY && !(ordered(value(e, kNear)) < bound)) sm.entry[atomicAdd(&sm.many, 1)] = (uint16_t)e;
+  __syncthreads();
+  const int many = sm.many, all = min(many, K), T = threads_a_key(many);
+  for (int i = tid; i < many; i += kSelThreads) {
+    const int e = sm.entry[i], w = (int)fast_div((uint32_t)e, a.div_row_keys);
+    const double x = of_ordered((uint32_t)(sm.key[e] >> 32));
+    sm.value[i] = ordered(x - sm.row_top[w] + sm.row_rest[w]);
+  }
+  __syncthreads();
+  for (int i0 = 0; i0 < many; i0 += kSelThreads / T) {
+    const int i = i0 + tid / T;
+    const unsigned long long v = i < many ? sm.value[i] : 0;
+    const int e = i < many ? sm.entry[i] : 0;
+    const uint32_t w = fast_div((uint32_t)e, a.div_row_keys);
+    int place = 0;
+#pragma unroll 4
+    for (int j = tid & (T - 1); j < many; j += T) {
+      const unsigned long long u = sm.value[j];
+      place += u > v;
+      if (u == v) {
+        // equal values: by row, logit (different logits of a row can have the same value in
+        // 64 bits) and token
+        const int f = sm.entry[j];
+        place += fast_div((uint32_t)f, a.div_row_keys) == w ? sm.key[f] > sm.key[e] : f < e;
+      }
+    }
+    for (int q = 1; q < T; q <<= 1) place += __shfl_xor_sync(0xffffffffu, place, q);
+    if (i < many && (tid & (T - 1)) == 0 && place < K) {
+      sm.best_row[place] = row0 + (int)w;
+      sm.best_token[place] = (int)~(uint32_t)sm.key[e];
+      sm.best_score[place] = (float)__longlong_as_double((long long)(v >> 63 ? v ^ 0x8000000000000000ull : ~v));
     }
   }
   __syncthreads();
@@ -214,7 +322,12 @@ __device__ void join_request(const BeamSelectArgs& a, SelectSmem& sm, int req) {
     for (int base = 0; base < K; base += 32) {
       const int i = base + lane;
       bool goes = i < all;
-      for (int e = 0; e < a.n_ends; ++e) goes = goes && sm.best_token[i] != a.ends[e];
+      const int token = goes ? sm.best_token[i] : -1;
+#pragma unroll
+      for (int e = 0; e < kMaxEnds; ++e) {
+        const int x = __shfl_sync(0xffffffffu, end, e);
+        goes = goes && (e >= a.n_ends || token != x);
+      }
       const unsigned m = __ballot_sync(0xffffffffu, goes);
       const int at = placed + __popc(m & ((1u << lane) - 1));
       if (goes && at < W) {
@@ -233,154 +346,308 @@ __device__ void join_request(const BeamSelectArgs& a, SelectSmem& sm, int req) {
 }
 
 template <bool kFp32>
-__global__ void __launch_bounds__(kSelThreads) beam_select_kernel(const BeamSelectArgs a) {
-  constexpr int kE = kFp32 ? 4 : 8;           // logits of a 16-byte word
-  constexpr int kPer = kSelVecs * kE;         // of a thread in a chunk
+__global__ void __launch_bounds__(kSelThreads, 2) beam_select_kernel(const BeamSelectArgs a) {
+  constexpr int kE = kFp32 ? 4 : 8;            // logits of a 16-byte word
+  constexpr int kPer = kSelVecs * kE;          // of a thread in a chunk
+  constexpr int kSize = kFp32 ? 4 : 2;
   constexpr int kChunk = kSelThreads * kPer;
-  __shared__ SelectSmem sm;
-  pdl_launch_dependents();
-  pdl_wait();
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ __align__(16) SelectSmem sm;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int item = blockIdx.x, row = (int)fast_div((uint32_t)item, a.div_parts);
   const int part = item - row * a.parts, req = (int)fast_div((uint32_t)row, a.div_width);
   const int K = a.n_cands;
   if (tid == 0) {
-    sm.many = 0;
-    sm.valid = kSelBuffer;
+    sm.many = sm.hits = 0;
+    for (int i = 0; i < kSelStages; ++i) {
+      mbar_init(&sm.full[i], 1);
+      mbar_init(&sm.empty[i], kSelWarps);
+    }
+    fence_barrier_init();
   }
+  pdl_launch_dependents();
+  pdl_wait();
   if (isfinite(a.scores[row])) {
     const int begin = (int)min((int64_t)part * a.part_chunks * kChunk, (int64_t)a.vocab);
     const int end = (int)min((int64_t)begin + (int64_t)a.part_chunks * kChunk, (int64_t)a.vocab);
-    const uint8_t* base = static_cast<const uint8_t*>(a.logits) + row * a.ld * (kFp32 ? 4 : 2);
-    const bool vec = (reinterpret_cast<uintptr_t>(base) & 15) == 0;
-    float bound = -INFINITY, top = -FLT_MAX, sum = 0.f;
-    int best = 0;
-    for (int at = begin; at < end; at += kChunk) {
-      float x[kPer];
-#pragma unroll
-      for (int j = 0; j < kSelVecs; ++j) {
-        const int v = at + (j * kSelThreads + tid) * kE;
-        if (vec && v + kE <= end) {
-          const uint4 u = *reinterpret_cast<const uint4*>(base + (int64_t)v * (kFp32 ? 4 : 2));
-          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-          for (int e = 0; e < kE; ++e)
-            x[j * kE + e] = kFp32 ? __uint_as_float(w[e & 3])
-                                  : __uint_as_float(e & 1 ? w[e / 2 & 3] & 0xFFFF0000u : w[e / 2 & 3] << 16);
-        } else {
-#pragma unroll
-          for (int e = 0; e < kE; ++e)
-            x[j * kE + e] = v + e >= end ? -INFINITY
-                            : kFp32 ? reinterpret_cast<const float*>(base)[v + e]
-                                    : bf16_to_f(reinterpret_cast<const uint16_t*>(base)[v + e]);
-        }
+    const int chunks = (end - begin + kChunk - 1) / kChunk;
+    const int per_cell = (chunks + kSelCells - 1) / kSelCells;  // chunks
+    const uint8_t* base = static_cast<const uint8_t*>(a.logits) + row * a.ld * kSize;
+    const int off = (int)(reinterpret_cast<uintptr_t>(base) & 15);  // of every chunk's first logit
+    // the row's 16-byte words that hold nothing else
+    const uint8_t* inner0 = base + (-off & 15);
+    const uint8_t* inner1 = base + (int64_t)a.vocab * kSize;
+    inner1 -= reinterpret_cast<uintptr_t>(inner1) & 15;
+    auto raw = [&](int v) {
+      return kFp32 ? reinterpret_cast<const float*>(base)[v] : bf16_to_f(reinterpret_cast<const uint16_t*>(base)[v]);
+    };
+    auto issue = [&](int c, int slot) {
+      const uint8_t* first = base + (begin + (int64_t)c * kChunk) * kSize - off;
+      const uint8_t* last = base + min(begin + (int64_t)(c + 1) * kChunk, (int64_t)end) * kSize;
+      last += -reinterpret_cast<uintptr_t>(last) & 15;
+      const uint8_t *from = first < inner0 ? inner0 : first, *to = last > inner1 ? inner1 : last;
+      if (to > from) {
+        const uint32_t bytes = (uint32_t)(to - from);
+        mbar_arrive_expect_tx(&sm.full[slot], bytes);
+        bulk_load_plain(ring + slot * kSelStageBytes + (from - first), from, bytes, &sm.full[slot]);
+      } else {
+        mbar_arrive(&sm.full[slot]);
       }
-      auto token = [&](int i) { return at + (i / kE * kSelThreads + tid) * kE + i % kE; };
-      float mx = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) mx = fmaxf(mx, x[i]);  // (NaN falls out)
+    };
+    if (tid == 0)
+      for (int c = 0; c < min(chunks, kSelStages); ++c) issue(c, c);
+    __syncthreads();
 
-      // the sum of exponentials, from the thread's largest logit so far on
-      {
-        const float t = fmaxf(top, fminf(mx, FLT_MAX));
-        float s = 0.f;
+    float top = -INFINITY, power = power_of(-INFINITY), sum = 0.f, of_cell = -INFINITY;
+    int slot = 0, cell = 0, in_cell = 0;
+    uint32_t parity = 0;
+    bool ok = true;
+    for (int c = 0; c < chunks; ++c) {
+      const int at = begin + c * kChunk;
+      const int many = min(end - at, kChunk);
+      const uint4* words = reinterpret_cast<const uint4*>(ring + slot * kSelStageBytes) + tid;
+      ok = mbar_wait(&sm.full[slot], parity, a.status) && ok;
+      // The thread's words; logits behind the part's last are -infinity.
+      uint32_t w[4 * kSelVecs];
+      if (off == 0 && many == kChunk) {
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) s += ex2_approx((x[i] - t) * kLog2e);
-        if (!(s < INFINITY)) {  // infinities and NaN among them
-          s = 0.f;
+        for (int j = 0; j < kSelVecs; ++j) *reinterpret_cast<uint4*>(w + 4 * j) = words[j * kSelThreads];
+      } else {
 #pragma unroll
-          for (int i = 0; i < kPer; ++i)
-            if (x[i] == x[i]) s += ex2_approx((fminf(x[i], FLT_MAX) - t) * kLog2e);
-        }
-        sum = sum * ex2_approx((top - t) * kLog2e) + s;
-        top = t;
-      }
-
-      const bool first = at == begin;
-      if (first) {
-        const float g = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        if ((lane & 1) == 0) sm.group[tid >> 1] = g;
-        __syncthreads();
-        if (tid < kSelThreads / 2) {
-          const float mine = sm.group[tid];
-          int r = 0;
-          for (int j = 0; j < kSelThreads / 2; ++j)
-            r += sm.group[j] > mine || (sm.group[j] == mine && j < tid);
-          if (r == K - 1) sm.bound = mine;
-        }
-        __syncthreads();
-        bound = sm.bound;
-      }
-      auto passes = [&](float y) { return first ? y >= bound && y > -INFINITY : y > bound; };
-      bool fails = false;
-      if (first ? mx >= bound : mx > bound) {
-        int n = 0;
+        for (int j = 0; j < kSelVecs; ++j) {
+          const int e0 = (j * kSelThreads + tid) * kE;
+          const uint4 u = words[j * kSelThreads], v = words[j * kSelThreads + (off != 0)];
+          uint32_t y[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};  // bytes off .. off + 15 of them
+          if (off & 8) {
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) n += passes(x[i]);
-        if (n) {
-          int to = atomicAdd(&sm.many, n);
-          if (to + n <= kSelBuffer) {
+            for (int i = 0; i < 6; ++i) y[i] = y[i + 2];
+          }
+          if (off & 4) {
 #pragma unroll
-            for (int i = 0; i < kPer; ++i)
-              if (passes(x[i])) sm.keys[best + to++] = key_of(x[i], token(i));
-          } else {
-            atomicMin(&sm.valid, to);
-            fails = true;
+            for (int i = 0; i < 5; ++i) y[i] = y[i + 1];
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[4 * j + i] = __funnelshift_r(y[i], y[i + 1], (off & 2) * 8);
+          const uint8_t* p = base + (int64_t)(at + e0) * kSize;
+          if (e0 < many && (p < inner0 || p + 16 > inner1 || e0 + kE > many)) {  // the edges of row and part
+#pragma unroll
+            for (int e = 0; e < kE; ++e) {
+              const float x = e0 + e < many ? raw(at + e0 + e) : -INFINITY;
+              if constexpr (kFp32) w[4 * j + e % 4] = __float_as_uint(x);
+              else if (e & 1) w[4 * j + e / 2 % 4] |= __float_as_uint(x) & 0xFFFF0000u;
+              else w[4 * j + e / 2 % 4] = __float_as_uint(x) >> 16;
+            }
+          } else if (e0 >= many) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[4 * j + i] = kFp32 ? 0xFF800000u : 0xFF80FF80u;
           }
         }
       }
-      if (__syncthreads_or(fails)) {
-        const int n = sm.valid;
-        __syncthreads();
-        if (tid == 0) sm.valid = kSelBuffer;
-        best = rank_keys(sm, best, n, K);
-#pragma unroll 1
-        for (int i = 0; i < kPer; ++i) {
-          float y = 0.f;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.empty[slot]);
+
+      // the largest (NaN falls out)
+      uint32_t m = w[0];
+      float mx;
+      if constexpr (kFp32) {
 #pragma unroll
-          for (int q = 0; q < kPer; ++q)
-            if (q == i) y = x[q];
-          const unsigned long long least = best == K ? sm.keys[K - 1] : 0;
-          const unsigned long long key = key_of(y, token(i));
-          if (fails && passes(y) && key > least) sm.keys[best + atomicAdd(&sm.many, 1)] = key;
-          __syncthreads();
-          const int more = sm.many;
-          __syncthreads();
-          if (more) best = rank_keys(sm, best, more, K);
-        }
-        if (best == K) bound = fmaxf(bound, of_ordered((uint32_t)(sm.keys[K - 1] >> 32)));
-      } else if (sm.many > kSelRank) {
-        const int n = sm.many;
-        __syncthreads();
-        best = rank_keys(sm, best, n, K);
-        if (best == K) bound = fmaxf(bound, of_ordered((uint32_t)(sm.keys[K - 1] >> 32)));
+        for (int i = 1; i < 4 * kSelVecs; ++i)
+          m = __float_as_uint(fmaxf(__uint_as_float(m), __uint_as_float(w[i])));
+        mx = fmaxf(__uint_as_float(m), -INFINITY);
       } else {
-        __syncthreads();
+#pragma unroll
+        for (int i = 1; i < 4 * kSelVecs; ++i) m = max_bf16x2(m, w[i]);
+        mx = fmaxf(fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u)), -INFINITY);
+      }
+      top = fmaxf(top, mx);
+      of_cell = fmaxf(of_cell, mx);
+      if (++in_cell == per_cell || c + 1 == chunks) {
+        sm.cell[tid][cell] = __bfloat16_as_ushort(__float2bfloat16_ru(of_cell));
+        ++cell;
+        in_cell = 0;
+        of_cell = -INFINITY;
+      }
+
+      // the sum of exponentials
+      const float r = fmaxf(power, power_of(mx));
+      float2 s = {sum * ex2_approx(power - r), 0.f}, t = {0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < kPer / 2; ++i) {
+        const float2 x = kFp32 ? make_float2(__uint_as_float(w[2 * i % (4 * kSelVecs)]),
+                                             __uint_as_float(w[(2 * i + 1) % (4 * kSelVecs)]))
+                               : make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+        const float2 q = fma2(x, make_float2(kLog2e, kLog2e), make_float2(-r, -r));
+        const float2 e = make_float2(ex2_approx(q.x), ex2_approx(q.y));
+        if (i & 1) t = add2(t, e); else s = add2(s, e);
+      }
+      s = add2(s, t);
+      sum = s.x + s.y;
+      power = r;
+      if (tid == 0 && c + kSelStages < chunks) {  // the stage's next chunk, once every warp has taken this one
+        ok = mbar_wait(&sm.empty[slot], parity, a.status) && ok;
+        issue(c + kSelStages, slot);
+      }
+      if (++slot == kSelStages) {
+        slot = 0;
+        parity ^= 1;
       }
     }
-    const int n = sm.many;
+
+    // What the warps know of the sum; the bound, and the cells that reach it.
+    uint32_t o = ordered(top), v = 0;
+    const uint32_t warp_top = __reduce_max_sync(0xffffffffu, o);
+    int r = __reduce_max_sync(0xffffffffu, (int)power);
+    auto fixed_sum = [&](float x) {  // of the warp, in multiples of 2^(r - 32)
+      unsigned long long f = __float2ull_rn(x * 4294967296.f);
+      for (int q = 16; q; q >>= 1) f += __shfl_xor_sync(0xffffffffu, f, q);
+      return f;
+    };
+    unsigned long long fixed = fixed_sum(sum * ex2_approx(power - (float)r));
+    o = max(o, __shfl_xor_sync(0xffffffffu, o, 1));
+    if ((lane & 1) == 0) sm.pair[tid / 2] = o;
+    if (lane == 0) {
+      sm.warp_top[warp] = warp_top;
+      sm.warp_power[warp] = r;
+      sm.warp_sum[warp] = fixed;
+    }
+    const bool bad = __syncthreads_or(!(sum < INFINITY));
+    if (tid < kSelThreads / 2) {
+      o = sm.pair[tid];
+      int place = 0;
+#pragma unroll 8
+      for (int j = 0; j < kSelThreads / 2; j += 4) {
+        const uint4 x = *reinterpret_cast<const uint4*>(sm.pair + j);
+        place += (x.x > o || (x.x == o && j < tid)) + (x.y > o || (x.y == o && j + 1 < tid)) +
+                 (x.z > o || (x.z == o && j + 2 < tid)) + (x.w > o || (x.w == o && j + 3 < tid));
+      }
+      if (place == K - 1) sm.bound = o;
+    }
     __syncthreads();
-    if (n) best = rank_keys(sm, best, n, K);
+    v = sm.bound;
+    o = sm.warp_top[0];
+#pragma unroll
+    for (int q = 1; q < kSelWarps; ++q) o = max(o, sm.warp_top[q]);
+    const float most = fminf(of_ordered(o), FLT_MAX);  // the part's largest
+    v = max(v, ordered(-INFINITY) + 1);  // (-infinity never passes)
+    uint16_t* hit = reinterpret_cast<uint16_t*>(ring);  // (no copy is on its way any more)
+    {
+      uint32_t reach = 0;  // the thread's cells that do
+      const uint4* p = reinterpret_cast<const uint4*>(sm.cell[tid]);
+#pragma unroll
+      for (int i = 0; i < kSelCells / 8; ++i) {
+        const uint4 u = p[i];
+        const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          reach |= (uint32_t)(ordered(__uint_as_float(x[k] << 16)) >= v) << (8 * i + 2 * k) |
+                   (uint32_t)(ordered(__uint_as_float(x[k] & 0xFFFF0000u)) >= v) << (8 * i + 2 * k + 1);
+      }
+      reach &= (1u << cell) - 1;
+      const int mine = __popc(reach);
+      int to = mine;
+#pragma unroll
+      for (int q = 1; q < 32; q <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, to, q);
+        if (lane >= q) to += x;
+      }
+      int first = 0;
+      if (lane == 31) first = atomicAdd(&sm.hits, to);
+      to += __shfl_sync(0xffffffffu, first, 31) - mine;
+      for (; reach; reach &= reach - 1) hit[to++] = (uint16_t)((__ffs(reach) - 1) * kSelThreads + tid);
+    }
+    __syncthreads();
+    // Logit `lane` of the thread's in chunk d of a cell: its token, or -1.
+    auto token_of = [&](int h, int d) {
+      const int c = h / kSelThreads * per_cell + d, thread = h % kSelThreads;
+      const int e = (lane / kE * kSelThreads + thread) * kE + lane % kE;
+      const int64_t t = begin + (int64_t)c * kChunk + e;
+      return d < per_cell && lane < kPer && t < end ? (int)t : -1;
+    };
+    const int hits = sm.hits;
+    constexpr int kAtOnce = 8;
+    for (int h0 = warp; h0 < hits; h0 += kAtOnce * kSelWarps) {
+      for (int d = 0; d < per_cell; ++d) {
+        float x[kAtOnce];
+        int t[kAtOnce];
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+          const int h = h0 + i * kSelWarps;
+          t[i] = h < hits ? token_of(hit[h], d) : -1;
+          x[i] = t[i] >= 0 ? raw(t[i]) : -INFINITY;
+        }
+        uint32_t passes = 0;
+        int many = 0;
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+          const bool p = x[i] == x[i] && ordered(x[i]) >= v;
+          passes |= (uint32_t)p << i;
+          many += __popc(__ballot_sync(0xffffffffu, p));
+        }
+        int to = 0;
+        if (lane == 0) to = atomicAdd(&sm.many, many);
+        to = __shfl_sync(0xffffffffu, to, 0);
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+          const unsigned m = __ballot_sync(0xffffffffu, passes >> i & 1);
+          const int at = to + __popc(m & ((1u << lane) - 1));
+          if ((passes >> i & 1) && at < kSelBuffer) sm.keys[at] = key_of(x[i], t[i]);
+          to += __popc(m);
+        }
+      }
+    }
+    __syncthreads();
+    int best = 0;
+    if (sm.many > kSelBuffer) {  // a warp a cell and chunk, what can still count
+      __syncthreads();
+      if (tid == 0) sm.many = 0;
+      __syncthreads();
+      for (int h0 = 0; h0 < hits; h0 += kSelWarps) {
+        const int h = h0 + warp < hits ? hit[h0 + warp] : -1;
+        const float most = h < 0 ? -INFINITY : bf16_to_f(sm.cell[h % kSelThreads][h / kSelThreads]);
+        for (int d = 0; d < per_cell; ++d) {
+          const unsigned long long least = best == K ? sm.keys[K - 1] : 0;
+          const int first = begin + (h / kSelThreads * per_cell + d) * kChunk + h % kSelThreads * kE;
+          const bool may = h >= 0 && key_of(most, first) > least;
+          if (!__syncthreads_or(may)) continue;
+          const int t = may ? token_of(h, d) : -1;
+          const float x = t >= 0 ? raw(t) : -INFINITY;
+          const unsigned long long key = key_of(x, t);
+          if (x == x && ordered(x) >= v && key > least) sm.keys[best + atomicAdd(&sm.many, 1)] = key;
+          __syncthreads();
+          const int n = sm.many;
+          __syncthreads();
+          if (n) best = rank_keys(sm, best, n, K);
+        }
+      }
+    }
 
     // the part's list and sum
-    float all = top;
-    for (int o = 16; o; o >>= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, o));
-    if (lane == 0) sm.warp_top[warp] = all;
-    __syncthreads();
-    all = sm.warp_top[0];
+    const int n = sm.many;
+    if (n) best = rank_keys(sm, best, n, K);
 #pragma unroll
-    for (int q = 1; q < kSelWarps; ++q) all = fmaxf(all, sm.warp_top[q]);
-    double d = (double)sum * (double)ex2_approx((top - all) * kLog2e);
-    for (int o = 16; o; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-    if (lane == 0) sm.warp_sum[warp] = d;
-    __syncthreads();
-    if (tid == 0) {
-      d = 0.;
-#pragma unroll
-      for (int q = 0; q < kSelWarps; ++q) d += sm.warp_sum[q];
-      a.sums[item] = {d, all};
+    for (int q = 0; q < kSelWarps; ++q) r = max(r, sm.warp_power[q]);
+    if (bad || (is_far(most) && most > -INFINITY)) {  // once more, NaN left out
+      sum = 0.f;
+      for (int v = begin + tid; v < end; v += kSelThreads) {
+        const float y = raw(v);
+        if (y > -INFINITY)
+          sum += ex2_approx(is_far(most) ? (fminf(y, FLT_MAX) - most) * kLog2e : fmaf(y, kLog2e, -(float)r));
+      }
+      fixed = fixed_sum(sum);
+      __syncthreads();  // (what the warps left was read)
+      if (lane == 0) {
+        sm.warp_power[warp] = r;
+        sm.warp_sum[warp] = fixed;
+      }
+      __syncthreads();
     }
-    if (tid < K) a.lists[(int64_t)item * K + tid] = tid < best ? sm.keys[tid] : 0;
+    if (tid == 0) {
+      fixed = 0;
+#pragma unroll
+      for (int q = 0; q < kSelWarps; ++q) fixed += sm.warp_sum[q] >> min(r - sm.warp_power[q], 63);
+      a.sums[item] = {fixed, most, r};
+    }
+    if (tid < K) a.lists[(int64_t)item * K + tid] = tid < best && ok ? sm.keys[tid] : 0;
   }
   // The last of the request's CTAs joins them.
   __syncthreads();
@@ -391,27 +658,34 @@ __global__ void __launch_bounds__(kSelThreads) beam_select_kernel(const BeamSele
     fence_acq_rel_gpu();
   }
   __syncthreads();
-  if (sm.last) join_request(a, sm, req);
+  if (sm.last) join_request(a, *reinterpret_cast<JoinSmem*>(ring), req);
 }
 
-// Parts of a row: enough for two CTAs an SM.
-static int parts_most(int64_t rows, int width, int num_sms) {
-  const int64_t want = (2 * num_sms + rows - 1) / rows;
-  return (int)std::max<int64_t>(1, std::min<int64_t>(want, kSelLists / width));
+// Parts of a row: as many as two CTAs an SM allow, and a request's lists have room.
+static int parts_most(int64_t rows, int width, int cands, int num_sms) {
+  return (int)std::max<int64_t>(1, std::min<int64_t>(2 * num_sms / rows, kSelKeys / (width * cands)));
 }
 int64_t beam_parts_all(int64_t rows, int num_sms) { return rows + 2 * num_sms; }
 
+template <bool kFp32>
+static cudaError_t launch_select(const BeamSelectArgs& a, int64_t ctas, cudaStream_t st) {
+  const int smem = kSelRingBytes;
+  cudaError_t e = cudaFuncSetAttribute(beam_select_kernel<kFp32>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  return launch_k(beam_select_kernel<kFp32>, dim3((unsigned)ctas), dim3(kSelThreads), smem, st, a);
+}
+
 cudaError_t launch_beam_select(BeamSelectArgs a, int num_sms, cudaStream_t st) {
-  const int chunk = kSelThreads * kSelVecs * (a.fp32 ? 4 : 8);
+  const int chunk = kSelChunkBytes / (a.fp32 ? 4 : 2);
   const int chunks = (a.vocab + chunk - 1) / chunk;
   const int64_t rows = (int64_t)a.n_reqs * a.width;
-  a.parts = std::min(chunks, parts_most(rows, a.width, num_sms));
+  a.parts = std::min(chunks, parts_most(rows, a.width, a.n_cands, num_sms));
   a.part_chunks = (chunks + a.parts - 1) / a.parts;
   a.parts = (chunks + a.part_chunks - 1) / a.part_chunks;
   a.div_parts = make_fastdiv((uint32_t)a.parts);
   a.div_width = make_fastdiv((uint32_t)a.width);
-  return launch_k(a.fp32 ? beam_select_kernel<true> : beam_select_kernel<false>,
-                  dim3((unsigned)(rows * a.parts)), dim3(kSelThreads), 0, st, a);
+  a.div_row_keys = make_fastdiv((uint32_t)(a.parts * a.n_cands));
+  return a.fp32 ? launch_select<true>(a, rows * a.parts, st) : launch_select<false>(a, rows * a.parts, st);
 }
 
 // ---------------------------------------------------------------------------

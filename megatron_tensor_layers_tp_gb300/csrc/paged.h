@@ -120,10 +120,12 @@ constexpr int kMaxBeamCands = 64;  // of a request
 constexpr int kMaxEnds = 8;
 
 // The K best logits of a part of a row, in order: (ordered value << 32) | ~token, 0 where
-// there are fewer; and its sum of exponentials, from its largest logit on.
+// there are fewer; its largest logit; and its sum of exponentials, of 2^power, times 2^32
+// (from the largest logit on where that is far from 0: beam.cu).
 struct BeamPart {
-  double sum;
+  unsigned long long sum;
   float top;
+  int power;
 };
 struct BeamSelectArgs {
   const void* logits;
@@ -137,10 +139,11 @@ struct BeamSelectArgs {
   float* next_scores;
   int32_t *parents, *tokens;
   int parts, part_chunks;     // parts of a row, chunks of a part
-  FastDiv div_parts, div_width;
+  FastDiv div_parts, div_width, div_row_keys;  // by parts, width, parts * n_cands
   BeamPart* sums;             // [rows][parts]
   unsigned long long* lists;  // [rows][parts][n_cands]
   int* tickets;               // [n_reqs], zero on entry and exit
+  int* status;
 };
 // The most parts that up to `rows` rows are cut into, all together.
 int64_t beam_parts_all(int64_t rows, int num_sms);

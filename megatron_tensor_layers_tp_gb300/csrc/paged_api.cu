@@ -427,6 +427,7 @@ tp_status tp_beam_select(const tp_model* m, const void* logits, int64_t ld_logit
     a.tickets = reinterpret_cast<int*>(base);
     a.sums = reinterpret_cast<BeamPart*>(base + w.sums);
     a.lists = reinterpret_cast<unsigned long long*>(base + w.lists);
+    a.status = m->status;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     return cuda_status(
         launch(m, "beam_select", st, [&] { return launch_beam_select(a, m->num_sms, st); }));

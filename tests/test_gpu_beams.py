@@ -190,6 +190,29 @@ def test_beam_select_infinities_nan_and_lowest_values(fp32):
     assert b.parents[9:12].tolist() == [-1] * 3
 
 
+@pytest.mark.parametrize("first,n", [(0, 300), (40000, 900), (57000, 2000), (8100, 200), (65000, 535)])
+def test_beam_select_allowed_tokens_in_one_place(first, n):
+    """A grammar that allows a run of the vocabulary: all other threads see nothing."""
+    rng = np.random.default_rng(first + n)
+    V = 65535
+    x, scores = beams_case(rng, 2, 4, V, False)
+    x[:, :first] = -np.inf
+    x[:, first + n:] = -np.inf
+    for K in (4, 64):
+        check_select(f64(x), scores, 4, K, (), run_select(model(vocab=V), x, scores, 4, K))
+
+
+@pytest.mark.parametrize("tail", [1, 7, 260, 500, 1280, 2047])
+@pytest.mark.parametrize("fp32", [False, True])
+def test_beam_select_short_last_parts(tail, fp32):
+    rng = np.random.default_rng(tail)
+    V = 3 * 8192 + tail
+    x, scores = beams_case(rng, 2, 2, V, fp32)
+    x[:, 3 * 8192:] += 4.0
+    for K in (2, 60):
+        check_select(f64(x), scores, 2, K, (), run_select(model(vocab=V), x, scores, 2, K))
+
+
 def test_beam_select_negative_zero_is_zero():
     x = torch.zeros((1, 3000))
     x[0, ::2] = -0.0
