@@ -9,8 +9,8 @@
 // ring in shared memory, and a thread takes 16-byte words of them into registers.
 // The warps run through the ring without waiting for each other.
 // The K best: a thread leaves the largest logit of each chunk in shared memory.
-// Behind the last chunk the K-th largest of 128 maxima (two threads each) bounds the
-// K-th largest logit from below, and the logits of the few cells (a thread's of a
+// Behind the last chunk the K-th largest of at least 2 K maxima (two to eight threads
+// each) bounds the K-th largest logit from below, and the logits of the few cells (a thread's of a
 // chunk) that reach the bound are read once more, from L2: what passes is ranked by
 // counting.  Where more passes than the buffer holds (equal logits) the cells are gone
 // through a warp a cell, and ranked in between.
@@ -128,8 +128,8 @@ struct SelectSmem {
   int many;  // keys in the buffer
   int hits;  // cells that reach the bound
   int last;
-  __align__(16) uint32_t pair[kSelThreads / 2];
-  uint32_t bound;  // largest logits of two threads; of them the K-th largest
+  __align__(16) uint32_t group[kSelThreads / 2];
+  uint32_t bound;  // the K-th largest of the groups' largest logits
   uint32_t warp_top[kSelWarps];
   int warp_power[kSelWarps];
   unsigned long long warp_sum[kSelWarps];
@@ -494,7 +494,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) beam_select_kernel(const BeamS
     }
 
     // What the warps know of the sum; the bound, and the cells that reach it.
-    uint32_t o = ordered(top), v = 0;
+    uint32_t o = ordered(top);
     const uint32_t warp_top = __reduce_max_sync(0xffffffffu, o);
     int r = __reduce_max_sync(0xffffffffu, (int)power);
     auto fixed_sum = [&](float x) {  // of the warp, in multiples of 2^(r - 32)
@@ -503,27 +503,31 @@ __global__ void __launch_bounds__(kSelThreads, 2) beam_select_kernel(const BeamS
       return f;
     };
     unsigned long long fixed = fixed_sum(sum * ex2_approx(power - (float)r));
-    o = max(o, __shfl_xor_sync(0xffffffffu, o, 1));
-    if ((lane & 1) == 0) sm.pair[tid / 2] = o;
+    // groups of threads, twice as many as the bound's place
+    const int groups = K > 32 ? 128 : K > 16 ? 64 : 32, size = kSelThreads / groups;
+    for (int q = 1; q < size; q <<= 1) o = max(o, __shfl_xor_sync(0xffffffffu, o, q));
+    const int mine = tid / size, turn = tid & (size - 1);
+    if (turn == 0) sm.group[mine] = o;
     if (lane == 0) {
       sm.warp_top[warp] = warp_top;
       sm.warp_power[warp] = r;
       sm.warp_sum[warp] = fixed;
     }
     const bool bad = __syncthreads_or(!(sum < INFINITY));
-    if (tid < kSelThreads / 2) {
-      o = sm.pair[tid];
+    {
       int place = 0;
-#pragma unroll 8
-      for (int j = 0; j < kSelThreads / 2; j += 4) {
-        const uint4 x = *reinterpret_cast<const uint4*>(sm.pair + j);
-        place += (x.x > o || (x.x == o && j < tid)) + (x.y > o || (x.y == o && j + 1 < tid)) +
-                 (x.z > o || (x.z == o && j + 2 < tid)) + (x.w > o || (x.w == o && j + 3 < tid));
+      const int j0 = turn * (groups / size), j1 = j0 + groups / size;
+#pragma unroll 4
+      for (int j = j0; j < j1; j += 4) {
+        const uint4 x = *reinterpret_cast<const uint4*>(sm.group + j);
+        place += (x.x > o || (x.x == o && j < mine)) + (x.y > o || (x.y == o && j + 1 < mine)) +
+                 (x.z > o || (x.z == o && j + 2 < mine)) + (x.w > o || (x.w == o && j + 3 < mine));
       }
-      if (place == K - 1) sm.bound = o;
+      for (int q = 1; q < size; q <<= 1) place += __shfl_xor_sync(0xffffffffu, place, q);
+      if (place == K - 1 && turn == 0) sm.bound = o;
     }
     __syncthreads();
-    v = sm.bound;
+    uint32_t v = sm.bound;
     o = sm.warp_top[0];
 #pragma unroll
     for (int q = 1; q < kSelWarps; ++q) o = max(o, sm.warp_top[q]);

@@ -167,12 +167,13 @@ struct PageNote {
   int32_t rows;
 };
 constexpr int kShareCtas = 1024;  // CTAs at most
-struct ShareHeader {              // zero between calls, but for counts
-  unsigned arrived[4];            // CTAs at each barrier
-  unsigned done, bad;
-  int32_t counts[2][kShareCtas];
+struct ShareHeader {
+  unsigned arrived[3], bad;  // CTAs at each barrier; the verdict (the first and it are zero between calls)
+  int2 counts[kShareCtas];         // of each CTA's pages and rows
+  int32_t open[kMaxStepSeqs];      // fork: the page that each row goes on writing to, or -1
 };
-constexpr size_t kShareNotes = 16384;  // where the notes begin in the workspace
+constexpr size_t kShareNotes = 49152;  // where the notes begin in the workspace
+static_assert(sizeof(ShareHeader) <= kShareNotes, "the notes lie behind the header");
 
 struct ForkArgs {
   int n_pages, ld_table, page_size;

@@ -21,29 +21,28 @@
 namespace tpk {
 
 constexpr int kShThreads = 512, kShWarps = kShThreads / 32;
-constexpr int kShRows = 8;  // rows of a tile, 32 columns wide
+constexpr int kShRows = 8;   // rows of a tile, 32 columns wide
+constexpr int kShPages = 4;  // consecutive pages of a thread
+constexpr unsigned kAll = 0xffffffffu;
 
-// Sum of v over the CTA; all threads get it.
-__device__ __forceinline__ int block_sum(int v) {
-  __shared__ int sums[kShWarps];
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = v;
-  __syncthreads();
-  int all = 0;
-#pragma unroll
-  for (int w = 0; w < kShWarps; ++w) all += sums[w];
-  return all;
+// Two sums in one word: pages below, rows above.
+__device__ __forceinline__ unsigned long long two(int pages, int rows) {
+  return (unsigned long long)(unsigned)rows << 32 | (unsigned)pages;
 }
-// Threads before this one with the flag set; *total: those of the CTA.
-__device__ __forceinline__ int block_rank(bool flag, int* total) {
-  __shared__ int sums[kShWarps];
+// Sum of v over the CTA's threads before this one; *total: over all of them.
+__device__ __forceinline__ unsigned long long block_scan(unsigned long long v, unsigned long long* total) {
+  __shared__ unsigned long long sums[kShWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const unsigned m = __ballot_sync(0xffffffffu, flag);
+  unsigned long long x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned long long y = __shfl_up_sync(kAll, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();  // (the sums of the scan before were read)
+  if (lane == 31) sums[warp] = x;
   __syncthreads();
-  if (lane == 0) sums[warp] = __popc(m);
-  __syncthreads();
-  int before = __popc(m & ((1u << lane) - 1)), all = 0;
+  unsigned long long before = x - v, all = 0;
 #pragma unroll
   for (int w = 0; w < kShWarps; ++w) {
     if (w < warp) before += sums[w];
@@ -81,26 +80,31 @@ __device__ __forceinline__ bool grid_wait(ShareHeader* h, int which, int* status
   return ok;
 }
 
-// The last CTA to come here clears the header.
-__device__ __forceinline__ void leave(ShareHeader* h) {
-  __syncthreads();
-  if (threadIdx.x != 0) return;
-  bool last = gridDim.x == 1;
-  if (!last) {
-    fence_acq_rel_gpu();
-    last = atomicAdd(&h->done, 1u) == gridDim.x - 1;
-  }
-  if (last) {
-    h->arrived[0] = h->arrived[1] = h->arrived[2] = h->arrived[3] = 0;
-    h->done = h->bad = 0;
-  }
+// The counters of the later barriers are made zero before the first one, that of the
+// first (and the verdict) behind the second, when every CTA is through.
+__device__ __forceinline__ void renew_later(ShareHeader* h) {
+  if (blockIdx.x == 0 && threadIdx.x == 0) h->arrived[1] = h->arrived[2] = 0;
+}
+__device__ __forceinline__ void renew_first(ShareHeader* h) {
+  if (blockIdx.x == 0 && threadIdx.x == 0) h->arrived[0] = h->bad = 0;
 }
 
-// The CTA's share of n things: [first, end).
+// The CTA's share of n things: [first, end), from a multiple of four on.
 __device__ __forceinline__ void share_of(int n, int* first, int* end) {
   const int64_t G = gridDim.x, c = blockIdx.x;
-  *first = (int)(c * n / G);
-  *end = (int)((c + 1) * n / G);
+  *first = (int)(c * n / G) & ~3;
+  *end = c + 1 == G ? n : (int)((c + 1) * n / G) & ~3;
+}
+
+// What the CTAs before this one counted, and all of them.
+__device__ __forceinline__ unsigned long long before_this(const ShareHeader* h, unsigned long long* all) {
+  __shared__ unsigned long long before;
+  int2 c = {0, 0};
+  if (threadIdx.x < gridDim.x) c = __ldcg(&h->counts[threadIdx.x]);  // (no more CTAs than threads)
+  const unsigned long long x = block_scan(two(c.x, c.y), all);
+  if (threadIdx.x == blockIdx.x) before = x;
+  __syncthreads();
+  return before;
 }
 
 // Adds what comes to the same page in consecutive calls in one go.
@@ -120,167 +124,198 @@ struct RefRun {
   }
 };
 
-// Row b of the fork: its source and the tokens it keeps; false: out of bounds.
-__device__ __forceinline__ bool fork_row(const ForkArgs& a, int b, int* old, int* src, int* keep) {
-  int o = a.old_lens[b], s = a.src[b], k = 0;
-  bool ok = o >= 0 && o <= a.cap && s >= -1 && s < a.n_seqs;
-  if (ok && s >= 0) {
-    const int have = a.old_lens[s];
-    k = a.keep_lens ? a.keep_lens[b] : have;
-    ok = have >= 0 && have <= a.cap && k >= 0 && k <= have;
-  }
-  *old = ok ? o : 0;
-  *src = ok ? s : -1;
-  *keep = ok ? k : 0;
-  return ok;
+__device__ __forceinline__ uint2 note_of(const PageNote* notes, int p) {
+  return __ldcg(reinterpret_cast<const uint2*>(notes + p));
 }
+
+// A page that rows held before and none holds after.
+__device__ __forceinline__ bool is_gone(uint2 note) { return note.x >> 16 && !(note.x & 0xFFFF) && !note.y; }
 
 __global__ void __launch_bounds__(kShThreads) fork_pages_kernel(const ForkArgs a) {
   __shared__ uint32_t copied[kMaxStepSeqs / 32];  // the CTA's rows that take a page
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n = a.n_seqs, P = a.page_size;
+  pdl_launch_dependents();
+  pdl_wait();
   const int first = a.free_state[0], count = a.free_state[1];
+  renew_later(a.head);
   auto pages = [&](int len) { return (int)fast_div((uint32_t)len + P - 1, a.div_page); };
-  bool bad = first < 0 || first >= a.n_pages || count < 0 || count > a.n_pages;
+  bool bad = false;
 
   // Pass 1: references, and the new rows as if no page were copied.
   const int row_tiles = (n + kShRows - 1) / kShRows;
   const int col_tiles = max(1, (min(a.ld_table, pages(a.cap)) + 31) / 32);
-  for (int64_t t = (int64_t)blockIdx.x * kShWarps + warp; t < (int64_t)row_tiles * col_tiles;
-       t += (int64_t)gridDim.x * kShWarps) {
-    const int b0 = (int)(t / col_tiles) * kShRows, col = (int)(t % col_tiles) * 32 + lane;
+  // (neighbouring tiles on different SMs: rows that share little take longest)
+  for (int t = warp * gridDim.x + blockIdx.x; t < row_tiles * col_tiles; t += gridDim.x * kShWarps) {
+    const int b0 = t / col_tiles * kShRows, col0 = t % col_tiles * 32, col = col0 + lane;
+    // the tile's rows, a lane each: tokens before, source, tokens kept
+    const int row = b0 + lane;
+    const bool mine = lane < kShRows && row < n;
     int old = 0, src = -1, keep = 0;
-    if (lane < kShRows && b0 + lane < n) bad |= !fork_row(a, b0 + lane, &old, &src, &keep);
-    int was[kShRows], is[kShRows], part[kShRows];
-#pragma unroll
-    for (int r = 0; r < kShRows; ++r) {
-      const int b = b0 + r, o = __shfl_sync(0xffffffffu, old, r), s = __shfl_sync(0xffffffffu, src, r);
-      const int k = __shfl_sync(0xffffffffu, keep, r);
-      was[r] = b < n && col < pages(o) ? a.table[(int64_t)b * a.ld_table + col] : -1;
-      is[r] = s >= 0 && col < pages(k) ? a.table[(int64_t)s * a.ld_table + col] : -1;
-      part[r] = (col + 1) * (int64_t)P > k;  // the row goes on writing to it
-      bad |= (b < n && col < pages(o) && (uint32_t)was[r] >= (uint32_t)a.n_pages) ||
-             (s >= 0 && col < pages(k) && (uint32_t)is[r] >= (uint32_t)a.n_pages);
-    }
-    RefRun before = {0, 0}, after = {0, 0};
-#pragma unroll
-    for (int r = 0; r < kShRows; ++r) {
-      if ((uint32_t)was[r] < (uint32_t)a.n_pages) before.add(a.notes, was[r], 0x10000u);
-      if ((uint32_t)is[r] < (uint32_t)a.n_pages) {
-        a.table_out[(int64_t)(b0 + r) * a.ld_table + col] = is[r];
-        if (part[r]) atomicMax(&a.notes[is[r]].first, (uint32_t)(n - b0 - r));
-        else after.add(a.notes, is[r], 1u);
+    if (mine) {
+      old = a.old_lens[row];
+      src = a.src[row];
+      if (a.keep_lens) keep = a.keep_lens[row];
+      if (old < 0 || old > a.cap || src < -1 || src >= n || (a.keep_lens && src >= 0 && (keep < 0 || keep > a.cap))) {
+        bad = true;
+        old = keep = 0;
+        src = -1;
       }
     }
-    before.flush(a.notes);
-    after.flush(a.notes);
+    // (with keep_lens the source's length is only looked at behind the tables)
+    int have = src >= 0 ? a.old_lens[src] : 0;
+    if (src < 0) keep = 0;
+    if (!a.keep_lens) {
+      keep = have;
+      if (keep < 0 || keep > a.cap) {
+        bad = true;
+        keep = 0;
+      }
+    }
+    int was[kShRows], is[kShRows], open = 0;
+#pragma unroll
+    for (int r = 0; r < kShRows; ++r) {
+      const int o = pages(__shfl_sync(kAll, old, r)), s = __shfl_sync(kAll, src, r), k = __shfl_sync(kAll, keep, r);
+      was[r] = col < o ? a.table[(int64_t)(b0 + r) * a.ld_table + col] : -1;
+      is[r] = col < pages(k) ? a.table[(int64_t)s * a.ld_table + col] : -1;
+      if (col < o && (uint32_t)was[r] >= (uint32_t)a.n_pages) {
+        bad = true;
+        was[r] = -1;
+      }
+      if (col < pages(k) && (uint32_t)is[r] >= (uint32_t)a.n_pages) {
+        bad = true;
+        is[r] = -1;
+      }
+      open |= (is[r] >= 0 && (int64_t)(col + 1) * P > k) << r;  // the row goes on writing to it
+    }
+    if (mine) {
+      bad = bad || keep > have || have > a.cap;
+      if (col0 == 0) {
+        a.new_lens[row] = keep;
+        if ((int)fast_div((uint32_t)keep, a.div_page) * P == keep) a.head->open[row] = -1;
+      }
+    }
+    bool alike = true;  // all rows before and after hold one page, or none
+#pragma unroll
+    for (int r = 0; r < kShRows; ++r) {
+      if (is[r] >= 0) a.table_out[(int64_t)(b0 + r) * a.ld_table + col] = is[r];
+      if (open >> r & 1) {
+        a.head->open[b0 + r] = is[r];
+        atomicMax(&a.notes[is[r]].first, (uint32_t)(n - b0 - r));
+        is[r] = -1;  // (counted as full pages below)
+      }
+      alike = alike && was[r] == was[0] && is[r] == was[0];
+    }
+    if (__all_sync(kAll, alike)) {
+      if (was[0] >= 0) atomicAdd(&a.notes[was[0]].refs, (uint32_t)kShRows << 16 | kShRows);
+    } else {  // each page of the tile once
+      uint32_t done = 0;  // of `is`: counted with a page of `was`
+#pragma unroll
+      for (int r = 0; r < kShRows; ++r) {
+        uint32_t refs = 0;
+        bool again = was[r] < 0;
+#pragma unroll
+        for (int q = 0; q < kShRows; ++q) {
+          if (q < r) again = again || was[q] == was[r];
+          else if (was[q] == was[r]) refs += 0x10000u;
+          if (is[q] == was[r]) {
+            refs += 1;
+            done |= 1u << q;
+          }
+        }
+        if (!again) atomicAdd(&a.notes[was[r]].refs, refs);
+      }
+      RefRun after = {0, 0};
+#pragma unroll
+      for (int r = 0; r < kShRows; ++r)
+        if (is[r] >= 0 && !(done >> r & 1)) after.add(a.notes, is[r], 1u);
+      after.flush(a.notes);
+    }
   }
+  bad = bad || first < 0 || first >= a.n_pages || count < 0 || count > a.n_pages;
   if (__syncthreads_or(bad) && tid == 0) atomicOr(&a.head->bad, 1u);
   if (!grid_wait(a.head, 0, a.status)) return;
 
   // Pass 2: pages that no row holds any more, rows that take a page.
-  bad = *(volatile unsigned*)&a.head->bad;
   int p0, p1, b0, b1;
   share_of(a.n_pages, &p0, &p1);
   share_of(n, &b0, &b1);
-  auto gone = [&](uint2 note) { return note.x >> 16 && !(note.x & 0xFFFF) && !note.y; };
-  auto note_of = [&](int p) { return __ldcg(reinterpret_cast<const uint2*>(a.notes + p)); };
-  // the page that row b goes on writing to, or -1
-  auto open_page = [&](int b, int* keep, int* src) {
-    int old;
-    fork_row(a, b, &old, src, keep);
-    const int full = (int)fast_div((uint32_t)*keep, a.div_page);
-    if (*src < 0 || full * P == *keep) return -1;
-    return a.table[(int64_t)*src * a.ld_table + full];
+  bad = __ldcg(&a.head->bad);
+  // The thread's pages and row of the share's turn `at`; those of the first turn, mostly the only
+  // one, stay in registers for pass 3.
+  uint2 note[kShPages];
+  int from, keep;  // the page that the row goes on writing to, or -1; its tokens
+  const int turns = max((p1 - p0 + kShPages * kShThreads - 1) / (kShPages * kShThreads), (b1 - b0 + kShThreads - 1) / kShThreads);
+  auto fetch = [&](int turn) {
+    const int row = b0 + turn * kShThreads + tid, page = p0 + (turn * kShThreads + tid) * kShPages;
+    from = row < b1 && !bad ? __ldcg(&a.head->open[row]) : -1;
+    keep = row < b1 ? __ldcg(&a.new_lens[row]) : 0;
+#pragma unroll
+    for (int i = 0; i < kShPages; ++i) note[i] = page + i < p1 ? note_of(a.notes, page + i) : make_uint2(0, 0);
   };
   int freed = 0, taken = 0;
-  if (!bad) {
-    for (int p = p0 + tid; p < p1; p += kShThreads) freed += gone(note_of(p));
-    for (int base = b0; base < b1; base += kShThreads) {
-      const int b = base + tid;
-      bool copy = false;
-      if (b < b1) {
-        int keep, src;
-        const int p = open_page(b, &keep, &src);
-        if (p >= 0) {
-          const uint2 note = note_of(p);
-          copy = (note.x & 0xFFFF) || note.y != (uint32_t)(n - b);
-        }
-      }
-      const unsigned m = __ballot_sync(0xffffffffu, copy);
-      if (lane == 0) copied[(base - b0) / 32 + warp] = m;
-      taken += copy;
+  for (int turn = turns - 1; turn >= 0; --turn) {
+    fetch(turn);
+    bool copy = false;
+    if (from >= 0) {
+      const uint2 x = note_of(a.notes, from);
+      copy = (x.x & 0xFFFF) || x.y != (uint32_t)(n - (b0 + turn * kShThreads + tid));
     }
+    const unsigned m = __ballot_sync(kAll, copy);
+    if (lane == 0 && b0 + turn * kShThreads < b1) copied[turn * kShWarps + warp] = m;
+    taken += copy;
+#pragma unroll
+    for (int i = 0; i < kShPages; ++i) freed += is_gone(note[i]);
   }
-  freed = block_sum(freed);
-  taken = block_sum(taken);
-  if (tid == 0) {
-    a.head->counts[0][blockIdx.x] = freed;
-    a.head->counts[1][blockIdx.x] = taken;
-  }
+  unsigned long long all;
+  block_scan(two(freed, taken), &all);
+  if (tid == 0) a.head->counts[blockIdx.x] = make_int2((int)all, (int)(all >> 32));
   if (!grid_wait(a.head, 1, a.status)) return;
 
   // Pass 3: the ring, the rows' own pages, the moves.
-  int f_before = 0, f_all = 0, t_before = 0, t_all = 0;
-  for (int c = tid; c < (int)gridDim.x; c += kShThreads) {
-    const int f = __ldcg(&a.head->counts[0][c]), t = __ldcg(&a.head->counts[1][c]);
-    f_all += f;
-    t_all += t;
-    if (c < (int)blockIdx.x) {
-      f_before += f;
-      t_before += t;
-    }
-  }
-  f_all = block_sum(f_all);
-  t_all = block_sum(t_all);
-  f_before = block_sum(f_before);
-  t_before = block_sum(t_before);
+  renew_first(a.head);
+  unsigned long long before = before_this(a.head, &all);
+  const int f_all = (int)all, t_all = (int)(all >> 32);
   bad = bad || t_all > count || count + f_all > a.n_pages;
   auto ring_at = [&](int i) {
     i += first;
     return i >= a.n_pages ? i - a.n_pages : i;
   };
-  for (int base = p0; base < p1; base += kShThreads) {
-    const int p = base + tid;
-    uint2 note = make_uint2(0, 0);
-    if (p < p1) {
-      note = note_of(p);
-      if (note.x || note.y) *reinterpret_cast<uint2*>(a.notes + p) = make_uint2(0, 0);
+  for (int turn = 0; turn < turns; ++turn) {
+    if (turn) fetch(turn);
+    const int row = b0 + turn * kShThreads + tid, page = p0 + (turn * kShThreads + tid) * kShPages;
+    const bool copy = !bad && row < b1 && (copied[turn * kShWarps + warp] >> lane & 1);
+    int gone = 0;
+#pragma unroll
+    for (int i = 0; i < kShPages; ++i) gone += is_gone(note[i]);
+    unsigned long long here;
+    const unsigned long long mine = before + block_scan(two(gone, copy), &here);
+    before += here;
+    int to_ring = (int)mine;
+    const int move = (int)(mine >> 32), to = copy ? a.free_ring[ring_at(move)] : 0;
+#pragma unroll
+    for (int i = 0; i < kShPages; ++i) {
+      const uint2 x = note[i];
+      if (!x.x && !x.y) continue;  // (also what lies behind the share)
+      *reinterpret_cast<uint2*>(a.notes + page + i) = make_uint2(0, 0);
+      if (bad) continue;
+      if (is_gone(x)) a.free_ring[ring_at(count + to_ring++)] = page + i;
+      if (a.holders) {
+        const int full = x.x & 0xFFFF;
+        a.holders[page + i] = full ? full : x.y != 0;
+      }
     }
-    if (bad) continue;
-    int many;
-    const int at = f_before + block_rank(gone(note), &many);
-    f_before += many;
-    if (gone(note)) a.free_ring[ring_at(count + at)] = p;
-    if (a.holders && (note.x || note.y)) {
-      const int full = note.x & 0xFFFF;
-      a.holders[p] = full ? full : note.y != 0;
-    }
-  }
-  for (int base = b0; base < b1; base += kShThreads) {
-    const int b = base + tid;
-    const bool copy = !bad && b < b1 && (copied[(base - b0) / 32 + warp] >> lane & 1);
-    int many;
-    const int at = t_before + block_rank(copy, &many);
-    t_before += many;
-    if (b >= b1) continue;
-    if (bad) {
-      a.new_lens[b] = a.old_lens[b];
-      continue;
-    }
-    int keep, src;
-    const int p = open_page(b, &keep, &src);
-    a.new_lens[b] = keep;
     if (copy) {
-      const int full = (int)fast_div((uint32_t)keep, a.div_page), to = a.free_ring[ring_at(at)];
+      const int full = (int)fast_div((uint32_t)keep, a.div_page);
       const bool out = (uint32_t)to >= (uint32_t)a.n_pages;
       if (out) record_status(a.status, kStatusTableRange);
-      a.table_out[(int64_t)b * a.ld_table + full] = to;
+      a.table_out[(int64_t)row * a.ld_table + full] = to;
       if (a.holders && !out) a.holders[to] = 1;
-      a.moves[3 * at] = p;
-      a.moves[3 * at + 1] = to;
-      a.moves[3 * at + 2] = keep - full * P;
+      a.moves[3 * move] = from;
+      a.moves[3 * move + 1] = to;
+      a.moves[3 * move + 2] = keep - full * P;
     }
+    if (bad && row < b1) a.new_lens[row] = a.old_lens[row];
   }
   if (bad) {  // the old rows again
     const int64_t words = (int64_t)n * a.ld_table;
@@ -293,103 +328,124 @@ __global__ void __launch_bounds__(kShThreads) fork_pages_kernel(const ForkArgs a
     a.free_next[1] = bad ? count : count - t_all + f_all;
     *a.n_moves = bad ? 0 : t_all;
   }
-  leave(a.head);
 }
 
 __global__ void __launch_bounds__(kShThreads) compact_pages_kernel(const CompactArgs a) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n = a.n_seqs, P = a.page_size;
+  pdl_launch_dependents();
+  pdl_wait();
   auto pages = [&](int len) { return (int)fast_div((uint32_t)len + P - 1, a.div_page); };
   const int first = a.free_state[0], count = a.free_state[1];
+  renew_later(a.head);
   bool bad = false;
 
-  // Pass 1: references.
+  // A tile's pages, -1 where a row holds none.  The warp's first tile stays in registers.
   const int row_tiles = (n + kShRows - 1) / kShRows;
   const int col_tiles = max(1, (min(a.ld_table, pages(a.cap)) + 31) / 32);
-  auto for_tiles = [&](auto&& f) {
-    for (int64_t t = (int64_t)blockIdx.x * kShWarps + warp; t < (int64_t)row_tiles * col_tiles;
-         t += (int64_t)gridDim.x * kShWarps) {
-      const int b0 = (int)(t / col_tiles) * kShRows, col = (int)(t % col_tiles) * 32 + lane;
-      int len = 0;
-      if (lane < kShRows && b0 + lane < n) {
-        len = a.lens[b0 + lane];
-        if (len < 0 || len > a.cap) {
-          bad = true;
-          len = 0;
-        }
+  const int tiles = row_tiles * col_tiles, tile0 = warp * gridDim.x + blockIdx.x;
+  auto fetch = [&](int t, int (&page)[kShRows]) {
+    const int b0 = t / col_tiles * kShRows, col = t % col_tiles * 32 + lane;
+    int len = 0;
+    if (lane < kShRows && b0 + lane < n) {
+      len = a.lens[b0 + lane];
+      if (len < 0 || len > a.cap) {
+        bad = true;
+        len = 0;
       }
-      int page[kShRows];
+    }
 #pragma unroll
-      for (int r = 0; r < kShRows; ++r) {
-        const bool held = col < pages(__shfl_sync(0xffffffffu, len, r));
-        page[r] = held ? a.table[(int64_t)(b0 + r) * a.ld_table + col] : -1;
-        if (held && (uint32_t)page[r] >= (uint32_t)a.n_pages) {
-          bad = true;
-          page[r] = -1;
-        }
+    for (int r = 0; r < kShRows; ++r) {
+      const bool held = col < pages(__shfl_sync(kAll, len, r));
+      page[r] = held ? a.table[(int64_t)(b0 + r) * a.ld_table + col] : -1;
+      if (held && (uint32_t)page[r] >= (uint32_t)a.n_pages) {
+        bad = true;
+        page[r] = -1;
       }
-      f(b0, col, page);
     }
   };
-  for_tiles([&](int, int, const int(&page)[kShRows]) {
+  // Pass 1: references.
+  int kept[kShRows];
+#pragma unroll
+  for (int r = 0; r < kShRows; ++r) kept[r] = -1;
+  auto refer = [&](const int (&page)[kShRows]) {
     RefRun run = {0, 0};
 #pragma unroll
     for (int r = 0; r < kShRows; ++r)
       if (page[r] >= 0) run.add(a.notes, page[r], 1u);
     run.flush(a.notes);
-  });
+  };
+  if (tile0 < tiles) {
+    fetch(tile0, kept);
+    refer(kept);
+  }
+  for (int t = tile0 + gridDim.x * kShWarps; t < tiles; t += gridDim.x * kShWarps) {
+    int page[kShRows];
+    fetch(t, page);
+    refer(page);
+  }
   if (__syncthreads_or(bad) && tid == 0) atomicOr(&a.head->bad, 1u);
   if (!grid_wait(a.head, 0, a.status)) return;
 
   // Pass 2: pages held, by share.
-  bad = *(volatile unsigned*)&a.head->bad;
+  bad = __ldcg(&a.head->bad);
   int p0, p1;
   share_of(a.n_pages, &p0, &p1);
+  uint32_t refs[kShPages];  // the thread's pages of a turn; the first turn's stay for pass 3
+  const int turns = (p1 - p0 + kShPages * kShThreads - 1) / (kShPages * kShThreads);
+  auto look = [&](int turn) {
+    const int page = p0 + (turn * kShThreads + tid) * kShPages;
+#pragma unroll
+    for (int i = 0; i < kShPages; ++i) refs[i] = page + i < p1 ? __ldcg(&a.notes[page + i].refs) : 0;
+  };
+  auto count_held = [&] {
+    int many = 0;
+#pragma unroll
+    for (int i = 0; i < kShPages; ++i) many += refs[i] != 0;
+    return many;
+  };
   int held = 0;
-  for (int p = p0 + tid; p < p1; p += kShThreads) held += __ldcg(&a.notes[p].refs) != 0;
-  held = block_sum(held);
-  if (tid == 0) a.head->counts[0][blockIdx.x] = held;
+  for (int turn = turns - 1; turn >= 0; --turn) {
+    look(turn);
+    held += count_held();
+  }
+  unsigned long long all;
+  block_scan(two(held, 0), &all);
+  if (tid == 0) a.head->counts[blockIdx.x] = make_int2((int)all, 0);
   if (!grid_wait(a.head, 1, a.status)) return;
 
   // Pass 3: with h held pages below p, the free page p < U is the (p - h)-th hole, the
   // held page p >= U the (U - 1 - h)-th to move, from the highest on.
-  int before = 0, used = 0;
-  for (int c = tid; c < (int)gridDim.x; c += kShThreads) {
-    const int h = __ldcg(&a.head->counts[0][c]);
-    used += h;
-    if (c < (int)blockIdx.x) before += h;
-  }
-  used = block_sum(used);
-  before = block_sum(before);
-  for (int base = p0; base < p1; base += kShThreads) {
-    const int p = base + tid;
-    uint32_t refs = 0;
-    if (p < p1) {
-      refs = __ldcg(&a.notes[p].refs);
-      if (refs) a.notes[p].refs = 0;
-    }
-    int many;
-    const int h = before + block_rank(refs != 0, &many);
-    before += many;
-    if (p >= p1) continue;
-    if (bad) {
-      if (a.ring_out != a.ring) a.ring_out[p] = a.ring[p];
-      continue;
-    }
-    a.ring_out[p] = p;
-    if (p == used - 1) *a.n_moves = p - h + (refs == 0);  // the holes
-    if (p < used && !refs) {
-      a.moves[3 * (p - h) + 1] = p;
-      a.moves[3 * (p - h) + 2] = P;
-    } else if (p >= used && refs) {
-      const int move = used - 1 - h;
-      a.moves[3 * move] = p;
-      *reinterpret_cast<int2*>(&a.notes[p].move) = make_int2(move, (int)refs);
-      if (a.holders) a.holders[p] = 0;
-    } else if (p < used && a.holders) {
-      a.holders[p] = (int)refs;
-    } else if (a.holders) {
-      a.holders[p] = 0;
+  renew_first(a.head);
+  unsigned long long before = before_this(a.head, &all);
+  const int used = (int)all;
+  for (int turn = 0; turn < turns; ++turn) {
+    if (turn) look(turn);
+    const int page = p0 + (turn * kShThreads + tid) * kShPages;
+    unsigned long long here;
+    int h = (int)(before + block_scan(two(count_held(), 0), &here));
+    before += here;
+#pragma unroll
+    for (int i = 0; i < kShPages; ++i) {
+      const int p = page + i;
+      if (p >= p1) break;
+      if (refs[i]) a.notes[p].refs = 0;
+      if (bad) {
+        if (a.ring_out != a.ring) a.ring_out[p] = a.ring[p];
+        continue;
+      }
+      a.ring_out[p] = p;
+      if (p == used - 1) *a.n_moves = p - h + (refs[i] == 0);  // the holes
+      if (a.holders) a.holders[p] = p < used ? (int)refs[i] : 0;  // (holes: when their pages come)
+      if (p < used && !refs[i]) {
+        a.moves[3 * (p - h) + 1] = p;
+        a.moves[3 * (p - h) + 2] = P;
+      } else if (p >= used && refs[i]) {
+        const int move = used - 1 - h;
+        a.moves[3 * move] = p;
+        *reinterpret_cast<int2*>(&a.notes[p].move) = make_int2(move, (int)refs[i]);
+      }
+      h += refs[i] != 0;
     }
   }
   if (!grid_wait(a.head, 2, a.status)) return;
@@ -402,46 +458,52 @@ __global__ void __launch_bounds__(kShThreads) compact_pages_kernel(const Compact
         a.table_out[i] = a.table[i];
     }
   } else {
-    for_tiles([&](int b0, int col, const int(&page)[kShRows]) {
+    auto rename = [&](int t, int (&page)[kShRows]) {
+      const int b0 = t / col_tiles * kShRows, col = t % col_tiles * 32 + lane;
+      int2 note[kShRows];
 #pragma unroll
-      for (int r = 0; r < kShRows; ++r) {
-        if (page[r] < 0) continue;
-        int to = page[r];
-        if (to >= used) {
-          const int2 note = __ldcg(reinterpret_cast<const int2*>(&a.notes[to].move));
-          to = __ldcg(&a.moves[3 * note.x + 1]);
-          if (a.holders) a.holders[to] = note.y;  // (every row that holds it writes the same)
+      for (int r = 0; r < kShRows; ++r)
+        if (page[r] >= used) note[r] = __ldcg(reinterpret_cast<const int2*>(&a.notes[page[r]].move));
+#pragma unroll
+      for (int r = 0; r < kShRows; ++r)
+        if (page[r] >= used) {
+          page[r] = __ldcg(&a.moves[3 * note[r].x + 1]);
+          if (a.holders) a.holders[page[r]] = note[r].y;  // (every row that holds it writes the same)
         }
-        a.table_out[(int64_t)(b0 + r) * a.ld_table + col] = to;
-      }
-    });
-  }
-  if (blockIdx.x == 0) {
-    if (tid == 0) {
-      if (bad) record_status(a.status, kStatusTableRange);
-      if (bad || used == 0) *a.n_moves = 0;
-      a.free_next[0] = bad ? first : used == a.n_pages ? 0 : used;
-      a.free_next[1] = bad ? count : a.n_pages - used;
+#pragma unroll
+      for (int r = 0; r < kShRows; ++r)
+        if (page[r] >= 0) a.table_out[(int64_t)(b0 + r) * a.ld_table + col] = page[r];
+    };
+    if (tile0 < tiles) rename(tile0, kept);
+    for (int t = tile0 + gridDim.x * kShWarps; t < tiles; t += gridDim.x * kShWarps) {
+      int page[kShRows];
+      fetch(t, page);
+      rename(t, page);
     }
   }
-  leave(a.head);
+  if (blockIdx.x == 0 && tid == 0) {
+    if (bad) record_status(a.status, kStatusTableRange);
+    if (bad || used == 0) *a.n_moves = 0;
+    a.free_next[0] = bad ? first : used == a.n_pages ? 0 : used;
+    a.free_next[1] = bad ? count : a.n_pages - used;
+  }
 }
 
 template <typename Args>
 static cudaError_t launch_shared(void (*kernel)(Args), const Args& a, int64_t entries, int num_sms,
                                  cudaStream_t st) {
-  const int64_t tiles = (entries + kShThreads * kShRows - 1) / (kShThreads * kShRows);
-  const int64_t by_pages = (a.n_pages + 4095) / 4096;
-  const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(std::max(tiles, by_pages), std::min(num_sms, kShareCtas)));
+  const int64_t tiles = (entries + 2047) / 2048, by_pages = (a.n_pages + 2047) / 2048;
+  const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(std::max(tiles, by_pages), std::min({num_sms, kShareCtas, kShThreads})));
+  if (grid == 1) return launch_k(kernel, dim3(1), dim3(kShThreads), 0, st, a);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kShThreads);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].id = cudaLaunchAttributeCooperative;  // all CTAs at once
   attr[0].val.cooperative = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = grid > 1 ? 1 : 0;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
