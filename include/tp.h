@@ -818,6 +818,7 @@ tp_status tp_compact_pages(const tp_model* m, const tp_pages_t* pages, const tp_
  *   moves   : [max_moves][3]; n_moves [1] on the device says how many there are
  *   k, v    : HOST arrays [n_layers] of the layers' caches (read during the call only),
  *             16-byte aligned, no two of them overlapping; pages gives n_pages and page_size
+ * n_kv_heads * page_size <= 2^23 (TP_ERR_UNSUPPORTED otherwise).
  * No page may be both read and written by the moves, nor written twice.  Errors on the
  * device (TP_ERR_TABLE_RANGE): a move with a page outside [0, n_pages) or tokens outside
  * [0, page_size] is left out, n_moves is cut to [0, max_moves]. */

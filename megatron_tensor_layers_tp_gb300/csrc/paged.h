@@ -211,10 +211,12 @@ struct CopyPagesArgs {
   int row;                    // 16-byte words of a token's head
   int copies, kv_r, layers;
   FastDiv div_heads, div_kv;  // by copies * kv_r, by kv_r
+  int run_pieces, move_pieces;  // of a head's page, of a move
+  FastDiv div_run, div_move;
   const int32_t *moves, *n_moves;
   int* status;
   uint4* pools[2 * kCopyLayers];
 };
-cudaError_t launch_copy_pages(const CopyPagesArgs& a, int num_sms, cudaStream_t st);
+cudaError_t launch_copy_pages(CopyPagesArgs a, int num_sms, cudaStream_t st);
 
 }  // namespace tpk

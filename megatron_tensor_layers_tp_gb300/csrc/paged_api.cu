@@ -591,6 +591,8 @@ tp_status tp_copy_pages(const tp_model* m, const tp_pages_t* pages, const int32_
     if (!moves || !n_moves || !k || !v) return TP_ERR_ARG;
     for (int i = 0; i < n_layers; ++i)
       if (!k[i] || !v[i] || !aligned16(k[i]) || !aligned16(v[i])) return TP_ERR_ARG;
+    // (a launch's pieces of a move are counted in 32 bits)
+    if ((int64_t)m->cfg.n_kv_heads * pages->page_size > (1 << 23)) return TP_ERR_UNSUPPORTED;
     CopyPagesArgs a;
     memset(&a, 0, sizeof(a));
     a.n_pages = pages->n_pages;

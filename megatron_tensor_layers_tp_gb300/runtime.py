@@ -807,11 +807,12 @@ class TPModel:
         _check(parents, "parents", i32, (n,), dev)
         _check(tokens, "tokens", i32, (n,), dev)
         _check(lens, "lens", i32, (n,), dev)
-        _check(history, "history", i32, (n, None), dev, rows=True)
+        # (any row length, but named: the whole check of a contiguous tensor is its first line)
+        _check(history, "history", i32, (n, history.shape[-1]), dev, rows=True)
         if out is None:
             out = self._out(history.shape, i32, stream)
         else:
-            _check(out, "out", i32, (n, None), dev, rows=True)
+            _check(out, "out", i32, (n, out.shape[-1]), dev, rows=True)
         if lens_out is None:
             lens_out = self._out((n,), i32, stream)
         else:
