@@ -192,7 +192,7 @@ __device__ __noinline__ int rank_keys(SelectSmem& sm, int best, int n, int K) {
 constexpr float kNear = 0x1p-21f;
 __device__ void join_request(const BeamSelectArgs& a, JoinSmem& sm, int req) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int W = a.width, K = a.n_cands, per_row = a.parts * K, N = W * per_row;
+  const int W = a.width, K = a.n_cands, per_row = a.parts * a.list, N = W * per_row;
   const int row0 = req * W;
   const unsigned long long* keys = a.lists + (int64_t)row0 * per_row;
   // (the first keys of the thread are on their way while the rows' sums are joined)
@@ -256,7 +256,7 @@ __device__ void join_request(const BeamSelectArgs& a, JoinSmem& sm, int req) {
   auto value = [&](int e, float side) { return sm.below[e] + sm.near[e] + side * (fabsf(sm.below[e]) + fabsf(sm.near[e])); };
   uint32_t bound = ordered(-INFINITY) + 1;
   if (N > kSelSmall) {
-    // a warp takes every eighth key, each lane's at another depth of its list
+    // a warp takes every eighth key, each lane's at another place of its list
     float most = -INFINITY;
     for (int e0 = lane * kSelWarps; e0 < N; e0 += kSelThreads) {
       const int e = e0 + ((lane + warp) & (kSelWarps - 1));
@@ -498,9 +498,11 @@ __global__ void __launch_bounds__(kSelThreads, 2) beam_select_kernel(const BeamS
     const uint32_t warp_top = __reduce_max_sync(0xffffffffu, o);
     int r = __reduce_max_sync(0xffffffffu, (int)power);
     auto fixed_sum = [&](float x) {  // of the warp, in multiples of 2^(r - 32)
-      unsigned long long f = __float2ull_rn(x * 4294967296.f);
-      for (int q = 16; q; q >>= 1) f += __shfl_xor_sync(0xffffffffu, f, q);
-      return f;
+      const unsigned long long f = __float2ull_rn(x * 4294967296.f);  // < 2^62
+      const uint32_t lo = __reduce_add_sync(0xffffffffu, (uint32_t)f & 0x3FFFFFFu);
+      const uint32_t mid = __reduce_add_sync(0xffffffffu, (uint32_t)(f >> 26) & 0x3FFFFFFu);
+      const uint32_t hi = __reduce_add_sync(0xffffffffu, (uint32_t)(f >> 52));
+      return ((unsigned long long)hi << 52) + ((unsigned long long)mid << 26) + lo;
     };
     unsigned long long fixed = fixed_sum(sum * ex2_approx(power - (float)r));
     // groups of threads, twice as many as the bound's place
@@ -560,43 +562,42 @@ __global__ void __launch_bounds__(kSelThreads, 2) beam_select_kernel(const BeamS
       for (; reach; reach &= reach - 1) hit[to++] = (uint16_t)((__ffs(reach) - 1) * kSelThreads + tid);
     }
     __syncthreads();
-    // Logit `lane` of the thread's in chunk d of a cell: its token, or -1.
-    auto token_of = [&](int h, int d) {
-      const int c = h / kSelThreads * per_cell + d, thread = h % kSelThreads;
-      const int e = (lane / kE * kSelThreads + thread) * kE + lane % kE;
-      const int64_t t = begin + (int64_t)c * kChunk + e;
-      return d < per_cell && lane < kPer && t < end ? (int)t : -1;
+    // Logit i of those that an item, one chunk of a cell, stands for: its token, or -1.
+    const int hits = sm.hits, items = hits * per_cell;
+    auto token_of = [&](int item, int i) {
+      const int h = per_cell == 1 ? item : item / per_cell, d = item - h * per_cell;
+      const int cell = hit[h], thread = cell % kSelThreads;
+      const int e = (i / kE * kSelThreads + thread) * kE + i % kE;
+      const int64_t t = begin + ((int64_t)cell / kSelThreads * per_cell + d) * kChunk + e;
+      return t < end ? (int)t : -1;
     };
-    const int hits = sm.hits;
-    constexpr int kAtOnce = 8;
-    for (int h0 = warp; h0 < hits; h0 += kAtOnce * kSelWarps) {
-      for (int d = 0; d < per_cell; ++d) {
-        float x[kAtOnce];
-        int t[kAtOnce];
+    constexpr int kAtOnce = 8, kTogether = 32 / kPer;  // items that a warp reads at once, by one load
+    for (int x0 = warp * kTogether; x0 < items; x0 += kAtOnce * kSelWarps * kTogether) {
+      float x[kAtOnce];
+      int t[kAtOnce];
 #pragma unroll
-        for (int i = 0; i < kAtOnce; ++i) {
-          const int h = h0 + i * kSelWarps;
-          t[i] = h < hits ? token_of(hit[h], d) : -1;
-          x[i] = t[i] >= 0 ? raw(t[i]) : -INFINITY;
-        }
-        uint32_t passes = 0;
-        int many = 0;
+      for (int i = 0; i < kAtOnce; ++i) {
+        const int item = x0 + i * kSelWarps * kTogether + lane / kPer;
+        t[i] = item < items ? token_of(item, lane % kPer) : -1;
+        x[i] = t[i] >= 0 ? raw(t[i]) : -INFINITY;
+      }
+      uint32_t passes = 0;
+      int many = 0;
 #pragma unroll
-        for (int i = 0; i < kAtOnce; ++i) {
-          const bool p = x[i] == x[i] && ordered(x[i]) >= v;
-          passes |= (uint32_t)p << i;
-          many += __popc(__ballot_sync(0xffffffffu, p));
-        }
-        int to = 0;
-        if (lane == 0) to = atomicAdd(&sm.many, many);
-        to = __shfl_sync(0xffffffffu, to, 0);
+      for (int i = 0; i < kAtOnce; ++i) {
+        const bool p = x[i] == x[i] && ordered(x[i]) >= v;
+        passes |= (uint32_t)p << i;
+        many += __popc(__ballot_sync(0xffffffffu, p));
+      }
+      int to = 0;
+      if (lane == 0) to = atomicAdd(&sm.many, many);
+      to = __shfl_sync(0xffffffffu, to, 0);
 #pragma unroll
-        for (int i = 0; i < kAtOnce; ++i) {
-          const unsigned m = __ballot_sync(0xffffffffu, passes >> i & 1);
-          const int at = to + __popc(m & ((1u << lane) - 1));
-          if ((passes >> i & 1) && at < kSelBuffer) sm.keys[at] = key_of(x[i], t[i]);
-          to += __popc(m);
-        }
+      for (int i = 0; i < kAtOnce; ++i) {
+        const unsigned m = __ballot_sync(0xffffffffu, passes >> i & 1);
+        const int at = to + __popc(m & ((1u << lane) - 1));
+        if ((passes >> i & 1) && at < kSelBuffer) sm.keys[at] = key_of(x[i], t[i]);
+        to += __popc(m);
       }
     }
     __syncthreads();
@@ -613,7 +614,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) beam_select_kernel(const BeamS
           const int first = begin + (h / kSelThreads * per_cell + d) * kChunk + h % kSelThreads * kE;
           const bool may = h >= 0 && key_of(most, first) > least;
           if (!__syncthreads_or(may)) continue;
-          const int t = may ? token_of(h, d) : -1;
+          const int t = may && lane < kPer ? token_of((h0 + warp) * per_cell + d, lane) : -1;
           const float x = t >= 0 ? raw(t) : -INFINITY;
           const unsigned long long key = key_of(x, t);
           if (x == x && ordered(x) >= v && key > least) sm.keys[best + atomicAdd(&sm.many, 1)] = key;
@@ -627,7 +628,8 @@ __global__ void __launch_bounds__(kSelThreads, 2) beam_select_kernel(const BeamS
 
     // the part's list and sum
     const int n = sm.many;
-    if (n) best = rank_keys(sm, best, n, K);
+    if (n > a.list) best = rank_keys(sm, 0, n, K);
+    else best += n;  // (in any order)
 #pragma unroll
     for (int q = 0; q < kSelWarps; ++q) r = max(r, sm.warp_power[q]);
     if (bad || (is_far(most) && most > -INFINITY)) {  // once more, NaN left out
@@ -651,7 +653,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) beam_select_kernel(const BeamS
       for (int q = 0; q < kSelWarps; ++q) fixed += sm.warp_sum[q] >> min(r - sm.warp_power[q], 63);
       a.sums[item] = {fixed, most, r};
     }
-    if (tid < K) a.lists[(int64_t)item * K + tid] = tid < best && ok ? sm.keys[tid] : 0;
+    if (tid < a.list) a.lists[(int64_t)item * a.list + tid] = tid < best && ok ? sm.keys[tid] : 0;
   }
   // The last of the request's CTAs joins them.
   __syncthreads();
@@ -670,6 +672,8 @@ static int parts_most(int64_t rows, int width, int cands, int num_sms) {
   return (int)std::max<int64_t>(1, std::min<int64_t>(2 * num_sms / rows, kSelKeys / (width * cands)));
 }
 int64_t beam_parts_all(int64_t rows, int num_sms) { return rows + 2 * num_sms; }
+// What passes the bound is mostly less than twice K: it is not ranked then.
+int beam_list_most(int cands) { return std::min(std::max(2 * cands, 32), kMaxBeamCands); }
 
 template <bool kFp32>
 static cudaError_t launch_select(const BeamSelectArgs& a, int64_t ctas, cudaStream_t st) {
@@ -686,9 +690,10 @@ cudaError_t launch_beam_select(BeamSelectArgs a, int num_sms, cudaStream_t st) {
   a.parts = std::min(chunks, parts_most(rows, a.width, a.n_cands, num_sms));
   a.part_chunks = (chunks + a.parts - 1) / a.parts;
   a.parts = (chunks + a.part_chunks - 1) / a.part_chunks;
+  a.list = std::min(beam_list_most(a.n_cands), kSelKeys / (a.width * a.parts));
   a.div_parts = make_fastdiv((uint32_t)a.parts);
   a.div_width = make_fastdiv((uint32_t)a.width);
-  a.div_row_keys = make_fastdiv((uint32_t)(a.parts * a.n_cands));
+  a.div_row_keys = make_fastdiv((uint32_t)(a.parts * a.list));
   return a.fp32 ? launch_select<true>(a, rows * a.parts, st) : launch_select<false>(a, rows * a.parts, st);
 }
 

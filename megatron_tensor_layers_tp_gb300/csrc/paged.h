@@ -119,8 +119,8 @@ constexpr int kMaxBeams = 32;      // of a request
 constexpr int kMaxBeamCands = 64;  // of a request
 constexpr int kMaxEnds = 8;
 
-// The K best logits of a part of a row, in order: (ordered value << 32) | ~token, 0 where
-// there are fewer; its largest logit; and its sum of exponentials, of 2^power, times 2^32
+// The K best logits of a part of a row, and some others: (ordered value << 32) | ~token, 0
+// behind the last; its largest logit; and its sum of exponentials, of 2^power, times 2^32
 // (from the largest logit on where that is far from 0: beam.cu).
 struct BeamPart {
   unsigned long long sum;
@@ -138,15 +138,17 @@ struct BeamSelectArgs {
   int32_t *cand_rows, *cand_tokens;
   float* next_scores;
   int32_t *parents, *tokens;
-  int parts, part_chunks;     // parts of a row, chunks of a part
-  FastDiv div_parts, div_width, div_row_keys;  // by parts, width, parts * n_cands
+  int parts, part_chunks, list;  // parts of a row, chunks and keys of a part
+  FastDiv div_parts, div_width, div_row_keys;  // by parts, width, parts * list
   BeamPart* sums;             // [rows][parts]
-  unsigned long long* lists;  // [rows][parts][n_cands]
+  unsigned long long* lists;  // [rows][parts][list]
   int* tickets;               // [n_reqs], zero on entry and exit
   int* status;
 };
 // The most parts that up to `rows` rows are cut into, all together.
 int64_t beam_parts_all(int64_t rows, int num_sms);
+// The most keys of a part's list.
+int beam_list_most(int cands);
 cudaError_t launch_beam_select(BeamSelectArgs a, int num_sms, cudaStream_t st);
 
 struct BeamAdvanceArgs {

@@ -97,7 +97,7 @@ BeamWs beam_ws(const tp_model* m, int n_reqs, int width, int n_cands) {
   BeamWs w;
   w.sums = kMaxStepSeqs * sizeof(int);
   w.lists = align_up(w.sums + parts * sizeof(BeamPart), 256);
-  w.total = w.lists + parts * n_cands * sizeof(unsigned long long);
+  w.total = w.lists + parts * beam_list_most(n_cands) * sizeof(unsigned long long);
   return w;
 }
 
