@@ -93,11 +93,12 @@ __device__ __forceinline__ float power_of(float top) {
   return rintf(fminf(fmaxf(top, -kFar), kFar) * kLog2e);
 }
 
-// log of s * 2^-32, s >= 1, to 10^-8: with s = 2^k m, 2/3 < m <= 4/3 and
-// z = (m - 1) / (m + 1), it is k log 2 + 2 (z + z^3 / 3 + z^5 / 5 + ...); z in two fp32
-// numbers, the powers from its first.  (log in 64 bits took 2900 cycles instead of about
-// 300, on the path of every request.)
-__device__ __forceinline__ double log_fixed(unsigned long long s) {
+// The log of s * 2^(r - 32) - top * log2(e) * log(2), s >= 1, with log2(e) as the sums have it
+// (kLog2e), to 10^-8: with s * 2^-32 = 2^k m, 2/3 < m <= 4/3, and z = (m - 1) / (m + 1), log m
+// is 2 (z + z^3 / 3 + z^5 / 5 + ...); z in two fp32 numbers, the powers from its first.  (log
+// in 64 bits took 2900 cycles, on the path of every request; 64-bit operations take 60 each.)
+__device__ __forceinline__ double log_sum(unsigned long long s, int r, float top) {
+  constexpr double kLn2 = 0.693147180559945309417;
   const int lead = __clzll((long long)s);
   const unsigned long long x = s << lead;
   float m = (float)(uint32_t)(x >> 40) * 0x1p-23f;             // in [1, 2), exact
@@ -109,8 +110,8 @@ __device__ __forceinline__ double log_fixed(unsigned long long s) {
     ++k;
   }
   const float a = m - 1.f, b = m + 1.f, bl = m - (b - 1.f) + ml;
-  const float z = a / b;
-  const float zl = (fmaf(-z, b, a) + ml - z * bl) / b;
+  const float z = __fdividef(a, b);  // (what it is off by is in zl)
+  const float zl = __fdividef(fmaf(-z, b, a) + ml - z * bl, b);
   const float y = z * z;
   float p = 1.f / 13.f;
   p = fmaf(p, y, 1.f / 11.f);
@@ -118,7 +119,8 @@ __device__ __forceinline__ double log_fixed(unsigned long long s) {
   p = fmaf(p, y, 1.f / 7.f);
   p = fmaf(p, y, 1.f / 5.f);
   p = fmaf(p, y, 1.f / 3.f);
-  return fma((double)k, 0.693147180559945309417, (double)(2.f * z)) + (double)(2.f * fmaf(z * y, p, zl));
+  return fma((double)(k + r), kLn2, fma((double)top, -(double)kLog2e * kLn2, (double)(2.f * z))) +
+         (double)(2.f * fmaf(z * y, p, zl));
 }
 
 struct SelectSmem {
@@ -145,8 +147,8 @@ struct JoinSmem {  // lies in the ring
   uint16_t entry[kSelKeys];            // these
   int many;
   uint32_t warp_bound[kSelWarps];
-  double row_top[kMaxBeams], row_rest[kMaxBeams];  // largest logit; score - log of the sum
-  float row_near[kMaxBeams];
+  double row_rest[kMaxBeams];  // score - log of the sum, from the largest logit on
+  float row_top[kMaxBeams], row_near[kMaxBeams];  // the largest logit; row_rest (-infinity: not in use)
   int best_row[kMaxBeamCands], best_token[kMaxBeamCands];
   float best_score[kMaxBeamCands];
 };
@@ -230,11 +232,10 @@ __device__ void join_request(const BeamSelectArgs& a, JoinSmem& sm, int req) {
     }
     for (int q = 1; q < group; q <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, q);
     if (of_row == 0 && w < W) {
-      double log = log_fixed(max(sum, 1ull));  // of the sum, from the largest logit on
-      if (!far) log += 0.693147180559945309417 * ((double)r - (double)top * (double)kLog2e);
+      const double rest = (double)score - log_sum(max(sum, 1ull), far ? 0 : r, far ? 0.f : top);
       sm.row_top[w] = top;
-      sm.row_rest[w] = isfinite(score) ? (double)score - log : -INFINITY;
-      sm.row_near[w] = (float)sm.row_rest[w];
+      sm.row_rest[w] = rest;
+      sm.row_near[w] = isfinite(score) ? (float)rest : -INFINITY;
     }
   }
   __syncthreads();
@@ -275,14 +276,22 @@ __device__ void join_request(const BeamSelectArgs& a, JoinSmem& sm, int req) {
     for (int q = 1; q < kSelWarps; ++q) v = min(v, sm.warp_bound[q]);
     bound = max(v, bound);
   }
-  for (int e = tid; e < N; e += kSelThreads)
-    if (sm.near[e] > -INFINITY && !(ordered(value(e, kNear)) < bound)) sm.entry[atomicAdd(&sm.many, 1)] = (uint16_t)e;
+  for (int e0 = warp * 32; e0 < N; e0 += kSelThreads) {
+    const int e = e0 + lane;
+    const bool passes = e < N && sm.near[e] > -INFINITY && !(ordered(value(e, kNear)) < bound);
+    const unsigned m = __ballot_sync(0xffffffffu, passes);
+    if (!m) continue;
+    int to = 0;
+    if (lane == 0) to = atomicAdd(&sm.many, __popc(m));
+    to = __shfl_sync(0xffffffffu, to, 0) + __popc(m & ((1u << lane) - 1));
+    if (passes) sm.entry[to] = (uint16_t)e;
+  }
   __syncthreads();
   const int many = sm.many, all = min(many, K), T = threads_a_key(many);
   for (int i = tid; i < many; i += kSelThreads) {
     const int e = sm.entry[i], w = (int)fast_div((uint32_t)e, a.div_row_keys);
     const double x = of_ordered((uint32_t)(sm.key[e] >> 32));
-    sm.value[i] = ordered(x - sm.row_top[w] + sm.row_rest[w]);
+    sm.value[i] = ordered(x - (double)sm.row_top[w] + sm.row_rest[w]);
   }
   __syncthreads();
   for (int i0 = 0; i0 < many; i0 += kSelThreads / T) {
@@ -699,7 +708,7 @@ cudaError_t launch_beam_select(BeamSelectArgs a, int num_sms, cudaStream_t st) {
 
 // ---------------------------------------------------------------------------
 // Texts behind their parents: bytes in, bytes out, a CTA 4096 ids of a row.
-constexpr int kAdvThreads = 256, kAdvIds = 4096;
+constexpr int kAdvThreads = 256;
 
 __global__ void __launch_bounds__(kAdvThreads) beam_advance_kernel(const BeamAdvanceArgs a, int pieces,
                                                                   FastDiv div_pieces) {
@@ -739,8 +748,8 @@ __global__ void __launch_bounds__(kAdvThreads) beam_advance_kernel(const BeamAdv
   }
 }
 
-cudaError_t launch_beam_advance(const BeamAdvanceArgs& a, int num_sms, cudaStream_t st) {
-  const int pieces = (int)std::max<int64_t>(1, (std::min(a.ld, a.ld_out) + kAdvIds - 1) / kAdvIds);
+cudaError_t launch_beam_advance(const BeamAdvanceArgs& a, cudaStream_t st) {
+  const int pieces = (int)beam_advance_pieces(std::min(a.ld, a.ld_out));
   return launch_k(beam_advance_kernel, dim3((unsigned)((int64_t)a.n_rows * pieces)), dim3(kAdvThreads), 0, st, a,
                   pieces, make_fastdiv((uint32_t)pieces));
 }

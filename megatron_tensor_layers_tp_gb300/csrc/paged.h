@@ -159,7 +159,9 @@ struct BeamAdvanceArgs {
   int32_t *out, *lens_out;
   int* status;
 };
-cudaError_t launch_beam_advance(const BeamAdvanceArgs& a, int num_sms, cudaStream_t st);
+constexpr int kAdvIds = 4096;  // of a CTA
+inline int64_t beam_advance_pieces(int64_t room) { return (room + kAdvIds - 1) / kAdvIds; }  // of a row
+cudaError_t launch_beam_advance(const BeamAdvanceArgs& a, cudaStream_t st);
 
 // What the fork and the compaction keep of a page in the workspace.
 struct PageNote {

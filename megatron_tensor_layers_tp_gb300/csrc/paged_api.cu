@@ -443,7 +443,8 @@ tp_status tp_beam_advance(const tp_model* m, int32_t n_rows, const int32_t* pare
     if (n_rows == 0) return TP_OK;
     if (!parents || !tokens || !history || !lens || !out || !lens_out || ld_history < 1 || ld_out < 1)
       return TP_ERR_ARG;
-    if (std::min(ld_history, ld_out) > kMaxLength || n_rows > kMaxLength) return TP_ERR_UNSUPPORTED;
+    const int64_t room = std::min(ld_history, ld_out);
+    if (room > kMaxLength || n_rows * beam_advance_pieces(room) > INT32_MAX) return TP_ERR_UNSUPPORTED;
     const Span text{history, n_rows * ld_history * 4}, to{out, n_rows * ld_out * 4};
     const Span words[4] = {{parents, n_rows * 4ll}, {tokens, n_rows * 4ll}, {lens, n_rows * 4ll},
                            {lens_out, n_rows * 4ll}};
@@ -464,7 +465,7 @@ tp_status tp_beam_advance(const tp_model* m, int32_t n_rows, const int32_t* pare
     a.status = m->status;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     return cuda_status(
-        launch(m, "beam_advance", st, [&] { return launch_beam_advance(a, m->num_sms, st); }));
+        launch(m, "beam_advance", st, [&] { return launch_beam_advance(a, st); }));
   });
 }
 

@@ -693,6 +693,15 @@ def altered(c, over):
     return out
 
 
+def copy_too_wide(m):
+    wide = TPModel(make_config(256 * 64, 256, 256, 64, 256, 64, 0, 1, max_positions=8), [], max_tokens=1)
+    p = B.tp_pages_t()
+    p.n_pages, p.page_size = 2, 65536
+    import ctypes
+    at = (ctypes.c_void_p * 1)(2**40)  # (refused before anything looks at it)
+    return B.tp_copy_pages(wide.handle, p, 2**40, 2**40, 1, 1, at, at, 0)
+
+
 def test_refusals_of_the_c_calls():
     ARG, UNS, WS = (B.STATUS[s] for s in ("TP_ERR_ARG", "TP_ERR_UNSUPPORTED", "TP_ERR_WORKSPACE"))
     rng = np.random.default_rng(50)
@@ -738,7 +747,10 @@ def test_refusals_of_the_c_calls():
                dict(o_=t.data_ptr()), dict(o_=t.data_ptr() + 40), dict(l_=n.data_ptr()), dict(l_=t.data_ptr()),
                dict(o_=p.data_ptr()), dict(l_=q.data_ptr() + 4)):
         assert advance(**kw) == ARG, kw
+    # (refused before anything looks at such rows)
     assert advance(ld=2**30 + 1, ldo=2**30 + 1, o_=t.data_ptr() + 2**50) == UNS
+    assert advance(n_=2**20, ld=2**24, ldo=2**24, o_=t.data_ptr() + 2**60, l_=t.data_ptr() + 2**59) == UNS
+    assert copy_too_wide(m) == UNS
 
     c = fork_case(rng, 2, 2, 8, 50)
     pages, fork = device_case(c)
