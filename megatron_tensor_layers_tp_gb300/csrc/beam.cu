@@ -332,10 +332,10 @@ __device__ void join_request(const BeamSelectArgs& a, JoinSmem& sm, int req) {
       const int i = base + lane;
       bool goes = i < all;
       const int token = goes ? sm.best_token[i] : -1;
-#pragma unroll
-      for (int e = 0; e < kMaxEnds; ++e) {
+#pragma unroll 1
+      for (int e = 0; e < a.n_ends; ++e) {
         const int x = __shfl_sync(0xffffffffu, end, e);
-        goes = goes && (e >= a.n_ends || token != x);
+        goes = goes && token != x;
       }
       const unsigned m = __ballot_sync(0xffffffffu, goes);
       const int at = placed + __popc(m & ((1u << lane) - 1));
@@ -545,29 +545,20 @@ __global__ void __launch_bounds__(kSelThreads, 2) beam_select_kernel(const BeamS
     const float most = fminf(of_ordered(o), FLT_MAX);  // the part's largest
     v = max(v, ordered(-INFINITY) + 1);  // (-infinity never passes)
     uint16_t* hit = reinterpret_cast<uint16_t*>(ring);  // (no copy is on its way any more)
-    {
-      uint32_t reach = 0;  // the thread's cells that do
-      const uint4* p = reinterpret_cast<const uint4*>(sm.cell[tid]);
+    const float least = of_ordered(v);
+    uint32_t reach = 0;  // the thread's cells that do
 #pragma unroll
-      for (int i = 0; i < kSelCells / 8; ++i) {
-        const uint4 u = p[i];
-        const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+    for (int i = 0; i < kSelCells / 8; ++i) {
+      const uint4 u = reinterpret_cast<const uint4*>(sm.cell[tid])[i];
+      const uint32_t x[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          reach |= (uint32_t)(ordered(__uint_as_float(x[k] << 16)) >= v) << (8 * i + 2 * k) |
-                   (uint32_t)(ordered(__uint_as_float(x[k] & 0xFFFF0000u)) >= v) << (8 * i + 2 * k + 1);
-      }
-      reach &= (1u << cell) - 1;
-      const int mine = __popc(reach);
-      int to = mine;
-#pragma unroll
-      for (int q = 1; q < 32; q <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, to, q);
-        if (lane >= q) to += x;
-      }
-      int first = 0;
-      if (lane == 31) first = atomicAdd(&sm.hits, to);
-      to += __shfl_sync(0xffffffffu, first, 31) - mine;
+      for (int k = 0; k < 4; ++k)
+        reach |= (uint32_t)(__uint_as_float(x[k] << 16) >= least) << (8 * i + 2 * k) |
+                 (uint32_t)(__uint_as_float(x[k] & 0xFFFF0000u) >= least) << (8 * i + 2 * k + 1);
+    }
+    reach &= (1u << cell) - 1;
+    if (reach) {
+      int to = atomicAdd(&sm.hits, __popc(reach));
       for (; reach; reach &= reach - 1) hit[to++] = (uint16_t)((__ffs(reach) - 1) * kSelThreads + tid);
     }
     __syncthreads();
@@ -580,7 +571,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) beam_select_kernel(const BeamS
       const int64_t t = begin + ((int64_t)cell / kSelThreads * per_cell + d) * kChunk + e;
       return t < end ? (int)t : -1;
     };
-    constexpr int kAtOnce = 8, kTogether = 32 / kPer;  // items that a warp reads at once, by one load
+    constexpr int kAtOnce = 4, kTogether = 32 / kPer;  // items that a warp reads at once, by one load
     for (int x0 = warp * kTogether; x0 < items; x0 += kAtOnce * kSelWarps * kTogether) {
       float x[kAtOnce];
       int t[kAtOnce];
@@ -594,7 +585,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) beam_select_kernel(const BeamS
       int many = 0;
 #pragma unroll
       for (int i = 0; i < kAtOnce; ++i) {
-        const bool p = x[i] == x[i] && ordered(x[i]) >= v;
+        const bool p = x[i] >= least;  // (not NaN)
         passes |= (uint32_t)p << i;
         many += __popc(__ballot_sync(0xffffffffu, p));
       }
@@ -619,14 +610,14 @@ __global__ void __launch_bounds__(kSelThreads, 2) beam_select_kernel(const BeamS
         const int h = h0 + warp < hits ? hit[h0 + warp] : -1;
         const float most = h < 0 ? -INFINITY : bf16_to_f(sm.cell[h % kSelThreads][h / kSelThreads]);
         for (int d = 0; d < per_cell; ++d) {
-          const unsigned long long least = best == K ? sm.keys[K - 1] : 0;
+          const unsigned long long worst = best == K ? sm.keys[K - 1] : 0;
           const int first = begin + (h / kSelThreads * per_cell + d) * kChunk + h % kSelThreads * kE;
-          const bool may = h >= 0 && key_of(most, first) > least;
+          const bool may = h >= 0 && key_of(most, first) > worst;
           if (!__syncthreads_or(may)) continue;
           const int t = may && lane < kPer ? token_of((h0 + warp) * per_cell + d, lane) : -1;
           const float x = t >= 0 ? raw(t) : -INFINITY;
           const unsigned long long key = key_of(x, t);
-          if (x == x && ordered(x) >= v && key > least) sm.keys[best + atomicAdd(&sm.many, 1)] = key;
+          if (x >= least && key > worst) sm.keys[best + atomicAdd(&sm.many, 1)] = key;
           __syncthreads();
           const int n = sm.many;
           __syncthreads();

@@ -20,7 +20,6 @@
 
 namespace tpk {
 
-constexpr int kShThreads = 512, kShWarps = kShThreads / 32;
 constexpr int kShRows = 8;   // rows of a tile, 32 columns wide
 constexpr int kShPages = 4;  // consecutive pages of a thread
 constexpr unsigned kAll = 0xffffffffu;
@@ -30,8 +29,10 @@ __device__ __forceinline__ unsigned long long two(int pages, int rows) {
   return (unsigned long long)(unsigned)rows << 32 | (unsigned)pages;
 }
 // Sum of v over the CTA's threads before this one; *total: over all of them.
+template <int kThreads>
 __device__ __forceinline__ unsigned long long block_scan(unsigned long long v, unsigned long long* total) {
-  __shared__ unsigned long long sums[kShWarps];
+  __shared__ unsigned long long sums[kThreads / 32];
+  constexpr int kWarps = kThreads / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   unsigned long long x = v;
 #pragma unroll
@@ -44,7 +45,7 @@ __device__ __forceinline__ unsigned long long block_scan(unsigned long long v, u
   __syncthreads();
   unsigned long long before = x - v, all = 0;
 #pragma unroll
-  for (int w = 0; w < kShWarps; ++w) {
+  for (int w = 0; w < kWarps; ++w) {
     if (w < warp) before += sums[w];
     all += sums[w];
   }
@@ -97,11 +98,12 @@ __device__ __forceinline__ void share_of(int n, int* first, int* end) {
 }
 
 // What the CTAs before this one counted, and all of them.
+template <int kThreads>
 __device__ __forceinline__ unsigned long long before_this(const ShareHeader* h, unsigned long long* all) {
   __shared__ unsigned long long before;
   int2 c = {0, 0};
   if (threadIdx.x < gridDim.x) c = __ldcg(&h->counts[threadIdx.x]);  // (no more CTAs than threads)
-  const unsigned long long x = block_scan(two(c.x, c.y), all);
+  const unsigned long long x = block_scan<kThreads>(two(c.x, c.y), all);
   if (threadIdx.x == blockIdx.x) before = x;
   __syncthreads();
   return before;
@@ -131,7 +133,9 @@ __device__ __forceinline__ uint2 note_of(const PageNote* notes, int p) {
 // A page that rows held before and none holds after.
 __device__ __forceinline__ bool is_gone(uint2 note) { return note.x >> 16 && !(note.x & 0xFFFF) && !note.y; }
 
-__global__ void __launch_bounds__(kShThreads) fork_pages_kernel(const ForkArgs a) {
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads) fork_pages_kernel(const ForkArgs a) {
+  constexpr int kWarps = kThreads / 32;
   __shared__ uint32_t copied[kMaxStepSeqs / 32];  // the CTA's rows that take a page
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n = a.n_seqs, P = a.page_size;
@@ -146,7 +150,7 @@ __global__ void __launch_bounds__(kShThreads) fork_pages_kernel(const ForkArgs a
   const int row_tiles = (n + kShRows - 1) / kShRows;
   const int col_tiles = max(1, (min(a.ld_table, pages(a.cap)) + 31) / 32);
   // (neighbouring tiles on different SMs: rows that share little take longest)
-  for (int t = warp * gridDim.x + blockIdx.x; t < row_tiles * col_tiles; t += gridDim.x * kShWarps) {
+  for (int t = warp * gridDim.x + blockIdx.x; t < row_tiles * col_tiles; t += gridDim.x * kWarps) {
     const int b0 = t / col_tiles * kShRows, col0 = t % col_tiles * 32, col = col0 + lane;
     // the tile's rows, a lane each: tokens before, source, tokens kept
     const int row = b0 + lane;
@@ -245,9 +249,9 @@ __global__ void __launch_bounds__(kShThreads) fork_pages_kernel(const ForkArgs a
   // one, stay in registers for pass 3.
   uint2 note[kShPages];
   int from, keep;  // the page that the row goes on writing to, or -1; its tokens
-  const int turns = max((p1 - p0 + kShPages * kShThreads - 1) / (kShPages * kShThreads), (b1 - b0 + kShThreads - 1) / kShThreads);
+  const int turns = max((p1 - p0 + kShPages * kThreads - 1) / (kShPages * kThreads), (b1 - b0 + kThreads - 1) / kThreads);
   auto fetch = [&](int turn) {
-    const int row = b0 + turn * kShThreads + tid, page = p0 + (turn * kShThreads + tid) * kShPages;
+    const int row = b0 + turn * kThreads + tid, page = p0 + (turn * kThreads + tid) * kShPages;
     from = row < b1 && !bad ? __ldcg(&a.head->open[row]) : -1;
     keep = row < b1 ? __ldcg(&a.new_lens[row]) : 0;
 #pragma unroll
@@ -259,22 +263,22 @@ __global__ void __launch_bounds__(kShThreads) fork_pages_kernel(const ForkArgs a
     bool copy = false;
     if (from >= 0) {
       const uint2 x = note_of(a.notes, from);
-      copy = (x.x & 0xFFFF) || x.y != (uint32_t)(n - (b0 + turn * kShThreads + tid));
+      copy = (x.x & 0xFFFF) || x.y != (uint32_t)(n - (b0 + turn * kThreads + tid));
     }
     const unsigned m = __ballot_sync(kAll, copy);
-    if (lane == 0 && b0 + turn * kShThreads < b1) copied[turn * kShWarps + warp] = m;
+    if (lane == 0 && b0 + turn * kThreads < b1) copied[turn * kWarps + warp] = m;
     taken += copy;
 #pragma unroll
     for (int i = 0; i < kShPages; ++i) freed += is_gone(note[i]);
   }
   unsigned long long all;
-  block_scan(two(freed, taken), &all);
+  block_scan<kThreads>(two(freed, taken), &all);
   if (tid == 0) a.head->counts[blockIdx.x] = make_int2((int)all, (int)(all >> 32));
   if (!grid_wait(a.head, 1, a.status)) return;
 
   // Pass 3: the ring, the rows' own pages, the moves.
   renew_first(a.head);
-  unsigned long long before = before_this(a.head, &all);
+  unsigned long long before = before_this<kThreads>(a.head, &all);
   const int f_all = (int)all, t_all = (int)(all >> 32);
   bad = bad || t_all > count || count + f_all > a.n_pages;
   auto ring_at = [&](int i) {
@@ -283,13 +287,13 @@ __global__ void __launch_bounds__(kShThreads) fork_pages_kernel(const ForkArgs a
   };
   for (int turn = 0; turn < turns; ++turn) {
     if (turn) fetch(turn);
-    const int row = b0 + turn * kShThreads + tid, page = p0 + (turn * kShThreads + tid) * kShPages;
-    const bool copy = !bad && row < b1 && (copied[turn * kShWarps + warp] >> lane & 1);
+    const int row = b0 + turn * kThreads + tid, page = p0 + (turn * kThreads + tid) * kShPages;
+    const bool copy = !bad && row < b1 && (copied[turn * kWarps + warp] >> lane & 1);
     int gone = 0;
 #pragma unroll
     for (int i = 0; i < kShPages; ++i) gone += is_gone(note[i]);
     unsigned long long here;
-    const unsigned long long mine = before + block_scan(two(gone, copy), &here);
+    const unsigned long long mine = before + block_scan<kThreads>(two(gone, copy), &here);
     before += here;
     int to_ring = (int)mine;
     const int move = (int)(mine >> 32), to = copy ? a.free_ring[ring_at(move)] : 0;
@@ -319,7 +323,7 @@ __global__ void __launch_bounds__(kShThreads) fork_pages_kernel(const ForkArgs a
   }
   if (bad) {  // the old rows again
     const int64_t words = (int64_t)n * a.ld_table;
-    for (int64_t i = (int64_t)blockIdx.x * kShThreads + tid; i < words; i += (int64_t)gridDim.x * kShThreads)
+    for (int64_t i = (int64_t)blockIdx.x * kThreads + tid; i < words; i += (int64_t)gridDim.x * kThreads)
       a.table_out[i] = a.table[i];
   }
   if (blockIdx.x == 0 && tid == 0) {
@@ -330,7 +334,9 @@ __global__ void __launch_bounds__(kShThreads) fork_pages_kernel(const ForkArgs a
   }
 }
 
-__global__ void __launch_bounds__(kShThreads) compact_pages_kernel(const CompactArgs a) {
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads) compact_pages_kernel(const CompactArgs a) {
+  constexpr int kWarps = kThreads / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n = a.n_seqs, P = a.page_size;
   pdl_launch_dependents();
@@ -379,7 +385,7 @@ __global__ void __launch_bounds__(kShThreads) compact_pages_kernel(const Compact
     fetch(tile0, kept);
     refer(kept);
   }
-  for (int t = tile0 + gridDim.x * kShWarps; t < tiles; t += gridDim.x * kShWarps) {
+  for (int t = tile0 + gridDim.x * kWarps; t < tiles; t += gridDim.x * kWarps) {
     int page[kShRows];
     fetch(t, page);
     refer(page);
@@ -392,9 +398,9 @@ __global__ void __launch_bounds__(kShThreads) compact_pages_kernel(const Compact
   int p0, p1;
   share_of(a.n_pages, &p0, &p1);
   uint32_t refs[kShPages];  // the thread's pages of a turn; the first turn's stay for pass 3
-  const int turns = (p1 - p0 + kShPages * kShThreads - 1) / (kShPages * kShThreads);
+  const int turns = (p1 - p0 + kShPages * kThreads - 1) / (kShPages * kThreads);
   auto look = [&](int turn) {
-    const int page = p0 + (turn * kShThreads + tid) * kShPages;
+    const int page = p0 + (turn * kThreads + tid) * kShPages;
 #pragma unroll
     for (int i = 0; i < kShPages; ++i) refs[i] = page + i < p1 ? __ldcg(&a.notes[page + i].refs) : 0;
   };
@@ -410,20 +416,20 @@ __global__ void __launch_bounds__(kShThreads) compact_pages_kernel(const Compact
     held += count_held();
   }
   unsigned long long all;
-  block_scan(two(held, 0), &all);
+  block_scan<kThreads>(two(held, 0), &all);
   if (tid == 0) a.head->counts[blockIdx.x] = make_int2((int)all, 0);
   if (!grid_wait(a.head, 1, a.status)) return;
 
   // Pass 3: with h held pages below p, the free page p < U is the (p - h)-th hole, the
   // held page p >= U the (U - 1 - h)-th to move, from the highest on.
   renew_first(a.head);
-  unsigned long long before = before_this(a.head, &all);
+  unsigned long long before = before_this<kThreads>(a.head, &all);
   const int used = (int)all;
   for (int turn = 0; turn < turns; ++turn) {
     if (turn) look(turn);
-    const int page = p0 + (turn * kShThreads + tid) * kShPages;
+    const int page = p0 + (turn * kThreads + tid) * kShPages;
     unsigned long long here;
-    int h = (int)(before + block_scan(two(count_held(), 0), &here));
+    int h = (int)(before + block_scan<kThreads>(two(count_held(), 0), &here));
     before += here;
 #pragma unroll
     for (int i = 0; i < kShPages; ++i) {
@@ -454,7 +460,7 @@ __global__ void __launch_bounds__(kShThreads) compact_pages_kernel(const Compact
   if (bad) {
     if (a.table_out != a.table) {
       const int64_t words = (int64_t)n * a.ld_table;
-      for (int64_t i = (int64_t)blockIdx.x * kShThreads + tid; i < words; i += (int64_t)gridDim.x * kShThreads)
+      for (int64_t i = (int64_t)blockIdx.x * kThreads + tid; i < words; i += (int64_t)gridDim.x * kThreads)
         a.table_out[i] = a.table[i];
     }
   } else {
@@ -475,7 +481,7 @@ __global__ void __launch_bounds__(kShThreads) compact_pages_kernel(const Compact
         if (page[r] >= 0) a.table_out[(int64_t)(b0 + r) * a.ld_table + col] = page[r];
     };
     if (tile0 < tiles) rename(tile0, kept);
-    for (int t = tile0 + gridDim.x * kShWarps; t < tiles; t += gridDim.x * kShWarps) {
+    for (int t = tile0 + gridDim.x * kWarps; t < tiles; t += gridDim.x * kWarps) {
       int page[kShRows];
       fetch(t, page);
       rename(t, page);
@@ -489,32 +495,35 @@ __global__ void __launch_bounds__(kShThreads) compact_pages_kernel(const Compact
   }
 }
 
+// CTAs of 512 threads, one an SM at most; a single one has 256 (two requests of four beams:
+// 6.5 us instead of 7.4).
+constexpr int kMany = 512, kFew = 256;
+
 template <typename Args>
-static cudaError_t launch_shared(void (*kernel)(Args), const Args& a, int64_t entries, int num_sms,
+static cudaError_t launch_shared(void (*many)(Args), void (*few)(Args), const Args& a, int num_sms,
                                  cudaStream_t st) {
-  const int64_t tiles = (entries + 2047) / 2048, by_pages = (a.n_pages + 2047) / 2048;
-  const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(std::max(tiles, by_pages), std::min({num_sms, kShareCtas, kShThreads})));
-  if (grid == 1) return launch_k(kernel, dim3(1), dim3(kShThreads), 0, st, a);
+  const int64_t cols = std::min<int64_t>(a.ld_table, (a.cap + (int64_t)a.page_size - 1) / a.page_size);
+  const int64_t tiles = (cols * a.n_seqs + 2047) / 2048, by_pages = (a.n_pages + 2047) / 2048;
+  const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(std::max(tiles, by_pages), std::min({num_sms, kShareCtas, kMany})));
+  if (grid == 1) return launch_k(few, dim3(1), dim3(kFew), 0, st, a);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kShThreads);
+  cfg.blockDim = dim3(kMany);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeCooperative;  // all CTAs at once
   attr[0].val.cooperative = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, a);
+  return cudaLaunchKernelEx(&cfg, many, a);
 }
 
 cudaError_t launch_fork_pages(const ForkArgs& a, int num_sms, cudaStream_t st) {
-  const int64_t cols = std::min<int64_t>(a.ld_table, (a.cap + (int64_t)a.page_size - 1) / a.page_size);
-  return launch_shared(fork_pages_kernel, a, cols * a.n_seqs, num_sms, st);
+  return launch_shared(fork_pages_kernel<kMany>, fork_pages_kernel<kFew>, a, num_sms, st);
 }
 
 cudaError_t launch_compact_pages(const CompactArgs& a, int num_sms, cudaStream_t st) {
-  const int64_t cols = std::min<int64_t>(a.ld_table, (a.cap + (int64_t)a.page_size - 1) / a.page_size);
-  return launch_shared(compact_pages_kernel, a, cols * a.n_seqs, num_sms, st);
+  return launch_shared(compact_pages_kernel<kMany>, compact_pages_kernel<kFew>, a, num_sms, st);
 }
 
 }  // namespace tpk
