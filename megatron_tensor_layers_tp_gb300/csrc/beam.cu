@@ -10,10 +10,10 @@
 // The warps run through the ring without waiting for each other.
 // The K best: a thread leaves the largest logit of each chunk in shared memory.
 // Behind the last chunk the K-th largest of at least 2 K maxima (two to eight threads
-// each) bounds the K-th largest logit from below, and the logits of the few cells (a thread's of a
-// chunk) that reach the bound are read once more, from L2: what passes is ranked by
-// counting.  Where more passes than the buffer holds (equal logits) the cells are gone
-// through a warp a cell, and ranked in between.
+// each) bounds the K-th largest logit from below, and the logits of the few cells (a
+// thread's of a chunk) that reach the bound are read once more, from L2: what passes
+// is the part's list.  Where more passes than the buffer holds (equal logits) the
+// cells are gone through a warp a cell, and ranked in between.
 //
 // Sums: of 2^(x log2(e) - r), r the thread's largest x log2(e) so far, rounded to a whole
 // number, so that sums are brought to one r exactly; added in fp32 (at most V / 256
@@ -21,6 +21,16 @@
 // matter: equal rows get equal sums.  What log2(e) in fp32 (c) is off by cancels, as x
 // counts from M in the same units: M c - r.  Rows with NaN, and those whose largest
 // logit is beyond 2^20, are summed once more, from M on.
+//
+// 64 requests of 4 rows of 128256 logits, bf16, K = 8: 19.5 us, 65.7 MB from memory (9.7 us at
+// the copy rate).  The last logits are there after 12 us; what follows is a chain of short
+// steps, 7 us in all: the bound 0.8, the cells 1.1, the list 0.4, the ticket 1.1, the rows'
+// sums 1.2, values 0.7, ranks 1.2.  13 requests of 16 rows of 152064, fp32, K = 32: 29 us
+// (114 MB: 16.8).  One request of 4 rows of 32000: 8.6 us, the chain alone.
+// Measured before: what passes a running bound pushed to the buffer as it streams by, with a
+// barrier a chunk: 25 and 43 us; the same by plain loads, two CTAs' widths in flight: 105 and
+// 136.  A request's CTAs as a cluster that joins through distributed shared memory: 0.2 to
+// 0.4 us less, for a second way through the join; not kept.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <float.h>
@@ -38,7 +48,7 @@ namespace tpk {
 constexpr int kSelThreads = 256, kSelWarps = kSelThreads / 32;
 constexpr int kSelVecs = 4;         // 16-byte words of a thread in a chunk
 constexpr int kSelStages = 4;       // chunks in the ring
-constexpr int kSelCells = 24;       // of a thread: its largest logits, each of so many chunks
+constexpr int kSelCells = 40;       // of a thread: its largest logits, each of so many chunks
 constexpr int kSelChunkBytes = kSelThreads * kSelVecs * 16;
 constexpr int kSelStageBytes = kSelChunkBytes + 128;  // (rows off 16-byte boundaries take a word more)
 constexpr int kSelBuffer = 2 * kSelThreads - kMaxBeamCands;  // keys that may pass a bound
@@ -546,20 +556,20 @@ __global__ void __launch_bounds__(kSelThreads, 2) beam_select_kernel(const BeamS
     v = max(v, ordered(-INFINITY) + 1);  // (-infinity never passes)
     uint16_t* hit = reinterpret_cast<uint16_t*>(ring);  // (no copy is on its way any more)
     const float least = of_ordered(v);
-    uint32_t reach = 0;  // the thread's cells that do
-#pragma unroll
-    for (int i = 0; i < kSelCells / 8; ++i) {
-      const uint4 u = reinterpret_cast<const uint4*>(sm.cell[tid])[i];
+#pragma unroll 1
+    for (int c0 = 0; c0 < cell; c0 += 8) {  // the thread's cells that do
+      const uint4 u = *reinterpret_cast<const uint4*>(sm.cell[tid] + c0);
       const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+      uint32_t reach = 0;
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        reach |= (uint32_t)(__uint_as_float(x[k] << 16) >= least) << (8 * i + 2 * k) |
-                 (uint32_t)(__uint_as_float(x[k] & 0xFFFF0000u) >= least) << (8 * i + 2 * k + 1);
-    }
-    reach &= (1u << cell) - 1;
-    if (reach) {
-      int to = atomicAdd(&sm.hits, __popc(reach));
-      for (; reach; reach &= reach - 1) hit[to++] = (uint16_t)((__ffs(reach) - 1) * kSelThreads + tid);
+        reach |= (uint32_t)(__uint_as_float(x[k] << 16) >= least) << 2 * k |
+                 (uint32_t)(__uint_as_float(x[k] & 0xFFFF0000u) >= least) << (2 * k + 1);
+      reach &= (1u << min(cell - c0, 8)) - 1;
+      if (reach) {
+        int to = atomicAdd(&sm.hits, __popc(reach));
+        for (; reach; reach &= reach - 1) hit[to++] = (uint16_t)((c0 + __ffs(reach) - 1) * kSelThreads + tid);
+      }
     }
     __syncthreads();
     // Logit i of those that an item, one chunk of a cell, stands for: its token, or -1.
@@ -667,7 +677,9 @@ __global__ void __launch_bounds__(kSelThreads, 2) beam_select_kernel(const BeamS
   if (sm.last) join_request(a, *reinterpret_cast<JoinSmem*>(ring), req);
 }
 
-// Parts of a row: as many as two CTAs an SM allow, and a request's lists have room.
+// Parts of a row: as many as two CTAs an SM allow, and a request's lists have room.  (The two
+// large cases above, us: 21.6 and 31.7 with two CTAs an SM and four stages; three and three
+// 26.2 and 31.4; four and two 25.3 and 34.2.)
 static int parts_most(int64_t rows, int width, int cands, int num_sms) {
   return (int)std::max<int64_t>(1, std::min<int64_t>(2 * num_sms / rows, kSelKeys / (width * cands)));
 }

@@ -3,11 +3,11 @@ of cache pages against plain 64-bit implementations, and a beam search over the
 paged cache as a whole.
 
 Tolerance of a candidate's value (fp32 sums of exponentials, the rest in 64 bits): a
-logit's distance d from the thread's largest takes a subtraction, log2(e) rounded and a
-product, 3 * 2^-24 d, and with its weight in the sum d averages at most log V; each
+logit's distance d from the thread's largest takes log2(e) rounded and at most two
+roundings more, 3 * 2^-24 d, and with its weight in the sum d averages at most log V; each
 exponential is good to 2^-22; a thread's sum takes at most V / 256 + 8 additions in fp32 of
-positive terms, its rescaling at most as many products (2^-22 each with the power, and the
-final one).  All are relative errors of positive terms, so the logarithm is off by at most
+positive terms, and one factor for each chunk of 4096 logits or more and at the end (2^-22
+each, if it is no power of two).  All are relative errors of positive terms, so the logarithm is off by at most
   tol(V) = 3 * 2^-24 log V + 2^-22 + (V / 256 + 8) 2^-24 + (V / 4096 + 2) 2^-22,
 and the written score by 2^-24 of its value more.  Whole numbers have to be the same,
 unless two values of different rows lie within 2 tol(V) of each other.
