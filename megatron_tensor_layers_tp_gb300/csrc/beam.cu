@@ -25,7 +25,8 @@
 // 64 requests of 4 rows of 128256 logits, bf16, K = 8: 19.5 us, 65.7 MB from memory (9.7 us at
 // the copy rate).  The last logits are there after 12 us; what follows is a chain of short
 // steps, 7 us in all: the bound 0.8, the cells 1.1, the list 0.4, the ticket 1.1, the rows'
-// sums 1.2, values 0.7, ranks 1.2.  13 requests of 16 rows of 152064, fp32, K = 32: 29 us
+// sums 1.2, values 0.7, ranks 1.2.  The same rows of 128257 logits, off 16-byte boundaries:
+// 21.6.  13 requests of 16 rows of 152064, fp32, K = 32: 29 us
 // (114 MB: 16.8).  One request of 4 rows of 32000: 8.6 us, the chain alone.
 // Measured before: what passes a running bound pushed to the buffer as it streams by, with a
 // barrier a chunk: 25 and 43 us; the same by plain loads, two CTAs' widths in flight: 105 and
@@ -39,6 +40,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "paged.h"
 #include "ptx.cuh"
@@ -47,10 +49,10 @@ namespace tpk {
 
 constexpr int kSelThreads = 256, kSelWarps = kSelThreads / 32;
 constexpr int kSelVecs = 4;         // 16-byte words of a thread in a chunk
-constexpr int kSelStages = 4;       // chunks in the ring
+constexpr int kSelStages = 4;       // chunks in the ring, at most
 constexpr int kSelCells = 40;       // of a thread: its largest logits, each of so many chunks
 constexpr int kSelChunkBytes = kSelThreads * kSelVecs * 16;
-constexpr int kSelStageBytes = kSelChunkBytes + 128;  // (rows off 16-byte boundaries take a word more)
+constexpr int kSelStageBytes = kSelChunkBytes + 128;  // (rows off 16-byte boundaries look at a word more)
 constexpr int kSelBuffer = 2 * kSelThreads - kMaxBeamCands;  // keys that may pass a bound
 constexpr int kSelKeys = 2048;      // of a request's lists, at most
 constexpr int kSelSmall = 32;       // so many are ranked without a bound
@@ -162,9 +164,6 @@ struct JoinSmem {  // lies in the ring
   int best_row[kMaxBeamCands], best_token[kMaxBeamCands];
   float best_score[kMaxBeamCands];
 };
-constexpr int kSelRingBytes =
-    kSelStages * kSelStageBytes > (int)sizeof(JoinSmem) ? kSelStages * kSelStageBytes : (int)sizeof(JoinSmem);
-
 // How many threads count for one of m keys.
 __device__ __forceinline__ int threads_a_key(int m) { return m <= 32 ? 8 : m <= 64 ? 4 : m <= 128 ? 2 : 1; }
 
@@ -364,8 +363,11 @@ __device__ void join_request(const BeamSelectArgs& a, JoinSmem& sm, int req) {
   }
 }
 
-template <bool kFp32>
-__global__ void __launch_bounds__(kSelThreads, 2) beam_select_kernel(const BeamSelectArgs a) {
+// kStages: 4, for two CTAs an SM; 3, for three, where there are more CTAs than two an SM (their
+// steps behind the stream then run beside others' streams; us, with four stages and with
+// three: 800 rows of 128256, bf16: 51 and 46; 1024 rows of 8000, fp32: 25 and 21).
+template <bool kFp32, int kStages>
+__global__ void __launch_bounds__(kSelThreads, kStages == 4 ? 2 : 3) beam_select_kernel(const BeamSelectArgs a) {
   constexpr int kE = kFp32 ? 4 : 8;            // logits of a 16-byte word
   constexpr int kPer = kSelVecs * kE;          // of a thread in a chunk
   constexpr int kSize = kFp32 ? 4 : 2;
@@ -378,7 +380,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) beam_select_kernel(const BeamS
   const int K = a.n_cands;
   if (tid == 0) {
     sm.many = sm.hits = 0;
-    for (int i = 0; i < kSelStages; ++i) {
+    for (int i = 0; i < kStages; ++i) {
       mbar_init(&sm.full[i], 1);
       mbar_init(&sm.empty[i], kSelWarps);
     }
@@ -414,7 +416,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) beam_select_kernel(const BeamS
       }
     };
     if (tid == 0)
-      for (int c = 0; c < min(chunks, kSelStages); ++c) issue(c, c);
+      for (int c = 0; c < min(chunks, kStages); ++c) issue(c, c);
     __syncthreads();
 
     float top = -INFINITY, power = power_of(-INFINITY), sum = 0.f, of_cell = -INFINITY;
@@ -432,33 +434,41 @@ __global__ void __launch_bounds__(kSelThreads, 2) beam_select_kernel(const BeamS
 #pragma unroll
         for (int j = 0; j < kSelVecs; ++j) *reinterpret_cast<uint4*>(w + 4 * j) = words[j * kSelThreads];
       } else {
+        // bytes off .. off + 15 of two words, from their 32-bit word `kFrom` on
+        auto shift = [&](auto from) {
+          constexpr int kFrom = decltype(from)::value;
 #pragma unroll
-        for (int j = 0; j < kSelVecs; ++j) {
-          const int e0 = (j * kSelThreads + tid) * kE;
-          const uint4 u = words[j * kSelThreads], v = words[j * kSelThreads + (off != 0)];
-          uint32_t y[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};  // bytes off .. off + 15 of them
-          if (off & 8) {
+          for (int j = 0; j < kSelVecs; ++j) {
+            const uint4 u = words[j * kSelThreads], v = words[j * kSelThreads + 1];
+            const uint32_t y[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int i = 0; i < 6; ++i) y[i] = y[i + 2];
+            for (int i = 0; i < 4; ++i) w[4 * j + i] = __funnelshift_r(y[kFrom + i], y[kFrom + i + 1], (off & 2) * 8);
           }
-          if (off & 4) {
+        };
+        switch (off >> 2) {
+          case 0: shift(std::integral_constant<int, 0>()); break;
+          case 1: shift(std::integral_constant<int, 1>()); break;
+          case 2: shift(std::integral_constant<int, 2>()); break;
+          default: shift(std::integral_constant<int, 3>());
+        }
+        const uint8_t* at0 = base + (int64_t)at * kSize;
+        if (many < kChunk || at0 < inner0 || at0 + kSelChunkBytes > inner1) {  // the edges of row and part
 #pragma unroll
-            for (int i = 0; i < 5; ++i) y[i] = y[i + 1];
-          }
+          for (int j = 0; j < kSelVecs; ++j) {
+            const int e0 = (j * kSelThreads + tid) * kE;
+            const uint8_t* p = at0 + e0 * kSize;
+            if (e0 >= many) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) w[4 * j + i] = __funnelshift_r(y[i], y[i + 1], (off & 2) * 8);
-          const uint8_t* p = base + (int64_t)(at + e0) * kSize;
-          if (e0 < many && (p < inner0 || p + 16 > inner1 || e0 + kE > many)) {  // the edges of row and part
+              for (int i = 0; i < 4; ++i) w[4 * j + i] = kFp32 ? 0xFF800000u : 0xFF80FF80u;
+            } else if (p < inner0 || p + 16 > inner1 || e0 + kE > many) {
 #pragma unroll
-            for (int e = 0; e < kE; ++e) {
-              const float x = e0 + e < many ? raw(at + e0 + e) : -INFINITY;
-              if constexpr (kFp32) w[4 * j + e % 4] = __float_as_uint(x);
-              else if (e & 1) w[4 * j + e / 2 % 4] |= __float_as_uint(x) & 0xFFFF0000u;
-              else w[4 * j + e / 2 % 4] = __float_as_uint(x) >> 16;
+              for (int e = 0; e < kE; ++e) {
+                const float x = e0 + e < many ? raw(at + e0 + e) : -INFINITY;
+                if constexpr (kFp32) w[4 * j + e % 4] = __float_as_uint(x);
+                else if (e & 1) w[4 * j + e / 2 % 4] |= __float_as_uint(x) & 0xFFFF0000u;
+                else w[4 * j + e / 2 % 4] = __float_as_uint(x) >> 16;
+              }
             }
-          } else if (e0 >= many) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w[4 * j + i] = kFp32 ? 0xFF800000u : 0xFF80FF80u;
           }
         }
       }
@@ -502,11 +512,11 @@ __global__ void __launch_bounds__(kSelThreads, 2) beam_select_kernel(const BeamS
       s = add2(s, t);
       sum = s.x + s.y;
       power = r;
-      if (tid == 0 && c + kSelStages < chunks) {  // the stage's next chunk, once every warp has taken this one
+      if (tid == 0 && c + kStages < chunks) {  // the stage's next chunk, once every warp has taken this one
         ok = mbar_wait(&sm.empty[slot], parity, a.status) && ok;
-        issue(c + kSelStages, slot);
+        issue(c + kStages, slot);
       }
-      if (++slot == kSelStages) {
+      if (++slot == kStages) {
         slot = 0;
         parity ^= 1;
       }
@@ -687,12 +697,13 @@ int64_t beam_parts_all(int64_t rows, int num_sms) { return rows + 2 * num_sms; }
 // What passes the bound is mostly less than twice K: it is not ranked then.
 int beam_list_most(int cands) { return std::min(std::max(2 * cands, 32), kMaxBeamCands); }
 
-template <bool kFp32>
+template <bool kFp32, int kStages>
 static cudaError_t launch_select(const BeamSelectArgs& a, int64_t ctas, cudaStream_t st) {
-  const int smem = kSelRingBytes;
-  cudaError_t e = cudaFuncSetAttribute(beam_select_kernel<kFp32>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const int smem = std::max(kStages * kSelStageBytes, (int)sizeof(JoinSmem));
+  cudaError_t e = cudaFuncSetAttribute(beam_select_kernel<kFp32, kStages>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  return launch_k(beam_select_kernel<kFp32>, dim3((unsigned)ctas), dim3(kSelThreads), smem, st, a);
+  return launch_k(beam_select_kernel<kFp32, kStages>, dim3((unsigned)ctas), dim3(kSelThreads), smem, st, a);
 }
 
 cudaError_t launch_beam_select(BeamSelectArgs a, int num_sms, cudaStream_t st) {
@@ -706,7 +717,9 @@ cudaError_t launch_beam_select(BeamSelectArgs a, int num_sms, cudaStream_t st) {
   a.div_parts = make_fastdiv((uint32_t)a.parts);
   a.div_width = make_fastdiv((uint32_t)a.width);
   a.div_row_keys = make_fastdiv((uint32_t)(a.parts * a.list));
-  return a.fp32 ? launch_select<true>(a, rows * a.parts, st) : launch_select<false>(a, rows * a.parts, st);
+  const int64_t ctas = rows * a.parts;
+  if (ctas > 2 * num_sms) return a.fp32 ? launch_select<true, 3>(a, ctas, st) : launch_select<false, 3>(a, ctas, st);
+  return a.fp32 ? launch_select<true, 4>(a, ctas, st) : launch_select<false, 4>(a, ctas, st);
 }
 
 // ---------------------------------------------------------------------------
