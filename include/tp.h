@@ -702,7 +702,9 @@ tp_status tp_process_logits(const tp_model* m, const tp_bf16* logits, int64_t ld
  *   tp_copy_pages    -> the pages that several beams go on writing to, all layers
  *   tp_step_tables   -> with tokens as the ids of the next forward
  * Any other sharing of pages goes through tp_fork_pages too: several answers to
- * one prompt, a prefix kept in a row of its own, a row that ends. */
+ * one prompt, a prefix kept in a row of its own, a row that ends.  A next beam without a
+ * parent (fewer continuations than beams) has no text and no pages; it may take part in
+ * the step as a row of the one token 0, since its score keeps it out of the next selection. */
 
 /* A selection's sizes, inputs and outputs.  Beams are rows as above. */
 typedef struct {

@@ -13,7 +13,7 @@
 // each) bounds the K-th largest logit from below, and the logits of the few cells (a
 // thread's of a chunk) that reach the bound are read once more, from L2: what passes
 // is the part's list.  Where more passes than the buffer holds (equal logits) the
-// cells are gone through a warp a cell, and ranked in between.
+// cells are gone through a warp a cell, as long as they can still count, and ranked in between.
 //
 // Sums: of 2^(x log2(e) - r), r the thread's largest x log2(e) so far, rounded to a whole
 // number, so that sums are brought to one r exactly; added in fp32 (at most V / 256
@@ -26,8 +26,9 @@
 // the copy rate).  The last logits are there after 12 us; what follows is a chain of short
 // steps, 7 us in all: the bound 0.8, the cells 1.1, the list 0.4, the ticket 1.1, the rows'
 // sums 1.2, values 0.7, ranks 1.2.  The same rows of 128257 logits, off 16-byte boundaries:
-// 21.6.  13 requests of 16 rows of 152064, fp32, K = 32: 29 us
-// (114 MB: 16.8).  One request of 4 rows of 32000: 8.6 us, the chain alone.
+// 21.7.  13 requests of 16 rows of 152064, fp32, K = 32: 29 us (114 MB: 16.8).  One request of
+// 4 rows of 32000: 8.7 us, the chain alone.  All logits equal: 8 requests of 16 rows, K = 64,
+// 0.3 ms.
 // Measured before: what passes a running bound pushed to the buffer as it streams by, with a
 // barrier a chunk: 25 and 43 us; the same by plain loads, two CTAs' widths in flight: 105 and
 // 136.  A request's CTAs as a cluster that joins through distributed shared memory: 0.2 to
@@ -141,6 +142,7 @@ struct SelectSmem {
   uint64_t full[kSelStages], empty[kSelStages];
   int many;  // keys in the buffer
   int hits;  // cells that reach the bound
+  int picked, pick[kSelWarps];
   int last;
   __align__(16) uint32_t group[kSelThreads / 2];
   uint32_t bound;  // the K-th largest of the groups' largest logits
@@ -156,7 +158,7 @@ struct JoinSmem {  // lies in the ring
     };
     unsigned long long value[kSelKeys];  // of those that may be among the K best, bits in order
   };
-  uint16_t entry[kSelKeys];            // these
+  uint32_t entry[kSelKeys];            // these: row << 16 | number
   int many;
   uint32_t warp_bound[kSelWarps];
   double row_rest[kMaxBeams];  // score - log of the sum, from the largest logit on
@@ -293,47 +295,58 @@ __device__ void join_request(const BeamSelectArgs& a, JoinSmem& sm, int req) {
     int to = 0;
     if (lane == 0) to = atomicAdd(&sm.many, __popc(m));
     to = __shfl_sync(0xffffffffu, to, 0) + __popc(m & ((1u << lane) - 1));
-    if (passes) sm.entry[to] = (uint16_t)e;
+    if (passes) sm.entry[to] = fast_div((uint32_t)e, a.div_row_keys) << 16 | (uint32_t)e;
   }
   __syncthreads();
-  const int many = sm.many, all = min(many, K), T = threads_a_key(many);
+  const int many = sm.many, all = min(many, K);
   for (int i = tid; i < many; i += kSelThreads) {
-    const int e = sm.entry[i], w = (int)fast_div((uint32_t)e, a.div_row_keys);
-    const double x = of_ordered((uint32_t)(sm.key[e] >> 32));
+    const uint32_t e = sm.entry[i], w = e >> 16;
+    const double x = of_ordered((uint32_t)(sm.key[e & 0xFFFF] >> 32));
     sm.value[i] = ordered(x - (double)sm.row_top[w] + sm.row_rest[w]);
   }
   __syncthreads();
-  for (int i0 = 0; i0 < many; i0 += kSelThreads / T) {
-    const int i = i0 + tid / T;
-    const unsigned long long v = i < many ? sm.value[i] : 0;
-    const int e = i < many ? sm.entry[i] : 0;
-    const uint32_t w = fast_div((uint32_t)e, a.div_row_keys);
-    int place = 0;
+  // As many as there are threads are ranked at a time (mostly all): the K best so far, in front,
+  // and those from `next` on.
+  for (int best = 0, next = 0; next < many;) {
+    const int m = min(best + many - next, kSelThreads), T = threads_a_key(m), shift = next - best;
+    const int i = tid / T, at = i < best ? i : i + shift;
+    const unsigned long long v = i < m ? sm.value[at] : 0;
+    const uint32_t e = i < m ? sm.entry[at] : 0;
+    const unsigned long long k = sm.key[e & 0xFFFF];
+    int place = i < m ? 0 : K;
 #pragma unroll 4
-    for (int j = tid & (T - 1); j < many; j += T) {
-      const unsigned long long u = sm.value[j];
+    for (int j = tid & (T - 1); j < m; j += T) {
+      const int other = j < best ? j : j + shift;
+      const unsigned long long u = sm.value[other];
       place += u > v;
       if (u == v) {
         // equal values: by row, logit (different logits of a row can have the same value in
         // 64 bits) and token
-        const int f = sm.entry[j];
-        place += fast_div((uint32_t)f, a.div_row_keys) == w ? sm.key[f] > sm.key[e] : f < e;
+        const uint32_t f = sm.entry[other];
+        place += (f ^ e) >> 16 ? f < e : sm.key[f & 0xFFFF] > k;
       }
     }
     for (int q = 1; q < T; q <<= 1) place += __shfl_xor_sync(0xffffffffu, place, q);
-    if (i < many && (tid & (T - 1)) == 0 && place < K) {
-      sm.best_row[place] = row0 + (int)w;
-      sm.best_token[place] = (int)~(uint32_t)sm.key[e];
-      sm.best_score[place] = (float)__longlong_as_double((long long)(v >> 63 ? v ^ 0x8000000000000000ull : ~v));
+    __syncthreads();
+    if ((tid & (T - 1)) == 0 && place < K) {
+      sm.value[place] = v;
+      sm.entry[place] = e;
     }
+    __syncthreads();
+    next += m - best;
+    best = min(m, K);
   }
-  __syncthreads();
   if (tid < K) {
     const bool there = tid < all;
-    a.cand_scores[req * K + tid] = there ? sm.best_score[tid] : -INFINITY;
-    a.cand_rows[req * K + tid] = there ? sm.best_row[tid] : -1;
-    a.cand_tokens[req * K + tid] = there ? sm.best_token[tid] : -1;
+    const uint32_t e = there ? sm.entry[tid] : 0;
+    const unsigned long long v = sm.value[tid];
+    const float score = there ? (float)__longlong_as_double((long long)(v >> 63 ? v ^ 0x8000000000000000ull : ~v)) : -INFINITY;
+    const int from = there ? row0 + (int)(e >> 16) : -1, token = there ? (int)~(uint32_t)sm.key[e & 0xFFFF] : -1;
+    a.cand_scores[req * K + tid] = sm.best_score[tid] = score;
+    a.cand_rows[req * K + tid] = sm.best_row[tid] = from;
+    a.cand_tokens[req * K + tid] = sm.best_token[tid] = token;
   }
+  __syncthreads();
   // The next beams: the first W whose token ends no text.
   if (warp == 0) {
     int placed = 0;
@@ -582,23 +595,23 @@ __global__ void __launch_bounds__(kSelThreads, kStages == 4 ? 2 : 3) beam_select
       }
     }
     __syncthreads();
-    // Logit i of those that an item, one chunk of a cell, stands for: its token, or -1.
-    const int hits = sm.hits, items = hits * per_cell;
-    auto token_of = [&](int item, int i) {
-      const int h = per_cell == 1 ? item : item / per_cell, d = item - h * per_cell;
-      const int cell = hit[h], thread = cell % kSelThreads;
-      const int e = (i / kE * kSelThreads + thread) * kE + i % kE;
-      const int64_t t = begin + ((int64_t)cell / kSelThreads * per_cell + d) * kChunk + e;
+    // Logit i of those that a thread has in chunk d of a cell: its token, or -1.
+    auto token_of = [&](int cell, int d, int i) {
+      const int thread = cell % kSelThreads, e = (i / kE * kSelThreads + thread) * kE + i % kE;
+      const int64_t t = begin + ((int64_t)(cell / kSelThreads) * per_cell + d) * kChunk + e;
       return t < end ? (int)t : -1;
     };
+    const int hits = sm.hits, items = hits * per_cell;  // an item: one chunk of a cell
     constexpr int kAtOnce = 4, kTogether = 32 / kPer;  // items that a warp reads at once, by one load
-    for (int x0 = warp * kTogether; x0 < items; x0 += kAtOnce * kSelWarps * kTogether) {
+    const int once = hits <= kSelBuffer ? items : 0;  // (of more cells more would pass than there is room for)
+    for (int x0 = warp * kTogether; x0 < once; x0 += kAtOnce * kSelWarps * kTogether) {
       float x[kAtOnce];
       int t[kAtOnce];
 #pragma unroll
       for (int i = 0; i < kAtOnce; ++i) {
         const int item = x0 + i * kSelWarps * kTogether + lane / kPer;
-        t[i] = item < items ? token_of(item, lane % kPer) : -1;
+        const int h = per_cell == 1 ? item : item / per_cell;
+        t[i] = item < items ? token_of(hit[h], item - h * per_cell, lane % kPer) : -1;
         x[i] = t[i] >= 0 ? raw(t[i]) : -INFINITY;
       }
       uint32_t passes = 0;
@@ -622,22 +635,35 @@ __global__ void __launch_bounds__(kSelThreads, kStages == 4 ? 2 : 3) beam_select
     }
     __syncthreads();
     int best = 0;
-    if (sm.many > kSelBuffer) {  // a warp a cell and chunk, what can still count
+    if (sm.many > kSelBuffer || hits > kSelBuffer) {  // a warp a cell, of those that can still count, until there are none
+      constexpr uint16_t kDone = 0xFFFF;
       __syncthreads();
       if (tid == 0) sm.many = 0;
-      __syncthreads();
-      for (int h0 = 0; h0 < hits; h0 += kSelWarps) {
-        const int h = h0 + warp < hits ? hit[h0 + warp] : -1;
-        const float most = h < 0 ? -INFINITY : bf16_to_f(sm.cell[h % kSelThreads][h / kSelThreads]);
+      while (true) {
+        if (tid == 0) sm.picked = 0;
+        __syncthreads();
+        const unsigned long long worst = best == K ? sm.keys[K - 1] : 0;
+        for (int h = tid; h < hits; h += kSelThreads) {
+          const int c = hit[h];
+          if (c == kDone) continue;
+          const float most = bf16_to_f(sm.cell[c % kSelThreads][c / kSelThreads]);
+          if (key_of(most, max(token_of(c, 0, 0), 0)) <= worst) {
+            hit[h] = kDone;
+            continue;
+          }
+          const int to = atomicAdd(&sm.picked, 1);
+          if (to >= kSelWarps) break;
+          sm.pick[to] = c;
+          hit[h] = kDone;
+        }
+        __syncthreads();
+        const int picked = min(sm.picked, kSelWarps);
+        if (picked == 0) break;
         for (int d = 0; d < per_cell; ++d) {
-          const unsigned long long worst = best == K ? sm.keys[K - 1] : 0;
-          const int first = begin + (h / kSelThreads * per_cell + d) * kChunk + h % kSelThreads * kE;
-          const bool may = h >= 0 && key_of(most, first) > worst;
-          if (!__syncthreads_or(may)) continue;
-          const int t = may && lane < kPer ? token_of((h0 + warp) * per_cell + d, lane) : -1;
+          const int t = warp < picked && lane < kPer ? token_of(sm.pick[warp], d, lane) : -1;
           const float x = t >= 0 ? raw(t) : -INFINITY;
           const unsigned long long key = key_of(x, t);
-          if (x >= least && key > worst) sm.keys[best + atomicAdd(&sm.many, 1)] = key;
+          if (x >= least && (best < K || key > sm.keys[K - 1])) sm.keys[best + atomicAdd(&sm.many, 1)] = key;
           __syncthreads();
           const int n = sm.many;
           __syncthreads();
