@@ -144,6 +144,19 @@ def test_beam_select_orders_that_flood_the_bound(shape, fp32, V):
             assert b.cand_tokens[0].tolist() == list(range(K)) and set(b.cand_rows[0].tolist()) == {0}
 
 
+@pytest.mark.parametrize("levels", [1, 2, 40])
+@pytest.mark.parametrize("fp32", [False, True])
+@pytest.mark.parametrize("R_,W,K,V", [(3, 16, 64, 20001), (1, 32, 64, 9000), (9, 5, 64, 128256)])
+def test_beam_select_few_values(R_, W, K, V, fp32, levels):
+    """Many equal logits in every row, among rows with equal scores: more than a list holds."""
+    rng = np.random.default_rng(100 * V + levels)
+    x = f32(rng.integers(0, levels, (R_ * W, V)) / 8)
+    scores = rng.integers(-2, 1, R_ * W).astype(np.float32)
+    x = x if fp32 else x.bfloat16()
+    ends = [0, V - 1]
+    check_select(f64(x), scores, W, K, ends, run_select(model(vocab=V), x, scores, W, K, ends))
+
+
 @pytest.mark.parametrize("V", [1000, 32003, 32001, 128257])
 @pytest.mark.parametrize("fp32", [False, True])
 def test_beam_select_equal_beams_tie_to_the_lower_row(V, fp32):
