@@ -238,8 +238,13 @@ __device__ void join_request(const BeamSelectArgs& a, JoinSmem& sm, int req) {
     unsigned long long sum = 0;
     for (int i = of_row; i < a.parts; i += 32) {
       const BeamPart x = i == of_row ? own : p[i];
-      if (far && x.sum) sum += (unsigned long long)((double)x.sum * (double)ex2_approx((x.top - top) * kLog2e));
-      if (!far && !is_far(x.top)) sum += x.sum >> min(max(r - x.power, 0), 63);
+      if (!far && !is_far(x.top)) {
+        sum += x.sum >> min(max(r - x.power, 0), 63);
+      } else if (x.sum) {  // the row's, the part's or both sums count from the largest logit on
+        const float d = !far ? fmaf(x.top, kLog2e, -(float)r)
+                        : is_far(x.top) ? (x.top - top) * kLog2e : fmaf(-top, kLog2e, (float)x.power);
+        sum += (unsigned long long)((double)x.sum * (double)ex2_approx(d));
+      }
     }
     for (int q = 1; q < group; q <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, q);
     if (of_row == 0 && w < W) {

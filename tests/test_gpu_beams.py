@@ -249,6 +249,24 @@ def test_beam_select_large_and_flat_logits():
     check_select(f64(x), scores, 1, 30, (), b)
 
 
+@pytest.mark.parametrize("fp32", [False, True])
+def test_beam_select_logits_on_both_sides_of_what_counts_as_far(fp32):
+    """Parts of a row whose largest logits lie on both sides of 2^20 or -2^20, where the units of
+    their sums change."""
+    V, far, n = 40000, 2.0**20, 12
+    step = 1 / 16 if fp32 else 2.0**12  # (of numbers below 2^20)
+    x = np.full((2 * n, V), -1e9)
+    for i in range(n):
+        x[i, 100] = far + (0.125 * i if fp32 else 0)
+        x[i, 30000:30003] = far - step * (1 + 3 * i)
+        x[n + i, 100] = -far + step * 3 * i
+        x[n + i, 30000:30003] = -far - (0.125 * (1 + i) if fp32 else 2.0**13)
+    x = f32(x) if fp32 else f32(x).bfloat16()
+    for K in (1, 4):
+        scores = np.zeros(2 * n, dtype=np.float32)
+        check_select(f64(x), scores, 1, K, (), run_select(model(vocab=V), x, scores, 1, K))
+
+
 def test_beam_select_ends():
     """Every row's best tokens end the text; with K = W (1 + ends) the next beams are all found."""
     rng = np.random.default_rng(7)
