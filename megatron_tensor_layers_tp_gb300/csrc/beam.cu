@@ -56,7 +56,6 @@ constexpr int kSelChunkBytes = kSelThreads * kSelVecs * 16;
 constexpr int kSelStageBytes = kSelChunkBytes + 128;  // (rows off 16-byte boundaries look at a word more)
 constexpr int kSelBuffer = 2 * kSelThreads - kMaxBeamCands;  // keys that may pass a bound
 constexpr int kSelKeys = 2048;      // of a request's lists, at most
-constexpr int kSelSmall = 32;       // so many are ranked without a bound
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Bits whose order as whole numbers is that of the values (-0 as 0).
@@ -136,6 +135,10 @@ __device__ __forceinline__ double log_sum(unsigned long long s, int r, float top
          (double)(2.f * fmaf(z * y, p, zl));
 }
 
+struct BoundSmem {
+  __align__(16) uint32_t group[kSelThreads / 2];
+  uint32_t bound;
+};
 struct SelectSmem {
   unsigned long long keys[kSelBuffer + kMaxBeamCands + 2];  // the best so far, then the buffer
   __align__(16) uint16_t cell[kSelThreads][kSelCells];  // bf16, rounded up
@@ -144,8 +147,7 @@ struct SelectSmem {
   int hits;  // cells that reach the bound
   int picked, pick[kSelWarps];
   int last;
-  __align__(16) uint32_t group[kSelThreads / 2];
-  uint32_t bound;  // the K-th largest of the groups' largest logits
+  BoundSmem bound;
   uint32_t warp_top[kSelWarps];
   int warp_power[kSelWarps];
   unsigned long long warp_sum[kSelWarps];
@@ -160,7 +162,7 @@ struct JoinSmem {  // lies in the ring
   };
   uint32_t entry[kSelKeys];            // these: row << 16 | number
   int many;
-  uint32_t warp_bound[kSelWarps];
+  BoundSmem bound;
   double row_rest[kMaxBeams];  // score - log of the sum, from the largest logit on
   float row_top[kMaxBeams], row_near[kMaxBeams];  // the largest logit; row_rest (-infinity: not in use)
   int best_row[kMaxBeamCands], best_token[kMaxBeamCands];
@@ -168,6 +170,30 @@ struct JoinSmem {  // lies in the ring
 };
 // How many threads count for one of m keys.
 __device__ __forceinline__ int threads_a_key(int m) { return m <= 32 ? 8 : m <= 64 ? 4 : m <= 128 ? 2 : 1; }
+
+// The K-th largest of the threads' o, or of groups' largest where half as many groups are
+// enough: at least K of the threads' values reach it.  All threads, together; .y: whether
+// one of them has `flag`.
+__device__ __forceinline__ int groups_of(int K) { return K > 32 ? 128 : K > 16 ? 64 : 32; }
+__device__ __forceinline__ uint2 bound_of(BoundSmem& sm, uint32_t o, int K, bool flag) {
+  const int groups = groups_of(K), size = kSelThreads / groups;
+  const int mine = threadIdx.x / size, turn = threadIdx.x & (size - 1);
+  for (int q = 1; q < size; q <<= 1) o = max(o, __shfl_xor_sync(0xffffffffu, o, q));
+  if (turn == 0) sm.group[mine] = o;
+  const uint32_t any = __syncthreads_or(flag);
+  int place = 0;
+  const int j0 = turn * (groups / size), j1 = j0 + groups / size;
+#pragma unroll 4
+  for (int j = j0; j < j1; j += 4) {
+    const uint4 x = *reinterpret_cast<const uint4*>(sm.group + j);
+    place += (x.x > o || (x.x == o && j < mine)) + (x.y > o || (x.y == o && j + 1 < mine)) +
+             (x.z > o || (x.z == o && j + 2 < mine)) + (x.w > o || (x.w == o && j + 3 < mine));
+  }
+  for (int q = 1; q < size; q <<= 1) place += __shfl_xor_sync(0xffffffffu, place, q);
+  if (place == K - 1 && turn == 0) sm.bound = o;
+  __syncthreads();
+  return make_uint2(sm.bound, any);
+}
 
 // Ranks the keys, `best` sorted ones and n more, and keeps the K best: their
 // number.  All threads, together; the keys are visible on entry and exit.
@@ -208,13 +234,20 @@ __device__ void join_request(const BeamSelectArgs& a, JoinSmem& sm, int req) {
   const int W = a.width, K = a.n_cands, per_row = a.parts * a.list, N = W * per_row;
   const int row0 = req * W;
   const unsigned long long* keys = a.lists + (int64_t)row0 * per_row;
-  // (the first keys of the thread are on their way while the rows' sums are joined)
-  unsigned long long key[4];
-  auto fetch = [&](int e0) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) key[i] = e0 + i * kSelThreads < N ? keys[e0 + i * kSelThreads] : 0;
+  // A thread's keys are one of each run of as many keys as there are groups, every run turned
+  // further: a row's may be the best of all, and lists may be in order.  (The first are on their
+  // way while the rows' sums are joined.)
+  const int groups = groups_of(K), size = kSelThreads / groups;
+  auto number = [&](int i) {
+    const int run = i * size + (tid & (size - 1));
+    return run * groups + ((tid / size + 37 * run) & (groups - 1));
   };
-  fetch(tid);
+  unsigned long long key[4];
+  auto fetch = [&](int i0) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) key[i] = number(i0 + i) < N ? keys[number(i0 + i)] : 0;
+  };
+  fetch(0);
   const int end = warp == 0 && lane < a.n_ends ? a.ends[lane] : -1;
   if (tid == 0) sm.many = 0;
   // A row a group of as many lanes as it has parts (up to 32, a power of two).
@@ -256,51 +289,27 @@ __device__ void join_request(const BeamSelectArgs& a, JoinSmem& sm, int req) {
   }
   __syncthreads();
 
-  for (int e0 = tid; e0 < N; e0 += 4 * kSelThreads) {
-    if (e0 != tid) fetch(e0);
+  auto value = [](float below, float near, float side) { return below + near + side * (fabsf(below) + fabsf(near)); };
+  float most = -INFINITY;
+  for (int i0 = 0; i0 * kSelThreads < N; i0 += 4) {
+    if (i0) fetch(i0);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int e = e0 + i * kSelThreads;
-      if (e >= N) break;
+      const int e = number(i0 + i);
+      if (e >= N) continue;
       const int w = (int)fast_div((uint32_t)e, a.div_row_keys);
-      const float x = of_ordered((uint32_t)(key[i] >> 32));
+      const float below = of_ordered((uint32_t)(key[i] >> 32)) - sm.row_top[w];
+      const float near = key[i] ? sm.row_near[w] : -INFINITY;  // (-infinity: none)
       sm.key[e] = key[i];
-      // (-infinity: none)
-      sm.below[e] = x - sm.row_top[w], sm.near[e] = key[i] ? sm.row_near[w] : -INFINITY;
+      sm.below[e] = below, sm.near[e] = near;
+      if (near > -INFINITY) most = fmaxf(most, value(below, near, -kNear));
     }
   }
-  __syncthreads();
-  auto value = [&](int e, float side) { return sm.below[e] + sm.near[e] + side * (fabsf(sm.below[e]) + fabsf(sm.near[e])); };
-  uint32_t bound = ordered(-INFINITY) + 1;
-  if (N > kSelSmall) {
-    // a warp takes every eighth key, each lane's at another place of its list
-    float most = -INFINITY;
-    for (int e0 = lane * kSelWarps; e0 < N; e0 += kSelThreads) {
-      const int e = e0 + ((lane + warp) & (kSelWarps - 1));
-      if (e < N && sm.near[e] > -INFINITY) most = fmaxf(most, value(e, -kNear));
-    }
-    uint32_t o = ordered(most), v = 0;
-    for (int r = 0; r < (K + kSelWarps - 1) / kSelWarps; ++r) {
-      v = __reduce_max_sync(0xffffffffu, o);
-      const unsigned m = __ballot_sync(0xffffffffu, o == v);
-      if (lane == __ffs(m) - 1) o = 0;
-    }
-    if (lane == 0) sm.warp_bound[warp] = v;
-    __syncthreads();
-    v = sm.warp_bound[0];
-#pragma unroll
-    for (int q = 1; q < kSelWarps; ++q) v = min(v, sm.warp_bound[q]);
-    bound = max(v, bound);
-  }
-  for (int e0 = warp * 32; e0 < N; e0 += kSelThreads) {
-    const int e = e0 + lane;
-    const bool passes = e < N && sm.near[e] > -INFINITY && !(ordered(value(e, kNear)) < bound);
-    const unsigned m = __ballot_sync(0xffffffffu, passes);
-    if (!m) continue;
-    int to = 0;
-    if (lane == 0) to = atomicAdd(&sm.many, __popc(m));
-    to = __shfl_sync(0xffffffffu, to, 0) + __popc(m & ((1u << lane) - 1));
-    if (passes) sm.entry[to] = fast_div((uint32_t)e, a.div_row_keys) << 16 | (uint32_t)e;
+  const uint32_t bound = max(bound_of(sm.bound, ordered(most), K, false).x, ordered(-INFINITY) + 1);
+  for (int e = tid; e < N; e += kSelThreads) {
+    const float below = sm.below[e], near = sm.near[e];
+    if (near > -INFINITY && !(ordered(value(below, near, kNear)) < bound))
+      sm.entry[atomicAdd(&sm.many, 1)] = fast_div((uint32_t)e, a.div_row_keys) << 16 | (uint32_t)e;
   }
   __syncthreads();
   const int many = sm.many, all = min(many, K);
@@ -324,7 +333,7 @@ __device__ void join_request(const BeamSelectArgs& a, JoinSmem& sm, int req) {
       const int other = j < best ? j : j + shift;
       const unsigned long long u = sm.value[other];
       place += u > v;
-      if (u == v) {
+      if (u == v && j != i) {
         // equal values: by row, logit (different logits of a row can have the same value in
         // 64 bits) and token
         const uint32_t f = sm.entry[other];
@@ -517,7 +526,7 @@ __global__ void __launch_bounds__(kSelThreads, kStages == 4 ? 2 : 3) beam_select
 
       // the sum of exponentials
       const float r = fmaxf(power, power_of(mx));
-      float2 s = {sum * ex2_approx(power - r), 0.f}, t = {0.f, 0.f};
+      float2 s = {0.f, 0.f}, t = {0.f, 0.f};
 #pragma unroll
       for (int i = 0; i < kPer / 2; ++i) {
         const float2 x = kFp32 ? make_float2(__uint_as_float(w[2 * i % (4 * kSelVecs)]),
@@ -528,9 +537,10 @@ __global__ void __launch_bounds__(kSelThreads, kStages == 4 ? 2 : 3) beam_select
         if (i & 1) t = add2(t, e); else s = add2(s, e);
       }
       s = add2(s, t);
-      sum = s.x + s.y;
+      sum = fmaf(sum, ex2_approx(power - r), s.x + s.y);
       power = r;
-      if (tid == 0 && c + kStages < chunks) {  // the stage's next chunk, once every warp has taken this one
+      // the stage's next chunk, once every warp has taken this one; the warps in turn
+      if (lane == 0 && warp == (c & (kSelWarps - 1)) && c + kStages < chunks) {
         ok = mbar_wait(&sm.empty[slot], parity, a.status) && ok;
         issue(c + kStages, slot);
       }
@@ -552,31 +562,14 @@ __global__ void __launch_bounds__(kSelThreads, kStages == 4 ? 2 : 3) beam_select
       return ((unsigned long long)hi << 52) + ((unsigned long long)mid << 26) + lo;
     };
     unsigned long long fixed = fixed_sum(sum * ex2_approx(power - (float)r));
-    // groups of threads, twice as many as the bound's place
-    const int groups = K > 32 ? 128 : K > 16 ? 64 : 32, size = kSelThreads / groups;
-    for (int q = 1; q < size; q <<= 1) o = max(o, __shfl_xor_sync(0xffffffffu, o, q));
-    const int mine = tid / size, turn = tid & (size - 1);
-    if (turn == 0) sm.group[mine] = o;
     if (lane == 0) {
       sm.warp_top[warp] = warp_top;
       sm.warp_power[warp] = r;
       sm.warp_sum[warp] = fixed;
     }
-    const bool bad = __syncthreads_or(!(sum < INFINITY));
-    {
-      int place = 0;
-      const int j0 = turn * (groups / size), j1 = j0 + groups / size;
-#pragma unroll 4
-      for (int j = j0; j < j1; j += 4) {
-        const uint4 x = *reinterpret_cast<const uint4*>(sm.group + j);
-        place += (x.x > o || (x.x == o && j < mine)) + (x.y > o || (x.y == o && j + 1 < mine)) +
-                 (x.z > o || (x.z == o && j + 2 < mine)) + (x.w > o || (x.w == o && j + 3 < mine));
-      }
-      for (int q = 1; q < size; q <<= 1) place += __shfl_xor_sync(0xffffffffu, place, q);
-      if (place == K - 1 && turn == 0) sm.bound = o;
-    }
-    __syncthreads();
-    uint32_t v = sm.bound;
+    const uint2 x = bound_of(sm.bound, o, K, !(sum < INFINITY));
+    const bool bad = x.y;
+    uint32_t v = x.x;
     o = sm.warp_top[0];
 #pragma unroll
     for (int q = 1; q < kSelWarps; ++q) o = max(o, sm.warp_top[q]);
@@ -617,26 +610,14 @@ __global__ void __launch_bounds__(kSelThreads, kStages == 4 ? 2 : 3) beam_select
         const int item = x0 + i * kSelWarps * kTogether + lane / kPer;
         const int h = per_cell == 1 ? item : item / per_cell;
         t[i] = item < items ? token_of(hit[h], item - h * per_cell, lane % kPer) : -1;
-        x[i] = t[i] >= 0 ? raw(t[i]) : -INFINITY;
+        x[i] = raw(max(t[i], begin));
       }
-      uint32_t passes = 0;
-      int many = 0;
 #pragma unroll
-      for (int i = 0; i < kAtOnce; ++i) {
-        const bool p = x[i] >= least;  // (not NaN)
-        passes |= (uint32_t)p << i;
-        many += __popc(__ballot_sync(0xffffffffu, p));
-      }
-      int to = 0;
-      if (lane == 0) to = atomicAdd(&sm.many, many);
-      to = __shfl_sync(0xffffffffu, to, 0);
-#pragma unroll
-      for (int i = 0; i < kAtOnce; ++i) {
-        const unsigned m = __ballot_sync(0xffffffffu, passes >> i & 1);
-        const int at = to + __popc(m & ((1u << lane) - 1));
-        if ((passes >> i & 1) && at < kSelBuffer) sm.keys[at] = key_of(x[i], t[i]);
-        to += __popc(m);
-      }
+      for (int i = 0; i < kAtOnce; ++i)
+        if (t[i] >= 0 && x[i] >= least) {  // (not NaN)
+          const int to = atomicAdd(&sm.many, 1);
+          if (to < kSelBuffer) sm.keys[to] = key_of(x[i], t[i]);
+        }
     }
     __syncthreads();
     int best = 0;
