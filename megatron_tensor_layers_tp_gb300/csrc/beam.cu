@@ -154,13 +154,12 @@ struct SelectSmem {
 };
 struct JoinSmem {  // lies in the ring
   unsigned long long key[kSelKeys];    // of the lists
-  union {
-    struct {
-      float below[kSelKeys], near[kSelKeys];  // their values' parts: from the row's largest logit on; the row's
-    };
-    unsigned long long value[kSelKeys];  // of those that may be among the K best, bits in order
-  };
-  uint32_t entry[kSelKeys];            // these: row << 16 | number
+  float below[kSelKeys], near[kSelKeys];  // their values' parts: from the row's largest logit on; the row's
+  uint32_t entry[kSelKeys];            // of those that may be among the K best: row << 16 | number
+  // of those that are ranked at a time: values (bits in order) and keys, entries
+  ulonglong2 ranked[kSelThreads];
+  uint32_t its_entry[kSelThreads];
+  unsigned long long best_value[kMaxBeamCands];
   int many;
   BoundSmem bound;
   double row_rest[kMaxBeams];  // score - log of the sum, from the largest logit on
@@ -313,37 +312,33 @@ __device__ void join_request(const BeamSelectArgs& a, JoinSmem& sm, int req) {
   }
   __syncthreads();
   const int many = sm.many, all = min(many, K);
-  for (int i = tid; i < many; i += kSelThreads) {
-    const uint32_t e = sm.entry[i], w = e >> 16;
-    const double x = of_ordered((uint32_t)(sm.key[e & 0xFFFF] >> 32));
-    sm.value[i] = ordered(x - (double)sm.row_top[w] + sm.row_rest[w]);
-  }
-  __syncthreads();
   // As many as there are threads are ranked at a time (mostly all): the K best so far, in front,
-  // and those from `next` on.
+  // and those from `next` on.  Equal values go by row, logit (different logits of a row can have
+  // the same value in 64 bits) and token.
   for (int best = 0, next = 0; next < many;) {
-    const int m = min(best + many - next, kSelThreads), T = threads_a_key(m), shift = next - best;
-    const int i = tid / T, at = i < best ? i : i + shift;
-    const unsigned long long v = i < m ? sm.value[at] : 0;
-    const uint32_t e = i < m ? sm.entry[at] : 0;
-    const unsigned long long k = sm.key[e & 0xFFFF];
+    const int m = min(best + many - next, kSelThreads), T = threads_a_key(m);
+    if (tid < m) {
+      const uint32_t e = sm.entry[tid < best ? tid : tid - best + next];
+      const unsigned long long k = sm.key[e & 0xFFFF];
+      const double x = of_ordered((uint32_t)(k >> 32));
+      sm.ranked[tid] = make_ulonglong2(
+          tid < best ? sm.best_value[tid] : ordered(x - (double)sm.row_top[e >> 16] + sm.row_rest[e >> 16]), k);
+      sm.its_entry[tid] = e;
+    }
+    __syncthreads();
+    const int i = tid / T;
+    const ulonglong2 v = sm.ranked[i];
+    const uint32_t e = sm.its_entry[i], w = e >> 16;
     int place = i < m ? 0 : K;
 #pragma unroll 4
     for (int j = tid & (T - 1); j < m; j += T) {
-      const int other = j < best ? j : j + shift;
-      const unsigned long long u = sm.value[other];
-      place += u > v;
-      if (u == v && j != i) {
-        // equal values: by row, logit (different logits of a row can have the same value in
-        // 64 bits) and token
-        const uint32_t f = sm.entry[other];
-        place += (f ^ e) >> 16 ? f < e : sm.key[f & 0xFFFF] > k;
-      }
+      const ulonglong2 u = sm.ranked[j];
+      const uint32_t row = sm.its_entry[j] >> 16;
+      place += (u.x > v.x) | ((u.x == v.x) & ((row < w) | ((row == w) & (u.y > v.y))));
     }
     for (int q = 1; q < T; q <<= 1) place += __shfl_xor_sync(0xffffffffu, place, q);
-    __syncthreads();
     if ((tid & (T - 1)) == 0 && place < K) {
-      sm.value[place] = v;
+      sm.best_value[place] = v.x;
       sm.entry[place] = e;
     }
     __syncthreads();
@@ -353,7 +348,7 @@ __device__ void join_request(const BeamSelectArgs& a, JoinSmem& sm, int req) {
   if (tid < K) {
     const bool there = tid < all;
     const uint32_t e = there ? sm.entry[tid] : 0;
-    const unsigned long long v = sm.value[tid];
+    const unsigned long long v = there ? sm.best_value[tid] : 0;
     const float score = there ? (float)__longlong_as_double((long long)(v >> 63 ? v ^ 0x8000000000000000ull : ~v)) : -INFINITY;
     const int from = there ? row0 + (int)(e >> 16) : -1, token = there ? (int)~(uint32_t)sm.key[e & 0xFFFF] : -1;
     a.cand_scores[req * K + tid] = sm.best_score[tid] = score;
