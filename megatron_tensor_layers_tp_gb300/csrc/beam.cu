@@ -562,9 +562,9 @@ __global__ void __launch_bounds__(kSelThreads, kStages == 4 ? 2 : 3) beam_select
       sm.warp_power[warp] = r;
       sm.warp_sum[warp] = fixed;
     }
-    const uint2 x = bound_of(sm.bound, o, K, !(sum < INFINITY));
-    const bool bad = x.y;
-    uint32_t v = x.x;
+    const uint2 found = bound_of(sm.bound, o, K, !(sum < INFINITY));
+    const bool bad = found.y;
+    uint32_t v = found.x;
     o = sm.warp_top[0];
 #pragma unroll
     for (int q = 1; q < kSelWarps; ++q) o = max(o, sm.warp_top[q]);
@@ -685,10 +685,8 @@ __global__ void __launch_bounds__(kSelThreads, kStages == 4 ? 2 : 3) beam_select
   // The last of the request's CTAs joins them.
   __syncthreads();
   if (tid == 0) {
-    fence_acq_rel_gpu();
-    sm.last = atomicAdd(a.tickets + req, 1) == a.width * a.parts - 1;
+    sm.last = atomic_add_acq_rel_gpu(a.tickets + req, 1) == a.width * a.parts - 1;
     if (sm.last) a.tickets[req] = 0;
-    fence_acq_rel_gpu();
   }
   __syncthreads();
   if (sm.last) join_request(a, *reinterpret_cast<JoinSmem*>(ring), req);

@@ -71,19 +71,16 @@ __device__ __forceinline__ bool grid_wait(ShareHeader* h, int which, int* status
   __shared__ int ok;
   __syncthreads();
   if (threadIdx.x == 0) {
-    fence_acq_rel_gpu();
-    atomicAdd(&h->arrived[which], 1u);
+    red_add_release_gpu(&h->arrived[which], 1u);
     ok = 1;
-    volatile unsigned* p = &h->arrived[which];
     const long long t0 = clock64();
-    while (*p < gridDim.x) {
+    while (ld_acquire_gpu(&h->arrived[which]) < gridDim.x) {
       if (clock64() - t0 > kWaitLimitCycles) {
         record_status(status, kStatusTimeout);
         ok = 0;
         break;
       }
     }
-    fence_acq_rel_gpu();
   }
   __syncthreads();
   return ok;
