@@ -167,21 +167,24 @@ struct JoinSmem {  // lies in the ring
   int best_row[kMaxBeamCands], best_token[kMaxBeamCands];
   float best_score[kMaxBeamCands];
 };
-// How many threads count for one of m keys.
-__device__ __forceinline__ int threads_a_key(int m) { return m <= 32 ? 8 : m <= 64 ? 4 : m <= 128 ? 2 : 1; }
+// How many threads count for one of m keys (as powers of two, here and below: divisions by
+// other numbers are long).
+__device__ __forceinline__ int log_threads_a_key(int m) { return m <= 32 ? 3 : m <= 64 ? 2 : m <= 128 ? 1 : 0; }
 
 // The K-th largest of the threads' o, or of groups' largest where half as many groups are
 // enough: at least K of the threads' values reach it.  All threads, together; .y: whether
 // one of them has `flag`.
-__device__ __forceinline__ int groups_of(int K) { return K > 32 ? 128 : K > 16 ? 64 : 32; }
+__device__ __forceinline__ int log_groups_of(int K) { return K > 32 ? 7 : K > 16 ? 6 : 5; }
+constexpr int kLogThreads = 8;
+static_assert(kSelThreads == 1 << kLogThreads, "");
 __device__ __forceinline__ uint2 bound_of(BoundSmem& sm, uint32_t o, int K, bool flag) {
-  const int groups = groups_of(K), size = kSelThreads / groups;
-  const int mine = threadIdx.x / size, turn = threadIdx.x & (size - 1);
+  const int log_size = kLogThreads - log_groups_of(K), size = 1 << log_size;
+  const int mine = threadIdx.x >> log_size, turn = threadIdx.x & (size - 1);
   for (int q = 1; q < size; q <<= 1) o = max(o, __shfl_xor_sync(0xffffffffu, o, q));
   if (turn == 0) sm.group[mine] = o;
   const uint32_t any = __syncthreads_or(flag);
   int place = 0;
-  const int j0 = turn * (groups / size), j1 = j0 + groups / size;
+  const int share = kSelThreads >> 2 * log_size, j0 = turn * share, j1 = j0 + share;
 #pragma unroll 4
   for (int j = j0; j < j1; j += 4) {
     const uint4 x = *reinterpret_cast<const uint4*>(sm.group + j);
@@ -197,13 +200,13 @@ __device__ __forceinline__ uint2 bound_of(BoundSmem& sm, uint32_t o, int K, bool
 // Ranks the keys, `best` sorted ones and n more, and keeps the K best: their
 // number.  All threads, together; the keys are visible on entry and exit.
 __device__ __noinline__ int rank_keys(SelectSmem& sm, int best, int n, int K) {
-  const int m = best + n, tid = threadIdx.x, T = threads_a_key(m);
+  const int m = best + n, tid = threadIdx.x, log_t = log_threads_a_key(m), T = 1 << log_t;
   constexpr int kMost = (kSelBuffer + kMaxBeamCands) / kSelThreads;
   unsigned long long key[kMost];
   int rank[kMost];
 #pragma unroll
   for (int i = 0; i < kMost; ++i) {
-    const int at = tid / T + i * kSelThreads;
+    const int at = (tid >> log_t) + i * kSelThreads;
     key[i] = at < m ? sm.keys[at] : 0;
     rank[i] = K;
     if (i * kSelThreads >= m) break;
@@ -236,10 +239,10 @@ __device__ void join_request(const BeamSelectArgs& a, JoinSmem& sm, int req) {
   // A thread's keys are one of each run of as many keys as there are groups, every run turned
   // further: a row's may be the best of all, and lists may be in order.  (The first are on their
   // way while the rows' sums are joined.)
-  const int groups = groups_of(K), size = kSelThreads / groups;
+  const int log_groups = log_groups_of(K), groups = 1 << log_groups, log_size = kLogThreads - log_groups;
   auto number = [&](int i) {
-    const int run = i * size + (tid & (size - 1));
-    return run * groups + ((tid / size + 37 * run) & (groups - 1));
+    const int run = (i << log_size) + (tid & ((1 << log_size) - 1));
+    return (run << log_groups) + (((tid >> log_size) + 37 * run) & (groups - 1));
   };
   unsigned long long key[4];
   auto fetch = [&](int i0) {
@@ -250,10 +253,11 @@ __device__ void join_request(const BeamSelectArgs& a, JoinSmem& sm, int req) {
   const int end = warp == 0 && lane < a.n_ends ? a.ends[lane] : -1;
   if (tid == 0) sm.many = 0;
   // A row a group of as many lanes as it has parts (up to 32, a power of two).
-  const int group = a.parts > 16 ? 32 : a.parts > 8 ? 16 : a.parts > 4 ? 8 : a.parts > 2 ? 4 : a.parts;
+  const int log_group = a.parts > 16 ? 5 : a.parts > 8 ? 4 : a.parts > 4 ? 3 : a.parts > 2 ? 2 : a.parts - 1;
+  const int group = 1 << log_group;
   const int of_row = tid & (group - 1);
-  for (int w0 = 0; w0 < W; w0 += kSelThreads / group) {
-    const int w = w0 + tid / group;
+  for (int w0 = 0; w0 < W; w0 += kSelThreads >> log_group) {
+    const int w = w0 + (tid >> log_group);
     const float score = w < W ? a.scores[row0 + w] : -INFINITY;
     const BeamPart* p = a.sums + (int64_t)(row0 + min(w, W - 1)) * a.parts;
     const BeamPart own = of_row < a.parts ? p[of_row] : BeamPart{0, -INFINITY, INT_MIN};
@@ -316,7 +320,7 @@ __device__ void join_request(const BeamSelectArgs& a, JoinSmem& sm, int req) {
   // and those from `next` on.  Equal values go by row, logit (different logits of a row can have
   // the same value in 64 bits) and token.
   for (int best = 0, next = 0; next < many;) {
-    const int m = min(best + many - next, kSelThreads), T = threads_a_key(m);
+    const int m = min(best + many - next, kSelThreads), log_t = log_threads_a_key(m), T = 1 << log_t;
     if (tid < m) {
       const uint32_t e = sm.entry[tid < best ? tid : tid - best + next];
       const unsigned long long k = sm.key[e & 0xFFFF];
@@ -326,7 +330,7 @@ __device__ void join_request(const BeamSelectArgs& a, JoinSmem& sm, int req) {
       sm.its_entry[tid] = e;
     }
     __syncthreads();
-    const int i = tid / T;
+    const int i = tid >> log_t;
     const ulonglong2 v = sm.ranked[i];
     const uint32_t e = sm.its_entry[i], w = e >> 16;
     int place = i < m ? 0 : K;
@@ -414,7 +418,6 @@ __global__ void __launch_bounds__(kSelThreads, kStages == 4 ? 2 : 3) beam_select
     const int begin = (int)min((int64_t)part * a.part_chunks * kChunk, (int64_t)a.vocab);
     const int end = (int)min((int64_t)begin + (int64_t)a.part_chunks * kChunk, (int64_t)a.vocab);
     const int chunks = (end - begin + kChunk - 1) / kChunk;
-    const int per_cell = (chunks + kSelCells - 1) / kSelCells;  // chunks
     const uint8_t* base = static_cast<const uint8_t*>(a.logits) + row * a.ld * kSize;
     const int off = (int)(reinterpret_cast<uintptr_t>(base) & 15);  // of every chunk's first logit
     // the row's 16-byte words that hold nothing else
@@ -512,7 +515,7 @@ __global__ void __launch_bounds__(kSelThreads, kStages == 4 ? 2 : 3) beam_select
       }
       top = fmaxf(top, mx);
       of_cell = fmaxf(of_cell, mx);
-      if (++in_cell == per_cell || c + 1 == chunks) {
+      if (++in_cell == a.per_cell || c + 1 == chunks) {
         sm.cell[tid][cell] = __bfloat16_as_ushort(__float2bfloat16_ru(of_cell));
         ++cell;
         in_cell = 0;
@@ -589,12 +592,12 @@ __global__ void __launch_bounds__(kSelThreads, kStages == 4 ? 2 : 3) beam_select
     }
     __syncthreads();
     // Logit i of those that a thread has in chunk d of a cell: its token, or -1.
-    auto token_of = [&](int cell, int d, int i) {
-      const int thread = cell % kSelThreads, e = (i / kE * kSelThreads + thread) * kE + i % kE;
-      const int64_t t = begin + ((int64_t)(cell / kSelThreads) * per_cell + d) * kChunk + e;
+    auto token_of = [&](int cell, int d, uint32_t i) {
+      const int thread = cell & (kSelThreads - 1), e = (i / kE * kSelThreads + thread) * kE + i % kE;
+      const int64_t t = begin + ((int64_t)(cell >> kLogThreads) * a.per_cell + d) * kChunk + e;
       return t < end ? (int)t : -1;
     };
-    const int hits = sm.hits, items = hits * per_cell;  // an item: one chunk of a cell
+    const int hits = sm.hits, items = hits * a.per_cell;  // an item: one chunk of a cell
     constexpr int kAtOnce = 4, kTogether = 32 / kPer;  // items that a warp reads at once, by one load
     const int once = hits <= kSelBuffer ? items : 0;  // (of more cells more would pass than there is room for)
     for (int x0 = warp * kTogether; x0 < once; x0 += kAtOnce * kSelWarps * kTogether) {
@@ -603,8 +606,8 @@ __global__ void __launch_bounds__(kSelThreads, kStages == 4 ? 2 : 3) beam_select
 #pragma unroll
       for (int i = 0; i < kAtOnce; ++i) {
         const int item = x0 + i * kSelWarps * kTogether + lane / kPer;
-        const int h = per_cell == 1 ? item : item / per_cell;
-        t[i] = item < items ? token_of(hit[h], item - h * per_cell, lane % kPer) : -1;
+        const int h = (int)fast_div((uint32_t)item, a.div_cell);
+        t[i] = item < items ? token_of(hit[h], item - h * a.per_cell, lane % kPer) : -1;
         x[i] = raw(max(t[i], begin));
       }
 #pragma unroll
@@ -627,7 +630,7 @@ __global__ void __launch_bounds__(kSelThreads, kStages == 4 ? 2 : 3) beam_select
         for (int h = tid; h < hits; h += kSelThreads) {
           const int c = hit[h];
           if (c == kDone) continue;
-          const float most = bf16_to_f(sm.cell[c % kSelThreads][c / kSelThreads]);
+          const float most = bf16_to_f(sm.cell[c & (kSelThreads - 1)][c >> kLogThreads]);
           if (key_of(most, max(token_of(c, 0, 0), 0)) <= worst) {
             hit[h] = kDone;
             continue;
@@ -640,7 +643,7 @@ __global__ void __launch_bounds__(kSelThreads, kStages == 4 ? 2 : 3) beam_select
         __syncthreads();
         const int picked = min(sm.picked, kSelWarps);
         if (picked == 0) break;
-        for (int d = 0; d < per_cell; ++d) {
+        for (int d = 0; d < a.per_cell; ++d) {
           const int t = warp < picked && lane < kPer ? token_of(sm.pick[warp], d, lane) : -1;
           const float x = t >= 0 ? raw(t) : -INFINITY;
           const unsigned long long key = key_of(x, t);
@@ -719,6 +722,8 @@ cudaError_t launch_beam_select(BeamSelectArgs a, int num_sms, cudaStream_t st) {
   a.part_chunks = (chunks + a.parts - 1) / a.parts;
   a.parts = (chunks + a.part_chunks - 1) / a.part_chunks;
   a.list = std::min(beam_list_most(a.n_cands), kSelKeys / (a.width * a.parts));
+  a.per_cell = (a.part_chunks + kSelCells - 1) / kSelCells;
+  a.div_cell = make_fastdiv((uint32_t)a.per_cell);
   a.div_parts = make_fastdiv((uint32_t)a.parts);
   a.div_width = make_fastdiv((uint32_t)a.width);
   a.div_row_keys = make_fastdiv((uint32_t)(a.parts * a.list));

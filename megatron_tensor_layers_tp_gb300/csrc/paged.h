@@ -139,7 +139,8 @@ struct BeamSelectArgs {
   float* next_scores;
   int32_t *parents, *tokens;
   int parts, part_chunks, list;  // parts of a row, chunks and keys of a part
-  FastDiv div_parts, div_width, div_row_keys;  // by parts, width, parts * list
+  int per_cell;                // chunks of a cell
+  FastDiv div_parts, div_width, div_row_keys, div_cell;  // by parts, width, parts * list, per_cell
   BeamPart* sums;             // [rows][parts]
   unsigned long long* lists;  // [rows][parts][list]
   int* tickets;               // [n_reqs], zero on entry and exit
