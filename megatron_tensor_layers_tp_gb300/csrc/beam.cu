@@ -22,17 +22,20 @@
 // counts from M in the same units: M c - r.  Rows with NaN, and those whose largest
 // logit is beyond 2^20, are summed once more, from M on.
 //
-// 64 requests of 4 rows of 128256 logits, bf16, K = 8: 19.5 us, 65.7 MB from memory (9.7 us at
-// the copy rate).  The last logits are there after 12 us; what follows is a chain of short
-// steps, 7 us in all: the bound 0.8, the cells 1.1, the list 0.4, the ticket 1.1, the rows'
-// sums 1.2, values 0.7, ranks 1.2.  The same rows of 128257 logits, off 16-byte boundaries:
-// 21.7.  13 requests of 16 rows of 152064, fp32, K = 32: 29 us (114 MB: 16.8).  One request of
-// 4 rows of 32000: 8.7 us, the chain alone.  All logits equal: 8 requests of 16 rows, K = 64,
-// 0.3 ms.
+// 64 requests of 4 rows of 128256 logits, bf16, K = 8: 18.4 us, 65.7 MB from memory (9.7 us at
+// the copy rate).  The last logits are there after 11 to 12 us (a chunk takes a warp 240
+// instructions, some 900 cycles, of which it waits 200 for logits); what follows is a chain of
+// short steps, 6 us in all: the bound 0.9, the cells 0.7, the list 0.4, the ticket 0.8, the rows'
+// sums 1.2, values 0.8, ranks 0.6, the next beams 0.3.  Code that a CTA runs once costs its way
+// from L2: what is short wins there over what has more in flight.  The same rows of 128257 logits,
+// off 16-byte boundaries: 20.3.  13 requests of 16 rows of 152064, fp32, K = 32: 27.8 us (114 MB:
+// 16.8).  One request of 4 rows of 32000: 7.6 us, the chain alone.  All logits equal: 8 requests
+// of 16 rows, K = 64, 0.16 ms.
 // Measured before: what passes a running bound pushed to the buffer as it streams by, with a
 // barrier a chunk: 25 and 43 us; the same by plain loads, two CTAs' widths in flight: 105 and
 // 136.  A request's CTAs as a cluster that joins through distributed shared memory: 0.2 to
-// 0.4 us less, for a second way through the join; not kept.
+// 0.4 us less than a ticket between two fences, and as much as the ticket that has them in
+// itself.  The next chunk's words ahead of this one's sums: 0.5 to 1 us more.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <float.h>
@@ -226,10 +229,9 @@ __device__ __noinline__ int rank_keys(SelectSmem& sm, int best, int n, int K) {
 }
 
 // The request's parts joined: its candidates and next beams.  All keys of its lists
-// get their values in fp32, off by at most kNear of their parts; the least of the warps'
-// ceil(K / 8)-th largest lane maxima bounds the K-th value from below, and what may reach
-// it gets its value in 64 bits (of which the GPU does few at a time) and is ranked by
-// counting.
+// get their values in fp32, off by at most kNear of their parts; groups of threads bound the
+// K-th value from below as they do among the logits, and what may reach it gets its value in
+// 64 bits (of which the GPU does few at a time) and is ranked by counting.
 constexpr float kNear = 0x1p-21f;
 __device__ void join_request(const BeamSelectArgs& a, JoinSmem& sm, int req) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -391,7 +393,8 @@ __device__ void join_request(const BeamSelectArgs& a, JoinSmem& sm, int req) {
 
 // kStages: 4, for two CTAs an SM; 3, for three, where there are more CTAs than two an SM (their
 // steps behind the stream then run beside others' streams; us, with four stages and with
-// three: 800 rows of 128256, bf16: 51 and 46; 1024 rows of 8000, fp32: 25 and 21).
+// three: 800 rows of 128256, bf16: 47 and 43; 400: 31 and 24; 1024 rows of 8000, fp32: 23 and 19;
+// 512 rows of 32000, K = 64: 28 and 29).
 template <bool kFp32, int kStages>
 __global__ void __launch_bounds__(kSelThreads, kStages == 4 ? 2 : 3) beam_select_kernel(const BeamSelectArgs a) {
   constexpr int kE = kFp32 ? 4 : 8;            // logits of a 16-byte word
@@ -696,7 +699,7 @@ __global__ void __launch_bounds__(kSelThreads, kStages == 4 ? 2 : 3) beam_select
 }
 
 // Parts of a row: as many as two CTAs an SM allow, and a request's lists have room.  (The two
-// large cases above, us: 21.6 and 31.7 with two CTAs an SM and four stages; three and three
+// large cases above, us, at the time: 21.6 and 31.7 with two CTAs an SM and four stages; three and three
 // 26.2 and 31.4; four and two 25.3 and 34.2.)
 static int parts_most(int64_t rows, int width, int cands, int num_sms) {
   return (int)std::max<int64_t>(1, std::min<int64_t>(2 * num_sms / rows, kSelKeys / (width * cands)));

@@ -10,13 +10,14 @@
 // other between the passes.  A wait gives up after about 2 s and reports it.
 // The counts lie in the workspace, zero between calls.
 //
-// Latency bounds both: dependent look-ups (lengths, tables, counts), 1.5 to 2 us for a
+// Latency bounds both: dependent look-ups (lengths, tables, counts), 1.5 us for a
 // wait of 152 CTAs, and scattered atomics at one a cycle and SM.  128 requests of 8
-// beams, up to 501 pages each, 165000 pages: the fork 13.1 us, of that two waits
-// 3.5.  With 125 CTAs 15.4, with 63 20.7; with the pages of a share looked up again
-// in the last pass, sums over pages and rows one by one and a closing ticket 22.
-// The compaction of 800 such rows, 194000 pages: 15.1 us with three waits; its tables'
-// entries read twice instead of kept in registers, 98 CTAs: 25.7.
+// beams, up to 501 pages each, 165000 pages: the fork 12.5 us, of that two waits
+// 3.  Measured before: waits by fences beside the atomics 13.1; with 125 CTAs 15.4, with 63
+// 20.7; with the pages of a share looked up again in the last pass, sums over pages and rows
+// one by one and a closing ticket 22.  The compaction of 800 such rows, 194000 pages:
+// 14.5 us with three waits (fences beside them 15.1); its tables' entries read twice instead
+// of kept in registers, 98 CTAs: 25.7.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
