@@ -190,6 +190,8 @@ struct ForkArgs {
   int n_seqs, cap;
   const int32_t *old_lens, *src, *keep_lens;
   int32_t *table_out, *new_lens, *moves, *n_moves;
+  int col_tiles, page_share, row_share;  // tiles along a table row; pages and rows of a CTA
+  FastDiv div_cols;                      // by col_tiles
   ShareHeader* head;
   PageNote* notes;
   int* status;
@@ -204,6 +206,8 @@ struct CompactArgs {
   int n_seqs, cap;
   const int32_t* lens;
   int32_t *moves, *n_moves;
+  int col_tiles, page_share, row_share;  // as in a fork
+  FastDiv div_cols;
   ShareHeader* head;
   PageNote* notes;
   int* status;

@@ -12,12 +12,12 @@
 //
 // Latency bounds both: dependent look-ups (lengths, tables, counts), 1.5 us for a
 // wait of 152 CTAs, and scattered atomics at one a cycle and SM.  128 requests of 8
-// beams, up to 501 pages each, 165000 pages: the fork 12.5 us, of that two waits
-// 3.  Measured before: waits by fences beside the atomics 13.1; with 125 CTAs 15.4, with 63
-// 20.7; with the pages of a share looked up again in the last pass, sums over pages and rows
-// one by one and a closing ticket 22.  The compaction of 800 such rows, 194000 pages:
-// 14.5 us with three waits (fences beside them 15.1); its tables' entries read twice instead
-// of kept in registers, 98 CTAs: 25.7.
+// beams, up to 501 pages each, 165000 pages: the fork 11.8 us, of that two waits
+// 3.  Measured before: shares by 64-bit divisions 12.5; waits by fences beside the atomics 13.1;
+// with 125 CTAs 15.4, with 63 20.7; with the pages of a share looked up again in the last pass,
+// sums over pages and rows one by one and a closing ticket 22.  The compaction of 800 such
+// rows, 194000 pages: 14.1 us with three waits (14.5; 15.1); its tables' entries read twice
+// instead of kept in registers, 98 CTAs: 25.7.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -96,11 +96,15 @@ __device__ __forceinline__ void renew_first(ShareHeader* h) {
   if (blockIdx.x == 0 && threadIdx.x == 0) h->arrived[0] = h->bad = 0;
 }
 
-// The CTA's share of n things: [first, end), from a multiple of four on.
-__device__ __forceinline__ void share_of(int n, int* first, int* end) {
-  const int64_t G = gridDim.x, c = blockIdx.x;
-  *first = (int)(c * n / G) & ~3;
-  *end = c + 1 == G ? n : (int)((c + 1) * n / G) & ~3;
+// The CTA's share of n things: [first, end), `share` (a multiple of four) for all but the last ones.
+__device__ __forceinline__ void share_of(int n, int share, int* first, int* end) {
+  *first = (int)min((int64_t)blockIdx.x * share, (int64_t)n);
+  *end = (int)min((int64_t)*first + share, (int64_t)n);
+}
+// A tile's first row and column.
+__device__ __forceinline__ int2 tile_at(int t, int col_tiles, const FastDiv& div_cols) {
+  const int row = (int)fast_div((uint32_t)t, div_cols);
+  return make_int2(row * kShRows, (t - row * col_tiles) * 32);
 }
 
 // What the CTAs before this one counted, and all of them.
@@ -140,7 +144,7 @@ __device__ __forceinline__ uint2 note_of(const PageNote* notes, int p) {
 __device__ __forceinline__ bool is_gone(uint2 note) { return note.x >> 16 && !(note.x & 0xFFFF) && !note.y; }
 
 template <int kThreads>
-__global__ void __launch_bounds__(kThreads) fork_pages_kernel(const ForkArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) fork_pages_kernel(const ForkArgs a) {
   constexpr int kWarps = kThreads / 32;
   __shared__ uint32_t copied[kMaxStepSeqs / 32];  // the CTA's rows that take a page
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -154,10 +158,11 @@ __global__ void __launch_bounds__(kThreads) fork_pages_kernel(const ForkArgs a) 
 
   // Pass 1: references, and the new rows as if no page were copied.
   const int row_tiles = (n + kShRows - 1) / kShRows;
-  const int col_tiles = max(1, (min(a.ld_table, pages(a.cap)) + 31) / 32);
+  const int col_tiles = a.col_tiles;
   // (neighbouring tiles on different SMs: rows that share little take longest)
   for (int t = warp * gridDim.x + blockIdx.x; t < row_tiles * col_tiles; t += gridDim.x * kWarps) {
-    const int b0 = t / col_tiles * kShRows, col0 = t % col_tiles * 32, col = col0 + lane;
+    const int2 at = tile_at(t, col_tiles, a.div_cols);
+    const int b0 = at.x, col0 = at.y, col = col0 + lane;
     // the tile's rows, a lane each: tokens before, source, tokens kept
     const int row = b0 + lane;
     const bool mine = lane < kShRows && row < n;
@@ -248,8 +253,8 @@ __global__ void __launch_bounds__(kThreads) fork_pages_kernel(const ForkArgs a) 
 
   // Pass 2: pages that no row holds any more, rows that take a page.
   int p0, p1, b0, b1;
-  share_of(a.n_pages, &p0, &p1);
-  share_of(n, &b0, &b1);
+  share_of(a.n_pages, a.page_share, &p0, &p1);
+  share_of(n, a.row_share, &b0, &b1);
   bad = __ldcg(&a.head->bad);
   // The thread's pages and row of the share's turn `at`; those of the first turn, mostly the only
   // one, stay in registers for pass 3.
@@ -341,7 +346,7 @@ __global__ void __launch_bounds__(kThreads) fork_pages_kernel(const ForkArgs a) 
 }
 
 template <int kThreads>
-__global__ void __launch_bounds__(kThreads) compact_pages_kernel(const CompactArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) compact_pages_kernel(const CompactArgs a) {
   constexpr int kWarps = kThreads / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n = a.n_seqs, P = a.page_size;
@@ -354,10 +359,11 @@ __global__ void __launch_bounds__(kThreads) compact_pages_kernel(const CompactAr
 
   // A tile's pages, -1 where a row holds none.  The warp's first tile stays in registers.
   const int row_tiles = (n + kShRows - 1) / kShRows;
-  const int col_tiles = max(1, (min(a.ld_table, pages(a.cap)) + 31) / 32);
+  const int col_tiles = a.col_tiles;
   const int tiles = row_tiles * col_tiles, tile0 = warp * gridDim.x + blockIdx.x;
   auto fetch = [&](int t, int (&page)[kShRows]) {
-    const int b0 = t / col_tiles * kShRows, col = t % col_tiles * 32 + lane;
+    const int2 at = tile_at(t, col_tiles, a.div_cols);
+    const int b0 = at.x, col = at.y + lane;
     int len = 0;
     if (lane < kShRows && b0 + lane < n) {
       len = a.lens[b0 + lane];
@@ -402,7 +408,7 @@ __global__ void __launch_bounds__(kThreads) compact_pages_kernel(const CompactAr
   // Pass 2: pages held, by share.
   bad = __ldcg(&a.head->bad);
   int p0, p1;
-  share_of(a.n_pages, &p0, &p1);
+  share_of(a.n_pages, a.page_share, &p0, &p1);
   uint32_t refs[kShPages];  // the thread's pages of a turn; the first turn's stay for pass 3
   const int turns = (p1 - p0 + kShPages * kThreads - 1) / (kShPages * kThreads);
   auto look = [&](int turn) {
@@ -471,7 +477,8 @@ __global__ void __launch_bounds__(kThreads) compact_pages_kernel(const CompactAr
     }
   } else {
     auto rename = [&](int t, int (&page)[kShRows]) {
-      const int b0 = t / col_tiles * kShRows, col = t % col_tiles * 32 + lane;
+      const int2 at = tile_at(t, col_tiles, a.div_cols);
+      const int b0 = at.x, col = at.y + lane;
       int2 note[kShRows];
 #pragma unroll
       for (int r = 0; r < kShRows; ++r)
@@ -502,15 +509,21 @@ __global__ void __launch_bounds__(kThreads) compact_pages_kernel(const CompactAr
 }
 
 // CTAs of 512 threads, one an SM at most; a single one has 256 (two requests of four beams:
-// 6.5 us instead of 7.4).
+// 6.5 us instead of 7.4, and 5.8 with the registers of a whole SM: more look-ups in flight).
 constexpr int kMany = 512, kFew = 256;
 
+static int share_size(int n, int ctas) { return ((n + ctas - 1) / ctas + 3) & ~3; }
+
 template <typename Args>
-static cudaError_t launch_shared(void (*many)(Args), void (*few)(Args), const Args& a, int num_sms,
+static cudaError_t launch_shared(void (*many)(Args), void (*few)(Args), Args a, int num_sms,
                                  cudaStream_t st) {
   const int64_t cols = std::min<int64_t>(a.ld_table, (a.cap + (int64_t)a.page_size - 1) / a.page_size);
   const int64_t tiles = (cols * a.n_seqs + 2047) / 2048, by_pages = (a.n_pages + 2047) / 2048;
   const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(std::max(tiles, by_pages), std::min({num_sms, kShareCtas, kMany})));
+  a.col_tiles = (int)std::max<int64_t>(1, (cols + 31) / 32);
+  a.div_cols = make_fastdiv((uint32_t)a.col_tiles);
+  a.page_share = share_size(a.n_pages, grid);
+  a.row_share = share_size(a.n_seqs, grid);
   if (grid == 1) return launch_k(few, dim3(1), dim3(kFew), 0, st, a);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
