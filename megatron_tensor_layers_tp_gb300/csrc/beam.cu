@@ -146,9 +146,10 @@ struct SelectSmem {
   unsigned long long keys[kSelBuffer + kMaxBeamCands + 2];  // the best so far, then the buffer
   __align__(16) uint16_t cell[kSelThreads][kSelCells];  // bf16, rounded up
   uint64_t full[kSelStages], empty[kSelStages];
-  int many;  // keys in the buffer
+  int many;  // keys in the buffer, while cells are picked
   int hits;  // cells that reach the bound
   int picked, pick[kSelWarps];
+  int warp_many[kSelWarps];
   int last;
   BoundSmem bound;
   uint32_t warp_top[kSelWarps];
@@ -596,13 +597,17 @@ __global__ void __launch_bounds__(kSelThreads, kStages == 4 ? 2 : 3) beam_select
     __syncthreads();
     // Logit i of those that a thread has in chunk d of a cell: its token, or -1.
     auto token_of = [&](int cell, int d, uint32_t i) {
-      const int thread = cell & (kSelThreads - 1), e = (i / kE * kSelThreads + thread) * kE + i % kE;
-      const int64_t t = begin + ((int64_t)(cell >> kLogThreads) * a.per_cell + d) * kChunk + e;
-      return t < end ? (int)t : -1;
+      const int thread = cell & (kSelThreads - 1), in_thread = (int)(i / kE * kSelThreads * kE + i % kE);
+      const int t = begin + ((cell >> kLogThreads) * a.per_cell + d) * kChunk + thread * kE + in_thread;
+      return t < end ? t : -1;  // (in 32 bits: no more than 40 chunks past 2^30)
     };
     const int hits = sm.hits, items = hits * a.per_cell;  // an item: one chunk of a cell
     constexpr int kAtOnce = 4, kTogether = 32 / kPer;  // items that a warp reads at once, by one load
     const int once = hits <= kSelBuffer ? items : 0;  // (of more cells more would pass than there is room for)
+    constexpr int kWarpKeys = 64;  // of a warp, behind the cells' numbers in the ring
+    unsigned long long* mine_keys =
+        reinterpret_cast<unsigned long long*>(ring + kSelCells * kSelThreads * 2) + warp * kWarpKeys;
+    int mine_many = 0;
     for (int x0 = warp * kTogether; x0 < once; x0 += kAtOnce * kSelWarps * kTogether) {
       float x[kAtOnce];
       int t[kAtOnce];
@@ -614,18 +619,29 @@ __global__ void __launch_bounds__(kSelThreads, kStages == 4 ? 2 : 3) beam_select
         x[i] = raw(max(t[i], begin));
       }
 #pragma unroll
-      for (int i = 0; i < kAtOnce; ++i)
-        if (t[i] >= 0 && x[i] >= least) {  // (not NaN)
-          const int to = atomicAdd(&sm.many, 1);
-          if (to < kSelBuffer) sm.keys[to] = key_of(x[i], t[i]);
-        }
+      for (int i = 0; i < kAtOnce; ++i) {
+        const bool p = t[i] >= 0 && x[i] >= least;  // (not NaN)
+        const unsigned m = __ballot_sync(0xffffffffu, p);
+        const int to = mine_many + __popc(m & ((1u << lane) - 1));
+        if (p && to < kWarpKeys) mine_keys[to] = key_of(x[i], t[i]);
+        mine_many += __popc(m);
+      }
     }
+    if (lane == 0) sm.warp_many[warp] = mine_many;
     __syncthreads();
-    int best = 0;
-    if (sm.many > kSelBuffer || hits > kSelBuffer) {  // a warp a cell, of those that can still count, until there are none
-      constexpr uint16_t kDone = 0xFFFF;
+    int best = 0, n = 0, before = 0, longest = 0;
+#pragma unroll
+    for (int q = 0; q < kSelWarps; ++q) {
+      if (q == warp) before = n;
+      n += sm.warp_many[q];
+      longest = max(longest, sm.warp_many[q]);
+    }
+    if (longest <= kWarpKeys && max(n, hits) <= kSelBuffer) {
+      for (int l = lane; l < mine_many; l += 32) sm.keys[before + l] = mine_keys[l];
       __syncthreads();
-      if (tid == 0) sm.many = 0;
+    } else {  // a warp a cell, of those that can still count, until there are none
+      n = 0;
+      constexpr uint16_t kDone = 0xFFFF;
       while (true) {
         if (tid == 0) sm.picked = 0;
         __syncthreads();
@@ -660,7 +676,6 @@ __global__ void __launch_bounds__(kSelThreads, kStages == 4 ? 2 : 3) beam_select
     }
 
     // the part's list and sum
-    const int n = sm.many;
     if (n > a.list) best = rank_keys(sm, 0, n, K);
     else best += n;  // (in any order)
 #pragma unroll
