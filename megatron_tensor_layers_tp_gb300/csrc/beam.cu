@@ -22,15 +22,15 @@
 // counts from M in the same units: M c - r.  Rows with NaN, and those whose largest
 // logit is beyond 2^20, are summed once more, from M on.
 //
-// 64 requests of 4 rows of 128256 logits, bf16, K = 8: 18.4 us, 65.7 MB from memory (9.7 us at
+// 64 requests of 4 rows of 128256 logits, bf16, K = 8: 18.5 us, 65.7 MB from memory (9.7 us at
 // the copy rate).  The last logits are there after 11 to 12 us (a chunk takes a warp 240
 // instructions, some 900 cycles, of which it waits 200 for logits); what follows is a chain of
 // short steps, 6 us in all: the bound 0.9, the cells 0.7, the list 0.4, the ticket 0.8, the rows'
 // sums 1.2, values 0.8, ranks 0.6, the next beams 0.3.  Code that a CTA runs once costs its way
 // from L2: what is short wins there over what has more in flight.  The same rows of 128257 logits,
-// off 16-byte boundaries: 20.3.  13 requests of 16 rows of 152064, fp32, K = 32: 27.8 us (114 MB:
-// 16.8).  One request of 4 rows of 32000: 7.6 us, the chain alone.  All logits equal: 8 requests
-// of 16 rows, K = 64, 0.16 ms.
+// off 16-byte boundaries: 20.5.  13 requests of 16 rows of 152064, fp32, K = 32: 27.8 us (114 MB:
+// 16.8).  One request of 4 rows of 32000: 7.7 us, the chain alone.  All logits equal: 8 requests
+// of 16 rows, K = 64, 0.17 ms.
 // Measured before: what passes a running bound pushed to the buffer as it streams by, with a
 // barrier a chunk: 25 and 43 us; the same by plain loads, two CTAs' widths in flight: 105 and
 // 136.  A request's CTAs as a cluster that joins through distributed shared memory: 0.2 to
@@ -395,7 +395,7 @@ __device__ void join_request(const BeamSelectArgs& a, JoinSmem& sm, int req) {
 // kStages: 4, for two CTAs an SM; 3, for three, where there are more CTAs than two an SM (their
 // steps behind the stream then run beside others' streams; us, with four stages and with
 // three: 800 rows of 128256, bf16: 47 and 43; 400: 31 and 24; 1024 rows of 8000, fp32: 23 and 19;
-// 512 rows of 32000, K = 64: 28 and 29).
+// 512 rows of 32000, K = 64: 28 and 29, before cells were collected by votes).
 template <bool kFp32, int kStages>
 __global__ void __launch_bounds__(kSelThreads, kStages == 4 ? 2 : 3) beam_select_kernel(const BeamSelectArgs a) {
   constexpr int kE = kFp32 ? 4 : 8;            // logits of a 16-byte word
