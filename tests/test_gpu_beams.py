@@ -215,6 +215,29 @@ def test_beam_select_allowed_tokens_in_one_place(first, n):
         check_select(f64(x), scores, 4, K, (), run_select(model(vocab=V), x, scores, 4, K))
 
 
+@pytest.mark.parametrize("fp32", [False, True])
+@pytest.mark.parametrize("whole,single", [(13, 30), (14, 0), (3, 300), (10, 128)])
+def test_beam_select_allowed_tokens_of_few_threads(whole, single, fp32):
+    """The allowed tokens are all that some threads have of a chunk, and one of others: few for
+    the CTA, many for one of its warps."""
+    rng = np.random.default_rng(whole)
+    e = 4 if fp32 else 8  # logits of a 16-byte word; a thread has every 256th of 1024
+    V, rows = 1024 * e, 40
+    x = np.full((rows, V), -np.inf)
+    for row in x:
+        threads = rng.permutation(256)
+        for t in threads[:whole]:
+            for j in range(4):
+                at = (256 * j + t) * e
+                row[at:at + e] = rng.standard_normal(e)
+        for t in threads[whole:whole + single]:
+            row[(256 * rng.integers(4) + t) * e + rng.integers(e)] = rng.standard_normal()
+    x = f32(x) if fp32 else f32(x).bfloat16()
+    scores = np.zeros(rows, dtype=np.float32)
+    for K in (64, 5):
+        check_select(f64(x), scores, 1, K, (), run_select(model(vocab=V), x, scores, 1, K))
+
+
 @pytest.mark.parametrize("tail", [1, 7, 260, 500, 1280, 2047])
 @pytest.mark.parametrize("fp32", [False, True])
 def test_beam_select_short_last_parts(tail, fp32):
