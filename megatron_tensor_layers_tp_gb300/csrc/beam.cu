@@ -552,8 +552,10 @@ __global__ void __launch_bounds__(kSelThreads, kStages == 4 ? 2 : 3) beam_select
       }
     }
 
-    // What the warps know of the sum; the bound, and the cells that reach it.
-    uint32_t o = ordered(top);
+    // What the warps know of the sum; the bound, and the cells that reach it.  (+infinity counts
+    // as the largest number here already: a bound above it would pass over logits that are its
+    // equals.)
+    uint32_t o = ordered(fminf(top, FLT_MAX));
     const uint32_t warp_top = __reduce_max_sync(0xffffffffu, o);
     int r = __reduce_max_sync(0xffffffffu, (int)power);
     auto fixed_sum = [&](float x) {  // of the warp, in multiples of 2^(r - 32)
@@ -575,7 +577,7 @@ __global__ void __launch_bounds__(kSelThreads, kStages == 4 ? 2 : 3) beam_select
     o = sm.warp_top[0];
 #pragma unroll
     for (int q = 1; q < kSelWarps; ++q) o = max(o, sm.warp_top[q]);
-    const float most = fminf(of_ordered(o), FLT_MAX);  // the part's largest
+    const float most = of_ordered(o);  // the part's largest
     v = max(v, ordered(-INFINITY) + 1);  // (-infinity never passes)
     uint16_t* hit = reinterpret_cast<uint16_t*>(ring);  // (no copy is on its way any more)
     const float least = of_ordered(v);

@@ -203,6 +203,24 @@ def test_beam_select_infinities_nan_and_lowest_values(fp32):
     assert b.parents[9:12].tolist() == [-1] * 3
 
 
+@pytest.mark.parametrize("V", [200, 20011, 70000])
+@pytest.mark.parametrize("K", [1, 3, 40])
+def test_beam_select_infinity_ties_with_the_largest_number(V, K):
+    """+infinity counts as the largest fp32 number: whichever has the lower token is first, also
+    where K and more threads hold infinities."""
+    x = np.full((6, V), -1.0)
+    x[0, 5], x[0, 100] = FMAX, np.inf
+    x[1, 5], x[1, 100] = np.inf, FMAX
+    x[2, [17, 50]], x[2, 60:190] = FMAX, np.inf
+    x[3, 60:190], x[3, [61, 100, 189]] = np.inf, FMAX
+    x[4, 3:V:2], x[4, 4:V:2] = np.inf, FMAX
+    x[5, V - 1], x[5, 0] = np.inf, FMAX
+    scores = np.array([-1, -1, -2, -2, -3, 0], dtype=np.float32)
+    check_select(x, scores, 1, K, (), run_select(model(vocab=V), f32(x), scores, 1, K))
+    if K >= 2:
+        check_select(x, scores, 2, K, (), run_select(model(vocab=V), f32(x), scores, 2, K))
+
+
 @pytest.mark.parametrize("first,n", [(0, 300), (40000, 900), (57000, 2000), (8100, 200), (65000, 535)])
 def test_beam_select_allowed_tokens_in_one_place(first, n):
     """A grammar that allows a run of the vocabulary: all other threads see nothing."""
