@@ -760,6 +760,14 @@ tp_status tp_beam_advance(const tp_model* m, int32_t n_rows, const int32_t* pare
                           const int32_t* lens, int32_t* out, int64_t ld_out, int32_t* lens_out,
                           void* stream);
 
+/* The same on rows that lie further apart than they are long: texts end at room (1..ld_history)
+ * and room_out (1..ld_out) ids instead of at the row strides, and nothing behind these is read or
+ * written. */
+tp_status tp_beam_advance_rooms(const tp_model* m, int32_t n_rows, const int32_t* parents,
+                                const int32_t* tokens, const int32_t* history, int64_t ld_history,
+                                int64_t room, const int32_t* lens, int32_t* out, int64_t ld_out,
+                                int64_t room_out, int32_t* lens_out, void* stream);
+
 /* Workspace bytes of tp_fork_pages and tp_compact_pages for caches of up to n_pages
  * pages (0 for sizes outside the limits).  As tp_step_workspace_bytes, apart from it. */
 size_t tp_share_workspace_bytes(const tp_model* m, int32_t n_pages);

@@ -165,6 +165,9 @@ _SIGS = {
                                  c_size_t, c_void_p]),
     "tp_beam_advance": (c_int32, [c_void_p, c_int32, c_void_p, c_void_p, c_void_p, c_int64, c_void_p,
                                   c_void_p, c_int64, c_void_p, c_void_p]),
+    "tp_beam_advance_rooms": (c_int32, [c_void_p, c_int32, c_void_p, c_void_p, c_void_p, c_int64,
+                                        c_int64, c_void_p, c_void_p, c_int64, c_int64, c_void_p,
+                                        c_void_p]),
     "tp_share_workspace_bytes": (c_size_t, [c_void_p, c_int32]),
     "tp_fork_pages": (c_int32, [c_void_p, POINTER(tp_pages_t), POINTER(tp_fork_t), c_void_p, c_size_t,
                                 c_void_p]),
@@ -377,6 +380,12 @@ def tp_beam_advance(model, n_rows, parents, tokens, history, ld_history, lens, o
                     stream) -> int:
     return lib().tp_beam_advance(model, n_rows, parents, tokens, history, ld_history, lens, out, ld_out,
                                  lens_out, stream)
+
+
+def tp_beam_advance_rooms(model, n_rows, parents, tokens, history, ld_history, room, lens, out, ld_out,
+                          room_out, lens_out, stream) -> int:
+    return lib().tp_beam_advance_rooms(model, n_rows, parents, tokens, history, ld_history, room, lens,
+                                       out, ld_out, room_out, lens_out, stream)
 
 
 def tp_share_workspace_bytes(model, n_pages: int) -> int:

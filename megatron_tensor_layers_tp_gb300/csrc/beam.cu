@@ -768,13 +768,13 @@ __global__ void __launch_bounds__(kAdvThreads) beam_advance_kernel(const BeamAdv
   int64_t n = 0;
   if (p >= 0) {
     n = a.lens[p];
-    const int64_t most = min(a.ld, a.ld_out);
+    const int64_t most = min(a.room, a.room_out);
     if (n < 0 || n > most) {
       bad = true;
       n = max((int64_t)0, min(n, most));
     }
   }
-  const bool room = p >= 0 && n < a.ld_out;
+  const bool room = p >= 0 && n < a.room_out;
   if (p >= 0 && !room) bad = true;
   int32_t* out = a.out + row * a.ld_out;
   if (piece == 0 && tid == 0) {
@@ -795,7 +795,7 @@ __global__ void __launch_bounds__(kAdvThreads) beam_advance_kernel(const BeamAdv
 }
 
 cudaError_t launch_beam_advance(const BeamAdvanceArgs& a, cudaStream_t st) {
-  const int pieces = (int)beam_advance_pieces(std::min(a.ld, a.ld_out));
+  const int pieces = (int)beam_advance_pieces(std::min(a.room, a.room_out));
   return launch_k(beam_advance_kernel, dim3((unsigned)((int64_t)a.n_rows * pieces)), dim3(kAdvThreads), 0, st, a,
                   pieces, make_fastdiv((uint32_t)pieces));
 }

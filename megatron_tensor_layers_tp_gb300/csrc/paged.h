@@ -155,7 +155,7 @@ cudaError_t launch_beam_select(BeamSelectArgs a, int num_sms, cudaStream_t st);
 struct BeamAdvanceArgs {
   int n_rows;
   const int32_t *parents, *tokens, *history;
-  int64_t ld, ld_out;
+  int64_t ld, ld_out, room, room_out;  // row strides; ids that a row has room for
   const int32_t* lens;
   int32_t *out, *lens_out;
   int* status;

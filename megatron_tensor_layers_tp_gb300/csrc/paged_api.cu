@@ -438,13 +438,22 @@ tp_status tp_beam_advance(const tp_model* m, int32_t n_rows, const int32_t* pare
                           const int32_t* tokens, const int32_t* history, int64_t ld_history,
                           const int32_t* lens, int32_t* out, int64_t ld_out, int32_t* lens_out,
                           void* stream) {
+  return tp_beam_advance_rooms(m, n_rows, parents, tokens, history, ld_history, ld_history, lens, out,
+                               ld_out, ld_out, lens_out, stream);
+}
+
+tp_status tp_beam_advance_rooms(const tp_model* m, int32_t n_rows, const int32_t* parents,
+                                const int32_t* tokens, const int32_t* history, int64_t ld_history,
+                                int64_t room, const int32_t* lens, int32_t* out, int64_t ld_out,
+                                int64_t room_out, int32_t* lens_out, void* stream) {
   return guarded(m, [&]() -> tp_status {
     if (n_rows < 0) return TP_ERR_ARG;
     if (n_rows == 0) return TP_OK;
-    if (!parents || !tokens || !history || !lens || !out || !lens_out || ld_history < 1 || ld_out < 1)
+    if (!parents || !tokens || !history || !lens || !out || !lens_out || room < 1 || room > ld_history ||
+        room_out < 1 || room_out > ld_out)
       return TP_ERR_ARG;
-    const int64_t room = std::min(ld_history, ld_out);
-    if (room > kMaxLength || n_rows * beam_advance_pieces(room) > INT32_MAX) return TP_ERR_UNSUPPORTED;
+    const int64_t most = std::min(room, room_out);
+    if (most > kMaxLength || n_rows * beam_advance_pieces(most) > INT32_MAX) return TP_ERR_UNSUPPORTED;
     const Span text{history, n_rows * ld_history * 4}, to{out, n_rows * ld_out * 4};
     const Span words[4] = {{parents, n_rows * 4ll}, {tokens, n_rows * 4ll}, {lens, n_rows * 4ll},
                            {lens_out, n_rows * 4ll}};
@@ -459,6 +468,8 @@ tp_status tp_beam_advance(const tp_model* m, int32_t n_rows, const int32_t* pare
     a.history = history;
     a.ld = ld_history;
     a.ld_out = ld_out;
+    a.room = room;
+    a.room_out = room_out;
     a.lens = lens;
     a.out = out;
     a.lens_out = lens_out;

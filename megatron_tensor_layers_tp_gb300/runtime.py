@@ -802,7 +802,8 @@ class TPModel:
                      lens_out: Optional[torch.Tensor] = None, stream=None):
         """Row b of out becomes row parents[b] of history [rows, room] and tokens[b] behind it.
         Returns (out, lens_out); ids of out behind a text are not written (undefined in a buffer
-        allocated here)."""
+        allocated here).  history and out may be views of wider rows: nothing beside them is read
+        or written."""
         n, dev, i32 = parents.shape[0], self.device, torch.int32
         _check(parents, "parents", i32, (n,), dev)
         _check(tokens, "tokens", i32, (n,), dev)
@@ -817,10 +818,11 @@ class TPModel:
             lens_out = self._out((n,), i32, stream)
         else:
             _check(lens_out, "lens_out", i32, (n,), dev)
-        B.check(B.tp_beam_advance(self.handle, n, parents.data_ptr(), tokens.data_ptr(),
-                                  history.data_ptr(), _ld(history), lens.data_ptr(), out.data_ptr(),
-                                  _ld(out), lens_out.data_ptr(), self._stream(stream)),
-                "tp_beam_advance")
+        B.check(B.tp_beam_advance_rooms(self.handle, n, parents.data_ptr(), tokens.data_ptr(),
+                                        history.data_ptr(), _ld(history), history.shape[1],
+                                        lens.data_ptr(), out.data_ptr(), _ld(out), out.shape[1],
+                                        lens_out.data_ptr(), self._stream(stream)),
+                "tp_beam_advance_rooms")
         return out, lens_out
 
     def fork_pages(self, pages: PageTable, fork: PageFork, ws: Optional[torch.Tensor] = None,

@@ -48,6 +48,10 @@ def test_calls_without_a_model_are_rejected():
     assert B.tp_copy_pages(None, p, 0, 0, 1, 1, None, None, 0) == ARG
 
 
+def test_texts_in_views_without_a_model_are_rejected():
+    assert B.tp_beam_advance_rooms(None, 1, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0) == B.STATUS["TP_ERR_ARG"]
+
+
 def ints(*shape):
     return torch.zeros(shape, dtype=torch.int32)
 

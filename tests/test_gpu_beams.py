@@ -398,6 +398,45 @@ def test_beam_advance_bad_parents_lengths_and_full_rows():
         assert m.check_device() == TABLE_RANGE and m.check_device() == 0
 
 
+@pytest.mark.parametrize("n,room,room_out,pad", [(1, 5, 5, 3), (4, 9, 9, 3), (6, 300, 200, 8), (5, 200, 300, 4),
+                                                 (3, 5000, 4999, 1)])
+def test_beam_advance_stays_within_views(n, room, room_out, pad):
+    """Texts that fill their view of a wider row, and lengths beyond it: nothing beside the views is
+    read or written."""
+    rng = np.random.default_rng(n + room)
+    m = model()
+    wide, wide_out = i32(rng.integers(0, 1000, (n, room + pad))), i32(np.full((n, room_out + pad), -3))
+    for off in (0, pad):
+        history, out = wide[:, off:off + room], wide_out[:, off:off + room_out]
+        lens = i32([min(room, room_out) + int(rng.integers(0, pad + 1)) for _ in range(n)])
+        parents, tokens = i32(rng.integers(0, n, n)), i32(rng.integers(1000, 2000, n))
+        wide_out.fill_(-3)
+        before, lens_out = out.tolist(), i32([0] * n)
+        m.beam_advance(parents, tokens, history, lens, out=out, lens_out=lens_out)
+        check_advance(parents, tokens, history, lens, out, lens_out, before)
+        beside = wide_out.clone()
+        beside[:, off:off + room_out] = -3
+        assert (beside == -3).all()
+        full = room >= room_out or any(lens.tolist()[p] > room for p in parents.tolist())
+        assert m.check_device() == (TABLE_RANGE if full else 0)
+
+
+def test_beam_advance_rooms_refusals():
+    m = model()
+    t, o, n, l = i32(np.zeros((4, 10))), i32(np.zeros((4, 10))), i32([1, 2, 3, 0]), i32([0] * 4)
+    p, q = i32([0, 1, 2, 3]), i32([5, 6, 7, 8])
+
+    def advance(ld=10, room=10, ldo=10, room_out=10):
+        return B.tp_beam_advance_rooms(m.handle, 4, p.data_ptr(), q.data_ptr(), t.data_ptr(), ld, room, n.data_ptr(),
+                                       o.data_ptr(), ldo, room_out, l.data_ptr(), 0)
+
+    assert advance() == 0 and advance(room=4, room_out=7) == 0
+    for kw in (dict(room=0), dict(room=11), dict(room_out=0), dict(room_out=11), dict(ld=9), dict(ldo=9)):
+        assert advance(**kw) == B.STATUS["TP_ERR_ARG"], kw
+    torch.cuda.synchronize()
+    m.check_device()
+
+
 # ---------------------------------------------------------------------------
 # forks
 # ---------------------------------------------------------------------------
