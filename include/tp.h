@@ -762,7 +762,7 @@ tp_status tp_beam_advance(const tp_model* m, int32_t n_rows, const int32_t* pare
 
 /* The same on rows that lie further apart than they are long: texts end at room (1..ld_history)
  * and room_out (1..ld_out) ids instead of at the row strides, and nothing behind these is read or
- * written. */
+ * written.  Rows of history and out may lie between each other's. */
 tp_status tp_beam_advance_rooms(const tp_model* m, int32_t n_rows, const int32_t* parents,
                                 const int32_t* tokens, const int32_t* history, int64_t ld_history,
                                 int64_t room, const int32_t* lens, int32_t* out, int64_t ld_out,

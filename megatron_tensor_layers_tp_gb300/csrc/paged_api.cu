@@ -106,6 +106,21 @@ int64_t span_bytes(int64_t rows, int64_t ld, int64_t cols, int elem) {
   return ((rows - 1) * ld + cols) * elem;
 }
 
+// Whether rows of 32-bit words overlap: `cols` of each `ld` from p on.  Rows at one stride may
+// lie between each other's.
+struct Rows {
+  const int32_t* p;
+  int64_t ld, cols;
+};
+bool overlap(const Rows& a, const Rows& b, int64_t rows) {
+  if (!overlap(a.p, span_bytes(rows, a.ld, a.cols, 4), b.p, span_bytes(rows, b.ld, b.cols, 4))) return false;
+  if (a.ld != b.ld) return true;
+  const int64_t ld = a.ld * 4;
+  const int64_t at = (int64_t)(reinterpret_cast<uintptr_t>(b.p) - reinterpret_cast<uintptr_t>(a.p)) % ld;
+  const int64_t behind = at < 0 ? at + ld : at;  // of a row of a: where one of b begins
+  return behind < a.cols * 4 || behind + b.cols * 4 > ld;
+}
+
 // Bytes of a layer's K or V pages.
 int64_t cache_bytes(const tp_config_t& c, const tp_pages_t* p) {
   return (int64_t)c.n_kv_heads * p->n_pages * p->page_size * c.head_dim * 2;
@@ -454,10 +469,13 @@ tp_status tp_beam_advance_rooms(const tp_model* m, int32_t n_rows, const int32_t
       return TP_ERR_ARG;
     const int64_t most = std::min(room, room_out);
     if (most > kMaxLength || n_rows * beam_advance_pieces(most) > INT32_MAX) return TP_ERR_UNSUPPORTED;
-    const Span text{history, n_rows * ld_history * 4}, to{out, n_rows * ld_out * 4};
+    const Span text{history, span_bytes(n_rows, ld_history, room, 4)};
+    const Span to{out, span_bytes(n_rows, ld_out, room_out, 4)};
     const Span words[4] = {{parents, n_rows * 4ll}, {tokens, n_rows * 4ll}, {lens, n_rows * 4ll},
                            {lens_out, n_rows * 4ll}};
-    if (overlap(text, to) || overlap(text, words[3])) return TP_ERR_ARG;
+    if (overlap(Rows{history, ld_history, room}, Rows{out, ld_out, room_out}, n_rows) ||
+        overlap(text, words[3]))
+      return TP_ERR_ARG;
     for (int i = 0; i < 4; ++i)
       if (overlap(to, words[i]) || (i < 3 && overlap(words[3], words[i]))) return TP_ERR_ARG;
     BeamAdvanceArgs a;

@@ -421,6 +421,40 @@ def test_beam_advance_stays_within_views(n, room, room_out, pad):
         assert m.check_device() == (TABLE_RANGE if full else 0)
 
 
+def test_beam_advance_views_that_lie_between_each_other():
+    """Views that share a buffer without overlapping: the end of one's rows beside the other's
+    begin, rows in turns, columns of the same rows.  Those that overlap by a word are refused."""
+    m, n, ld = model(), 4, 10
+    parents, tokens, lens = i32([3, 0, 2, 2]), i32([5, 6, 7, 8]), i32([1, 2, 3, 0])
+
+    def run(history, out):
+        history.copy_(torch.arange(n * history.shape[1]).view(n, -1))
+        out.fill_(-3)
+        before, old, lens_out = out.tolist(), history.clone(), i32([0] * n)
+        m.beam_advance(parents, tokens, history, lens, out=out, lens_out=lens_out)
+        check_advance(parents, tokens, old, lens, out, lens_out, before)
+        assert torch.equal(history, old) and m.check_device() == 0
+
+    flat = i32(np.zeros(2 * n * ld + 3))
+    run(flat[:n * ld].view(n, ld)[:, 3:], flat[n * ld:2 * n * ld].view(n, ld))
+    run(flat[n * ld:2 * n * ld].view(n, ld), flat[:n * ld].view(n, ld)[:, 3:])
+    turns = i32(np.zeros((n, 2, ld)))
+    run(turns[:, 0], turns[:, 1])
+    run(turns[:, 1], turns[:, 0])
+    both = i32(np.zeros((n, 3 * ld)))
+    run(both[:, 3:9], both[:, 9:30])
+    run(both[:, 9:], both[:, 2:9])
+    at = flat.data_ptr()
+    words = [t.data_ptr() for t in (parents, tokens)]
+
+    def refused(shift, room, ldo, room_out):
+        return B.tp_beam_advance_rooms(m.handle, n, *words, at, 2 * ld, room, lens.data_ptr(), at + 4 * shift, ldo, room_out,
+                                       torch.zeros_like(lens).data_ptr(), 0) == B.STATUS["TP_ERR_ARG"]
+
+    assert refused(10, 11, 20, 10) and refused(10, 10, 20, 11) and refused(0, 1, 20, 1) and refused(20, 10, 20, 11)
+    assert refused(10, 10, 19, 9) and refused(20, 1, 20, 1)
+
+
 def test_beam_advance_rooms_refusals():
     m = model()
     t, o, n, l = i32(np.zeros((4, 10))), i32(np.zeros((4, 10))), i32([1, 2, 3, 0]), i32([0] * 4)
