@@ -521,7 +521,9 @@ typedef struct {
                                   free_state it gives the same tables. */
   int32_t* holders;            /* [n_pages] or NULL (no two rows share a page): the rows
                                   that hold each page, written by tp_fork_pages and
-                                  tp_compact_pages.  Of free pages: any number below 2. */
+                                  tp_compact_pages.  Of free pages: any number below 2.
+                                  (A row that names a page in several columns, as padding
+                                  may do, counts as often.) */
 } tp_pages_t;
 
 /* One step of n_seqs sequences: sequence b goes from old_lens[b] to

@@ -166,8 +166,9 @@ cudaError_t launch_beam_advance(const BeamAdvanceArgs& a, cudaStream_t st);
 
 // What the fork and the compaction keep of a page in the workspace.
 struct PageNote {
-  uint32_t refs;   // rows that hold it; fork: before (<< 16) and after, as a full page.  Zero between calls
-  uint32_t first;  // fork: n_seqs - the first row that goes on writing to it.  Zero between calls
+  uint32_t refs;   // how often rows name it; fork: afterwards, as a full page.  Zero between calls
+  uint32_t first;  // fork: 1 + n_seqs - the first row that goes on writing to it, or 1 (held before).
+                   // Zero between calls
   int32_t move;    // compaction: of a page that moves, its move and its rows
   int32_t rows;
 };

@@ -140,8 +140,16 @@ __device__ __forceinline__ uint2 note_of(const PageNote* notes, int p) {
   return __ldcg(reinterpret_cast<const uint2*>(notes + p));
 }
 
+// The note of a page that a fork meets: how often rows name it afterwards as a full page (in 32
+// bits: rows may name one page in many columns, as padding does), and the largest of 1 (rows held
+// it before) and 1 + n - b (row b goes on writing to it).
+__device__ __forceinline__ uint32_t held_mark() { return 1; }
+__device__ __forceinline__ uint32_t open_mark(int n, int row) { return (uint32_t)(n - row) + 1; }
 // A page that rows held before and none holds after.
-__device__ __forceinline__ bool is_gone(uint2 note) { return note.x >> 16 && !(note.x & 0xFFFF) && !note.y; }
+__device__ __forceinline__ bool is_gone(uint2 note) { return !note.x && note.y == held_mark(); }
+__device__ __forceinline__ int holders_of(uint2 note) {
+  return note.x ? (int)min(note.x, (uint32_t)INT32_MAX) : note.y > held_mark();
+}
 
 template <int kThreads>
 __global__ void __launch_bounds__(kThreads, 1) fork_pages_kernel(const ForkArgs a) {
@@ -216,13 +224,13 @@ __global__ void __launch_bounds__(kThreads, 1) fork_pages_kernel(const ForkArgs 
       if (is[r] >= 0) a.table_out[(int64_t)(b0 + r) * a.ld_table + col] = is[r];
       if (open >> r & 1) {
         a.head->open[b0 + r] = is[r];
-        atomicMax(&a.notes[is[r]].first, (uint32_t)(n - b0 - r));
+        atomicMax(&a.notes[is[r]].first, open_mark(n, b0 + r));
         is[r] = -1;  // (counted as full pages below)
       }
       alike = alike && was[r] == was[0] && is[r] == was[0];
     }
     if (__all_sync(kAll, alike)) {
-      if (was[0] >= 0) atomicAdd(&a.notes[was[0]].refs, (uint32_t)kShRows << 16 | kShRows);
+      if (was[0] >= 0) atomicAdd(&a.notes[was[0]].refs, (uint32_t)kShRows);
     } else {  // each page of the tile once
       uint32_t done = 0;  // of `is`: counted with a page of `was`
 #pragma unroll
@@ -232,13 +240,13 @@ __global__ void __launch_bounds__(kThreads, 1) fork_pages_kernel(const ForkArgs 
 #pragma unroll
         for (int q = 0; q < kShRows; ++q) {
           if (q < r) again = again || was[q] == was[r];
-          else if (was[q] == was[r]) refs += 0x10000u;
           if (is[q] == was[r]) {
             refs += 1;
             done |= 1u << q;
           }
         }
-        if (!again) atomicAdd(&a.notes[was[r]].refs, refs);
+        if (!again && refs) atomicAdd(&a.notes[was[r]].refs, refs);
+        else if (!again) atomicMax(&a.notes[was[r]].first, held_mark());
       }
       RefRun after = {0, 0};
 #pragma unroll
@@ -274,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1) fork_pages_kernel(const ForkArgs 
     bool copy = false;
     if (from >= 0) {
       const uint2 x = note_of(a.notes, from);
-      copy = (x.x & 0xFFFF) || x.y != (uint32_t)(n - (b0 + turn * kThreads + tid));
+      copy = x.x || x.y != open_mark(n, b0 + turn * kThreads + tid);
     }
     const unsigned m = __ballot_sync(kAll, copy);
     if (lane == 0 && b0 + turn * kThreads < b1) copied[turn * kWarps + warp] = m;
@@ -315,10 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1) fork_pages_kernel(const ForkArgs 
       *reinterpret_cast<uint2*>(a.notes + page + i) = make_uint2(0, 0);
       if (bad) continue;
       if (is_gone(x)) a.free_ring[ring_at(count + to_ring++)] = page + i;
-      if (a.holders) {
-        const int full = x.x & 0xFFFF;
-        a.holders[page + i] = full ? full : x.y != 0;
-      }
+      if (a.holders) a.holders[page + i] = holders_of(x);
     }
     if (copy) {
       const int full = (int)fast_div((uint32_t)keep, a.div_page);

@@ -534,6 +534,37 @@ def test_fork_pages_most_rows_and_a_large_pool():
     assert m.check_device() == 0
 
 
+@pytest.mark.parametrize("rows,cols", [(4096, 16), (8192, 8), (8192, 9), (64, 1024), (1, 70000)])
+@pytest.mark.parametrize("cut", [0, 3])
+def test_fork_pages_rows_that_name_a_page_many_times(rows, cols, cut):
+    """Padding rows all of whose columns name one scratch page, 2^16 times and more: it stays theirs,
+    as often as they name it, and so does another row's page.  With `cut` they go on writing to it,
+    and all take pages of their own but for the last column."""
+    P, scratch = 8, 7
+    rng = np.random.default_rng(rows + cols)
+    n_pages = 50 + (rows + 1 if cut else 0)
+    table = np.full((rows + 1, cols), scratch)
+    table[rows, 0] = 9
+    c = dict(page=P, n_pages=n_pages, max_ctx=P * cols, table=table.tolist(), lens=[P * cols] * rows + [P],
+             src=list(range(rows + 1)), keep=[P * cols - cut] * rows + [P], first=int(rng.integers(0, n_pages)),
+             count=n_pages - 2)
+    free = [p for p in range(n_pages) if p not in (scratch, 9)]
+    ring = [-9] * n_pages
+    for i, p in enumerate(free):
+        ring[(c["first"] + i) % n_pages] = p
+    c["ring"] = ring
+    if cols > 1 and rows < 8192:
+        pages, fork = device_case(c)
+        model().fork_pages(pages, fork)
+        check_fork(c, pages, fork)
+        assert model().check_device() == 0
+    c.update(table=table[:rows].tolist(), lens=c["lens"][:rows], src=c["src"][:rows], keep=c["keep"][:rows])
+    pages, fork = device_case(c)
+    model().fork_pages(pages, fork)
+    check_fork(c, pages, fork)
+    assert model().check_device() == 0
+
+
 def test_fork_pages_across_requests_and_to_free_rows():
     """Any row may be any row's source: one prompt for all, rows that swap, a kept prefix."""
     rng = np.random.default_rng(22)
