@@ -801,8 +801,8 @@ typedef struct {
  * tp_copy_pages with the moves brings the new pages up to date; the next tp_step_tables
  * takes new table and lengths.  Errors on the device (TP_ERR_TABLE_RANGE): a length below
  * 0, above max_ctx or above ld_table * page_size, a source outside [-1, n_seqs), keep_lens
- * outside [0, old_lens[src]], a page number outside [0, n_pages) in a row, fewer free pages
- * than needed, a ring state outside the ring.  Then the new table and lengths are the old
+ * outside [0, old_lens[src]], a page number outside [0, n_pages) in a row or among the free
+ * ones taken, fewer free pages than needed, a ring state outside the ring.  Then the new table and lengths are the old
  * ones, nothing is moved, free_next = free_state and holders stays. */
 tp_status tp_fork_pages(const tp_model* m, const tp_pages_t* pages, const tp_fork_t* fork,
                         void* ws, size_t ws_bytes, void* stream);

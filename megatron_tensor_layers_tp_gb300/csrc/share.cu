@@ -93,7 +93,7 @@ __device__ __forceinline__ void renew_later(ShareHeader* h) {
   if (blockIdx.x == 0 && threadIdx.x == 0) h->arrived[1] = h->arrived[2] = 0;
 }
 __device__ __forceinline__ void renew_first(ShareHeader* h) {
-  if (blockIdx.x == 0 && threadIdx.x == 0) h->arrived[0] = h->bad = 0;
+  if (blockIdx.x == 0 && threadIdx.x == 0) h->arrived[0] = h->bad = h->bad_ring = 0;
 }
 
 // The CTA's share of n things: [first, end), `share` (a multiple of four) for all but the last ones.
@@ -162,7 +162,17 @@ __global__ void __launch_bounds__(kThreads, 1) fork_pages_kernel(const ForkArgs 
   const int first = a.free_state[0], count = a.free_state[1];
   renew_later(a.head);
   auto pages = [&](int len) { return (int)fast_div((uint32_t)len + P - 1, a.div_page); };
-  bool bad = false;
+  const bool bad_state = first < 0 || first >= a.n_pages || count < 0 || count > a.n_pages;
+  bool bad = bad_state;
+  auto ring_at = [&](int i) {
+    i += first;
+    return i >= a.n_pages ? i - a.n_pages : i;
+  };
+  // The ring's entries that rows may take (one a row at most).  How many they take is known in
+  // pass 3, when it is too late to look at all of them in every CTA: the first bad one counts.
+  const int may_take = bad_state ? 0 : min(n, count);
+  const int entry = blockIdx.x * kThreads + tid;
+  const int page_there = entry < may_take ? a.free_ring[ring_at(entry)] : 0;  // (on its way during pass 1)
 
   // Pass 1: references, and the new rows as if no page were copied.
   const int row_tiles = (n + kShRows - 1) / kShRows;
@@ -255,7 +265,9 @@ __global__ void __launch_bounds__(kThreads, 1) fork_pages_kernel(const ForkArgs 
       after.flush(a.notes);
     }
   }
-  bad = bad || first < 0 || first >= a.n_pages || count < 0 || count > a.n_pages;
+  if ((uint32_t)page_there >= (uint32_t)a.n_pages) atomicMax(&a.head->bad_ring, (unsigned)(n - entry));
+  for (int i = entry + gridDim.x * kThreads; i < may_take; i += gridDim.x * kThreads)
+    if ((uint32_t)a.free_ring[ring_at(i)] >= (uint32_t)a.n_pages) atomicMax(&a.head->bad_ring, (unsigned)(n - i));
   if (__syncthreads_or(bad) && tid == 0) atomicOr(&a.head->bad, 1u);
   if (!grid_wait(a.head, 0, a.status)) return;
 
@@ -264,6 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1) fork_pages_kernel(const ForkArgs 
   share_of(a.n_pages, a.page_share, &p0, &p1);
   share_of(n, a.row_share, &b0, &b1);
   bad = __ldcg(&a.head->bad);
+  const int good_entries = n - (int)__ldcg(&a.head->bad_ring);  // (n: all that rows may take)
   // The thread's pages and row of the share's turn `at`; those of the first turn, mostly the only
   // one, stay in registers for pass 3.
   uint2 note[kShPages];
@@ -299,11 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1) fork_pages_kernel(const ForkArgs 
   renew_first(a.head);
   unsigned long long before = before_this<kThreads>(a.head, &all);
   const int f_all = (int)all, t_all = (int)(all >> 32);
-  bad = bad || t_all > count || count + f_all > a.n_pages;
-  auto ring_at = [&](int i) {
-    i += first;
-    return i >= a.n_pages ? i - a.n_pages : i;
-  };
+  bad = bad || t_all > count || t_all > good_entries || count + f_all > a.n_pages;
   for (int turn = 0; turn < turns; ++turn) {
     if (turn) fetch(turn);
     const int row = b0 + turn * kThreads + tid, page = p0 + (turn * kThreads + tid) * kShPages;
@@ -327,10 +336,8 @@ __global__ void __launch_bounds__(kThreads, 1) fork_pages_kernel(const ForkArgs 
     }
     if (copy) {
       const int full = (int)fast_div((uint32_t)keep, a.div_page);
-      const bool out = (uint32_t)to >= (uint32_t)a.n_pages;
-      if (out) record_status(a.status, kStatusTableRange);
       a.table_out[(int64_t)row * a.ld_table + full] = to;
-      if (a.holders && !out) a.holders[to] = 1;
+      if (a.holders) a.holders[to] = 1;
       a.moves[3 * move] = from;
       a.moves[3 * move + 1] = to;
       a.moves[3 * move + 2] = keep - full * P;

@@ -683,6 +683,40 @@ def test_fork_pages_refuse_as_a_whole(what, reqs):
     assert m.check_device() == 0
 
 
+@pytest.mark.parametrize("bad", [-1, "past", 2**31 - 1, -2**31])
+@pytest.mark.parametrize("reqs,first", [(3, 0), (3, 21), (300, 0), (300, 3000), (2000, 5000)])
+def test_fork_pages_with_bad_free_pages(bad, reqs, first):
+    """A free entry of no page of the cache: refused as a whole when the fork would take it, whether it
+    is the first or the last one, and left where it is when the fork takes fewer."""
+    m, P, W = model(), 8, 4
+    n = W * reqs
+    n_pages = 2 * reqs + (W - 1) * reqs + 40  # two pages a request, W - 1 taken a request
+    first %= n_pages
+    table = np.full((n, 3), -5)
+    table[::W, 0], table[::W, 1] = np.arange(reqs), reqs + np.arange(reqs)
+    lens = np.zeros(n, dtype=np.int64)
+    lens[::W] = 12
+    free = list(range(2 * reqs, n_pages))
+    taken = (W - 1) * reqs
+    for at in (0, 1, taken // 2, taken - 1, taken, len(free) - 1):
+        ring = [-9] * n_pages
+        for i, p in enumerate(free):
+            ring[(first + i) % n_pages] = p
+        ring[(first + at) % n_pages] = n_pages if bad == "past" else bad
+        c = dict(page=P, n_pages=n_pages, max_ctx=24, table=table.tolist(), lens=lens.tolist(), ring=ring, first=first,
+                 count=len(free), src=[b // W * W for b in range(n)], keep=None)
+        pages, fork = device_case(c)
+        m.fork_pages(pages, fork)
+        if at >= taken:
+            check_fork(c, pages, fork)
+            assert m.check_device() == 0
+            continue
+        assert m.check_device() == TABLE_RANGE
+        assert fork.moves.count.item() == 0 and pages.free_next.tolist() == [first, len(free)]
+        assert pages.free_ring.tolist() == ring and pages.holders.tolist() == [-1] * n_pages
+        assert fork.table.tolist() == c["table"] and fork.new_lens.tolist() == c["lens"]
+
+
 def test_step_tables_refuse_to_touch_shared_pages():
     """With holders: a shared page is neither given back nor written to; a row's own pages are."""
     m = model()
