@@ -787,6 +787,9 @@ typedef struct {
   int32_t* new_lens;           /* [n_seqs]; another buffer than old_lens */
   int32_t* moves;              /* [n_seqs][3]: page, new page, tokens (see tp_copy_pages) */
   int32_t* n_moves;            /* [1] */
+  int32_t* holders;            /* [n_pages] or NULL: the new table's holders (pages->holders must
+                                  be there too, and is left as it is).  NULL: written to
+                                  pages->holders */
 } tp_fork_t;
 
 /* Forks, shortens and frees rows of the page table at once.  Full pages are shared.
@@ -796,14 +799,17 @@ typedef struct {
  * kept in it.  Pages that no row holds any more go behind the ring's end, by number
  * (usable from the next call on).  Columns behind a row's pages are not written.
  *   pages : table, free_ring and free_state are read, free_ring, free_next and (when not
- *           NULL) holders written.  As with tp_step_tables a free_next of its own makes
- *           the call a proposal.
+ *           NULL, and the fork has none of its own) holders written.  As with tp_step_tables a
+ *           free_next of its own makes the call a proposal.  With holders it needs holders of
+ *           its own as well: those of pages are the standing table's, and once a call has
+ *           written them for a table that is dropped, tp_step_tables may take shared pages
+ *           for a row's own (until a fork of every row onto itself).
  * tp_copy_pages with the moves brings the new pages up to date; the next tp_step_tables
  * takes new table and lengths.  Errors on the device (TP_ERR_TABLE_RANGE): a length below
  * 0, above max_ctx or above ld_table * page_size, a source outside [-1, n_seqs), keep_lens
  * outside [0, old_lens[src]], a page number outside [0, n_pages) in a row or among the free
  * ones taken, fewer free pages than needed, a ring state outside the ring.  Then the new table and lengths are the old
- * ones, nothing is moved, free_next = free_state and holders stays. */
+ * ones, nothing is moved, free_next = free_state and the holders are the old ones too. */
 tp_status tp_fork_pages(const tp_model* m, const tp_pages_t* pages, const tp_fork_t* fork,
                         void* ws, size_t ws_bytes, void* stream);
 

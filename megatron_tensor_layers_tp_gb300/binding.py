@@ -98,7 +98,7 @@ class tp_beams_t(Structure):
 class tp_fork_t(Structure):
     _fields_ = [("n_seqs", c_int32), ("max_ctx", c_int32)] + \
                [(n, c_void_p) for n in ("old_lens", "src", "keep_lens", "table", "new_lens", "moves",
-                                        "n_moves")]
+                                        "n_moves", "holders")]
 
 
 class TPError(RuntimeError):

@@ -189,6 +189,7 @@ struct ForkArgs {
   int32_t* free_ring;
   const int32_t* free_state;
   int32_t *free_next, *holders;
+  const int32_t* old_holders;  // not null: holders is another buffer, of which every page is written
   int n_seqs, cap;
   const int32_t *old_lens, *src, *keep_lens;
   int32_t *table_out, *new_lens, *moves, *n_moves;

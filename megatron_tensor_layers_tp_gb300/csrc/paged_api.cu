@@ -510,16 +510,18 @@ tp_status tp_fork_pages(const tp_model* m, const tp_pages_t* pages, const tp_for
     if (s != TP_OK) return s;
     if (!fork || fork->n_seqs < 1 || fork->max_ctx < 0 || pages->ld_table < 1 || !pages->table ||
         !pages->free_ring || !pages->free_state || !pages->free_next || !fork->old_lens || !fork->src ||
-        !fork->table || !fork->new_lens || !fork->moves || !fork->n_moves)
+        !fork->table || !fork->new_lens || !fork->moves || !fork->n_moves ||
+        (fork->holders && !pages->holders))
       return TP_ERR_ARG;
     if (fork->n_seqs > kMaxStepSeqs) return TP_ERR_UNSUPPORTED;
     const int64_t n = fork->n_seqs, table = n * pages->ld_table * 4;
-    const Span out[7] = {{fork->table, table}, {fork->new_lens, n * 4}, {fork->moves, n * 12},
-                         {fork->n_moves, 4}, {pages->free_ring, pages->n_pages * 4ll},
-                         {pages->free_next, 8}, {pages->holders, pages->holders ? pages->n_pages * 4ll : 0}};
+    const int64_t ring = pages->n_pages * 4ll;
+    const Span out[8] = {{fork->table, table}, {fork->new_lens, n * 4}, {fork->moves, n * 12},
+                         {fork->n_moves, 4}, {pages->free_ring, ring}, {pages->free_next, 8},
+                         {pages->holders, pages->holders ? ring : 0}, {fork->holders, fork->holders ? ring : 0}};
     const Span in[5] = {{pages->table, table}, {fork->old_lens, n * 4}, {fork->src, n * 4},
                         {fork->keep_lens, fork->keep_lens ? n * 4 : 0}, {pages->free_state, 8}};
-    for (int i = 0; i < 7; ++i) {
+    for (int i = 0; i < 8; ++i) {
       for (int j = 0; j < i; ++j)
         if (overlap(out[i], out[j])) return TP_ERR_ARG;
       for (int j = 0; j < 5; ++j)
@@ -537,7 +539,8 @@ tp_status tp_fork_pages(const tp_model* m, const tp_pages_t* pages, const tp_for
     a.free_ring = pages->free_ring;
     a.free_state = pages->free_state;
     a.free_next = pages->free_next;
-    a.holders = pages->holders;
+    a.holders = fork->holders ? fork->holders : pages->holders;
+    a.old_holders = fork->holders ? pages->holders : nullptr;
     a.n_seqs = fork->n_seqs;
     a.cap = length_cap(pages, fork->max_ctx);
     a.old_lens = fork->old_lens;

@@ -302,6 +302,12 @@ __global__ void __launch_bounds__(kThreads, 1) fork_pages_kernel(const ForkArgs 
     taken += copy;
 #pragma unroll
     for (int i = 0; i < kShPages; ++i) freed += is_gone(note[i]);
+    if (a.old_holders) {  // (before the pages that rows take get theirs)
+      const int page = p0 + (turn * kThreads + tid) * kShPages;
+#pragma unroll
+      for (int i = 0; i < kShPages; ++i)
+        if (page + i < p1) a.holders[page + i] = holders_of(note[i]);
+    }
   }
   unsigned long long all;
   block_scan<kThreads>(two(freed, taken), &all);
@@ -332,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1) fork_pages_kernel(const ForkArgs 
       *reinterpret_cast<uint2*>(a.notes + page + i) = make_uint2(0, 0);
       if (bad) continue;
       if (is_gone(x)) a.free_ring[ring_at(count + to_ring++)] = page + i;
-      if (a.holders) a.holders[page + i] = holders_of(x);
+      if (a.holders && !a.old_holders) a.holders[page + i] = holders_of(x);
     }
     if (copy) {
       const int full = (int)fast_div((uint32_t)keep, a.div_page);
@@ -348,6 +354,8 @@ __global__ void __launch_bounds__(kThreads, 1) fork_pages_kernel(const ForkArgs 
     const int64_t words = (int64_t)n * a.ld_table;
     for (int64_t i = (int64_t)blockIdx.x * kThreads + tid; i < words; i += (int64_t)gridDim.x * kThreads)
       a.table_out[i] = a.table[i];
+    if (a.old_holders)
+      for (int p = p0 + tid; p < p1; p += kThreads) a.holders[p] = a.old_holders[p];
   }
   if (blockIdx.x == 0 && tid == 0) {
     if (bad) record_status(a.status, kStatusTableRange);

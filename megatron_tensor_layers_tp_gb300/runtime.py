@@ -147,10 +147,14 @@ class PageTable:
                    torch.tensor([0, n_pages], dtype=torch.int32, device=device),
                    holders=torch.zeros(n_pages, dtype=torch.int32, device=device) if shared else None)
 
-    def with_table(self, table: torch.Tensor) -> "PageTable":
-        """The same pages, ring and ring state behind another table: what a fork writes to."""
-        return PageTable(self.page_size, table, self.free_ring, self.free_state, self.free_next,
-                         self.n_pages, self.holders)
+    def with_table(self, table: torch.Tensor, free_state: Optional[torch.Tensor] = None,
+                   holders: Optional[torch.Tensor] = None) -> "PageTable":
+        """The same pages, ring and ring state behind another table: what a fork writes to.  For a
+        proposal that is kept, with the state (its free_next) and the holders that it left."""
+        return PageTable(self.page_size, table, self.free_ring,
+                         self.free_state if free_state is None else free_state,
+                         self.free_next if free_state is None else None, self.n_pages,
+                         self.holders if holders is None else holders)
 
 
 class Step:
@@ -346,37 +350,44 @@ class PageFork:
     (None: all) of row src[b] (-1: none).
 
     old_lens, src, keep_lens [n_seqs] int32.  fork_pages fills table (of the page table's shape, in
-    another buffer), new_lens and moves (room for n_seqs).
+    another buffer), new_lens and moves (room for n_seqs), and holders [n_pages] int32 (None: the
+    page table's).  A fork that may be dropped again (free_next of its own) of a table with holders
+    needs holders of its own.
     """
 
     def __init__(self, max_ctx: int, old_lens: torch.Tensor, src: torch.Tensor,
                  keep_lens: Optional[torch.Tensor], table: torch.Tensor, new_lens: torch.Tensor,
-                 moves: PageMoves):
+                 moves: PageMoves, holders: Optional[torch.Tensor] = None):
         n, dev = old_lens.numel(), old_lens.device
         for name, t in (("old_lens", old_lens), ("src", src), ("keep_lens", keep_lens),
                         ("new_lens", new_lens)):
             if t is not None:
                 _check(t, name, torch.int32, (n,), dev)
         _check(table, "table", torch.int32, (None, None), dev)
+        if holders is not None:
+            _check(holders, "holders", torch.int32, (None,), dev)
         if moves.most < n or moves.table.device != dev:
             raise ValueError(f"moves: room for {n} on {dev} expected")
         self.n_seqs, self.max_ctx = n, max_ctx
         self.old_lens, self.src, self.keep_lens = old_lens, src, keep_lens
-        self.table, self.new_lens, self.moves = table, new_lens, moves
+        self.table, self.new_lens, self.moves, self.holders = table, new_lens, moves, holders
         c = self.c = B.tp_fork_t()
         c.n_seqs, c.max_ctx = n, max_ctx
         c.old_lens, c.src, c.keep_lens = _ptr(old_lens), _ptr(src), _ptr(keep_lens)
         c.table, c.new_lens = _ptr(table), _ptr(new_lens)
         c.moves, c.n_moves = moves._ptrs
+        c.holders = _ptr(holders)
 
     @classmethod
     def alloc(cls, pages: PageTable, max_ctx: int, old_lens: torch.Tensor, src: torch.Tensor,
-              keep_lens: Optional[torch.Tensor] = None,
-              table: Optional[torch.Tensor] = None) -> "PageFork":
-        """With its outputs (the table too, unless it is given) allocated."""
+              keep_lens: Optional[torch.Tensor] = None, table: Optional[torch.Tensor] = None,
+              own_holders: bool = False) -> "PageFork":
+        """With its outputs (the table too, unless it is given) allocated, holders of its own
+        among them where the fork may be dropped again."""
         return cls(max_ctx, old_lens, src, keep_lens,
                    torch.zeros_like(pages.table) if table is None else table,
-                   torch.zeros_like(old_lens), PageMoves.alloc(old_lens.numel(), old_lens.device))
+                   torch.zeros_like(old_lens), PageMoves.alloc(old_lens.numel(), old_lens.device),
+                   torch.zeros_like(pages.holders) if own_holders else None)
 
 
 class LayerPages:
@@ -837,6 +848,8 @@ class TPModel:
                 fork.table.device != self.device:
             raise ValueError("the page tables differ in row length, have too few rows, or are on "
                              "another device")
+        if fork.holders is not None and (pages.holders is None or fork.holders.numel() != pages.n_pages):
+            raise ValueError(f"the fork's holders: {pages.n_pages} of a page table with holders expected")
         if ws is None:
             ws = self.ensure_share_workspace(pages.n_pages, stream)
         B.check(B.tp_fork_pages(self.handle, pages.c, fork.c, *self._ws_args(ws),

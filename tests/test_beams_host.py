@@ -101,6 +101,27 @@ def test_fork_and_moves_checks():
             PageMoves(*bad)
 
 
+def test_holders_of_a_fork():
+    p = PageTable.alloc(3, 10, 16, 33, device="cpu", shared=True)
+    f = PageFork.alloc(p, 33, ints(3), ints(3), own_holders=True)
+    assert f.holders.shape == (10,) and f.c.holders == f.holders.data_ptr() != p.c.holders
+    assert not PageFork.alloc(p, 33, ints(3), ints(3)).c.holders
+    state = ints(2)
+    q = p.with_table(f.table, state, f.holders)
+    assert q.c.free_state == q.c.free_next == state.data_ptr() and q.c.holders == f.c.holders
+    assert q.c.free_ring == p.c.free_ring
+    with pytest.raises(ValueError):
+        PageFork(33, ints(3), ints(3), None, ints(3, 3), ints(3), PageMoves.alloc(3, device="cpu"), ints(10).long())
+    ws = torch.empty(1 << 16, dtype=torch.uint8)
+    with pytest.raises(B.TPError):  # on to the call
+        TPModel.fork_pages(Host(), p, f, ws=ws)
+    plain = PageTable.alloc(3, 10, 16, 33, device="cpu")
+    few = PageTable.alloc(3, 9, 16, 33, device="cpu", shared=True)
+    for pages in (plain, few):
+        with pytest.raises(ValueError):
+            TPModel.fork_pages(Host(), pages, f, ws=ws)
+
+
 def test_layer_pages_checks():
     def page(n=3):
         return torch.zeros((2, n, 1, 8, 64), dtype=torch.bfloat16)

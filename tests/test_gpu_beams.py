@@ -683,6 +683,83 @@ def test_fork_pages_refuse_as_a_whole(what, reqs):
     assert m.check_device() == 0
 
 
+def test_fork_pages_dropped_proposal():
+    """A fork with ring state and holders of its own can be dropped: the standing table's pages are
+    guarded as before.  One that is kept guards the new table's."""
+    m, P = model(), 8
+    pages = PageTable.alloc(3, 30, P, 80, shared=True)
+    m.step_tables(pages, Step.alloc(3, 100, 80, 80, i32([0, 0, 0]), i32([36, 0, 20])))
+    fork = PageFork.alloc(pages, 80, i32([36, 0, 20]), i32([0, 0, 2]))
+    m.fork_pages(pages, fork)
+    now = pages.with_table(fork.table)
+    lens = [36, 36, 20]
+    before = now.holders.tolist()
+    state = i32([0, 0])
+    propose = PageTable(P, now.table, now.free_ring, now.free_state, state, holders=now.holders)
+    new = PageFork.alloc(propose, 80, i32(lens), i32([0, -1, -1]), own_holders=True)
+    new.holders.fill_(9)
+    m.fork_pages(propose, new)
+    held = new.table[0, :5].tolist()
+    assert now.holders.tolist() == before and max(before) == 2
+    assert new.holders.tolist() == [int(p in held) for p in range(30)]
+
+    def step(pages, old, lens_):
+        s = Step.alloc(3, 20, 20, 80, i32(old), i32(lens_))
+        m.step_tables(PageTable(P, pages.table.clone(), pages.free_ring.clone(), pages.free_state.clone(),
+                                holders=pages.holders), s)
+        return m.check_device()
+
+    # dropped: row 1's pages are still row 0's too, what it has of its own may be given back
+    assert step(now, lens, [36, 0, 20]) == TABLE_RANGE and step(now, [36, 31, 20], [36, 32, 20]) == TABLE_RANGE
+    assert step(now, lens, [36, 32, 20]) == 0 and step(now, lens, [36, 36, 0]) == 0
+    # and a proposal that would share row 2's pages leaves them its own
+    other = PageFork.alloc(propose, 80, i32(lens), i32([2, 2, 2]), own_holders=True)
+    m.fork_pages(propose, other)
+    assert now.holders.tolist() == before and step(now, lens, [36, 36, 0]) == 0
+    # kept: the other way around
+    m.fork_pages(propose, new)
+    kept = now.with_table(new.table, state, new.holders)
+    assert step(kept, [36, 0, 0], [0, 0, 9]) == 0 and step(kept, [31, 0, 0], [32, 0, 0]) == 0
+
+
+@pytest.mark.parametrize("reqs,width,page,max_len", [(1, 1, 8, 0), (1, 4, 16, 100), (40, 8, 16, 500), (1000, 8, 64, 300)])
+def test_fork_pages_into_holders_of_its_own(reqs, width, page, max_len):
+    """Every page's number is written, whatever the buffer held; a refused fork leaves the old ones."""
+    rng = np.random.default_rng(reqs + max_len)
+    m = model()
+    c = fork_case(rng, reqs, width, page, max_len)
+    pages, fork = device_case(c)
+    own = PageFork(c["max_ctx"], fork.old_lens, fork.src, fork.keep_lens, fork.table, fork.new_lens, fork.moves,
+                   i32(np.full(c["n_pages"], 1 << 20)))
+    m.fork_pages(pages, own)
+    assert pages.holders.tolist() == [-1] * c["n_pages"] and m.check_device() == 0
+    held = R.fork(c["table"], c["lens"], c["src"], c["keep"], c["page"], c["ring"], c["first"], c["count"])[-1]
+    assert own.holders.tolist() == [held.get(p, 0) for p in range(c["n_pages"])]
+    pages.holders.copy_(torch.arange(c["n_pages"]))
+    fork.src[0] = -2
+    m.fork_pages(pages, own)
+    assert m.check_device() == TABLE_RANGE
+    assert own.holders.tolist() == pages.holders.tolist() == list(range(c["n_pages"]))
+
+
+def test_fork_pages_holders_refusals():
+    rng = np.random.default_rng(25)
+    m = model()
+    pages, fork = device_case(fork_case(rng, 2, 2, 8, 50))
+    own, ws = torch.zeros_like(pages.holders), m.share_workspace(pages.n_pages)
+
+    def call(its_own, **over):
+        return B.tp_fork_pages(m.handle, altered(pages.c, over), altered(fork.c, dict(holders=its_own)), ws.data_ptr(),
+                               ws.numel(), 0)
+
+    assert call(own.data_ptr()) == 0
+    for its_own, over in ((own.data_ptr(), dict(holders=0)), (pages.c.holders, {}), (pages.c.holders + 4, {}),
+                          (pages.c.free_ring, {}), (fork.c.src, {}), (pages.c.free_state, {})):
+        assert call(its_own, **over) == B.STATUS["TP_ERR_ARG"]
+    torch.cuda.synchronize()
+    m.check_device()
+
+
 @pytest.mark.parametrize("bad", [-1, "past", 2**31 - 1, -2**31])
 @pytest.mark.parametrize("reqs,first", [(3, 0), (3, 21), (300, 0), (300, 3000), (2000, 5000)])
 def test_fork_pages_with_bad_free_pages(bad, reqs, first):
