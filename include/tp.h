@@ -818,14 +818,14 @@ tp_status tp_fork_pages(const tp_model* m, const tp_pages_t* pages, const tp_for
  * to the next.
  *   lens  : [n_seqs] (1..8192: every row that holds pages); max_ctx as in tp_fork_t
  *   to    : its table, free_ring, free_next and (when not NULL) holders are written, each
- *           in a buffer of its own or that of pages; n_pages, page_size and ld_table
- *           are those of pages.  The ring becomes 0, 1, 2, ... with the pages from U on
+ *           in a buffer of its own or that of pages (what is pages' own is lost for the old
+ *           table); n_pages, page_size and ld_table are those of pages.  The ring becomes 0, 1, 2, ... with the pages from U on
  *           free.  Columns behind a row's pages are not written.
  *   moves : [max_moves][3] with max_moves >= n_pages / 2, n_moves [1]; for tp_copy_pages
  *           (whole pages)
  * Afterwards n_pages could be made U.  Errors on the device (TP_ERR_TABLE_RANGE): a length
- * or a page number out of bounds as for tp_fork_pages.  Then table, ring and state are
- * those of pages and nothing is moved. */
+ * or a page number out of bounds as for tp_fork_pages.  Then table, ring, state and (where
+ * pages has them) holders are those of pages and nothing is moved. */
 tp_status tp_compact_pages(const tp_model* m, const tp_pages_t* pages, const tp_pages_t* to,
                            int32_t n_seqs, int32_t max_ctx, const int32_t* lens,
                            int32_t* moves, int32_t max_moves, int32_t* n_moves, void* ws,

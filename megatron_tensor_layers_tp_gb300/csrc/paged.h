@@ -206,6 +206,7 @@ struct CompactArgs {
   FastDiv div_page;
   const int32_t *table, *ring, *free_state;
   int32_t *table_out, *ring_out, *free_next, *holders;
+  const int32_t* old_holders;  // not null: holders is another buffer
   int n_seqs, cap;
   const int32_t* lens;
   int32_t *moves, *n_moves;

@@ -576,13 +576,13 @@ tp_status tp_compact_pages(const tp_model* m, const tp_pages_t* pages, const tp_
     // (in and out of the same index may be the same buffer)
     const Span out[6] = {{to->table, table}, {to->free_ring, ring}, {to->free_next, 8},
                          {to->holders, to->holders ? ring : 0}, {moves, max_moves * 12ll}, {n_moves, 4}};
-    const Span in[4] = {{pages->table, table}, {pages->free_ring, ring}, {pages->free_state, 8},
-                        {lens, n * 4}};
+    const Span in[5] = {{pages->table, table}, {pages->free_ring, ring}, {pages->free_state, 8},
+                        {pages->holders, pages->holders ? ring : 0}, {lens, n * 4}};
     for (int i = 0; i < 6; ++i) {
       for (int j = 0; j < i; ++j)
         if (overlap(out[i], out[j])) return TP_ERR_ARG;
-      for (int j = 0; j < 4; ++j)
-        if (overlap(out[i], in[j]) && !(i == j && i < 3 && out[i].p == in[j].p)) return TP_ERR_ARG;
+      for (int j = 0; j < 5; ++j)
+        if (overlap(out[i], in[j]) && !(i == j && i < 4 && out[i].p == in[j].p)) return TP_ERR_ARG;
     }
     if (!ws || !aligned16(ws) || ws_bytes < tp_share_workspace_bytes(m, pages->n_pages))
       return TP_ERR_WORKSPACE;
@@ -599,6 +599,7 @@ tp_status tp_compact_pages(const tp_model* m, const tp_pages_t* pages, const tp_
     a.ring_out = to->free_ring;
     a.free_next = to->free_next;
     a.holders = to->holders;
+    a.old_holders = to->holders && to->holders != pages->holders ? pages->holders : nullptr;
     a.n_seqs = n_seqs;
     a.cap = length_cap(pages, max_ctx);
     a.lens = lens;

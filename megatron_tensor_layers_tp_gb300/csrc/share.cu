@@ -470,6 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1) compact_pages_kernel(const Compac
       if (refs[i]) a.notes[p].refs = 0;
       if (bad) {
         if (a.ring_out != a.ring) a.ring_out[p] = a.ring[p];
+        if (a.old_holders) a.holders[p] = a.old_holders[p];
         continue;
       }
       a.ring_out[p] = p;

@@ -890,6 +890,31 @@ def test_compact_pages_refuse_as_a_whole(what, in_place):
     assert out.holders.tolist() == [-1] * c["n_pages"]
 
 
+@pytest.mark.parametrize("rows", [2, 700])
+def test_compact_pages_refused_leaves_the_old_holders(rows):
+    """Into separate buffers: what a refused compaction leaves there is guarded as the old table is."""
+    m, P, n_pages = model(), 8, 3 * rows
+    table = np.arange(3 * rows).reshape(rows, 3)
+    table[:, 0] = 0
+    held = np.zeros(n_pages, dtype=np.int64)
+    np.add.at(held, table.ravel(), 1)
+    table[rows // 2, 1] = n_pages
+    pages = PageTable(P, i32(table), i32(np.arange(n_pages)), i32([0, 0]), holders=i32(held))
+    out = PageTable.alloc(rows, n_pages, P, 24, shared=True)
+    m.compact_pages(pages, i32([24] * rows), 24, PageMoves.alloc(n_pages // 2), out=out)
+    assert m.check_device() == TABLE_RANGE and m.check_device() == 0
+    assert out.table.tolist() == table.tolist() and out.holders.tolist() == held.tolist()
+    plain = PageTable(P, pages.table, pages.free_ring, pages.free_state)  # (without holders there are none to keep)
+    out.holders.fill_(-1)
+    m.compact_pages(plain, i32([24] * rows), 24, PageMoves.alloc(n_pages // 2), out=out)
+    assert m.check_device() == TABLE_RANGE and out.holders.tolist() == [-1] * n_pages
+    with pytest.raises(B.TPError):
+        both = i32(np.zeros(n_pages + 1))
+        pages = PageTable(P, pages.table, pages.free_ring, pages.free_state, holders=both[:-1])
+        m.compact_pages(pages, i32([24] * rows), 24, PageMoves.alloc(n_pages // 2),
+                        out=PageTable(P, out.table, out.free_ring, out.free_state, holders=both[1:]))
+
+
 # ---------------------------------------------------------------------------
 # copies
 # ---------------------------------------------------------------------------
