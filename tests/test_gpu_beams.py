@@ -350,6 +350,92 @@ def test_beam_select_many_rows_and_one_workspace():
     assert not ws[:8192 * 4].any()
 
 
+@pytest.mark.parametrize("V,fp32", [(70000, False), (73729, False), (36000, True), (40003, True)])
+def test_beam_select_more_ctas_than_two_an_sm(V, fp32):
+    """Whole rows of nine and more chunks, more of them than two CTAs an SM take at once: the ring of
+    three stages is gone through three times over."""
+    W = 4
+    rows = 2 * torch.cuda.get_device_properties(0).multi_processor_count // W * W + 4 * W
+    rng = np.random.default_rng(V)
+    x, scores = beams_case(rng, rows // W, W, V, fp32, idle=0.05)
+    check_select(f64(x), scores, W, 10, (3,), run_select(model(vocab=V), x, scores, W, 10, (3,)))
+
+
+@pytest.mark.parametrize("R_,W,K,V,fp32", [(1, 32, 64, 262145, True), (1, 32, 64, 400001, False), (103, 3, 6, 170001, True)])
+def test_beam_select_cells_of_several_chunks(R_, W, K, V, fp32):
+    """Parts of more than 40 chunks: rows that may not be cut, or are too many to be."""
+    rng = np.random.default_rng(V)
+    x, scores = beams_case(rng, R_, W, V, fp32)
+    check_select(f64(x), scores, W, K, (9,), run_select(model(vocab=V), x, scores, W, K, (9,)))
+
+
+@pytest.mark.parametrize("shape", ["equal", "rising", "steps", "late"])
+@pytest.mark.parametrize("V,fp32", [(262145, True), (400001, False)])
+def test_beam_select_cells_of_several_chunks_that_flood_the_bound(V, fp32, shape):
+    v = np.arange(V, dtype=np.float64)
+    row = dict(equal=0 * v, rising=v / V * 30, steps=np.floor(v / 5000),
+               late=np.where(v >= V - 900, 5.0 + v / V, 0.0))[shape]
+    x = f32(row).repeat(32, 1)
+    x = x if fp32 else x.bfloat16()
+    scores = np.full(32, -90.0, dtype=np.float32)
+    scores[[4, 20]] = -1.0
+    b = run_select(model(vocab=V), x, scores, 32, 64)
+    check_select(f64(x), scores, 32, 64, (), b)
+    assert set(b.cand_rows[0].tolist()) <= {4, 20}
+
+
+def tight_tol(V, fp32):
+    """What a candidate's value may be off by, with the additions that a thread makes: its exponentials
+    are good to 2^-22 and their arguments to 2^-24 of them twice (log2(e) and the product's rounding), of
+    the distance that averages at most log V, and half a unit's that sums count in; a chunk's are
+    added as two times two sums (fp32: 4 additions deep, bf16: 8), those in two more, chunks in
+    one more each, with a factor good to 2^-22 each and at the end; the 256 threads' sums of a part round
+    to multiples of 2^-32 (half of one), eight warps' and the part's lose up to one, of at least
+    2^-0.5; the logarithm is good to 10^-8."""
+    chunks = -(-V // (4096 if fp32 else 8192))
+    deep = (4 if fp32 else 8) + 2 + chunks
+    return 2**-22 + 2**-24 * (2 * np.log(V) + 0.5) + deep * 2**-24 + (chunks + 1) * 2**-22 + \
+        chunks * (256 * 2**-33 + 9 * 2**-32) * 2**0.5 + 1e-8
+
+
+@pytest.mark.parametrize("fp32", [False, True])
+@pytest.mark.parametrize("R_,W,V", [(20, 4, 4096), (20, 4, 8191), (1, 4, 128256), (40, 4, 32003), (100, 4, 50000)])
+def test_beam_select_sums_as_good_as_their_additions(R_, W, V, fp32):
+    rng = np.random.default_rng(V + R_)
+    x, _ = beams_case(rng, R_, W, V, fp32)
+    scores = (-2 * rng.random(R_ * W)).astype(np.float32)
+    K, t = 16, tight_tol(V, fp32)
+    b = run_select(model(vocab=V), x, scores, W, K)
+    x = f64(x)
+    for r, (pool, _) in enumerate(R.select(x, scores, W, K)):
+        rows, tokens, got = b.cand_rows[r].tolist(), b.cand_tokens[r].tolist(), b.cand_scores[r].double().tolist()
+        values = {row: R.row_values(x[row], scores[row]) for row in range(r * W, r * W + W)}
+        for i, (v, row, token) in enumerate(pool):
+            assert abs(got[i] - values[rows[i]][tokens[i]]) <= t + 2**-24 * abs(v)
+            assert (rows[i], tokens[i]) == (row, token) or abs(values[rows[i]][tokens[i]] - v) <= 2 * t
+
+
+@pytest.mark.parametrize("fp32", [False, True])
+@pytest.mark.parametrize("V,least", [(9001, 2000), (128256, 100000), (50001, 40000), (700, 1)])
+def test_beam_select_exact_sums_and_order(V, least, fp32):
+    """Rows that allow n tokens, all of logit 0: sums of ones, which are exact, so that values are
+    -log n to 10^-8 (and the written ones' rounding) and of two rows the one that allows a token
+    less comes first, wherever the tokens lie."""
+    rng = np.random.default_rng(V)
+    n, R_, W, K = V - least, 12, 2, 2
+    x = np.full((R_ * W, V), -np.inf)
+    for r in range(R_):
+        m = least + int(rng.integers(0, n))
+        for w, many in enumerate((m, m + 1) if r % 2 else (m + 1, m)):
+            x[2 * r + w, rng.permutation(V)[:many]] = 0
+    scores = np.repeat(-rng.integers(0, 3, R_), W).astype(np.float32)
+    b = run_select(model(vocab=V), f32(x) if fp32 else f32(x).bfloat16(), scores, W, K)
+    for r, (pool, _) in enumerate(R.select(x, scores, W, K)):
+        for i, (v, row, token) in enumerate(pool):
+            assert (b.cand_rows[r, i].item(), b.cand_tokens[r, i].item()) == (row, token)
+            assert abs(b.cand_scores[r, i].item() - v) <= 2**-24 * abs(v) + 1e-8
+
+
 # ---------------------------------------------------------------------------
 # texts
 # ---------------------------------------------------------------------------
@@ -396,6 +482,26 @@ def test_beam_advance_bad_parents_lengths_and_full_rows():
         m.beam_advance(i32(parents), i32(range(100, 106)), history, i32(lens), out=out, lens_out=lens_out)
         check_advance(i32(parents), i32(range(100, 106)), history, i32(lens), out, lens_out, before)
         assert m.check_device() == TABLE_RANGE and m.check_device() == 0
+
+
+@pytest.mark.parametrize("n,ld,pad,full", [(1, 1, 0, False), (1, 1, 0, True), (5, 9, 0, False), (12, 300, 3, False),
+                                           (64, 4096, 0, True), (7, 5000, 1, True)])
+def test_beam_advance_into_outputs_of_its_own(n, ld, pad, full):
+    rng = np.random.default_rng(n + ld)
+    m = model()
+    history = i32(rng.integers(0, 1000, (n, ld + pad)))[:, :ld]
+    lens = rng.integers(0, ld, n)
+    parents = rng.integers(-1, n, n)
+    parents[0] = n - 1
+    lens[n - 1] = ld if full else ld - 1
+    tokens = rng.integers(0, 1000, n)
+    out, lens_out = m.beam_advance(i32(parents), i32(tokens), history, i32(lens))
+    assert m.check_device() == (TABLE_RANGE if full else 0)
+    assert out.shape == history.shape and lens_out.shape == (n,)
+    old = history.tolist()
+    for b, p in enumerate(parents):
+        text = (old[p][:lens[p]] + [int(tokens[b])])[:ld] if p >= 0 else []
+        assert lens_out[b].item() == len(text) and out[b, :len(text)].tolist() == text
 
 
 @pytest.mark.parametrize("n,room,room_out,pad", [(1, 5, 5, 3), (4, 9, 9, 3), (6, 300, 200, 8), (5, 200, 300, 4),
