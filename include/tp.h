@@ -506,7 +506,8 @@ tp_status tp_selftest_wait_timeout(tp_model* m, int32_t milliseconds, void* stre
  * tp_load_shards ran on. */
 
 /* The page tables.  page_size: a multiple of 8, 8..65536, and n_pages *
- * page_size < 2^31 (TP_ERR_UNSUPPORTED otherwise). */
+ * page_size < 2^31 (TP_ERR_UNSUPPORTED otherwise).  Zero the structure before
+ * filling it: a pointer that a call may do without (holders) is then NULL. */
 typedef struct {
   int32_t n_pages;
   int32_t page_size;
@@ -744,7 +745,10 @@ size_t tp_beam_workspace_bytes(const tp_model* m, int32_t n_reqs, int32_t width,
  *            tp_process_logits write), row stride ld_logits >= vocab.  Rows not in use
  *            are not read.
  * Outputs overlap neither the inputs (but next_scores) nor each other.  vocab up to 2^30
- * (TP_ERR_UNSUPPORTED above).  Deterministic. */
+ * (TP_ERR_UNSUPPORTED above).  Deterministic: equal calls give equal bits, and equal rows of a
+ * call equal sums.  How a row's sum is grouped goes by the number of rows (and SMs), though: in
+ * another batch a request's scores may differ in the last bits of their sums, and candidates as
+ * close as that may come in the other order. */
 tp_status tp_beam_select(const tp_model* m, const void* logits, int64_t ld_logits, int32_t fp32,
                          const tp_beams_t* beams, void* ws, size_t ws_bytes, void* stream);
 
@@ -775,7 +779,7 @@ tp_status tp_beam_advance_rooms(const tp_model* m, int32_t n_rows, const int32_t
 size_t tp_share_workspace_bytes(const tp_model* m, int32_t n_pages);
 
 /* A fork of the page table: row b goes on as the first keep_lens[b] tokens of row
- * src[b]. */
+ * src[b].  Zero it before filling it, as tp_pages_t. */
 typedef struct {
   int32_t n_seqs;              /* 1..8192: every row that holds pages */
   int32_t max_ctx;             /* host: no length is larger */

@@ -310,8 +310,10 @@ class Beams:
     def alloc(cls, n_reqs: int, width: int, n_cands: Optional[int] = None,
               ends: Optional[torch.Tensor] = None, scores: Optional[torch.Tensor] = None,
               in_place: bool = False, device="cuda") -> "Beams":
-        """With its outputs allocated.  n_cands: by default enough for every next beam to be found,
-        width * (1 + ends), up to 64.  scores: by default those of a first step, one beam a request
+        """With its outputs allocated.  n_cands: by default width * (1 + ends), which is enough for
+        every next beam to be found, but 64 at most: where that is less (32 beams and two ending
+        ids, say), candidates that end their texts can leave next beams without a parent although
+        the request has continuations.  scores: by default those of a first step, one beam a request
         in use.  in_place: next_scores is scores."""
         if n_cands is None:
             n_cands = min(width * (1 + (0 if ends is None else ends.numel())), B.MAX_BEAM_CANDS)
