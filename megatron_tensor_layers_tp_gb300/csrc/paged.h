@@ -175,7 +175,6 @@ struct PageNote {
 constexpr int kShareCtas = 1024;  // CTAs at most
 struct ShareHeader {
   unsigned arrived[3], bad;  // CTAs at each barrier; the verdict (the first and it are zero between calls)
-  unsigned bad_ring, unused;       // fork: n_seqs - the first free entry of no page of the cache; zero between calls
   int2 counts[kShareCtas];         // of each CTA's pages and rows
   int32_t open[kMaxStepSeqs];      // fork: the page that each row goes on writing to, or -1
 };

@@ -93,7 +93,7 @@ __device__ __forceinline__ void renew_later(ShareHeader* h) {
   if (blockIdx.x == 0 && threadIdx.x == 0) h->arrived[1] = h->arrived[2] = 0;
 }
 __device__ __forceinline__ void renew_first(ShareHeader* h) {
-  if (blockIdx.x == 0 && threadIdx.x == 0) h->arrived[0] = h->bad = h->bad_ring = 0;
+  if (blockIdx.x == 0 && threadIdx.x == 0) h->arrived[0] = h->bad = 0;
 }
 
 // The CTA's share of n things: [first, end), `share` (a multiple of four) for all but the last ones.
@@ -145,6 +145,9 @@ __device__ __forceinline__ uint2 note_of(const PageNote* notes, int p) {
 // it before) and 1 + n - b (row b goes on writing to it).
 __device__ __forceinline__ uint32_t held_mark() { return 1; }
 __device__ __forceinline__ uint32_t open_mark(int n, int row) { return (uint32_t)(n - row) + 1; }
+// The verdict on a fork: this, or n - i where entry i is the first of the free ones that names no
+// page of the cache (it counts when rows take as many), or 0.
+constexpr unsigned kRefused = 0x80000000u;
 // A page that rows held before and none holds after.
 __device__ __forceinline__ bool is_gone(uint2 note) { return !note.x && note.y == held_mark(); }
 __device__ __forceinline__ int holders_of(uint2 note) {
@@ -162,18 +165,12 @@ __global__ void __launch_bounds__(kThreads, 1) fork_pages_kernel(const ForkArgs 
   const int first = a.free_state[0], count = a.free_state[1];
   renew_later(a.head);
   auto pages = [&](int len) { return (int)fast_div((uint32_t)len + P - 1, a.div_page); };
-  const bool bad_state = first < 0 || first >= a.n_pages || count < 0 || count > a.n_pages;
-  bool bad = bad_state;
+  bool bad = false;
   auto ring_at = [&](int i) {
     i += first;
     return i >= a.n_pages ? i - a.n_pages : i;
   };
-  // The ring's entries that rows may take (one a row at most).  How many they take is known in
-  // pass 3, when it is too late to look at all of them in every CTA: the first bad one counts.
-  const int may_take = bad_state ? 0 : min(n, count);
-  const int entry = blockIdx.x * kThreads + tid;
-  const int page_there = entry < may_take ? a.free_ring[ring_at(entry)] : 0;  // (on its way during pass 1)
-
+  auto ring_is_bad = [&] { return first < 0 || first >= a.n_pages || count < 0 || count > a.n_pages; };
   // Pass 1: references, and the new rows as if no page were copied.
   const int row_tiles = (n + kShRows - 1) / kShRows;
   const int col_tiles = a.col_tiles;
@@ -265,18 +262,22 @@ __global__ void __launch_bounds__(kThreads, 1) fork_pages_kernel(const ForkArgs 
       after.flush(a.notes);
     }
   }
-  if ((uint32_t)page_there >= (uint32_t)a.n_pages) atomicMax(&a.head->bad_ring, (unsigned)(n - entry));
-  for (int i = entry + gridDim.x * kThreads; i < may_take; i += gridDim.x * kThreads)
-    if ((uint32_t)a.free_ring[ring_at(i)] >= (uint32_t)a.n_pages) atomicMax(&a.head->bad_ring, (unsigned)(n - i));
-  if (__syncthreads_or(bad) && tid == 0) atomicOr(&a.head->bad, 1u);
+  // The ring's entries that rows may take, one a row: how many they do take is known in pass 3 only.
+  // The last warps begin, which mostly had no tile (1024 rows 11.4 us; by the first ones, before their tiles, 11.9).
+#pragma unroll 1
+  for (int i = ((kWarps - 1 - warp) * gridDim.x + blockIdx.x) * 32 + lane; i < n; i += gridDim.x * kThreads)
+    if (!ring_is_bad() && i < count && (uint32_t)a.free_ring[ring_at(i)] >= (uint32_t)a.n_pages)
+      atomicMax(&a.head->bad, (unsigned)(n - i));
+  bad = bad || ring_is_bad();
+  if (__syncthreads_or(bad) && tid == 0) atomicMax(&a.head->bad, kRefused);
   if (!grid_wait(a.head, 0, a.status)) return;
 
   // Pass 2: pages that no row holds any more, rows that take a page.
   int p0, p1, b0, b1;
   share_of(a.n_pages, a.page_share, &p0, &p1);
   share_of(n, a.row_share, &b0, &b1);
-  bad = __ldcg(&a.head->bad);
-  const int good_entries = n - (int)__ldcg(&a.head->bad_ring);  // (n: all that rows may take)
+  const unsigned verdict = __ldcg(&a.head->bad);
+  bad = verdict == kRefused;
   // The thread's pages and row of the share's turn `at`; those of the first turn, mostly the only
   // one, stay in registers for pass 3.
   uint2 note[kShPages];
@@ -318,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1) fork_pages_kernel(const ForkArgs 
   renew_first(a.head);
   unsigned long long before = before_this<kThreads>(a.head, &all);
   const int f_all = (int)all, t_all = (int)(all >> 32);
-  bad = bad || t_all > count || t_all > good_entries || count + f_all > a.n_pages;
+  bad = bad || t_all > count || t_all > n - (int)verdict || count + f_all > a.n_pages;
   for (int turn = 0; turn < turns; ++turn) {
     if (turn) fetch(turn);
     const int row = b0 + turn * kThreads + tid, page = p0 + (turn * kThreads + tid) * kShPages;
