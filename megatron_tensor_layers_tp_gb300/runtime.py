@@ -822,18 +822,21 @@ class TPModel:
         _check(tokens, "tokens", i32, (n,), dev)
         _check(lens, "lens", i32, (n,), dev)
         # (any row length, but named: the whole check of a contiguous tensor is its first line)
-        _check(history, "history", i32, (n, history.shape[-1]), dev, rows=True)
+        room = room_out = history.shape[-1]
+        _check(history, "history", i32, (n, room), dev, rows=True)
         if out is None:
-            out = self._out(history.shape, i32, stream)
+            out = self._out((n, room), i32, stream)
         else:
-            _check(out, "out", i32, (n, out.shape[-1]), dev, rows=True)
+            room_out = out.shape[-1]
+            _check(out, "out", i32, (n, room_out), dev, rows=True)
         if lens_out is None:
             lens_out = self._out((n,), i32, stream)
         else:
             _check(lens_out, "lens_out", i32, (n,), dev)
         B.check(B.tp_beam_advance_rooms(self.handle, n, parents.data_ptr(), tokens.data_ptr(),
-                                        history.data_ptr(), _ld(history), history.shape[1],
-                                        lens.data_ptr(), out.data_ptr(), _ld(out), out.shape[1],
+                                        history.data_ptr(), history.stride(0) if n > 1 else room, room,
+                                        lens.data_ptr(), out.data_ptr(),
+                                        out.stride(0) if n > 1 else room_out, room_out,
                                         lens_out.data_ptr(), self._stream(stream)),
                 "tp_beam_advance_rooms")
         return out, lens_out
