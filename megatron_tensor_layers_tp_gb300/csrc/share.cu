@@ -12,11 +12,11 @@
 //
 // Latency bounds both: dependent look-ups (lengths, tables, counts), 1.5 us for a
 // wait of 152 CTAs, and scattered atomics at one a cycle and SM.  128 requests of 8
-// beams, up to 501 pages each, 165000 pages: the fork 11.8 us, of that two waits
+// beams, up to 501 pages each, 165000 pages: the fork 11.4 to 11.7 us, of that two waits
 // 3.  Measured before: shares by 64-bit divisions 12.5; waits by fences beside the atomics 13.1;
 // with 125 CTAs 15.4, with 63 20.7; with the pages of a share looked up again in the last pass,
 // sums over pages and rows one by one and a closing ticket 22.  The compaction of 800 such
-// rows, 194000 pages: 14.1 us with three waits (14.5; 15.1); its tables' entries read twice
+// rows, 194000 pages: 13.8 to 14.1 us with three waits (14.5; 15.1); its tables' entries read twice
 // instead of kept in registers, 98 CTAs: 25.7.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -531,7 +531,8 @@ __global__ void __launch_bounds__(kThreads, 1) compact_pages_kernel(const Compac
 }
 
 // CTAs of 512 threads, one an SM at most; a single one has 256 (two requests of four beams:
-// 6.5 us instead of 7.4, and 5.8 with the registers of a whole SM: more look-ups in flight).
+// 6.5 us instead of 7.4, and 5.8 with the registers of a whole SM: more look-ups in flight; 5.9 with
+// the ring's entries looked at).
 constexpr int kMany = 512, kFew = 256;
 
 static int share_size(int n, int ctas) { return ((n + ctas - 1) / ctas + 3) & ~3; }
