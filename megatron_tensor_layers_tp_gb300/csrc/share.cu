@@ -171,6 +171,7 @@ __global__ void __launch_bounds__(kThreads, 1) fork_pages_kernel(const ForkArgs 
     return i >= a.n_pages ? i - a.n_pages : i;
   };
   auto ring_is_bad = [&] { return first < 0 || first >= a.n_pages || count < 0 || count > a.n_pages; };
+
   // Pass 1: references, and the new rows as if no page were copied.
   const int row_tiles = (n + kShRows - 1) / kShRows;
   const int col_tiles = a.col_tiles;
@@ -263,7 +264,8 @@ __global__ void __launch_bounds__(kThreads, 1) fork_pages_kernel(const ForkArgs 
     }
   }
   // The ring's entries that rows may take, one a row: how many they do take is known in pass 3 only.
-  // The last warps begin, which mostly had no tile (1024 rows 11.4 us; by the first ones, before their tiles, 11.9).
+  // The last warps begin, which mostly had no tile (1024 rows 11.4 us; by the first ones, before
+  // their tiles, 11.9).
 #pragma unroll 1
   for (int i = ((kWarps - 1 - warp) * gridDim.x + blockIdx.x) * 32 + lane; i < n; i += gridDim.x * kThreads)
     if (!ring_is_bad() && i < count && (uint32_t)a.free_ring[ring_at(i)] >= (uint32_t)a.n_pages)
